@@ -1,0 +1,74 @@
+// Launch interface of the linear attention with a decay for each head
+// (decay_api.cu and the kernels behind it).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+namespace gdr {
+
+// Pointers and sizes as documented in include/gdr.h. Strides are elements
+// between consecutive tokens; a head's channels are dense and head h of q and k
+// starts at (h / (H / Hk)) * dk.
+struct DecayArgs {
+  const void *q, *k, *v, *dO;
+  const float *g, *h0, *dhT;
+  void *o, *dq, *dk, *dv;
+  float *hT, *dg, *dh0;
+  int B, T, H, Hk, nk, nv;      // nk, nv: key and value widths
+  long long sq, sk, sv;
+  bool per_head;                // g is [H] instead of [B, T, H]
+  float scale;
+};
+
+// One call's cut of the sequences: `segments` runs of `seg_len` tokens (whole
+// chunks; the last may be shorter), and the workspace's arrays. States are
+// [B * H, slots, nk, nv] fp32.
+struct DecaySplit {
+  int segments = 1;
+  int seg_len = 0;
+  int slots = 0;              // state slots per (batch, head)
+  int parts = 1;              // partial sums of each boundary dot product
+  float* S = nullptr;         // slot p: the state entering segment p
+  float* D = nullptr;         // slot p: the gradient of that state (backward)
+  float* decay = nullptr;     // [B * H, segments] product of a segment's decays
+  float* dots = nullptr;      // [B * H, slots, parts] partial <S_p, D_p>
+  float* flow_f = nullptr;    // [B * H, T] read-out terms of the gate's gradient
+  float* flow_r = nullptr;    // [B * H, T] the other terms
+  float* dq_part = nullptr;   // [B, T, H, nk] per-head gradients of shared q, k
+  float* dk_part = nullptr;
+  float* dg_part = nullptr;   // [B * H, segments] sums for a per-head decay
+};
+
+// A log-decay at or below this clears the state: exp() of it is zero in fp32.
+constexpr float kDecayReset = -104.f;
+
+// Split-tf32 warp products (decay_warp.cu).
+cudaError_t launch_decay_states_warp(const DecayArgs& a, const DecaySplit& sp, bool reverse,
+                                     bool f32, cudaStream_t stream);
+cudaError_t launch_decay_fwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,
+                                  cudaStream_t stream);
+cudaError_t launch_decay_bwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,
+                                  cudaStream_t stream);
+// Chains the segments' states (decay_chain.cu); backward also chains the
+// states' gradients and writes the boundary dot products.
+cudaError_t launch_decay_chain(const DecayArgs& a, const DecaySplit& sp, bool backward,
+                               cudaStream_t stream);
+// The gate's gradient from the flow terms, and the sums over shared heads.
+cudaError_t launch_decay_gate_grad(const DecayArgs& a, const DecaySplit& sp, bool f32,
+                                   cudaStream_t stream);
+
+struct DecayStepArgs {
+  const void *q, *k, *v;
+  const float* g;
+  float* state;
+  void* o;
+  int N, H, Hk;
+  long long sq, sk, sv;
+  bool per_head;
+  float scale;
+};
+cudaError_t launch_decay_step(const DecayStepArgs& a, int nk, int nv, bool f32,
+                              cudaStream_t stream);
+
+}  // namespace gdr

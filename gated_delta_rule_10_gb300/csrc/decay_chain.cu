@@ -1,0 +1,189 @@
+// What joins the segments of the linear attention with a decay for each head:
+// the chain of the segments' states, and the gate's gradient.
+#include "common.cuh"
+#include "decay.h"
+
+namespace gdr {
+namespace {
+
+constexpr int kChainThreads = 256;
+
+__device__ __forceinline__ float block_sum(float x, float* red) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kChainThreads / 32; ++i) s += red[i];
+  return s;
+}
+
+// S_p = decay_{p-1} S_{p-1} + (segment p-1's own state), S_0 = h0; in place over
+// the slots, each thread carrying one float4 of the state along the chain (the
+// loads of the segments' own states do not wait for it). Backward: D_p =
+// decay_p D_{p+1} + (segment p's own gradient), D_P = dhT, and this block's part
+// of <S_p, D_p> for every p >= 1.
+template <bool BWD>
+__global__ void __launch_bounds__(kChainThreads) chain_kernel(const DecayArgs a,
+                                                              const DecaySplit sp) {
+  __shared__ float red[kChainThreads / 32];
+  const int bh = blockIdx.y, el = (blockIdx.x * kChainThreads + threadIdx.x) * 4;
+  const size_t st = static_cast<size_t>(a.nk) * a.nv;
+  float4* S = reinterpret_cast<float4*>(sp.S + bh * sp.slots * st + el);
+  const float* decay = sp.decay + static_cast<size_t>(bh) * sp.segments;
+  const size_t step = st / 4;
+  float4 s = a.h0 ? *reinterpret_cast<const float4*>(a.h0 + bh * st + el)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+  S[0] = s;
+#pragma unroll 4
+  for (int p = 1; p < sp.slots; ++p) {
+    const float4 x = S[p * step];
+    const float d = decay[p - 1];
+    s = make_float4(fmaf(d, s.x, x.x), fmaf(d, s.y, x.y), fmaf(d, s.z, x.z), fmaf(d, s.w, x.w));
+    S[p * step] = s;
+  }
+  if (!BWD) return;
+  float4* D = reinterpret_cast<float4*>(sp.D + bh * sp.slots * st + el);
+  float4 d = a.dhT ? *reinterpret_cast<const float4*>(a.dhT + bh * st + el)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = sp.segments; p >= 1; --p) {
+    if (p < sp.segments) {
+      const float4 x = D[p * step];
+      const float f = decay[p];
+      d = make_float4(fmaf(f, d.x, x.x), fmaf(f, d.y, x.y), fmaf(f, d.z, x.z), fmaf(f, d.w, x.w));
+    }
+    D[p * step] = d;
+    const float4 x = S[p * step];
+    const float dot = block_sum(x.x * d.x + x.y * d.y + x.z * d.z + x.w * d.w, red);
+    if (threadIdx.x == 0)
+      sp.dots[(static_cast<size_t>(bh) * sp.slots + p) * sp.parts + blockIdx.x] = dot;
+  }
+}
+
+// dg_t = <S, D> at the segment's end + sum of flow_j over the segment's tokens
+// j >= t; a clearing token has gradient 0 and nothing passes it. Tokens are
+// taken 256 at a time from the end; a step is the map x -> keep x + add, and
+// maps compose.
+__global__ void __launch_bounds__(kChainThreads) gate_grad_kernel(const DecayArgs a,
+                                                                  const DecaySplit sp) {
+  constexpr int kWarps = kChainThreads / 32;
+  __shared__ float w_add[kWarps];
+  __shared__ int w_keep[kWarps];
+  __shared__ float red[kWarps];
+  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+  const int t0 = seg * sp.seg_len, t1 = min(a.T, t0 + sp.seg_len);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float carry = 0.f, total = 0.f;
+  if (sp.dots)
+    for (int i = 0; i < sp.parts; ++i)
+      carry += sp.dots[(static_cast<size_t>(bh) * sp.slots + seg + 1) * sp.parts + i];
+  for (int end = t1; end > t0; end -= kChainThreads) {
+    const int t = end - 1 - static_cast<int>(threadIdx.x);
+    float add = 0.f;
+    int keep = 1;
+    const bool in = t >= t0;
+    const size_t at = (static_cast<size_t>(b) * a.T + t) * a.H + h;
+    if (in) {
+      const float g = a.per_head ? a.g[h] : a.g[at];
+      const size_t f = static_cast<size_t>(bh) * a.T + t;
+      add = sp.flow_f[f] + sp.flow_r[f];
+      if (g <= kDecayReset) {
+        keep = 0;
+        add = 0.f;
+      }
+    }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, add, off);
+      const int k = __shfl_up_sync(0xffffffffu, keep, off);
+      if (lane >= off && keep) add += y;
+      if (lane >= off) keep &= k;
+    }
+    if (lane == 31) {
+      w_add[warp] = add;
+      w_keep[warp] = keep;
+    }
+    __syncthreads();
+    float x = carry, next = carry;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i == warp) x = next;
+      next = w_keep[i] ? next + w_add[i] : w_add[i];
+    }
+    const float out = keep ? x + add : add;
+    carry = next;
+    if (in) {
+      if (a.per_head) total += out;
+      else a.dg[at] = out;
+    }
+    __syncthreads();
+  }
+  if (a.per_head) {
+    const float s = block_sum(total, red);
+    if (threadIdx.x == 0) sp.dg_part[static_cast<size_t>(bh) * sp.segments + seg] = s;
+  }
+}
+
+// Sum over batches and segments of a fixed decay's gradient, one warp per head.
+__global__ void __launch_bounds__(32) head_grad_kernel(const DecayArgs a, const DecaySplit sp) {
+  const int h = blockIdx.x, n = a.B * sp.segments;
+  float s = 0.f;
+  for (int i = threadIdx.x; i < n; i += 32)
+    s += sp.dg_part[(static_cast<size_t>(i / sp.segments) * a.H + h) * sp.segments +
+                    i % sp.segments];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (threadIdx.x == 0) a.dg[h] = s;
+}
+
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  uint2 u = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+// Gradients of a q and k head shared by `r` heads: the sum of theirs.
+template <typename T>
+__global__ void __launch_bounds__(256) shared_grad_kernel(const DecayArgs a, const DecaySplit sp,
+                                                          size_t n4, int r) {
+  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const float* src = blockIdx.y ? sp.dk_part : sp.dq_part;
+  T* dst = static_cast<T*>(blockIdx.y ? a.dk : a.dq);
+  const int v = a.nk / 4;
+  const size_t head = i / v;      // token * Hk + shared head
+  const int c = static_cast<int>(i % v) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < r; ++j) {
+    const float4 x = *reinterpret_cast<const float4*>(src + (head * r + j) * a.nk + c);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  store4(dst + head * a.nk + c, s);
+}
+
+}  // namespace
+
+cudaError_t launch_decay_chain(const DecayArgs& a, const DecaySplit& sp, bool backward,
+                               cudaStream_t stream) {
+  const dim3 grid(a.nk * a.nv / (4 * kChainThreads), a.B * a.H);
+  if (backward) chain_kernel<true><<<grid, kChainThreads, 0, stream>>>(a, sp);
+  else chain_kernel<false><<<grid, kChainThreads, 0, stream>>>(a, sp);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decay_gate_grad(const DecayArgs& a, const DecaySplit& sp, bool f32,
+                                   cudaStream_t stream) {
+  gate_grad_kernel<<<dim3(sp.segments, a.B * a.H), kChainThreads, 0, stream>>>(a, sp);
+  if (a.per_head) head_grad_kernel<<<a.H, 32, 0, stream>>>(a, sp);
+  if (sp.dq_part) {
+    const size_t n4 = static_cast<size_t>(a.B) * a.T * a.Hk * (a.nk / 4);
+    const dim3 grid(static_cast<unsigned>((n4 + 255) / 256), 2);
+    if (f32) shared_grad_kernel<float><<<grid, 256, 0, stream>>>(a, sp, n4, a.H / a.Hk);
+    else shared_grad_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, sp, n4, a.H / a.Hk);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace gdr

@@ -1,0 +1,174 @@
+// Single-token step of the linear attention with a decay for each head (decode):
+//   S <- e^g S + k v^T,   o = s S^T q,
+// one state of d_k x d_v per (sequence, head). Reading and writing the states
+// once (8 d_k d_v bytes each) is all the work there is, so the kernel is a
+// stream: one persistent CTA per SM walks the (sequence, head) items, their
+// states come in by bulk copies through a ring of three shared-memory stages,
+// two loads ahead, and go back by bulk stores. A thread owns four consecutive
+// value columns of d_k / RG rows; the read-out needs one sum over the row groups.
+#include "common.cuh"
+#include "decay.h"
+#include "tc.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStages = 3;
+
+template <int NK, int NV, int RG, int CG>
+struct __align__(16) Shared {
+  uint64_t full[4];   // kStages used; keeps what follows 16-byte aligned
+  float q[NK], k[NK], v[NV];
+  float4 red[RG][CG];
+  float alpha[4];
+};
+
+template <int NK, int NV, typename T>
+__global__ void __launch_bounds__(kThreads, 1) decay_step_kernel(const DecayStepArgs a) {
+  constexpr int CG = NV / 4, RG = kThreads / CG, RPT = NK / RG;
+  constexpr uint32_t kBytes = NK * NV * 4;
+  static_assert(NK <= kThreads && NV <= kThreads, "one element of each vector per thread");
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ Shared<NK, NV, RG, CG> sh;
+  const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
+  const int items = a.N * a.H, stride = static_cast<int>(gridDim.x), rep = a.H / a.Hk;
+  const int cnt = (items - static_cast<int>(blockIdx.x) + stride - 1) / stride;
+  const uint32_t rb = smem_u32(ring), fb = smem_u32(sh.full);
+  auto item = [&](int j) { return static_cast<int>(blockIdx.x) + j * stride; };
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) tc::mbar_init(fb + 8 * s, 1);
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  int issued = 0;   // (thread 0) states requested so far
+  auto load = [&](int j) {
+    const uint32_t s = j % kStages;
+    tc::mbar_arrive_expect_tx(fb + 8 * s, kBytes);
+    tc::bulk_load(rb + s * kBytes, a.state + static_cast<size_t>(item(j)) * NK * NV, kBytes,
+                  fb + 8 * s);
+    issued = j + 1;
+  };
+  if (tid == 0)
+    for (int j = 0; j < kStages - 1 && j < cnt; ++j) load(j);
+
+  struct Token {
+    T q, k, v;
+    float g;
+  };
+  auto fetch = [&](int j, Token& x) {   // one item ahead of its use
+    const int n = item(j) / a.H, h = item(j) % a.H;
+    if (tid < NK) {
+      x.q = static_cast<const T*>(a.q)[n * a.sq + (h / rep) * NK + tid];
+      x.k = static_cast<const T*>(a.k)[n * a.sk + (h / rep) * NK + tid];
+    }
+    if (tid < NV) x.v = static_cast<const T*>(a.v)[n * a.sv + h * NV + tid];
+    if (tid == 0) x.g = a.g[a.per_head ? h : item(j)];
+  };
+  Token cur{}, nxt{};
+  fetch(0, cur);
+
+  int j = 0;
+  for (; j < cnt; ++j) {
+    if (tid < NK) {
+      sh.q[tid] = a.scale * static_cast<float>(cur.q);
+      sh.k[tid] = static_cast<float>(cur.k);
+    }
+    if (tid < NV) sh.v[tid] = static_cast<float>(cur.v);
+    if (tid == 0) sh.alpha[0] = cur.g <= kDecayReset ? 0.f : expf(cur.g);
+    if (j + 1 < cnt) fetch(j + 1, nxt);
+    const uint32_t s = j % kStages;
+    if (__syncthreads_or(!tc::mbar_wait(fb + 8 * s, (j / kStages) & 1))) break;
+
+    float4* st = reinterpret_cast<float4*>(ring + s * kBytes);
+    const float4 v = *reinterpret_cast<const float4*>(sh.v + cg * 4);
+    const float al = sh.alpha[0];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int row = rg + i * RG;
+      const float k = sh.k[row], q = sh.q[row];
+      float4 x = st[row * CG + cg];
+      x.x = fmaf(al, x.x, k * v.x); x.y = fmaf(al, x.y, k * v.y);
+      x.z = fmaf(al, x.z, k * v.z); x.w = fmaf(al, x.w, k * v.w);
+      st[row * CG + cg] = x;
+      o.x = fmaf(q, x.x, o.x); o.y = fmaf(q, x.y, o.y);
+      o.z = fmaf(q, x.z, o.z); o.w = fmaf(q, x.w, o.w);
+    }
+    sh.red[rg][cg] = o;
+    tc::fence_proxy_async();
+    __syncthreads();
+    if (tid == 0) {
+      tc::bulk_store(a.state + static_cast<size_t>(item(j)) * NK * NV, rb + s * kBytes, kBytes);
+      tc::bulk_commit();
+      if (j + kStages - 1 < cnt) {
+        tc::bulk_wait_read<1>();   // the store before this one has read its stage
+        load(j + kStages - 1);
+      }
+    }
+    if (tid >= kThreads - CG) {   // the last row group sums: thread 0 is busy with the copies
+      float4 t = sh.red[0][cg];
+#pragma unroll
+      for (int g = 1; g < RG; ++g) {
+        const float4 x = sh.red[g][cg];
+        t.x += x.x; t.y += x.y; t.z += x.z; t.w += x.w;
+      }
+      T* out = static_cast<T*>(a.o) + static_cast<size_t>(item(j)) * NV + cg * 4;
+      store2(out, t.x, t.y);
+      store2(out + 2, t.z, t.w);
+    }
+    cur = nxt;
+  }
+  if (j < cnt) {
+    // a state did not land within the bounded wait: the remaining outputs read
+    // NaN, their states stay as they were, and no copy may outlive the CTA
+    const float nan = __int_as_float(0x7fc00000);
+    for (int jj = j; jj < cnt; ++jj)
+      for (int c = tid; c < NV; c += kThreads)
+        static_cast<T*>(a.o)[static_cast<size_t>(item(jj)) * NV + c] = static_cast<T>(nan);
+    if (tid == 0)
+      for (int jj = j; jj < issued; ++jj)
+        tc::mbar_wait(fb + 8 * (jj % kStages), (jj / kStages) & 1);
+  }
+  if (tid == 0) tc::bulk_wait_all<0>();
+}
+
+constexpr int kMaxDevices = 64;
+
+// The shared-memory opt-in and the SM count, set and read once per device.
+template <int NK, int NV, typename T>
+cudaError_t launch_t(const DecayStepArgs& a, cudaStream_t stream) {
+  constexpr int kSmem = kStages * NK * NV * 4;
+  auto kern = decay_step_kernel<NK, NV, T>;
+  static int sms_of[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  int sms = dev < kMaxDevices ? sms_of[dev] : 0;
+  if (sms == 0) {
+    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) !=
+            cudaSuccess ||
+        (err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+      return err;
+    if (dev < kMaxDevices) sms_of[dev] = sms;
+  }
+  const long long items = static_cast<long long>(a.N) * a.H;
+  kern<<<static_cast<unsigned>(items < sms ? items : sms), kThreads, kSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int NK, int NV>
+cudaError_t launch(const DecayStepArgs& a, bool f32, cudaStream_t stream) {
+  return f32 ? launch_t<NK, NV, float>(a, stream) : launch_t<NK, NV, __nv_bfloat16>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_decay_step(const DecayStepArgs& a, int nk, int nv, bool f32,
+                              cudaStream_t stream) {
+  if (nk == 64) return nv == 64 ? launch<64, 64>(a, f32, stream) : launch<64, 128>(a, f32, stream);
+  return nv == 64 ? launch<128, 64>(a, f32, stream) : launch<128, 128>(a, f32, stream);
+}
+
+}  // namespace gdr

@@ -531,6 +531,170 @@ gdr_status gdr_rmsnorm_gate(long long rows, int dv, gdr_dtype dtype, const void*
                             const void* z, const float* weight, float eps, void* y,
                             gdr_stream_t stream);
 
+/*
+ * Linear attention with a decay for each head: the rule without the erase,
+ *
+ *     S_t = alpha_t S_{t-1} + k_t v_t^T,   o_t = S_t^T (scale * q_t),
+ *     alpha_t = exp(g_t),
+ *
+ * one state S in R^{d_k x d_v} per (batch, head), in the layout and with the
+ * streaming protocol of gdr_chunk_fwd and gdr_recurrent_step. It is the masked
+ * linear attention that the delta rule reduces to when nothing is erased ("You
+ * could have come up with Kimi Delta Attention", section 1.1), with the scalar
+ * forget gate of LLMs from scratch ch. 11, section 11.2.
+ *
+ * Layouts: q, k [B,T,Hk,d_k] and v, o [B,T,H,d_v] in the call's dtype; H is a
+ * multiple of Hk and head h uses q and k of head h / (H / Hk). A head's channels
+ * and a token's heads are dense; consecutive tokens of q, k and v are q_stride,
+ * k_stride and v_stride elements apart (0: dense, Hk*d_k or H*d_v), batch rows
+ * T tokens apart, so that the parts of one fused projection can be passed as they
+ * are. g is the natural-log decay in fp32, [B,T,H], or [H] with decay_per_head;
+ * any finite value, and a value at or below -104 (minus infinity among them),
+ * whose exp is zero in fp32, clears the state before its token is written.
+ *
+ * Sizes: d_k, d_v in {64, 128}; T from 1 to 2^30; B * H <= 65535
+ * (GDR_ERR_UNSUPPORTED beyond; gdr_decay_step: B * H < 2^31). Pointers are 16-byte
+ * aligned (g and dg 4-byte) and strides multiples of 16 bytes. Outputs are dense
+ * and overlap no input, except that h0 and hT may be one buffer, and so may dhT
+ * and dh0. Non-finite inputs propagate.
+ */
+typedef struct {
+  int B, T, H;        /* batch, tokens, heads of v and o                      */
+  int Hk;             /* heads of q and k: a divisor of H                     */
+  int dk, dv;         /* key and value widths (64 or 128)                     */
+  int dtype;          /* gdr_dtype of q, k, v, o and their gradients          */
+  int decay_per_head; /* nonzero: g is [H], one fixed decay for each head     */
+  float scale;        /* read-out scale on q                                  */
+  long long q_stride, k_stride, v_stride; /* elements between tokens, 0: dense */
+} gdr_decay_shape;
+
+/* Device workspace bytes of gdr_decay_chunk_fwd (0 when B * H fills the GPU:
+ * otherwise the sequences are cut into segments whose states it holds). */
+gdr_status gdr_decay_chunk_fwd_workspace(const gdr_decay_shape* shape, size_t* bytes);
+
+/*
+ * The chunked form over whole prompts: h0 [B,H,d_k,d_v] fp32 or NULL (zero), hT
+ * the end state or NULL. o is rounded once to the dtype from fp32; the state is
+ * fp32. workspace: at least gdr_decay_chunk_fwd_workspace() bytes, 16-byte
+ * aligned; calls sharing one must be ordered on the stream.
+ */
+gdr_status gdr_decay_chunk_fwd(const gdr_decay_shape* shape, const void* q, const void* k,
+                               const void* v, const float* g, const float* h0, void* o,
+                               float* hT, void* workspace, size_t ws_bytes,
+                               gdr_stream_t stream);
+
+/*
+ * Gradients of L = <dO, o> + <dhT, hT> on the same inputs: dq, dk [B,T,Hk,d_k]
+ * (summed over the heads that share them), dv [B,T,H,d_v] in the dtype; dg fp32
+ * in g's shape (0 at a token that clears the state); dh0 [B,H,d_k,d_v] fp32 or
+ * NULL. dO [B,T,H,d_v] in the dtype, dense; dhT [B,H,d_k,d_v] fp32 or NULL (zero).
+ * Results do not depend on the run: no sum uses atomics.
+ */
+gdr_status gdr_decay_chunk_bwd_workspace(const gdr_decay_shape* shape, size_t* bytes);
+gdr_status gdr_decay_chunk_bwd(const gdr_decay_shape* shape, const void* q, const void* k,
+                               const void* v, const float* g, const float* h0, const void* dO,
+                               const float* dhT, void* dq, void* dk, void* dv, float* dg,
+                               float* dh0, void* workspace, size_t ws_bytes,
+                               gdr_stream_t stream);
+
+/*
+ * The recurrent form for decoding: T = 1, B sequences; state [B,H,d_k,d_v] fp32
+ * is read as S_{t-1} and overwritten with S_t, o [B,H,d_v].
+ */
+gdr_status gdr_decay_step(const gdr_decay_shape* shape, const void* q, const void* k,
+                          const void* v, const float* g, float* state, void* o,
+                          gdr_stream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, over `rows` dense rows of D
+ * columns:
+ *
+ *   residual_out = x + residual                 (rounded to dtype)
+ *   y = residual_out / sqrt(mean_c residual_out^2 + eps) * weight
+ *
+ * x, residual, residual_out in dtype, weight [D] fp32, arithmetic in fp32.
+ * gdr_add_rmsnorm writes y [rows,D] in dtype. gdr_add_rmsnorm_fp8 writes y in 8
+ * bits (e4m3) with one fp32 scale for each 128 columns (the last block may be
+ * shorter), scales [rows, ceil(D/128)]: scale = max |y| / 448 over the block, 1
+ * for a block of zeros, and y = scale * (the 8-bit value) up to its rounding.
+ * residual_out may be x or residual, and y (in dtype) x or residual when it is
+ * not residual_out; other overlaps are not allowed. Pointers are 16-byte aligned
+ * (scales 4-byte); D a multiple of 8, at most 8192, rows < 2^31
+ * (GDR_ERR_UNSUPPORTED beyond). rows = 0 launches nothing. A row with a
+ * non-finite value gives NaN.
+ */
+gdr_status gdr_add_rmsnorm(long long rows, int D, gdr_dtype dtype, const void* x,
+                           const void* residual, const float* weight, float eps,
+                           void* residual_out, void* y, gdr_stream_t stream);
+gdr_status gdr_add_rmsnorm_fp8(long long rows, int D, gdr_dtype dtype, const void* x,
+                               const void* residual, const float* weight, float eps,
+                               void* residual_out, void* y, float* scales,
+                               gdr_stream_t stream);
+
+/*
+ * Gradients of gdr_add_rmsnorm for dy of y and dres of residual_out (in dtype;
+ * dres may be NULL): dx [rows,D] in dtype is the gradient of x and of residual
+ * alike, dweight [D] fp32 (16-byte aligned) the weight's. sum is the forward's
+ * residual_out. dx may be dy, dres or sum. workspace: at least
+ * gdr_add_rmsnorm_bwd_workspace() bytes, 16-byte aligned. No sum uses atomics.
+ */
+gdr_status gdr_add_rmsnorm_bwd_workspace(long long rows, int D, size_t* bytes);
+gdr_status gdr_add_rmsnorm_bwd(long long rows, int D, gdr_dtype dtype, const void* dy,
+                               const void* sum, const float* weight, float eps,
+                               const void* dres, void* dx, float* dweight, void* workspace,
+                               size_t ws_bytes, gdr_stream_t stream);
+
+/*
+ * Rotary positions of q and k. With c, s the table rows of a token's position,
+ * the channel pairs (x, y) of the first `rot` channels of every head turn,
+ *
+ *   (x, y)_j -> (x c_j - y s_j, y c_j + x s_j),   j < rot / 2,
+ *
+ * pairs being channels (j, j + rot/2), or neighbours (2j, 2j + 1) with
+ * `interleaved`; channels from rot on are unchanged. `inverse` turns back, which
+ * is also the gradient of the forward. q [B,T,H,d], k [B,T,Hk,d] in dtype (either
+ * may have 0 heads), with token strides as in gdr_decay_shape for the inputs and
+ * the outputs; an output may be its input. positions [B,T] int32, or NULL for
+ * start + t. A position outside the table turns its token's pairs into NaN.
+ * cos_table, sin_table [table_length, rot/2] fp32, 16-byte aligned.
+ * rot and d are multiples of 16, rot <= d. Fewer than 2^31 groups of (token, 16
+ * channels, 4 heads).
+ */
+typedef struct {
+  int B, T, H, Hk, d;
+  int rot;
+  int dtype;
+  int interleaved, inverse;
+  int start, table_length;
+  long long q_stride, k_stride, q_out_stride, k_out_stride; /* 0: dense */
+} gdr_rotary_shape;
+gdr_status gdr_rotary(const gdr_rotary_shape* shape, const void* q, const void* k,
+                      const float* cos_table, const float* sin_table, const int* positions,
+                      void* q_out, void* k_out, gdr_stream_t stream);
+
+/*
+ * The tables: cos and sin of p * f_j, f_j = base^(-2j/rot), for p < length, computed
+ * in fp64 and rounded once. For contexts longer than a model was trained on
+ * (scaling NULL: as is):
+ *   GDR_ROPE_LINEAR  positions divided by factor
+ *   GDR_ROPE_BASE    the base times factor^(rot/(rot-2)): the lowest frequency is
+ *                    divided by factor, the highest kept
+ *   GDR_ROPE_RAMP    frequencies that turn at least `fast` times over
+ *                    original_length are kept, those that turn at most `slow`
+ *                    times divided by factor, a linear ramp in j between (its ends
+ *                    rounded outwards to whole j); cos and sin times magnitude
+ */
+enum { GDR_ROPE_NONE = 0, GDR_ROPE_LINEAR = 1, GDR_ROPE_BASE = 2, GDR_ROPE_RAMP = 3 };
+typedef struct {
+  int kind;
+  double factor;          /* >= 1 */
+  int original_length;    /* GDR_ROPE_RAMP only, like the rest */
+  double fast, slow;      /* fast > slow > 0 turns */
+  double magnitude;       /* > 0 */
+} gdr_rotary_scaling;
+gdr_status gdr_rotary_table(int length, int rot, double base, const gdr_rotary_scaling* scaling,
+                            float* cos_table, float* sin_table, gdr_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* gdr_status_string(gdr_status status);
 
