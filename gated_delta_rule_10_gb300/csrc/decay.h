@@ -50,6 +50,10 @@ cudaError_t launch_decay_fwd_warp(const DecayArgs& a, const DecaySplit& sp, bool
                                   cudaStream_t stream);
 cudaError_t launch_decay_bwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,
                                   cudaStream_t stream);
+// bf16 inputs on tcgen05, chunks of 128 tokens (decay_tc_fwd.cu).
+cudaError_t launch_decay_states_tc(const DecayArgs& a, const DecaySplit& sp, bool reverse,
+                                   cudaStream_t stream);
+cudaError_t launch_decay_fwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream);
 // Chains the segments' states (decay_chain.cu); backward also chains the
 // states' gradients and writes the boundary dot products.
 cudaError_t launch_decay_chain(const DecayArgs& a, const DecaySplit& sp, bool backward,

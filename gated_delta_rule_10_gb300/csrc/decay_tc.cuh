@@ -1,0 +1,267 @@
+// Shared parts of the tensor-core kernels of the linear attention with a decay
+// for each head (bf16, chunks of 128 tokens): the chunk's decay factors, bounded
+// waits and the conversion of a row-scaled operand into two bf16 tiles.
+#pragma once
+
+#include "common.cuh"
+#include "decay.h"
+#include "tc.cuh"
+
+namespace gdr {
+namespace dtc {
+
+constexpr int kC = 128;             // tokens per chunk
+constexpr uint32_t kTile = 16384;   // 128 rows of 64 bf16 columns, 128-byte swizzle
+
+// Decay factors of one chunk. Four blocks of 32 tokens; a pair (r, i) in
+// different blocks has e^{G_r - G_i} = row[r] * col[b][i] with b the block of r,
+// both factors sums over disjoint spans (no difference of long sums), and a pair
+// within a block takes the exponential of the difference of block-local sums.
+// A clearing token (kDecayReset) leaves the sums and zeroes the factors that
+// span it.
+__device__ __forceinline__ int col_at(int b) { return 16 * b * (b - 1); }   // 0, 32, 96
+struct Gates {
+  float loc[kC];        // log2 of the decay from the block's start through r
+  uint32_t allow[kC];   // bit i: token i of r's block reaches r
+  float row[kC];        // decay from the block's start through r
+  float col[192];       // col[col_at(b) + i]: decay from after i through the end of block b-1
+  float head[kC];       // decay from the chunk's start through r
+  float tail[kC];       // decay from after i through the chunk's end
+  float all;            // decay of the whole chunk
+  float pad[3];
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float a, float b) {
+  F2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(F2 d, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t round2(F2 x) {
+  float a, b;
+  unpack2(x, a, b);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ F2 widen2(uint32_t w) {
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// The log-decays of this lane's tokens 32 j + lane (0 past n).
+__device__ __forceinline__ void read_gates(float (&x)[4], const DecayArgs& a, size_t tok, int h,
+                                           int n) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = 32 * j + lane;
+    x[j] = r < n ? (a.per_head ? a.g[h] : __ldg(a.g + (tok + r) * a.H + h)) : 0.f;
+  }
+}
+
+__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * 1.4426950408889634f); }
+
+// One warp turns the chunk's log-decays into its factors, a block of 32 tokens
+// per lane and register, so that the four blocks' shuffles overlap. Running sums
+// are taken from both ends: a factor never comes from a difference of sums, and
+// the error of exp_fast, |x| 2^-23, is small where the factor is not.
+__device__ __forceinline__ void fill_gates(Gates& s, const float (&x)[4]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t to = 0xffffffffu >> (31 - lane);   // tokens up to this one
+  float up[4], down[4], total[4];
+  uint32_t clears[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const bool clear = x[b] <= kDecayReset;
+    clears[b] = __ballot_sync(0xffffffffu, clear);
+    up[b] = down[b] = clear ? 0.f : x[b];
+  }
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const float u = __shfl_up_sync(0xffffffffu, up[b], off);
+      const float d = __shfl_down_sync(0xffffffffu, down[b], off);
+      up[b] += lane >= off ? u : 0.f;
+      down[b] += lane + off < 32 ? d : 0.f;
+    }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    total[b] = __shfl_sync(0xffffffffu, up[b], 31);
+    if (clears[b]) total[b] = -INFINITY;
+    down[b] = __shfl_down_sync(0xffffffffu, down[b], 1);
+    if (lane == 31) down[b] = 0.f;
+    const uint32_t before = clears[b] & to;
+    s.loc[32 * b + lane] = up[b] * 1.4426950408889634f;
+    s.allow[32 * b + lane] = to & (0xffffffffu << (before ? 31 - __clz(before) : 0));
+    if (before) up[b] = -INFINITY;
+    if (clears[b] & ~to) down[b] = -INFINITY;
+  }
+  float pre = 0.f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int r = 32 * b + lane;
+    s.row[r] = exp_fast(up[b]);
+    s.head[r] = exp_fast(pre + up[b]);
+    float e = down[b];
+#pragma unroll
+    for (int w = b + 1; w < 4; ++w) {
+      s.col[col_at(w) + r] = exp_fast(e);
+      e += total[w];
+    }
+    s.tail[r] = exp_fast(e);
+    pre += total[b];
+  }
+  if (lane == 0) s.all = exp_fast(pre);
+}
+
+// Bounded mbarrier wait that also gives up once another role has aborted.
+__device__ __noinline__ bool wait_long(uint32_t mbar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < tc::kMaxPolls; ++i) {
+    if (tc::mbar_try_wait(mbar, parity, tc::kSuspendNs)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag) {
+  return tc::mbar_test(mbar, parity) || wait_long(mbar, parity, abort_flag);
+}
+// The same for a whole warp, with one answer. Every lane polls: with one lane
+// polling in a branch of its own, a hand-over took several times as long.
+__device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait(mbar, parity, abort_flag));
+}
+// One arrival for a whole warp.
+__device__ __forceinline__ void warp_arrive(uint32_t mbar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(mbar);
+}
+
+// Products issued by the lane with `go` set of a converged warp. The whole warp
+// runs the issuing code, so that descriptors stay in uniform registers; from a
+// branch of one lane every operand of every product is moved there first
+// (measured: 130 cycles a product).
+__device__ __forceinline__ void mma_if(uint32_t go, uint32_t d, uint64_t x, uint64_t y,
+                                       uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(x), "l"(y), "r"(id), "r"(accumulate), "r"(go));
+}
+__device__ __forceinline__ void mma_ta_if(uint32_t go, uint32_t d, uint32_t x, uint64_t y,
+                                          uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(x), "l"(y), "r"(id), "r"(accumulate), "r"(go));
+}
+__device__ __forceinline__ void commit_if(uint32_t go, uint32_t mbar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          mbar),
+      "r"(go)
+      : "memory");
+}
+
+// Chunks c0 .. c0 + 3 (32 columns) of row `r` of a 128 x 64 bf16 tile times f,
+// as hi + lo bf16 tiles (kTile apart): together they hold the product to 2^-17,
+// so the fp32 state they feed keeps its precision.
+__device__ __forceinline__ void split_row(const unsigned char* src, unsigned char* dst, int r,
+                                          int c0, float f) {
+  const F2 ff = pack2(f, f), minus = pack2(-1.f, -1.f);
+#pragma unroll 1
+  for (int c = c0; c < c0 + 4; c += 2) {
+    const uint32_t off[2] = {static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)),
+                             static_cast<uint32_t>(r * 128 + (((c + 1) ^ (r & 7)) << 4))};
+    uint4 u[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) u[p] = *reinterpret_cast<const uint4*>(src + off[p]);
+    uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint32_t w[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F2 x = mul2(widen2(w[i]), ff);
+        hi[p][i] = round2(x);
+        lo[p][i] = round2(fma2(widen2(hi[p][i]), minus, x));
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      *reinterpret_cast<uint4*>(dst + off[p]) = make_uint4(hi[p][0], hi[p][1], hi[p][2], hi[p][3]);
+      *reinterpret_cast<uint4*>(dst + kTile + off[p]) =
+          make_uint4(lo[p][0], lo[p][1], lo[p][2], lo[p][3]);
+    }
+  }
+}
+
+// 64 fp32 values as one row of a swizzled bf16 tile with 128-byte rows.
+__device__ __forceinline__ void round_row(unsigned char* dst, int r, const float (&x)[64]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) << 4)) =
+        make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
+                   pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
+}
+
+// S = all * S + (hi + lo) from 128 accumulator columns [hi 64 | lo 64].
+__device__ __forceinline__ void add_state(float (&S)[64], float all, uint32_t taddr) {
+  const F2 g = pack2(all, all);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    float hi[16], lo[16];
+    tc::tmem_ld16(taddr + 16 * p, hi);
+    tc::tmem_ld16(taddr + 64 + 16 * p, lo);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      float &a = S[16 * p + j], &b = S[16 * p + j + 1];
+      unpack2(fma2(g, pack2(a, b), add2(pack2(hi[j], hi[j + 1]), pack2(lo[j], lo[j + 1]))), a, b);
+    }
+  }
+}
+
+// 64 consecutive state values of one row; null: zeros.
+__device__ __forceinline__ void read_row(float (&S)[64], const float* src) {
+#pragma unroll
+  for (int j = 0; j < 64; j += 4) {
+    const float4 x = src ? *reinterpret_cast<const float4*>(src + j)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+  }
+}
+__device__ __forceinline__ void write_row(const float (&S)[64], float f, float* dst) {
+#pragma unroll
+  for (int j = 0; j < 64; j += 4)
+    *reinterpret_cast<float4*>(dst + j) =
+        make_float4(f * S[j], f * S[j + 1], f * S[j + 2], f * S[j + 3]);
+}
+
+}  // namespace dtc
+}  // namespace gdr

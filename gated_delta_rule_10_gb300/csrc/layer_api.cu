@@ -56,7 +56,6 @@ gdr::DecayArgs decay_args(const gdr_decay_shape* s) {
   return a;
 }
 
-constexpr int kDecayChunk = 64;
 constexpr int kMinRun = 4;          // chunks per segment, at least
 constexpr int kMaxBwdRun = 4096;    // tokens per segment of the backward, at most
 
@@ -66,8 +65,10 @@ constexpr int kMaxBwdRun = 4096;    // tokens per segment of the backward, at mo
 // The backward also bounds a segment's tokens: the gate's gradient is a running
 // sum from the segment's end.
 void cut(const gdr_decay_shape* s, bool backward, gdr::DecaySplit* sp) {
-  const int chunks = (s->T + kDecayChunk - 1) / kDecayChunk;
-  const long long ctas = static_cast<long long>(s->B) * s->H * (backward ? 2 : 1);
+  const int chunk = s->dtype == GDR_BF16 ? 128 : 64;
+  const int chunks = (s->T + chunk - 1) / chunk;
+  const long long ctas = static_cast<long long>(s->B) * s->H *
+                         (backward ? 2 : s->dtype == GDR_BF16 ? s->dv / 64 : 1);
   long long p = kSms / ctas;
   if (p > chunks / kMinRun) p = chunks / kMinRun;
   if (backward && p < (s->T + kMaxBwdRun - 1) / kMaxBwdRun)
@@ -75,7 +76,7 @@ void cut(const gdr_decay_shape* s, bool backward, gdr::DecaySplit* sp) {
   if (p < 1) p = 1;
   const int per = static_cast<int>((chunks + p - 1) / p);
   sp->segments = (chunks + per - 1) / per;
-  sp->seg_len = per * kDecayChunk;
+  sp->seg_len = per * chunk;
   sp->parts = s->dk * s->dv / 1024;
 }
 
@@ -169,10 +170,12 @@ gdr_status gdr_decay_chunk_fwd(const gdr_decay_shape* shape, const void* q, cons
   const cudaStream_t cs = stream_of(stream);
   cudaError_t err = cudaSuccess;
   if (sp.segments > 1) {
-    err = gdr::launch_decay_states_warp(a, sp, false, f32, cs);
+    err = f32 ? gdr::launch_decay_states_warp(a, sp, false, f32, cs)
+              : gdr::launch_decay_states_tc(a, sp, false, cs);
     if (err == cudaSuccess) err = gdr::launch_decay_chain(a, sp, false, cs);
   }
-  if (err == cudaSuccess) err = gdr::launch_decay_fwd_warp(a, sp, f32, cs);
+  if (err == cudaSuccess)
+    err = f32 ? gdr::launch_decay_fwd_warp(a, sp, f32, cs) : gdr::launch_decay_fwd_tc(a, sp, cs);
   return status_of(err);
 }
 
@@ -209,8 +212,9 @@ gdr_status gdr_decay_chunk_bwd(const gdr_decay_shape* shape, const void* q, cons
   const cudaStream_t cs = stream_of(stream);
   cudaError_t err = cudaSuccess;
   if (sp.S) {
-    err = gdr::launch_decay_states_warp(a, sp, false, f32, cs);
-    if (err == cudaSuccess) err = gdr::launch_decay_states_warp(a, sp, true, f32, cs);
+    for (int rev = 0; rev < 2 && err == cudaSuccess; ++rev)
+      err = f32 ? gdr::launch_decay_states_warp(a, sp, rev, f32, cs)
+                : gdr::launch_decay_states_tc(a, sp, rev, cs);
     if (err == cudaSuccess) err = gdr::launch_decay_chain(a, sp, true, cs);
   }
   if (err == cudaSuccess) err = gdr::launch_decay_bwd_warp(a, sp, f32, cs);

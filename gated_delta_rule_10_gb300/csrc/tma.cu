@@ -22,23 +22,33 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-}  // namespace
-
-bool make_bthd_tmap(CUtensorMap* map, const void* base, int B, int T, int H, int D) {
+bool encode(CUtensorMap* map, const void* base, int B, int T, int H, int D, long long stride,
+            int box_tokens) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
                               static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2,
-                                 static_cast<cuuint64_t>(H) * D * 2,
-                                 static_cast<cuuint64_t>(T) * H * D * 2};
-  const cuuint32_t box[4] = {64, 1, 64, 1};
+                                 static_cast<cuuint64_t>(stride) * 2,
+                                 static_cast<cuuint64_t>(T) * stride * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_tokens), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool make_bthd_tmap(CUtensorMap* map, const void* base, int B, int T, int H, int D) {
+  return encode(map, base, B, T, H, D, static_cast<long long>(H) * D, 64);
+}
+
+bool make_rows_tmap(CUtensorMap* map, const void* base, int B, int T, int H, int D,
+                    long long token_stride) {
+  return encode(map, base, B, T, H, D, token_stride, 128);
 }
 
 }  // namespace gdr

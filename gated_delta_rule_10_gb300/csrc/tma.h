@@ -15,4 +15,9 @@ namespace gdr {
 // driver refuses the description.
 bool make_bthd_tmap(CUtensorMap* map, const void* base, int B, int T, int H, int D);
 
+// The same view with `token_stride` elements between tokens (a multiple of 8),
+// batch rows T tokens apart, and a box of 64 channels x 1 head x 128 tokens.
+bool make_rows_tmap(CUtensorMap* map, const void* base, int B, int T, int H, int D,
+                    long long token_stride);
+
 }  // namespace gdr
