@@ -33,8 +33,13 @@ struct DecaySplit {
   float* D = nullptr;         // slot p: the gradient of that state (backward)
   float* decay = nullptr;     // [B * H, segments] product of a segment's decays
   float* dots = nullptr;      // [B * H, slots, parts] partial <S_p, D_p>
-  float* flow_f = nullptr;    // [B * H, T] read-out terms of the gate's gradient
-  float* flow_r = nullptr;    // [B * H, T] the other terms
+  // Terms of the gate's gradient by token, [flows, B * H, T] (the parts add up):
+  // what its row takes from before its block of 32 tokens, what its keys and values
+  // give to after it, and [nears, B * H, T] the difference within the block.
+  int flows = 1, nears = 1;
+  float* from = nullptr;
+  float* to = nullptr;
+  float* near = nullptr;
   float* dq_part = nullptr;   // [B, T, H, nk] per-head gradients of shared q, k
   float* dk_part = nullptr;
   float* dg_part = nullptr;   // [B * H, segments] sums for a per-head decay
@@ -50,10 +55,11 @@ cudaError_t launch_decay_fwd_warp(const DecayArgs& a, const DecaySplit& sp, bool
                                   cudaStream_t stream);
 cudaError_t launch_decay_bwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,
                                   cudaStream_t stream);
-// bf16 inputs on tcgen05, chunks of 128 tokens (decay_tc_fwd.cu).
+// bf16 inputs on tcgen05, chunks of 128 tokens (decay_tc.cu).
 cudaError_t launch_decay_states_tc(const DecayArgs& a, const DecaySplit& sp, bool reverse,
                                    cudaStream_t stream);
 cudaError_t launch_decay_fwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream);
+cudaError_t launch_decay_bwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream);
 // Chains the segments' states (decay_chain.cu); backward also chains the
 // states' gradients and writes the boundary dot products.
 cudaError_t launch_decay_chain(const DecayArgs& a, const DecaySplit& sp, bool backward,

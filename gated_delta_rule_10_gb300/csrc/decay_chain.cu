@@ -62,10 +62,16 @@ __global__ void __launch_bounds__(kChainThreads) chain_kernel(const DecayArgs a,
   }
 }
 
-// dg_t = <S, D> at the segment's end + sum of flow_j over the segment's tokens
-// j >= t; a clearing token has gradient 0 and nothing passes it. Tokens are
-// taken 256 at a time from the end; a step is the map x -> keep x + add, and
-// maps compose.
+// The gate's gradient. With c the product <S, D> at a block's end (32 tokens),
+//   dg_t = c + sum over the block's j >= t of (from_j - to_j + near_j),
+//   <S, D> at its start = c - sum of to + sum of from;
+// the near terms of a block sum to zero, so they stay out of what is passed on,
+// and with them the rounding of the block's largest products. A block whose decay
+// is below 2^-30 passes nothing on: what crosses it is 2^-30 of <S, D>, less than
+// the rounding of what is passed (so that error does not gather over a long
+// sequence of short memories): c is then the sum of to, and the start's the sum of
+// from. A clearing token's own gradient is 0. A warp takes a block; what passes
+// through blocks is a map c -> keep c + add, and maps compose.
 __global__ void __launch_bounds__(kChainThreads) gate_grad_kernel(const DecayArgs a,
                                                                   const DecaySplit sp) {
   constexpr int kWarps = kChainThreads / 32;
@@ -75,45 +81,52 @@ __global__ void __launch_bounds__(kChainThreads) gate_grad_kernel(const DecayArg
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
   const int t0 = seg * sp.seg_len, t1 = min(a.T, t0 + sp.seg_len);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t plane = static_cast<size_t>(a.B) * a.H * a.T;
   float carry = 0.f, total = 0.f;
   if (sp.dots)
     for (int i = 0; i < sp.parts; ++i)
       carry += sp.dots[(static_cast<size_t>(bh) * sp.slots + seg + 1) * sp.parts + i];
-  for (int end = t1; end > t0; end -= kChainThreads) {
-    const int t = end - 1 - static_cast<int>(threadIdx.x);
-    float add = 0.f;
-    int keep = 1;
-    const bool in = t >= t0;
+  const int blocks = (t1 - t0 + 31) / 32;
+  for (int last = blocks - 1; last >= 0; last -= kWarps) {
+    const int blk = last - warp, t = t0 + blk * 32 + lane;   // warp 0 the latest block
+    const bool in = blk >= 0 && t < t1;
     const size_t at = (static_cast<size_t>(b) * a.T + t) * a.H + h;
+    float g = 0.f, f = 0.f, e = 0.f, l = 0.f;
     if (in) {
-      const float g = a.per_head ? a.g[h] : a.g[at];
-      const size_t f = static_cast<size_t>(bh) * a.T + t;
-      add = sp.flow_f[f] + sp.flow_r[f];
-      if (g <= kDecayReset) {
-        keep = 0;
-        add = 0.f;
+      g = a.per_head ? a.g[h] : a.g[at];
+      const size_t p = static_cast<size_t>(bh) * a.T + t;
+      for (int i = 0; i < sp.flows; ++i) {
+        f += sp.from[p + i * plane];
+        e += sp.to[p + i * plane];
       }
+      for (int i = 0; i < sp.nears; ++i) l += sp.near[p + i * plane];
+    }
+    const bool clear = g <= kDecayReset;
+    float sum = g, suf = f - e + l;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      f += __shfl_xor_sync(0xffffffffu, f, off);
+      e += __shfl_xor_sync(0xffffffffu, e, off);
+      sum += __shfl_xor_sync(0xffffffffu, sum, off);
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const float y = __shfl_up_sync(0xffffffffu, add, off);
-      const int k = __shfl_up_sync(0xffffffffu, keep, off);
-      if (lane >= off && keep) add += y;
-      if (lane >= off) keep &= k;
+      const float y = __shfl_down_sync(0xffffffffu, suf, off);
+      if (lane + off < 32) suf += y;
     }
-    if (lane == 31) {
-      w_add[warp] = add;
+    const int keep = !(sum < -20.8f);   // (NaN keeps)
+    if (lane == 0) {
+      w_add[warp] = keep ? f - e : f;
       w_keep[warp] = keep;
     }
     __syncthreads();
-    float x = carry, next = carry;
+    float c = carry;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      if (i == warp) x = next;
-      next = w_keep[i] ? next + w_add[i] : w_add[i];
+      if (i == warp) c = carry;
+      carry = w_keep[i] ? carry + w_add[i] : w_add[i];
     }
-    const float out = keep ? x + add : add;
-    carry = next;
+    const float out = clear ? 0.f : (keep ? c : e) + suf;
     if (in) {
       if (a.per_head) total += out;
       else a.dg[at] = out;

@@ -1,0 +1,975 @@
+// Linear attention with a decay for each head, chunked, for bf16 inputs on
+// tcgen05: the forward, its three gradients and the segments' own states.
+//
+// One walk over a sequence serves all four results. It reads rows x_t, y_t of W
+// channels and z_t of 64 (a column slice of the third tensor), carries a state R
+// (W x 64, fp32) and writes, for every token t,
+//   out_t = f_t R^T x_t + s sum_i D_ti (x_t . y_i) z_i,
+// over the tokens i <= t of its chunk of 128, with D the decay between two tokens
+// and f_t = s e^{G_t}; after the chunk, R = e^{G_C} R + sum_i e^{G_C-G_i} y_i z_i^T.
+//   forward   x, y, z = q, k, v     R = S     out = o
+//   dq        x, y, z = dO, v, k    R = S^T   out = dq
+// Backward (REV) the chunks are taken from the end, i >= t, f_t = e^{G_C-G_t}, and
+// R = e^{G_C} R + s sum_i e^{G_i} y_i z_i^T:
+//   dv        x, y, z = k, q, dO    R = D     out = dv     (D: the gradient of S)
+//   dk        x, y, z = v, dO, q    R = D^T   out = dk
+//
+// Four products a chunk:
+//   A  = X Y^T                        (128 x 128, K = W)
+//   O1 = X R                          (128 x 64,  K = W)
+//   O2 = (A . D) Z                    (128 x 64,  K = 128, A . D from tensor memory)
+//   P  = Y^T [Z'hi | Z'lo]            (W x 128,   K = 128), Z' the decayed Z.
+// x, y and z go from TMA to the tensor cores as they are. A . D and the R of the
+// read-out are rounded to bf16 (the result is rounded to bf16 anyway); the decayed
+// Z' is split into two bf16 terms because it enters the fp32 state, whose error
+// would otherwise be bf16's. The two terms sit side by side, one N = 128 product.
+//
+// FINE (dq and dk): the gate's gradient needs f_t (R^T x_t) . p_t in fp32, p the
+// partner row (q or k). R is then split into hi + lo for O1 as well, in the space
+// of the second z tile, and the read-out also writes that product.
+//
+// Only R_{n+1} <- R_n is a chain, and it holds no product: P of any chunk can be
+// ready before R is. A and O1 are issued by one warp, P and O2 by another: the
+// issue of a product takes as long as the product (~52 cycles at any of these
+// shapes), and the waits of one warp pass while the other's products run (58 ->
+// 40 us for the products of 4 x 4096 x 16 x 128 alone). Each tile is loaded
+// again as soon as its last reader is done, about one chunk's time ahead.
+// The two column halves of a head re-read x and y (from L2) and repeat A.
+#include "decay_tc.cuh"
+#include "tma.h"
+
+namespace gdr {
+namespace {
+
+using namespace dtc;
+
+constexpr int kSmCount = 152;
+
+// ------------------------------------------------------------------ walk
+
+struct Walk {
+  int x_heads, y_heads, z_heads;   // heads of each tensor: H or Hk
+  int nz;                          // width of z and of the result
+  void* out;                       // [B, T, H, nz] bf16, or
+  float* part;                     // the same in fp32 (a head's part of a shared gradient)
+  const float* start;              // first state; null: zero
+  size_t start_bh, start_seg;      // its elements between (batch, head)s and segments
+  int row_step, col_step;          // its elements between rows (W) and columns (z)
+  float* end;                      // last state [B * H, W, nz], or null
+  const __nv_bfloat16* partner;    // FINE: rows whose dot product with the result is wanted
+  long long partner_stride;
+  float* flow;                     // [slices, B * H, T], that product
+};
+
+constexpr int kThreads = 512;   // 3 x 128: mask, state, read-out; products (2); gates (2)
+constexpr uint32_t kCols = 512;
+
+// Tensor-memory columns of chunk n: two buffers of A, whose columns 0..63 take
+// A . D as bf16 and 64..127 O2 once A has been read, two of O1, and P.
+struct Cols {
+  __device__ static uint32_t A(int n) { return (n & 1) * 128; }
+  __device__ static uint32_t O2(int n) { return A(n) + 64; }
+  __device__ static uint32_t O1(int n) { return 256 + (n & 1) * 64; }
+  static constexpr uint32_t P = 384;
+};
+
+enum : uint32_t {   // mbarriers, each a pair for even and odd chunks
+  bXY = 0, bZ = 2,                           // tiles landed
+  bMA = 4, bMO1 = 6, bMO2 = 8, bMP = 10,     // products complete
+  bMask = 12, bSplit = 14, bState = 16, bFree = 18,
+  bGates = 20, bGFree = 24,                  // four each: a ring of four chunks' gates
+  bEnd = 28, kBars = 30
+};
+
+template <int W, bool FINE>
+struct WalkSmem {
+  static constexpr uint32_t kWide = W / 64 * kTile, kZ = FINE ? 1 : 2;
+  static constexpr uint32_t oX = 0, oY = oX + 2 * kWide, oZ = oY + 2 * kWide,
+                            oSplit = oZ + kZ * kTile, oR = oSplit + 2 * kTile,
+                            kR = W * 128, oGates = oR + (FINE ? 2 : 1) * kR,
+                            oBar = oGates + 4 * sizeof(Gates), oSlot = oBar + 8 * kBars,
+                            oAbort = oSlot + 4, bytes = oAbort + 12;
+  static constexpr uint32_t launch = bytes + 1024;   // room to align the base
+};
+
+template <int W, bool REV, bool FINE>
+__global__ void __launch_bounds__(kThreads, 1)
+    decay_walk_tc(const DecayArgs a, const DecaySplit sp, const Walk w,
+                  const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
+                  const __grid_constant__ CUtensorMap tz) {
+  using L = WalkSmem<W, FINE>;
+  using C = Cols;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slices = w.nz / 64, slice = blockIdx.x % slices, seg = blockIdx.x / slices;
+  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+  const int t0 = seg * sp.seg_len, t1 = min(a.T, t0 + sp.seg_len);
+  const int cnt = (t1 - t0 + kC - 1) / kC;
+  const size_t tok = static_cast<size_t>(b) * a.T;
+  auto at = [&](int n) { return t0 + (REV ? cnt - 1 - n : n) * kC; };   // chunk n's first token
+  auto bar = [&](uint32_t i, int n) { return sb + L::oBar + 8 * (i + (n & 1)); };
+  auto par = [](int n) { return static_cast<uint32_t>(n >> 1) & 1u; };
+  auto bar4 = [&](uint32_t i, int n) { return sb + L::oBar + 8 * (i + (n & 3)); };
+  auto par4 = [](int n) { return static_cast<uint32_t>(n >> 2) & 1u; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::oAbort);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::oSlot);
+  auto gates = [&](int n) -> Gates& {
+    return *reinterpret_cast<Gates*>(smem + L::oGates + (n & 3) * sizeof(Gates));
+  };
+  auto zslot = [](int n) { return FINE ? 0u : static_cast<uint32_t>(n & 1) * kTile; };
+
+  if (warp == 13) tc::tmem_alloc(smem_u32(slot), kCols);
+  if (tid == 0) {
+    for (uint32_t i = 0; i < kBars; ++i) {
+      uint32_t count = i < bZ ? 2 : 1;   // x and y land on one barrier
+      if (i >= bMask && i < bGates) count = i == bSplit || i == bSplit + 1 ? 8 : 4;   // warps
+      if (i >= bGFree && i < bEnd) count = 8;
+      tc::mbar_init(sb + L::oBar + 8 * i, count);
+    }
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *slot;
+  const int quad = warp & 3, row = 32 * quad + lane;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+
+  // tiles of chunk n into their slots; the roles that see a slot's last reader
+  // finish ask for the next tile themselves (one lane)
+  auto load_wide = [&](uint32_t base, const CUtensorMap* m, int heads, int n) {
+    tc::mbar_arrive_expect_tx(bar(bXY, n), L::kWide);
+#pragma unroll
+    for (int blk = 0; blk < W / 64; ++blk)
+      tc::tma_load_4d(sb + base + (n & 1) * L::kWide + blk * kTile, m, 64 * blk,
+                      h / (a.H / heads), at(n), b, bar(bXY, n));
+  };
+  auto load_x = [&](int n) { load_wide(L::oX, &tx, w.x_heads, n); };
+  auto load_y = [&](int n) { load_wide(L::oY, &ty, w.y_heads, n); };
+  auto load_z = [&](int n) {
+    tc::mbar_arrive_expect_tx(bar(bZ, n), kTile);
+    tc::tma_load_4d(sb + L::oZ + zslot(n), &tz, 64 * slice, h / (a.H / w.z_heads), at(n), b,
+                    bar(bZ, n));
+  };
+  // half of the columns of this lane's token of Z'; its last reader is P(n - 1),
+  // whose completion the caller has waited for
+  auto split = [&](int n, int half) {
+    if (!warp_wait(bar4(bGates, n), par4(n), abort_flag) ||
+        !warp_wait(bar(bZ, n), par(n), abort_flag))
+      return false;
+    const Gates& g = gates(n);
+    split_row(smem + L::oZ + zslot(n), smem + L::oSplit, row, 4 * half,
+              REV ? a.scale * g.head[row] : g.tail[row]);
+    tc::fence_proxy_async();
+    warp_arrive(bar(bSplit, n));
+    return true;
+  };
+
+  if (warp < 4) {
+    // ---------------------------------------------- A . D, one token per lane
+    for (int n = 0; n < cnt; ++n) {
+      const bool ok = warp_wait(bar4(bGates, n), par4(n), abort_flag) &&
+                warp_wait(bar(bMA, n), par(n), abort_flag);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const Gates& g = gates(n);
+      const float lr = g.loc[row];
+      const uint32_t allow = g.allow[row];
+#pragma unroll 1
+      for (int cb = 0; cb < 4; ++cb) {
+        uint32_t r[16];
+        if (REV ? cb < quad : cb > quad) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = 0u;
+        } else {
+          float x[32];
+          tc::tmem_ld32(tl + C::A(n) + 32 * cb, x);
+          if (cb == quad) {
+            const float* f = g.loc + 32 * cb;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(f + i);
+              const float c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float e = exp2_fast(REV ? c[j] - lr : lr - c[j]);
+                x[i + j] = (allow >> (i + j)) & 1u ? x[i + j] * e : 0.f;
+              }
+            }
+          } else {
+            // forward: row[t] col[i]; backward: col[t] of this block pair, row[i]
+            const float fr = REV ? g.col[col_at(cb) + row] : g.row[row];
+            const float* f = REV ? g.row + 32 * cb : g.col + col_at(quad) + 32 * cb;
+            const F2 ff = pack2(fr, fr);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(f + i);
+              unpack2(mul2(pack2(x[i], x[i + 1]), mul2(ff, c.x)), x[i], x[i + 1]);
+              unpack2(mul2(pack2(x[i + 2], x[i + 3]), mul2(ff, c.y)), x[i + 2], x[i + 3]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        }
+        tc::tmem_st16(tl + C::A(n) + 16 * cb, r);   // over columns already read
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      warp_arrive(bar(bMask, n));
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------- the state, one row per lane, and
+    // half of Z'
+    int nx = 0, ny = 0;   // (tid 128) tiles requested
+    if (tid == 128)
+      for (; nx < min(2, cnt); ++nx, ++ny) {
+        load_x(nx);
+        load_y(ny);
+      }
+    __syncwarp();
+    const bool mine = row < W;
+    float R[64];
+    read_row(R, w.start && mine ? w.start + bh * w.start_bh + seg * w.start_seg +
+                                      static_cast<size_t>(row) * w.row_step +
+                                      static_cast<size_t>(64 * slice) * w.col_step
+                                : nullptr,
+             w.col_step);
+    if (mine) round_row<FINE>(smem + L::oR, L::kR, row, R);
+    tc::fence_proxy_async();
+    warp_arrive(bar(bState, 0));
+    bool ok = split(0, 0);
+    for (int n = 0; ok && n < cnt; ++n) {
+      ok = warp_wait(bar(bMP, n), par(n), abort_flag);
+      if (!ok) break;
+      if (tid == 128 && n + 2 < cnt && wait(bar(bMA, n), par(n), abort_flag)) {
+        load_y(n + 2);   // y's readers A(n) and P(n) are done
+        ny = n + 3;
+      }
+      __syncwarp();
+      tc::fence_after_sync();
+      const float all = gates(n).all;
+      warp_arrive(bar4(bGFree, n));
+      if (mine || W == 128) add_state(R, all, tl + C::P);
+      tc::fence_before_sync();
+      if (n + 1 < cnt) {
+        ok = split(n + 1, 0) && warp_wait(bar(bMO1, n), par(n), abort_flag);   // R_n has been read
+        if (ok) {
+          if (tid == 128 && n + 2 < cnt) {
+            load_x(n + 2);
+            nx = n + 3;
+          }
+          __syncwarp();
+          if (mine) round_row<FINE>(smem + L::oR, L::kR, row, R);
+          tc::fence_proxy_async();
+          warp_arrive(bar(bState, n + 1));
+        }
+      }
+    }
+    if (ok && mine && w.end && seg == (REV ? 0 : sp.segments - 1))
+      write_row(R, 1.f, w.end + (static_cast<size_t>(bh) * W + row) * w.nz + 64 * slice);
+    // no copy may outlive the CTA, whatever gave up (x and y of a chunk share a
+    // barrier: a y left alone by an abort gets its x, so that it completes)
+    if (tid == 128) {
+      if (nx < ny) load_x(nx);
+      for (int n = max(0, ny - 2); n < ny; ++n) tc::mbar_wait(bar(bXY, n), par(n));
+    }
+    __syncwarp();
+  } else if (warp < 12) {
+    // ---------------------------------------------- read-out, one token per lane, and
+    // the other half of Z'
+    constexpr int kAhead = FINE ? 1 : 2;
+    int nz = 0;   // (tid 256) tiles requested
+    if (tid == 256)
+      for (; nz < min(kAhead, cnt); ++nz) load_z(nz);
+    auto soon = [&](int n) {   // one tile only: the next one comes into L2 meanwhile
+      if (n < cnt) tc::tma_prefetch_4d(&tz, 64 * slice, h / (a.H / w.z_heads), at(n), b);
+    };
+    if (FINE && tid == 256) soon(1);
+    __syncwarp();
+    bool ok = true;
+    if (!FINE) ok = split(0, 1);
+    for (int n = 0; ok && n < cnt; ++n) {
+      const int t = at(n) + row;
+      const bool live = t < t1;
+      uint4 pr[FINE ? 8 : 1];
+      if (FINE) {   // the partner's row, on its way while the products run
+        const __nv_bfloat16* p = w.partner + static_cast<long long>(tok + t) * w.partner_stride +
+                                 (h / (a.H / w.z_heads)) * w.nz + 64 * slice;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          pr[i] = live ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+        // one z tile: its last reader O2(n - 1) was waited for below
+        ok = (n == 0 || warp_wait(bar(bMP, n - 1), par(n - 1), abort_flag)) && split(n, 1);
+      } else if (n + 1 < cnt) {
+        ok = warp_wait(bar(bMP, n), par(n), abort_flag) && split(n + 1, 1);
+      }
+      ok = ok && warp_wait(bar(bMO1, n), par(n), abort_flag) &&
+           warp_wait(bar(bMO2, n), par(n), abort_flag);
+      if (!ok) break;
+      if (tid == 256 && n + kAhead < cnt) {   // z's readers, Z'(n) and O2(n), are done
+        load_z(n + kAhead);
+        nz = n + kAhead + 1;
+        if (FINE) soon(n + 2);
+      }
+      __syncwarp();
+      tc::fence_after_sync();
+      const float f = REV ? gates(n).tail[row] : a.scale * gates(n).head[row];
+      warp_arrive(bar4(bGFree, n));
+      const F2 ff = pack2(f, f), ss = pack2(a.scale, a.scale);
+      const size_t to = ((tok + t) * a.H + h) * static_cast<size_t>(w.nz) + 64 * slice;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w.out) + to);
+      F2 dot = pack2(0.f, 0.f);
+      auto quarter = [&](int p, const uint4* q) {
+        float x[16], z[16];
+        tc::tmem_ld16(tl + C::O1(n) + 16 * p, x);
+        tc::tmem_ld16(tl + C::O2(n) + 16 * p, z);
+        F2 y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          y[i] = fma2(ff, pack2(x[2 * i], x[2 * i + 1]),
+                      mul2(ss, pack2(z[2 * i], z[2 * i + 1])));
+        if (FINE) {
+          const uint32_t v[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dot = fma2(pack2(x[2 * i], x[2 * i + 1]), widen2(v[i]), dot);
+          if (w.part) {
+            if (live) {
+              ulonglong2* d = reinterpret_cast<ulonglong2*>(w.part + to + 16 * p);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) d[i] = make_ulonglong2(y[2 * i], y[2 * i + 1]);
+            }
+            return;
+          }
+        }
+        if (live) {
+          dst[2 * p] = make_uint4(round2(y[0]), round2(y[1]), round2(y[2]), round2(y[3]));
+          dst[2 * p + 1] = make_uint4(round2(y[4]), round2(y[5]), round2(y[6]), round2(y[7]));
+        }
+      };
+      if constexpr (FINE) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) quarter(p, pr + 2 * p);
+        float d0, d1;
+        unpack2(dot, d0, d1);
+        if (live)
+          w.flow[(static_cast<size_t>(slice) * a.B * a.H + bh) * a.T + t] = f * (d0 + d1);
+      } else {
+#pragma unroll 1
+        for (int p = 0; p < 4; ++p) quarter(p, nullptr);
+      }
+      tc::fence_before_sync();
+      warp_arrive(bar(bFree, n));
+    }
+    if (tid == 256)
+      for (int n = max(0, nz - kAhead); n < nz; ++n) tc::mbar_wait(bar(bZ, n), par(n));
+    __syncwarp();
+  } else if (warp < 14) {
+    // ---------------------------------------------- products
+    const uint32_t go = lane == 0;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    constexpr uint32_t idA = tc::idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t idO = tc::idesc_bf16(128, 64, 0, 1);
+    constexpr uint32_t idP = tc::idesc_bf16(128, 128, 1, 1);
+    // K-major tiles of 64-column blocks: the K step's byte offset
+    auto kmaj = [](int k0) { return static_cast<uint64_t>((k0 >> 6) * kTile + (k0 & 63) * 2) >> 4; };
+    auto rows = [](int k0) { return static_cast<uint64_t>(k0 * 128) >> 4; };
+    uint32_t end = sb + L::oBar + 8 * bEnd;
+    if (warp == 12) {
+      const uint64_t dR = tc::smem_desc(sb + L::oR, 16, 1024);
+      for (int n = 0; n < cnt; ++n) {
+        if (!warp_wait(bar(bXY, n), par(n), abort_flag)) break;
+        // the read-out of chunk n - 2 frees the buffers of A and O1
+        if (n >= 2 && !warp_wait(bar(bFree, n), par(n - 2), abort_flag)) break;
+        tc::fence_after_sync();
+        const uint64_t dx = tc::smem_desc(sb + L::oX + (n & 1) * L::kWide, 16, 1024);
+        const uint64_t dy = tc::smem_desc(sb + L::oY + (n & 1) * L::kWide, 16, 1024);
+#pragma unroll
+        for (int k0 = 0; k0 < W; k0 += 16)
+          mma_if(go, tm + C::A(n), dx + kmaj(k0), dy + kmaj(k0), idA, k0 > 0);
+        commit_if(go, bar(bMA, n));
+        if (!warp_wait(bar(bState, n), par(n), abort_flag)) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k0 = 0; k0 < W; k0 += 16)
+          mma_if(go, tm + C::O1(n), dx + kmaj(k0), dR + rows(k0), idO, k0 > 0);
+        if (FINE) {
+#pragma unroll
+          for (int k0 = 0; k0 < W; k0 += 16)
+            mma_if(go, tm + C::O1(n), dx + kmaj(k0), dR + (L::kR >> 4) + rows(k0), idO, 1);
+        }
+        commit_if(go, bar(bMO1, n));
+      }
+    } else {
+      end += 8;
+      const uint64_t dSplit = tc::smem_desc(sb + L::oSplit, kTile, 1024);
+      for (int n = 0; n < cnt; ++n) {
+        // the state has added the last P before it made its half of this Z'
+        if (!warp_wait(bar(bSplit, n), par(n), abort_flag) ||
+            !warp_wait(bar(bXY, n), par(n), abort_flag))
+          break;
+        tc::fence_after_sync();
+        const uint64_t dy = tc::smem_desc(sb + L::oY + (n & 1) * L::kWide, kTile, 1024);
+#pragma unroll
+        for (int k0 = 0; k0 < kC; k0 += 16)
+          mma_if(go, tm + C::P, dy + rows(k0), dSplit + rows(k0), idP, k0 > 0);
+        commit_if(go, bar(bMP, n));
+        if (!warp_wait(bar(bMask, n), par(n), abort_flag)) break;
+        tc::fence_after_sync();
+        const uint64_t dz = tc::smem_desc(sb + L::oZ + zslot(n), 16, 1024);
+#pragma unroll
+        for (int k0 = 0; k0 < kC; k0 += 16)
+          mma_ta_if(go, tm + C::O2(n), tm + C::A(n) + k0 / 2, dz + rows(k0), idO, k0 > 0);
+        commit_if(go, bar(bMO2, n));
+      }
+    }
+    // nothing may still be reading shared memory when the CTA goes
+    commit_if(go, end);
+    tc::mbar_wait(end, 0);
+  } else {
+    // ---------------------------------------------- gates: the two warps take every
+    // other chunk, up to four chunks ahead of the readers
+    float x[4], y[4];
+    auto read = [&](float (&v)[4], int n) {
+      read_gates(v, a, tok + at(n), h, min(kC, t1 - at(n)));
+    };
+    const int first = warp - 14;
+    if (first < cnt) read(x, first);
+    for (int n = first; n < cnt; n += 2) {
+      // the next values are on their way while these are used
+      if (n + 2 < cnt) read(y, n + 2);
+      if (n >= 4 && !warp_wait(bar4(bGFree, n), par4(n - 4), abort_flag)) break;
+      fill_gates<REV>(gates(n), x);
+      warp_arrive(bar4(bGates, n));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = y[j];
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (*abort_flag) {
+    // a bounded wait gave up: this CTA's results read NaN
+    const float nan = __int_as_float(0x7fffffff);
+    for (int i = tid; i < (t1 - t0) * 64; i += kThreads) {
+      const size_t to = ((tok + t0 + i / 64) * a.H + h) * static_cast<size_t>(w.nz) + 64 * slice +
+                        i % 64;
+      if (w.part) w.part[to] = nan;
+      else static_cast<__nv_bfloat16*>(w.out)[to] = __float2bfloat16_rn(nan);
+    }
+    if (FINE)
+      for (int i = tid; i < t1 - t0; i += kThreads)
+        w.flow[(static_cast<size_t>(slice) * a.B * a.H + bh) * a.T + t0 + i] = nan;
+    if (w.end && seg == (REV ? 0 : sp.segments - 1))
+      for (int i = tid; i < W * 64; i += kThreads)
+        w.end[(static_cast<size_t>(bh) * W + i / 64) * w.nz + 64 * slice + i % 64] = nan;
+  }
+  if (warp == 13) tc::tmem_dealloc(tmem, kCols);
+}
+
+// ------------------------------------------------------------------ states
+
+// A segment's own end state, S = sum over its tokens of decay k v^T (REV: the
+// gradient of its start state from its own read-outs, s sum of decay q dO^T,
+// chunks in reverse), 64 value columns per CTA: the P product alone, V' double
+// buffered so that a chunk is split while the previous one is multiplied.
+constexpr int kStThreads = 224;   // 128: V' and state; loads; products; gates
+constexpr int kStStages = 3;
+
+enum : uint32_t { sFull = 0, sEmpty = 3, sSplit = 6, sP = 8, sGates = 10, sGFree = 12, sEnd = 14,
+                  kStBars = 15 };
+
+template <int NK>
+struct StSmem {
+  static constexpr uint32_t kWide = NK / 64 * kTile, kStage = kWide + kTile;
+  static constexpr uint32_t oSplit = kStStages * kStage, oGates = oSplit + 4 * kTile,
+                            oBar = oGates + 2 * sizeof(Gates), oSlot = oBar + 8 * kStBars + 4,
+                            oAbort = oSlot + 4, bytes = oAbort + 8;
+  static constexpr uint32_t launch = bytes + 1024;
+};
+
+template <int NK, bool REV>
+__global__ void __launch_bounds__(kStThreads, 1)
+    decay_states_tc(const DecayArgs a, const DecaySplit sp, const __grid_constant__ CUtensorMap tx,
+                    const __grid_constant__ CUtensorMap ty) {
+  using L = StSmem<NK>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slices = a.nv / 64, slice = blockIdx.x % slices;
+  const int seg = blockIdx.x / slices + (REV ? 1 : 0);   // segment 0's gradient is not needed
+  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
+  const int t0 = seg * sp.seg_len, t1 = min(a.T, t0 + sp.seg_len);
+  const int cnt = (t1 - t0 + kC - 1) / kC;
+  auto at = [&](int n) { return t0 + (REV ? cnt - 1 - n : n) * kC; };
+  auto bar = [&](uint32_t i) { return sb + L::oBar + 8 * i; };
+  auto bar2 = [&](uint32_t i, int n) { return bar(i + (n & 1)); };
+  auto par = [](int n) { return static_cast<uint32_t>(n >> 1) & 1u; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::oAbort);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::oSlot);
+  auto gates = [&](int n) -> Gates& {
+    return *reinterpret_cast<Gates*>(smem + L::oGates + (n & 1) * sizeof(Gates));
+  };
+  if (warp == 5) tc::tmem_alloc(smem_u32(slot), 256);
+  if (tid == 0) {
+    for (uint32_t i = 0; i < kStBars; ++i)
+      tc::mbar_init(bar(i), (i >= sSplit && i < sP) || (i >= sGFree && i < sEnd) ? 4 : 1);   // warps
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *slot;
+  const int row = 32 * (warp & 3) + lane;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+  const bool mine = row < NK;
+  const size_t st = static_cast<size_t>(NK) * a.nv;
+  float* dst = (REV ? sp.D : sp.S) +
+               (static_cast<size_t>(bh) * sp.slots + (REV ? seg : seg + 1)) * st + 64 * slice;
+
+  if (warp < 4) {
+    float S[64];
+    read_row(S, nullptr, 1);
+    float prod = 1.f;
+    auto split = [&](int n) {
+      if (!warp_wait(bar2(sGates, n), par(n), abort_flag) ||
+          !warp_wait(bar(sFull + n % kStStages), (n / kStStages) & 1, abort_flag))
+        return false;
+      const Gates& g = gates(n);
+      split_row(smem + (n % kStStages) * L::kStage + L::kWide,
+                smem + L::oSplit + (n & 1) * 2 * kTile, row, 0, REV ? g.head[row] : g.tail[row]);
+      split_row(smem + (n % kStStages) * L::kStage + L::kWide,
+                smem + L::oSplit + (n & 1) * 2 * kTile, row, 4, REV ? g.head[row] : g.tail[row]);
+      tc::fence_proxy_async();
+      warp_arrive(bar2(sSplit, n));
+      return true;
+    };
+    bool ok = split(0);
+    for (int n = 0; ok && n < cnt; ++n) {
+      if (n + 1 < cnt) ok = split(n + 1);
+      if (ok) ok = warp_wait(bar2(sP, n), par(n), abort_flag);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const float all = gates(n).all;
+      warp_arrive(bar2(sGFree, n));
+      if (mine || NK == 128) add_state(S, all, tl + (n & 1) * 128);
+      prod *= all;
+      tc::fence_before_sync();
+    }
+    if (ok) {
+      if (mine) write_row(S, REV ? a.scale : 1.f, dst + static_cast<size_t>(row) * a.nv);
+      if (!REV && tid == 0 && slice == 0)
+        sp.decay[static_cast<size_t>(bh) * sp.segments + seg] = prod;
+    }
+  } else if (warp == 4) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int n = 0; n < cnt; ++n) {
+        const int s = n % kStStages;
+        if (n >= kStStages && !wait(bar(sEmpty + s), (n / kStStages - 1) & 1, abort_flag)) break;
+        tc::mbar_arrive_expect_tx(bar(sFull + s), L::kStage);
+#pragma unroll
+        for (int blk = 0; blk < NK / 64; ++blk)
+          tc::tma_load_4d(sb + s * L::kStage + blk * kTile, &tx, 64 * blk, hk, at(n), b,
+                          bar(sFull + s));
+        tc::tma_load_4d(sb + s * L::kStage + L::kWide, &ty, 64 * slice, h, at(n), b,
+                        bar(sFull + s));
+        issued = n + 1;
+      }
+      for (int n = max(0, issued - kStStages); n < issued; ++n)
+        tc::mbar_wait(bar(sFull + n % kStStages), (n / kStStages) & 1);
+    }
+  } else if (warp == 5) {
+    const uint32_t go = lane == 0;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    constexpr uint32_t idP = tc::idesc_bf16(128, 128, 1, 1);
+    for (int n = 0; n < cnt; ++n) {
+      // (the state has read this accumulator, chunk n - 2's, before it made this V')
+      if (!warp_wait(bar2(sSplit, n), par(n), abort_flag)) break;
+      tc::fence_after_sync();
+      const uint64_t dx = tc::smem_desc(sb + (n % kStStages) * L::kStage, kTile, 1024);
+      const uint64_t dy = tc::smem_desc(sb + L::oSplit + (n & 1) * 2 * kTile, kTile, 1024);
+#pragma unroll
+      for (int k0 = 0; k0 < kC; k0 += 16)
+        mma_if(go, tm + (n & 1) * 128, dx + ((k0 * 128) >> 4), dy + ((k0 * 128) >> 4), idP, k0 > 0);
+      commit_if(go, bar2(sP, n));
+      commit_if(go, bar(sEmpty + n % kStStages));
+    }
+    commit_if(go, bar(sEnd));
+    tc::mbar_wait(bar(sEnd), 0);
+  } else {
+    float x[4], y[4];
+    auto read = [&](float (&z)[4], int n) {
+      read_gates(z, a, static_cast<size_t>(b) * a.T + at(n), h, min(kC, t1 - at(n)));
+    };
+    read(x, 0);
+    for (int n = 0; n < cnt; ++n) {
+      if (n + 1 < cnt) read(y, n + 1);
+      const bool ok = n < 2 || warp_wait(bar2(sGFree, n), par(n - 2), abort_flag);
+      if (!ok) break;
+      fill_gates<false>(gates(n), x);
+      warp_arrive(bar2(sGates, n));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = y[j];
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (*abort_flag)   // a bounded wait gave up: the state, and all that follows, reads NaN
+    for (int i = tid; i < NK * 64; i += kStThreads)
+      dst[static_cast<size_t>(i / 64) * a.nv + i % 64] = __int_as_float(0x7fffffff);
+  if (warp == 5) tc::tmem_dealloc(tmem, 256);
+}
+
+// ------------------------------------------------------------------ pairs
+
+// The pairs' part of the gate's gradient: with M_ri = s D_ri (q_r . k_i)
+// (dO_r . v_i) over the pairs i < r of a chunk, for every token t, blocks of 32,
+//   from_t = sum of M_ti over earlier blocks,   to_t = sum of M_rt over later ones,
+//   near_t = sum of M_ti - sum of M_rt within t's block.
+// Both products come twice, as they are and transposed, so that row sums and
+// column sums are each a sum along one lane's columns; everything is fp32, as the
+// sums' differences need it. The blocks' factors come out of the sums:
+// from_t = row[t] sum_i (A . dA)_ti col[i].
+// Chunks are independent: persistent CTAs take every gridDim.x-th, and a chunk's
+// tiles are asked for as soon as the products of the last one are complete.
+constexpr int kPairThreads = 320;   // 128: rows; 128: columns; products and loads; gates
+
+enum : uint32_t { pFull = 0, pDone = 1, pFree = 2, pGates = 4, pGFree = 6, pEnd = 8, kPairBars = 9 };
+
+template <int NK, int NV>
+struct PairSmem {
+  static constexpr uint32_t kK = NK / 64 * kTile, kV = NV / 64 * kTile;
+  static constexpr uint32_t oQ = 0, oK = kK, oV = 2 * kK, oO = oV + kV, oGates = oO + kV,
+                            oBar = oGates + 2 * sizeof(Gates), oSlot = oBar + 8 * kPairBars,
+                            oAbort = oSlot + 4, bytes = oAbort + 4;
+  static constexpr uint32_t launch = bytes + 1024;
+};
+
+template <int NK, int NV>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    decay_pairs_tc(const DecayArgs a, const DecaySplit sp, const __grid_constant__ CUtensorMap tq,
+                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                   const __grid_constant__ CUtensorMap to) {
+  using L = PairSmem<NK, NV>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunks = (a.T + kC - 1) / kC;
+  const long long jobs = static_cast<long long>(a.B) * a.H * chunks;
+  const int cnt = static_cast<int>((jobs - blockIdx.x + gridDim.x - 1) / gridDim.x);
+  // heads fastest: heads that share q and k, and rows of one batch, run together
+  auto job = [&](int n, int& b, int& h, int& t) {
+    const long long j = blockIdx.x + static_cast<long long>(n) * gridDim.x;
+    h = static_cast<int>(j % a.H);
+    const long long c = j / a.H;
+    t = static_cast<int>(c % chunks) * kC;
+    b = static_cast<int>(c / chunks);
+  };
+  auto bar = [&](uint32_t i) { return sb + L::oBar + 8 * i; };
+  auto bar2 = [&](uint32_t i, int n) { return bar(i + (n & 1)); };
+  auto par = [](int n) { return static_cast<uint32_t>(n >> 1) & 1u; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::oAbort);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::oSlot);
+  auto gates = [&](int n) -> Gates& {
+    return *reinterpret_cast<Gates*>(smem + L::oGates + (n & 1) * sizeof(Gates));
+  };
+  if (warp == 8) tc::tmem_alloc(smem_u32(slot), 512);
+  if (tid == 0) {
+    for (uint32_t i = 0; i < kPairBars; ++i)
+      tc::mbar_init(bar(i), i == pFree || i == pGFree || i == pGFree + 1 ? 8 : 1);   // warps
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *slot;
+  const int quad = warp & 3, row = 32 * quad + lane;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+  const size_t plane = static_cast<size_t>(a.B) * a.H * a.T;
+
+  if (warp < 8) {
+    // rows: A, dA in columns 0 and 128; columns: their transposes in 256 and 384
+    const bool cols = warp >= 4;
+    const uint32_t ta = tl + (cols ? 256 : 0);
+    float* far_out = (cols ? sp.to : sp.from) + (sp.flows - 1) * plane;
+    float* near_out = sp.near + (cols ? plane : 0);
+    for (int n = 0; n < cnt; ++n) {
+      int b, h, t;
+      job(n, b, h, t);
+      if (!warp_wait(bar2(pGates, n), par(n), abort_flag) ||
+          !warp_wait(bar(pDone), n & 1, abort_flag))
+        break;
+      tc::fence_after_sync();
+      const Gates& g = gates(n);
+      const float lr = g.loc[row];
+      const uint32_t mine = g.allow[row];
+      float far_sum = 0.f, near_sum = 0.f;
+#pragma unroll 1
+      for (int cb = cols ? quad : 0; cb <= (cols ? 3 : quad); ++cb) {
+        float x[32], y[32];
+        tc::tmem_ld32(ta + 32 * cb, x);
+        tc::tmem_ld32(ta + 128 + 32 * cb, y);
+        if (cb == quad) {
+          const float* f = g.loc + 32 * cb;
+          const uint32_t* m = g.allow + 32 * cb;
+          float acc[2] = {0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            // rows: i < r reaches r; columns: r > i is reached by i
+            const bool use = cols ? i > lane && (m[i] >> lane & 1u)
+                                  : i < lane && (mine >> i & 1u);
+            const float d = exp2_fast(cols ? f[i] - lr : lr - f[i]);
+            acc[i & 1] += use ? x[i] * y[i] * d : 0.f;
+          }
+          near_sum = acc[0] + acc[1];
+        } else {
+          const float fr = cols ? g.col[col_at(cb) + row] : g.row[row];
+          const float* f = cols ? g.row + 32 * cb : g.col + col_at(quad) + 32 * cb;
+          F2 acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(f + i);
+            acc[0] = fma2(mul2(pack2(x[i], x[i + 1]), pack2(y[i], y[i + 1])), c.x, acc[0]);
+            acc[1] = fma2(mul2(pack2(x[i + 2], x[i + 3]), pack2(y[i + 2], y[i + 3])), c.y, acc[1]);
+          }
+          float u, v;
+          unpack2(add2(acc[0], acc[1]), u, v);
+          far_sum = fmaf(fr, u + v, far_sum);
+        }
+      }
+      tc::fence_before_sync();
+      warp_arrive(bar(pFree));
+      warp_arrive(bar2(pGFree, n));
+      if (t + row < a.T) {
+        const size_t to_at = (static_cast<size_t>(b) * a.H + h) * a.T + t + row;
+        far_out[to_at] = a.scale * far_sum;
+        near_out[to_at] = (cols ? -a.scale : a.scale) * near_sum;
+      }
+    }
+  } else if (warp == 8) {
+    const uint32_t go = lane == 0;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 0);
+    auto kmaj = [](int k0) { return static_cast<uint64_t>((k0 >> 6) * kTile + (k0 & 63) * 2) >> 4; };
+    const uint64_t dq = tc::smem_desc(sb + L::oQ, 16, 1024), dk = tc::smem_desc(sb + L::oK, 16, 1024),
+                   dv = tc::smem_desc(sb + L::oV, 16, 1024), dO = tc::smem_desc(sb + L::oO, 16, 1024);
+    auto load = [&](int n) {
+      int b, h, t;
+      job(n, b, h, t);
+      const int hk = h / (a.H / a.Hk);
+      tc::mbar_arrive_expect_tx(bar(pFull), 2 * (L::kK + L::kV));
+#pragma unroll
+      for (int blk = 0; blk < NK / 64; ++blk) {
+        tc::tma_load_4d(sb + L::oQ + blk * kTile, &tq, 64 * blk, hk, t, b, bar(pFull));
+        tc::tma_load_4d(sb + L::oK + blk * kTile, &tk, 64 * blk, hk, t, b, bar(pFull));
+      }
+#pragma unroll
+      for (int blk = 0; blk < NV / 64; ++blk) {
+        tc::tma_load_4d(sb + L::oV + blk * kTile, &tv, 64 * blk, h, t, b, bar(pFull));
+        tc::tma_load_4d(sb + L::oO + blk * kTile, &to, 64 * blk, h, t, b, bar(pFull));
+      }
+    };
+    int issued = 0;
+    if (cnt > 0) {
+      if (lane == 0) load(0);
+      issued = 1;
+    }
+    for (int n = 0; n < cnt; ++n) {
+      if (!warp_wait(bar(pFull), n & 1, abort_flag)) break;
+      if (n >= 1 && !warp_wait(bar(pFree), (n - 1) & 1, abort_flag)) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int k0 = 0; k0 < NK; k0 += 16) {
+        mma_if(go, tm, dq + kmaj(k0), dk + kmaj(k0), id, k0 > 0);
+        mma_if(go, tm + 256, dk + kmaj(k0), dq + kmaj(k0), id, k0 > 0);
+      }
+#pragma unroll
+      for (int k0 = 0; k0 < NV; k0 += 16) {
+        mma_if(go, tm + 128, dO + kmaj(k0), dv + kmaj(k0), id, k0 > 0);
+        mma_if(go, tm + 384, dv + kmaj(k0), dO + kmaj(k0), id, k0 > 0);
+      }
+      commit_if(go, bar(pDone));
+      if (n + 1 < cnt) {
+        if (!warp_wait(bar(pDone), n & 1, abort_flag)) break;
+        if (lane == 0) load(n + 1);
+        issued = n + 2;
+        __syncwarp();
+      }
+    }
+    commit_if(go, bar(pEnd));
+    tc::mbar_wait(bar(pEnd), 0);
+    if (issued > 0) tc::mbar_wait(bar(pFull), (issued - 1) & 1);   // no copy may outlive the CTA
+  } else {
+    float x[4], y[4];
+    auto read = [&](float (&v)[4], int n) {
+      int b, h, t;
+      job(n, b, h, t);
+      read_gates(v, a, static_cast<size_t>(b) * a.T + t, h, min(kC, a.T - t));
+    };
+    if (cnt > 0) read(x, 0);
+    for (int n = 0; n < cnt; ++n) {
+      if (n + 1 < cnt) read(y, n + 1);
+      if (n >= 2 && !warp_wait(bar2(pGFree, n), par(n - 2), abort_flag)) break;
+      fill_gates<false>(gates(n), x);
+      warp_arrive(bar2(pGates, n));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = y[j];
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (*abort_flag)   // a bounded wait gave up: this CTA's sums read NaN
+    for (int n = 0; n < cnt; ++n) {
+      int b, h, t;
+      job(n, b, h, t);
+      for (int i = tid; i < kC; i += kPairThreads)
+        if (t + i < a.T)
+          sp.near[(static_cast<size_t>(b) * a.H + h) * a.T + t + i] = __int_as_float(0x7fffffff);
+    }
+  if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+template <class Kern>
+cudaError_t opt_in(Kern kern, uint32_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes));
+}
+
+struct Rows {   // one of the call's bf16 tensors
+  const void* p;
+  int heads, width;
+  long long stride;
+};
+bool map_of(CUtensorMap* m, const DecayArgs& a, const Rows& r) {
+  return make_rows_tmap(m, r.p, a.B, a.T, r.heads, r.width, r.stride);
+}
+
+template <int W, bool REV, bool FINE>
+cudaError_t walk_w(const DecayArgs& a, const DecaySplit& sp, Walk w, const Rows& x, const Rows& y,
+                   const Rows& z, cudaStream_t stream) {
+  using L = WalkSmem<W, FINE>;
+  static_assert(L::launch <= 232448, "shared memory budget of one CTA");
+  w.x_heads = x.heads; w.y_heads = y.heads; w.z_heads = z.heads; w.nz = z.width;
+  CUtensorMap tx, ty, tz;
+  if (!map_of(&tx, a, x) || !map_of(&ty, a, y) || !map_of(&tz, a, z)) return cudaErrorInvalidValue;
+  const cudaError_t err = opt_in(decay_walk_tc<W, REV, FINE>, L::launch);
+  if (err != cudaSuccess) return err;
+  decay_walk_tc<W, REV, FINE>
+      <<<dim3(sp.segments * (w.nz / 64), a.B * a.H), kThreads, L::launch, stream>>>(a, sp, w, tx,
+                                                                                     ty, tz);
+  return cudaGetLastError();
+}
+template <bool REV, bool FINE>
+cudaError_t walk(const DecayArgs& a, const DecaySplit& sp, const Walk& w, const Rows& x,
+                 const Rows& y, const Rows& z, cudaStream_t stream) {
+  return x.width == 64 ? walk_w<64, REV, FINE>(a, sp, w, x, y, z, stream)
+                       : walk_w<128, REV, FINE>(a, sp, w, x, y, z, stream);
+}
+
+// The walk's first state: S (or D), as rows of key channels or transposed, from
+// the segments' chain or the caller's.
+Walk from(const DecayArgs& a, const DecaySplit& sp, bool grad, bool transposed) {
+  Walk w{};
+  const size_t st = static_cast<size_t>(a.nk) * a.nv;
+  w.start = grad ? a.dhT : a.h0;
+  w.start_bh = st;
+  if (sp.segments > 1) {
+    w.start = grad ? sp.D + st : sp.S;   // segment p ends with D_{p+1}
+    w.start_bh = sp.slots * st;
+    w.start_seg = st;
+  }
+  w.row_step = transposed ? 1 : a.nv;
+  w.col_step = transposed ? a.nv : 1;
+  return w;
+}
+
+template <int NK, bool REV>
+cudaError_t states(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream) {
+  using L = StSmem<NK>;
+  static_assert(L::launch <= 232448, "shared memory budget of one CTA");
+  const long long so = static_cast<long long>(a.H) * a.nv;
+  CUtensorMap tx, ty;
+  if (!make_rows_tmap(&tx, REV ? a.q : a.k, a.B, a.T, a.Hk, NK, REV ? a.sq : a.sk) ||
+      !make_rows_tmap(&ty, REV ? a.dO : a.v, a.B, a.T, a.H, a.nv, REV ? so : a.sv))
+    return cudaErrorInvalidValue;
+  const cudaError_t err = opt_in(decay_states_tc<NK, REV>, L::launch);
+  if (err != cudaSuccess) return err;
+  const int segs = REV ? sp.segments - 1 : sp.slots - 1;
+  decay_states_tc<NK, REV><<<dim3(segs * (a.nv / 64), a.B * a.H), kStThreads, L::launch, stream>>>(
+      a, sp, tx, ty);
+  return cudaGetLastError();
+}
+
+template <int NK, int NV>
+cudaError_t pairs(const DecayArgs& a, const DecaySplit& sp, const Rows& q, const Rows& k,
+                  const Rows& v, const Rows& dO, cudaStream_t stream) {
+  using L = PairSmem<NK, NV>;
+  static_assert(L::launch <= 232448, "shared memory budget of one CTA");
+  CUtensorMap tq, tk, tv, to;
+  if (!map_of(&tq, a, q) || !map_of(&tk, a, k) || !map_of(&tv, a, v) || !map_of(&to, a, dO))
+    return cudaErrorInvalidValue;
+  const cudaError_t err = opt_in(decay_pairs_tc<NK, NV>, L::launch);
+  if (err != cudaSuccess) return err;
+  const long long jobs = static_cast<long long>(a.B) * a.H * ((a.T + kC - 1) / kC);
+  const unsigned grid = static_cast<unsigned>(jobs < kSmCount ? jobs : kSmCount);
+  decay_pairs_tc<NK, NV><<<grid, kPairThreads, L::launch, stream>>>(a, sp, tq, tk, tv, to);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decay_fwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream) {
+  Walk w = from(a, sp, false, false);
+  w.out = a.o;
+  w.end = a.hT;
+  return walk<false, false>(a, sp, w, Rows{a.q, a.Hk, a.nk, a.sq}, Rows{a.k, a.Hk, a.nk, a.sk},
+                            Rows{a.v, a.H, a.nv, a.sv}, stream);
+}
+
+cudaError_t launch_decay_bwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream) {
+  const Rows q{a.q, a.Hk, a.nk, a.sq}, k{a.k, a.Hk, a.nk, a.sk}, v{a.v, a.H, a.nv, a.sv},
+      dO{a.dO, a.H, a.nv, static_cast<long long>(a.H) * a.nv};
+  Walk w = from(a, sp, false, true);
+  w.out = a.dq;
+  w.part = sp.dq_part;
+  w.partner = static_cast<const __nv_bfloat16*>(a.q);
+  w.partner_stride = a.sq;
+  w.flow = sp.from;
+  cudaError_t err = walk<false, true>(a, sp, w, dO, v, k, stream);
+  if (err != cudaSuccess) return err;
+  w = from(a, sp, true, true);
+  w.out = a.dk;
+  w.part = sp.dk_part;
+  w.partner = static_cast<const __nv_bfloat16*>(a.k);
+  w.partner_stride = a.sk;
+  w.flow = sp.to;
+  if ((err = walk<true, true>(a, sp, w, v, dO, q, stream)) != cudaSuccess) return err;
+  w = from(a, sp, true, false);
+  w.out = a.dv;
+  w.end = a.dh0;
+  if ((err = walk<true, false>(a, sp, w, k, q, dO, stream)) != cudaSuccess) return err;
+  return a.nk == 64 ? (a.nv == 64 ? pairs<64, 64>(a, sp, q, k, v, dO, stream)
+                                  : pairs<64, 128>(a, sp, q, k, v, dO, stream))
+                    : (a.nv == 64 ? pairs<128, 64>(a, sp, q, k, v, dO, stream)
+                                  : pairs<128, 128>(a, sp, q, k, v, dO, stream));
+}
+
+cudaError_t launch_decay_states_tc(const DecayArgs& a, const DecaySplit& sp, bool reverse,
+                                   cudaStream_t stream) {
+  if ((reverse ? sp.segments : sp.slots) < 2) return cudaSuccess;
+  if (reverse)
+    return a.nk == 64 ? states<64, true>(a, sp, stream) : states<128, true>(a, sp, stream);
+  return a.nk == 64 ? states<64, false>(a, sp, stream) : states<128, false>(a, sp, stream);
+}
+
+}  // namespace gdr

@@ -22,7 +22,7 @@ constexpr uint32_t kTile = 16384;   // 128 rows of 64 bf16 columns, 128-byte swi
 __device__ __forceinline__ int col_at(int b) { return 16 * b * (b - 1); }   // 0, 32, 96
 struct Gates {
   float loc[kC];        // log2 of the decay from the block's start through r
-  uint32_t allow[kC];   // bit i: token i of r's block reaches r
+  uint32_t allow[kC];   // bit i: token i of r's block reaches r (backward: r reaches i)
   float row[kC];        // decay from the block's start through r
   float col[192];       // col[col_at(b) + i]: decay from after i through the end of block b-1
   float head[kC];       // decay from the chunk's start through r
@@ -88,6 +88,7 @@ __device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * 1.4426
 // per lane and register, so that the four blocks' shuffles overlap. Running sums
 // are taken from both ends: a factor never comes from a difference of sums, and
 // the error of exp_fast, |x| 2^-23, is small where the factor is not.
+template <bool REV>
 __device__ __forceinline__ void fill_gates(Gates& s, const float (&x)[4]) {
   const int lane = threadIdx.x & 31;
   const uint32_t to = 0xffffffffu >> (31 - lane);   // tokens up to this one
@@ -116,9 +117,12 @@ __device__ __forceinline__ void fill_gates(Gates& s, const float (&x)[4]) {
     if (lane == 31) down[b] = 0.f;
     const uint32_t before = clears[b] & to;
     s.loc[32 * b + lane] = up[b] * 1.4426950408889634f;
-    s.allow[32 * b + lane] = to & (0xffffffffu << (before ? 31 - __clz(before) : 0));
+    const uint32_t behind = clears[b] & ~to;
+    s.allow[32 * b + lane] =
+        REV ? (0xffffffffu << lane) & (behind ? (1u << (__ffs(behind) - 1)) - 1u : 0xffffffffu)
+            : to & (0xffffffffu << (before ? 31 - __clz(before) : 0));
     if (before) up[b] = -INFINITY;
-    if (clears[b] & ~to) down[b] = -INFINITY;
+    if (behind) down[b] = -INFINITY;
   }
   float pre = 0.f;
 #pragma unroll
@@ -222,13 +226,25 @@ __device__ __forceinline__ void split_row(const unsigned char* src, unsigned cha
   }
 }
 
-// 64 fp32 values as one row of a swizzled bf16 tile with 128-byte rows.
-__device__ __forceinline__ void round_row(unsigned char* dst, int r, const float (&x)[64]) {
+// 64 fp32 values as one row of a swizzled bf16 tile with 128-byte rows; with LO
+// also what the rounding left, as a second tile `lo` bytes on.
+template <bool LO>
+__device__ __forceinline__ void round_row(unsigned char* dst, uint32_t lo, int r,
+                                          const float (&x)[64]) {
+  const F2 minus = pack2(-1.f, -1.f);
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) << 4)) =
-        make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
-                   pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
+  for (int c = 0; c < 8; ++c) {
+    unsigned char* d = dst + r * 128 + ((c ^ (r & 7)) << 4);
+    uint32_t hi[4], rest[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = pack_bf16x2(x[8 * c + 2 * i], x[8 * c + 2 * i + 1]);
+      if (LO)
+        rest[i] = round2(fma2(widen2(hi[i]), minus, pack2(x[8 * c + 2 * i], x[8 * c + 2 * i + 1])));
+    }
+    *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (LO) *reinterpret_cast<uint4*>(d + lo) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+  }
 }
 
 // S = all * S + (hi + lo) from 128 accumulator columns [hi 64 | lo 64].
@@ -247,14 +263,10 @@ __device__ __forceinline__ void add_state(float (&S)[64], float all, uint32_t ta
   }
 }
 
-// 64 consecutive state values of one row; null: zeros.
-__device__ __forceinline__ void read_row(float (&S)[64], const float* src) {
+// 64 state values of one row, `step` elements apart; null: zeros.
+__device__ __forceinline__ void read_row(float (&S)[64], const float* src, int step) {
 #pragma unroll
-  for (int j = 0; j < 64; j += 4) {
-    const float4 x = src ? *reinterpret_cast<const float4*>(src + j)
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
-    S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
-  }
+  for (int j = 0; j < 64; ++j) S[j] = src ? src[static_cast<size_t>(j) * step] : 0.f;
 }
 __device__ __forceinline__ void write_row(const float (&S)[64], float f, float* dst) {
 #pragma unroll

@@ -9,10 +9,11 @@
 //   dv_i = s sum_{r>=i} e^{G_r-G_i} (q_r . k_i) dO_r + e^{G_C-G_i} D_{n+1}^T k_i
 //   dk_i = s sum_{r>=i} e^{G_r-G_i} (dO_r . v_i) q_r + e^{G_C-G_i} D_{n+1} v_i
 //   D_n  = e^{G_C} D_{n+1} + s sum_r e^{G_r} q_r dO_r^T.
-// The gate's gradient is a reverse running sum of flow_t over the tokens, where
-//   flow_t = s e^{G_t} q_t . (S_n dO_t) - e^{G_C-G_t} k_t . (D_{n+1} v_t)
-//            + sum_{i<=t} M_ti - sum_{r>=t} M_rt,  M_ri = s e^{G_r-G_i}
-//            (q_r . k_i)(dO_r . v_i).
+// The gate's gradient takes, with M_ri = s e^{G_r-G_i} (q_r . k_i)(dO_r . v_i) over
+// the pairs i < r, from every token (gate_grad_kernel joins them)
+//   what comes from before its block of 32: s e^{G_t} q_t . (S_n dO_t) + sum of M_ti
+//   what goes to after it: e^{G_C-G_t} k_t . (D_{n+1} v_t) + sum of M_rt
+//   and within the block the difference of its row's and its column's sums.
 // dq walks the chunks forward with S, dk and dv walk them backward with D; the
 // two walks are independent and run as two halves of one grid.
 //
@@ -321,15 +322,15 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_warp(const DecayArgs a, const
     store_state<NK, NV>(S, a.hT + static_cast<size_t>(w.bh) * NK * NV);
 }
 
-// blockIdx.z = 0: dq and the read-out flow, forward with S. 1: dk, dv and the
-// other flow terms, backward with D.
+// blockIdx.z = 0: dq and the states' part of what comes from before, forward with
+// S. 1: dk, dv and the other terms, backward with D.
 template <int NK, int NV, typename T>
 __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const DecaySplit sp) {
   extern __shared__ __align__(16) float sm[];
   float *S = sm, *Q = S + NK * (NV + 4), *K = Q + kC * (NK + 4), *V = K + kC * (NK + 4),
         *O = V + kC * (NV + 4), *A = O + kC * (NV + 4);
   __shared__ Gates gates;
-  __shared__ float flow[4][kC];
+  __shared__ float flow[6][kC];
   const Where w = where(a, sp, blockIdx.x);
   const int hk = w.h / (a.H / a.Hk);
   const bool rev = blockIdx.z == 1;
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
     const int t = w.t0 + (rev ? chunks - 1 - i : i) * kC, n = min(kC, w.t1 - t);
     __syncthreads();
     if (threadIdx.x < 32) load_gates(gates, a, w.b, w.h, t, n);
-    for (int j = threadIdx.x; j < 4 * kC; j += kThreads) flow[j / kC][j % kC] = 0.f;
+    for (int j = threadIdx.x; j < 6 * kC; j += kThreads) flow[j / kC][j % kC] = 0.f;
     load_tile<NK>(Q, rows_of<T>(a.q, w, t, a.sq, hk * NK), a.sq, n);
     load_tile<NK>(K, rows_of<T>(a.k, w, t, a.sk, hk * NK), a.sk, n);
     load_tile<NV>(V, rows_of<T>(a.v, w, t, a.sv, w.h * NV), a.sv, n);
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
         else dq[at] = static_cast<T>(a.scale * x);
       });
       if (threadIdx.x < n)
-        sp.flow_f[static_cast<size_t>(w.bh) * a.T + t + threadIdx.x] =
+        sp.from[static_cast<size_t>(w.bh) * a.T + t + threadIdx.x] =
             a.scale * (flow[0][threadIdx.x] + flow[1][threadIdx.x]);
       __syncthreads();
       scale_rows<NV>(V, gates.tail);
@@ -419,12 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
     __syncthreads();
     if (threadIdx.x < 2 * kC) {
       const int r = threadIdx.x & (kC - 1);
-      float x = 0.f;
-      if (threadIdx.x < kC)
-        for (int c = 0; c <= r; ++c) x += A[r * (kC + 4) + c];
-      else
-        for (int c = r; c < kC; ++c) x += A[c * (kC + 4) + r];
-      flow[2 + (threadIdx.x >> 6)][r] = x;
+      const int first = r & ~31, last = first + 32;
+      float near = 0.f, far = 0.f;
+      if (threadIdx.x < kC) {
+        for (int c = 0; c < first; ++c) far += A[r * (kC + 4) + c];
+        for (int c = first; c < r; ++c) near += A[r * (kC + 4) + c];
+      } else {
+        for (int c = r + 1; c < last; ++c) near += A[c * (kC + 4) + r];
+        for (int c = last; c < kC; ++c) far += A[c * (kC + 4) + r];
+      }
+      flow[2 + (threadIdx.x >> 6)][r] = far;
+      flow[4 + (threadIdx.x >> 6)][r] = near;
     }
     __syncthreads();
     dA.each([&](int r, int c, float& x) {
@@ -445,8 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
     });
     if (threadIdx.x < n) {
       const int r = threadIdx.x;
-      sp.flow_r[static_cast<size_t>(w.bh) * a.T + t + r] =
-          (flow[2][r] - flow[3][r]) - (flow[0][r] + flow[1][r]);
+      const size_t p = static_cast<size_t>(w.bh) * a.T + t + r;
+      const size_t plane = static_cast<size_t>(a.B) * a.H * a.T;
+      sp.from[p + plane] = flow[2][r];
+      sp.to[p] = flow[0][r] + flow[1][r];
+      sp.to[p + plane] = flow[3][r];
+      sp.near[p] = flow[4][r] - flow[5][r];
     }
     __syncthreads();
     if (threadIdx.x < kC) gates.head[threadIdx.x] *= a.scale;

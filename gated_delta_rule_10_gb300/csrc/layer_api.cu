@@ -68,7 +68,7 @@ void cut(const gdr_decay_shape* s, bool backward, gdr::DecaySplit* sp) {
   const int chunk = s->dtype == GDR_BF16 ? 128 : 64;
   const int chunks = (s->T + chunk - 1) / chunk;
   const long long ctas = static_cast<long long>(s->B) * s->H *
-                         (backward ? 2 : s->dtype == GDR_BF16 ? s->dv / 64 : 1);
+                         (s->dtype == GDR_BF16 ? s->dv / 64 : backward ? 2 : 1);
   long long p = kSms / ctas;
   if (p > chunks / kMinRun) p = chunks / kMinRun;
   if (backward && p < (s->T + kMaxBwdRun - 1) / kMaxBwdRun)
@@ -100,8 +100,12 @@ size_t lay_out(const gdr_decay_shape* s, bool backward, bool end_grad, char* bas
     take(&sp->D, bh * sp->slots * st);
     take(&sp->dots, bh * sp->slots * sp->parts);
   }
-  take(&sp->flow_f, bh * s->T);
-  take(&sp->flow_r, bh * s->T);
+  const bool tc = s->dtype == GDR_BF16;
+  sp->flows = tc ? s->dk / 64 + 1 : 2;   // the states' parts (by column slice), and the pairs
+  sp->nears = tc ? 2 : 1;                // rows, columns
+  take(&sp->from, sp->flows * bh * s->T);
+  take(&sp->to, sp->flows * bh * s->T);
+  take(&sp->near, sp->nears * bh * s->T);
   if (s->Hk != s->H) {
     take(&sp->dq_part, bh * s->T * s->dk);
     take(&sp->dk_part, bh * s->T * s->dk);
@@ -217,7 +221,8 @@ gdr_status gdr_decay_chunk_bwd(const gdr_decay_shape* shape, const void* q, cons
                 : gdr::launch_decay_states_tc(a, sp, rev, cs);
     if (err == cudaSuccess) err = gdr::launch_decay_chain(a, sp, true, cs);
   }
-  if (err == cudaSuccess) err = gdr::launch_decay_bwd_warp(a, sp, f32, cs);
+  if (err == cudaSuccess)
+    err = f32 ? gdr::launch_decay_bwd_warp(a, sp, f32, cs) : gdr::launch_decay_bwd_tc(a, sp, cs);
   if (err == cudaSuccess) err = gdr::launch_decay_gate_grad(a, sp, f32, cs);
   return status_of(err);
 }
