@@ -7,7 +7,7 @@
 namespace gdr {
 
 constexpr int kNormMaxWidth = 8192;   // columns of a row: what a CTA holds in registers
-constexpr int kNormBwdCtas = 608;     // 4 x 152 SMs: partial rows of the weight's gradient
+constexpr int kNormBwdCtas = 304;     // 2 x 152 SMs, of 256 threads: partial rows of dw
 
 struct AddNormArgs {
   const void *x, *res;

@@ -8,6 +8,7 @@ namespace {
 
 constexpr int kChainThreads = 256;
 
+template <int kThreads>
 __device__ __forceinline__ float block_sum(float x, float* red) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -16,7 +17,7 @@ __device__ __forceinline__ float block_sum(float x, float* red) {
   __syncthreads();
   float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < kChainThreads / 32; ++i) s += red[i];
+  for (int i = 0; i < kThreads / 32; ++i) s += red[i];
   return s;
 }
 
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kChainThreads) chain_kernel(const DecayArgs a,
     }
     D[p * step] = d;
     const float4 x = S[p * step];
-    const float dot = block_sum(x.x * d.x + x.y * d.y + x.z * d.z + x.w * d.w, red);
+    const float dot = block_sum<kChainThreads>(x.x * d.x + x.y * d.y + x.z * d.z + x.w * d.w, red);
     if (threadIdx.x == 0)
       sp.dots[(static_cast<size_t>(bh) * sp.slots + p) * sp.parts + blockIdx.x] = dot;
   }
@@ -64,36 +65,41 @@ __global__ void __launch_bounds__(kChainThreads) chain_kernel(const DecayArgs a,
 
 // The gate's gradient. With c the product <S, D> at a block's end (32 tokens),
 //   dg_t = c + sum over the block's j >= t of (from_j - to_j + near_j),
-//   <S, D> at its start = c - sum of to + sum of from;
-// the near terms of a block sum to zero, so they stay out of what is passed on,
+//   <S, D> at its start = c - sum of to + sum of from.
+// The near terms of a block sum to zero, so they stay out of what is passed on,
 // and with them the rounding of the block's largest products. A block whose decay
-// is below 2^-30 passes nothing on: what crosses it is 2^-30 of <S, D>, less than
-// the rounding of what is passed (so that error does not gather over a long
-// sequence of short memories): c is then the sum of to, and the start's the sum of
-// from. A clearing token's own gradient is 0. A warp takes a block; what passes
-// through blocks is a map c -> keep c + add, and maps compose.
-__global__ void __launch_bounds__(kChainThreads) gate_grad_kernel(const DecayArgs a,
+// is below 2^-30 passes nothing on (what crosses it is 2^-30 of <S, D>): c is then
+// its sum of to, and the start's its sum of from.
+// So c is known at both ends of every run of blocks between such blocks and the
+// segment's edges (from the states there). What the blocks' sums pass on, with
+// rounding that gathers like a random walk, misses the far end by a little; the
+// miss is spread evenly over the run, which takes two thirds of the walk's variance
+// away. A clearing token's gradient is 0.
+constexpr int kMaxBlocks = 128;   // blocks per segment: 4096 tokens
+constexpr int kGateThreads = 1024;
+
+__global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const DecayArgs a,
                                                                   const DecaySplit sp) {
-  constexpr int kWarps = kChainThreads / 32;
-  __shared__ float w_add[kWarps];
-  __shared__ int w_keep[kWarps];
+  constexpr int kWarps = kGateThreads / 32;
+  constexpr int kMine = kMaxBlocks / kWarps;   // blocks per warp
+  __shared__ float s_from[kMaxBlocks], s_to[kMaxBlocks], s_c[kMaxBlocks];
+  __shared__ int s_keep[kMaxBlocks], s_run[kMaxBlocks];
+  __shared__ int run_last[kMaxBlocks + 1];      // a run's latest block
+  __shared__ float run_share[kMaxBlocks + 1];   // and each block's share of its miss
   __shared__ float red[kWarps];
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
   const int t0 = seg * sp.seg_len, t1 = min(a.T, t0 + sp.seg_len);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t plane = static_cast<size_t>(a.B) * a.H * a.T;
-  float carry = 0.f, total = 0.f;
-  if (sp.dots)
-    for (int i = 0; i < sp.parts; ++i)
-      carry += sp.dots[(static_cast<size_t>(bh) * sp.slots + seg + 1) * sp.parts + i];
   const int blocks = (t1 - t0 + 31) / 32;
-  for (int last = blocks - 1; last >= 0; last -= kWarps) {
-    const int blk = last - warp, t = t0 + blk * 32 + lane;   // warp 0 the latest block
-    const bool in = blk >= 0 && t < t1;
-    const size_t at = (static_cast<size_t>(b) * a.T + t) * a.H + h;
+  bool clear[kMine];
+  float suf[kMine];   // the block's sum from this token on
+#pragma unroll
+  for (int m = 0; m < kMine; ++m) {
+    const int blk = warp + m * kWarps, t = t0 + blk * 32 + lane;
     float g = 0.f, f = 0.f, e = 0.f, l = 0.f;
-    if (in) {
-      g = a.per_head ? a.g[h] : a.g[at];
+    if (t < t1) {
+      g = a.per_head ? a.g[h] : a.g[(static_cast<size_t>(b) * a.T + t) * a.H + h];
       const size_t p = static_cast<size_t>(bh) * a.T + t;
       for (int i = 0; i < sp.flows; ++i) {
         f += sp.from[p + i * plane];
@@ -101,40 +107,84 @@ __global__ void __launch_bounds__(kChainThreads) gate_grad_kernel(const DecayArg
       }
       for (int i = 0; i < sp.nears; ++i) l += sp.near[p + i * plane];
     }
-    const bool clear = g <= kDecayReset;
-    float sum = g, suf = f - e + l;
+    clear[m] = g <= kDecayReset;
+    suf[m] = f - e + l;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       f += __shfl_xor_sync(0xffffffffu, f, off);
       e += __shfl_xor_sync(0xffffffffu, e, off);
-      sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      g += __shfl_xor_sync(0xffffffffu, g, off);
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const float y = __shfl_down_sync(0xffffffffu, suf, off);
-      if (lane + off < 32) suf += y;
+      const float y = __shfl_down_sync(0xffffffffu, suf[m], off);
+      if (lane + off < 32) suf[m] += y;
     }
-    const int keep = !(sum < -20.8f);   // (NaN keeps)
-    if (lane == 0) {
-      w_add[warp] = keep ? f - e : f;
-      w_keep[warp] = keep;
+    if (lane == 0 && blk < blocks) {
+      s_from[blk] = f;
+      s_to[blk] = e;
+      s_keep[blk] = !(g < -20.8f);   // (NaN keeps)
     }
-    __syncthreads();
-    float c = carry;
+  }
+  // <S, D> where the sequence starts from a state
+  float first = 0.f;
+  const bool given = seg == 0 && a.h0;
+  if (given && a.dh0) {
+    const size_t st = static_cast<size_t>(a.nk) * a.nv;
+    for (size_t i = threadIdx.x; i < st; i += kGateThreads)
+      first = fmaf(a.h0[bh * st + i], a.dh0[bh * st + i], first);
+    first = block_sum<kGateThreads>(first, red);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    auto edge = [&](int slot) {   // <S, D> at a segment's edge
+      float c = 0.f;
+      if (sp.dots)
+        for (int i = 0; i < sp.parts; ++i)
+          c += sp.dots[(static_cast<size_t>(bh) * sp.slots + slot) * sp.parts + i];
+      return c;
+    };
+    float c = edge(seg + 1);
+    const float start = seg > 0 ? edge(seg) : first;
+    int last = blocks - 1, run = 0;
+    for (int blk = blocks - 1; blk >= 0; --blk) {
+      const bool keep = s_keep[blk];
+      const float f = s_from[blk], e = s_to[blk];
+      s_c[blk] = keep ? c : e;
+      s_run[blk] = keep ? run : kMaxBlocks;
+      if (keep) c += f - e;
+      // a run's far end is a block that passes nothing, or the segment's start (not
+      // known where a given state's gradient was not asked for)
+      if (!keep || blk == 0) {
+        const int steps = last - blk + (keep ? 1 : 0);
+        const bool known = !keep || !given || a.dh0;
+        run_last[run] = last;
+        run_share[run] = known && steps > 0 ? (c - (keep ? start : e)) / static_cast<float>(steps)
+                                            : 0.f;
+        ++run;
+      }
+      if (!keep) {
+        c = f;
+        last = blk - 1;
+      }
+    }
+    run_last[kMaxBlocks] = 0;
+    run_share[kMaxBlocks] = 0.f;
+  }
+  __syncthreads();
+  float total = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i == warp) c = carry;
-      carry = w_keep[i] ? carry + w_add[i] : w_add[i];
-    }
-    const float out = clear ? 0.f : (keep ? c : e) + suf;
-    if (in) {
-      if (a.per_head) total += out;
-      else a.dg[at] = out;
-    }
-    __syncthreads();
+  for (int m = 0; m < kMine; ++m) {
+    const int blk = warp + m * kWarps, t = t0 + blk * 32 + lane;
+    if (t >= t1) continue;
+    const int run = s_run[blk];
+    const float c = s_c[blk] - run_share[run] * static_cast<float>(run_last[run] - blk);
+    const float out = clear[m] ? 0.f : c + suf[m];
+    if (a.per_head) total += out;
+    else a.dg[(static_cast<size_t>(b) * a.T + t) * a.H + h] = out;
   }
   if (a.per_head) {
-    const float s = block_sum(total, red);
+    const float s = block_sum<kGateThreads>(total, red);
     if (threadIdx.x == 0) sp.dg_part[static_cast<size_t>(bh) * sp.segments + seg] = s;
   }
 }
@@ -188,7 +238,7 @@ cudaError_t launch_decay_chain(const DecayArgs& a, const DecaySplit& sp, bool ba
 
 cudaError_t launch_decay_gate_grad(const DecayArgs& a, const DecaySplit& sp, bool f32,
                                    cudaStream_t stream) {
-  gate_grad_kernel<<<dim3(sp.segments, a.B * a.H), kChainThreads, 0, stream>>>(a, sp);
+  gate_grad_kernel<<<dim3(sp.segments, a.B * a.H), kGateThreads, 0, stream>>>(a, sp);
   if (a.per_head) head_grad_kernel<<<a.H, 32, 0, stream>>>(a, sp);
   if (sp.dq_part) {
     const size_t n4 = static_cast<size_t>(a.B) * a.T * a.Hk * (a.nk / 4);

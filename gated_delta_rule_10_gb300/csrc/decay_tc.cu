@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         !warp_wait(bar(bZ, n), par(n), abort_flag))
       return false;
     const Gates& g = gates(n);
-    split_row(smem + L::oZ + zslot(n), smem + L::oSplit, row, 4 * half,
+    split_row(sb + L::oZ + zslot(n), sb + L::oSplit, row, 4 * half,
               REV ? a.scale * g.head[row] : g.tail[row]);
     tc::fence_proxy_async();
     warp_arrive(bar(bSplit, n));
@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float e = exp2_fast(REV ? c[j] - lr : lr - c[j]);
                 x[i + j] = (allow >> (i + j)) & 1u ? x[i + j] * e : 0.f;
               }
+              r[i / 2] = pack_bf16x2(x[i], x[i + 1]);
+              r[i / 2 + 1] = pack_bf16x2(x[i + 2], x[i + 3]);
             }
           } else {
             // forward: row[t] col[i]; backward: col[t] of this block pair, row[i]
@@ -207,12 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(f + i);
-              unpack2(mul2(pack2(x[i], x[i + 1]), mul2(ff, c.x)), x[i], x[i + 1]);
-              unpack2(mul2(pack2(x[i + 2], x[i + 3]), mul2(ff, c.y)), x[i + 2], x[i + 3]);
+              r[i / 2] = round2(mul2(pack2(x[i], x[i + 1]), mul2(ff, c.x)));
+              r[i / 2 + 1] = round2(mul2(pack2(x[i + 2], x[i + 3]), mul2(ff, c.y)));
             }
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
         }
         tc::tmem_st16(tl + C::A(n) + 16 * cb, r);   // over columns already read
       }
@@ -324,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       F2 dot = pack2(0.f, 0.f);
       auto quarter = [&](int p, const uint4* q) {
         float x[16], z[16];
-        tc::tmem_ld16(tl + C::O1(n) + 16 * p, x);
-        tc::tmem_ld16(tl + C::O2(n) + 16 * p, z);
+        tmem_ld16x2(tl + C::O1(n) + 16 * p, tl + C::O2(n) + 16 * p, x, z);
         F2 y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -387,17 +386,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         const uint64_t dx = tc::smem_desc(sb + L::oX + (n & 1) * L::kWide, 16, 1024);
         const uint64_t dy = tc::smem_desc(sb + L::oY + (n & 1) * L::kWide, 16, 1024);
-#pragma unroll
+#pragma unroll 1
         for (int k0 = 0; k0 < W; k0 += 16)
           mma_if(go, tm + C::A(n), dx + kmaj(k0), dy + kmaj(k0), idA, k0 > 0);
         commit_if(go, bar(bMA, n));
         if (!warp_wait(bar(bState, n), par(n), abort_flag)) break;
         tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
         for (int k0 = 0; k0 < W; k0 += 16)
           mma_if(go, tm + C::O1(n), dx + kmaj(k0), dR + rows(k0), idO, k0 > 0);
         if (FINE) {
-#pragma unroll
+#pragma unroll 1
           for (int k0 = 0; k0 < W; k0 += 16)
             mma_if(go, tm + C::O1(n), dx + kmaj(k0), dR + (L::kR >> 4) + rows(k0), idO, 1);
         }
@@ -413,14 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         tc::fence_after_sync();
         const uint64_t dy = tc::smem_desc(sb + L::oY + (n & 1) * L::kWide, kTile, 1024);
-#pragma unroll
+#pragma unroll 1
         for (int k0 = 0; k0 < kC; k0 += 16)
           mma_if(go, tm + C::P, dy + rows(k0), dSplit + rows(k0), idP, k0 > 0);
         commit_if(go, bar(bMP, n));
         if (!warp_wait(bar(bMask, n), par(n), abort_flag)) break;
         tc::fence_after_sync();
         const uint64_t dz = tc::smem_desc(sb + L::oZ + zslot(n), 16, 1024);
-#pragma unroll
+#pragma unroll 1
         for (int k0 = 0; k0 < kC; k0 += 16)
           mma_ta_if(go, tm + C::O2(n), tm + C::A(n) + k0 / 2, dz + rows(k0), idO, k0 > 0);
         commit_if(go, bar(bMO2, n));
@@ -541,10 +540,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
           !warp_wait(bar(sFull + n % kStStages), (n / kStStages) & 1, abort_flag))
         return false;
       const Gates& g = gates(n);
-      split_row(smem + (n % kStStages) * L::kStage + L::kWide,
-                smem + L::oSplit + (n & 1) * 2 * kTile, row, 0, REV ? g.head[row] : g.tail[row]);
-      split_row(smem + (n % kStStages) * L::kStage + L::kWide,
-                smem + L::oSplit + (n & 1) * 2 * kTile, row, 4, REV ? g.head[row] : g.tail[row]);
+      split_row(sb + (n % kStStages) * L::kStage + L::kWide,
+                sb + L::oSplit + (n & 1) * 2 * kTile, row, 0, REV ? g.head[row] : g.tail[row]);
+      split_row(sb + (n % kStStages) * L::kStage + L::kWide,
+                sb + L::oSplit + (n & 1) * 2 * kTile, row, 4, REV ? g.head[row] : g.tail[row]);
       tc::fence_proxy_async();
       warp_arrive(bar2(sSplit, n));
       return true;

@@ -71,6 +71,30 @@ __device__ __forceinline__ F2 widen2(uint32_t w) {
   return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// 16 columns at each of two places, one wait for both.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&u)[16],
+                                            float (&v)[16]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta), "r"(tb)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    u[i] = __uint_as_float(r[i]);
+    v[i] = __uint_as_float(r[16 + i]);
+  }
+}
+
 // The log-decays of this lane's tokens 32 j + lane (0 past n).
 __device__ __forceinline__ void read_gates(float (&x)[4], const DecayArgs& a, size_t tok, int h,
                                            int n) {
@@ -152,8 +176,16 @@ __device__ __noinline__ bool wait_long(uint32_t mbar, uint32_t parity, volatile 
   *abort_flag = 1;
   return false;
 }
+// The first poll is in line and lets the hardware choose how long it may sleep.
 __device__ __forceinline__ bool wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag) {
-  return tc::mbar_test(mbar, parity) || wait_long(mbar, parity, abort_flag);
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(mbar), "r"(parity)
+      : "memory");
+  return done || wait_long(mbar, parity, abort_flag);
 }
 // The same for a whole warp, with one answer. Every lane polls: with one lane
 // polling in a branch of its own, a hand-over took several times as long.
@@ -193,11 +225,24 @@ __device__ __forceinline__ void commit_if(uint32_t go, uint32_t mbar) {
       : "memory");
 }
 
+__device__ __forceinline__ uint4 lds4(uint32_t addr) {
+  uint4 u;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(addr)
+               : "memory");
+  return u;
+}
+__device__ __forceinline__ void sts4(uint32_t addr, const uint32_t (&u)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(u[0]), "r"(u[1]),
+               "r"(u[2]), "r"(u[3])
+               : "memory");
+}
+
 // Chunks c0 .. c0 + 3 (32 columns) of row `r` of a 128 x 64 bf16 tile times f,
 // as hi + lo bf16 tiles (kTile apart): together they hold the product to 2^-17,
 // so the fp32 state they feed keeps its precision.
-__device__ __forceinline__ void split_row(const unsigned char* src, unsigned char* dst, int r,
-                                          int c0, float f) {
+__device__ __forceinline__ void split_row(uint32_t src, uint32_t dst, int r, int c0, float f) {
   const F2 ff = pack2(f, f), minus = pack2(-1.f, -1.f);
 #pragma unroll 1
   for (int c = c0; c < c0 + 4; c += 2) {
@@ -205,7 +250,7 @@ __device__ __forceinline__ void split_row(const unsigned char* src, unsigned cha
                              static_cast<uint32_t>(r * 128 + (((c + 1) ^ (r & 7)) << 4))};
     uint4 u[2];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) u[p] = *reinterpret_cast<const uint4*>(src + off[p]);
+    for (int p = 0; p < 2; ++p) u[p] = lds4(src + off[p]);
     uint32_t hi[2][4], lo[2][4];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
@@ -219,9 +264,8 @@ __device__ __forceinline__ void split_row(const unsigned char* src, unsigned cha
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      *reinterpret_cast<uint4*>(dst + off[p]) = make_uint4(hi[p][0], hi[p][1], hi[p][2], hi[p][3]);
-      *reinterpret_cast<uint4*>(dst + kTile + off[p]) =
-          make_uint4(lo[p][0], lo[p][1], lo[p][2], lo[p][3]);
+      sts4(dst + off[p], hi[p]);
+      sts4(dst + kTile + off[p], lo[p]);
     }
   }
 }
@@ -253,8 +297,7 @@ __device__ __forceinline__ void add_state(float (&S)[64], float all, uint32_t ta
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     float hi[16], lo[16];
-    tc::tmem_ld16(taddr + 16 * p, hi);
-    tc::tmem_ld16(taddr + 64 + 16 * p, lo);
+    tmem_ld16x2(taddr + 16 * p, taddr + 64 + 16 * p, hi, lo);
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
       float &a = S[16 * p + j], &b = S[16 * p + j + 1];

@@ -331,9 +331,9 @@ gdr_status gdr_rotary(const gdr_rotary_shape* s, const void* q, const void* k,
     return GDR_ERR_INVALID_ARG;
   if (!given16(cos_table) || !given16(sin_table) || !aligned(positions, 4))
     return GDR_ERR_INVALID_ARG;
-  // threads: one per token, 16 channels and 4 heads
+  // threads: one per token, 16 channels and 2 heads
   if (tokens > (1LL << 31) - 1 ||
-      tokens * (s->d / 16) * ((s->H + static_cast<long long>(s->Hk) + 3) / 4) > (1LL << 31) - 257)
+      tokens * (s->d / 16) * ((s->H + static_cast<long long>(s->Hk) + 1) / 2) > (1LL << 31) - 257)
     return GDR_ERR_UNSUPPORTED;
   gdr::RotaryArgs a{};
   a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;

@@ -15,8 +15,8 @@
 namespace gdr {
 namespace {
 
-constexpr int kHeads = 4;
-constexpr int kThreads = 256;
+constexpr int kHeads = 2;
+constexpr int kThreads = 128;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, int units,
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
     c0 = 8 * u;
     c1 = a.rot / 2 + 8 * u;
   }
-  float x[kHeads][2][8];
+  Raw8<T> raw[kHeads][2];
   const T* src[kHeads];
   T* dst[kHeads];
 #pragma unroll
@@ -53,12 +53,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
     dst[i] = is_q ? static_cast<T*>(a.q_out) + tok * a.sqo + static_cast<long long>(h) * a.d
                   : static_cast<T*>(a.k_out) + tok * a.sko + static_cast<long long>(hk) * a.d;
     if (h < a.H + a.Hk) {
-      load8(src[i] + c0, x[i][0]);
-      load8(src[i] + c1, x[i][1]);
+      raw[i][0].load(src[i] + c0);
+      raw[i][1].load(src[i] + c1);
     }
   }
+  float x[2][8], cs[8], sn[8];
   if (u < turned) {
-    float cs[8], sn[8];
     const int p = a.pos ? __ldg(a.pos + tok) : a.start + static_cast<int>(tok % a.T);
     if (p >= 0 && p < a.table_len) {
       load8(a.cos_t + static_cast<long long>(p) * (a.rot / 2) + 8 * u, cs);
@@ -71,23 +71,24 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
 #pragma unroll
       for (int j = 0; j < 8; ++j) sn[j] = -sn[j];
     }
+  }
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
+  for (int i = 0; i < kHeads; ++i) {
+    if (g + i * groups >= a.H + a.Hk) continue;
+    raw[i][0].get(x[0]);
+    raw[i][1].get(x[1]);
+    if (u < turned) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float &p0 = a.interleaved ? x[i][j >> 2][2 * (j & 3)] : x[i][0][j];
-        float &p1 = a.interleaved ? x[i][j >> 2][2 * (j & 3) + 1] : x[i][1][j];
+        float& p0 = a.interleaved ? x[j >> 2][2 * (j & 3)] : x[0][j];
+        float& p1 = a.interleaved ? x[j >> 2][2 * (j & 3) + 1] : x[1][j];
         const float e = p0, f = p1;
         p0 = e * cs[j] - f * sn[j];
         p1 = f * cs[j] + e * sn[j];
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (g + i * groups >= a.H + a.Hk) continue;
-    store8(dst[i] + c0, x[i][0]);
-    store8(dst[i] + c1, x[i][1]);
+    store8(dst[i] + c0, x[0]);
+    store8(dst[i] + c1, x[1]);
   }
 }
 

@@ -8,7 +8,7 @@ import ctypes
 
 import torch
 
-from ._binding import GDR_BF16, GDR_F32, GdrError, _check, _ptr, _stream, _vp, lib
+from ._binding import GDR_BF16, GDR_F32, GdrError, _check as _check_slow, _vp, lib
 
 _ll, _sz, _int, _f32 = ctypes.c_longlong, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 
@@ -66,17 +66,41 @@ def _lib():
     return _fns
 
 
+# A decode step makes these calls once per layer: the common case of each helper
+# below is a few attribute reads.
+
 def _call(name, device, *args):
-    with torch.cuda.device(device):
-        st = getattr(_lib(), name)(*args)
+    fn = getattr(_fns or _lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
     if st:
         raise GdrError(st, name)
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _check(t, name, dtype, device, shape=None):
+    if t is None or (t.dtype is dtype and t.device == device and device.type == "cuda" and
+                     t.is_contiguous() and (shape is None or t.shape == shape)):
+        return
+    _check_slow(t, name, dtype, device, shape)
+
+
 def _dtype(t):
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return GDR_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return GDR_F32
     raise ValueError("expected bf16 or fp32, got %s" % t.dtype)
 
@@ -97,6 +121,9 @@ def _used_on(stream, device, *tensors):
 def _rows(t, name, dtype, device, shape):
     """Checks a [B, T, heads, d] tensor whose heads and channels are dense and
     whose tokens are evenly spaced over the batch; returns elements per token."""
+    if t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape and \
+            t.is_contiguous():
+        return 0
     if not t.is_cuda or t.device != device:
         raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
     if t.dtype != dtype:
@@ -104,14 +131,22 @@ def _rows(t, name, dtype, device, shape):
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     B, T, H, d = shape
-    if t.is_contiguous():
-        return 0
     sb, st, sh, sd = t.stride()
     step = st if T > 1 else sb
     if (d > 1 and sd != 1) or (H > 1 and sh != d) or (T > 1 and B > 1 and sb != T * st) or \
             step < H * d:
         raise ValueError("%s must have dense heads and evenly spaced tokens" % name)
     return step
+
+
+def _tokens(t, name, dtype, device, shape):
+    """_rows of an [N, heads, d] tensor: one token of each of N sequences."""
+    if t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape and \
+            t.is_contiguous():
+        return 0
+    if t.dim() != 3:
+        raise ValueError("%s must be [N, heads, d]" % name)
+    return _rows(t.unsqueeze(1), name, dtype, device, (shape[0], 1) + tuple(shape[1:]))
 
 
 def _new_or(t, name, shape, dtype, device):
@@ -137,7 +172,7 @@ def _decay_shape(q, k, v, g, scale):
 
 def decay_chunk_fwd_workspace_bytes(shape):
     n = _sz(0)
-    st = _lib().gdr_decay_chunk_fwd_workspace(ctypes.byref(shape), ctypes.byref(n))
+    st = (_fns or _lib()).gdr_decay_chunk_fwd_workspace(ctypes.byref(shape), ctypes.byref(n))
     if st:
         raise GdrError(st, "gdr_decay_chunk_fwd_workspace")
     return n.value
@@ -215,13 +250,14 @@ def decay_step(q, k, v, g, state, *, scale=None, o=None, stream=None):
     """
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be [N, heads, d]")
-    N, H = v.shape[0], v.shape[1]
-    if g.dim() == 2:
-        _check(g, "g", torch.float32, q.device, (N, H))
-        g = g.view(N, 1, H)
-    s = _decay_shape(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g, scale)
-    dev = q.device
-    _check(state, "state", torch.float32, dev, (N, H, s.dk, s.dv))
+    N, H, dv = v.shape
+    Hk, dk = q.shape[1], q.shape[2]
+    dev, dt = q.device, q.dtype
+    s = DecayShape(N, 1, H, Hk, dk, dv, _dtype(q), int(g.dim() == 1),
+                   float(dk ** -0.5 if scale is None else scale), _tokens(q, "q", dt, dev, (N, Hk, dk)),
+                   _tokens(k, "k", dt, dev, (N, Hk, dk)), _tokens(v, "v", dt, dev, (N, H, dv)))
+    _check(g, "g", torch.float32, dev, (H,) if g.dim() == 1 else (N, H))
+    _check(state, "state", torch.float32, dev, (N, H, dk, dv))
     o, new_o = _new_or(o, "o", (N, H, s.dv), q.dtype, dev)
     _call("gdr_decay_step", dev, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state),
           _ptr(o), _stream(stream, dev))

@@ -658,7 +658,7 @@ gdr_status gdr_add_rmsnorm_bwd(long long rows, int D, gdr_dtype dtype, const voi
  * start + t. A position outside the table turns its token's pairs into NaN.
  * cos_table, sin_table [table_length, rot/2] fp32, 16-byte aligned.
  * rot and d are multiples of 16, rot <= d. Fewer than 2^31 groups of (token, 16
- * channels, 4 heads).
+ * channels, 2 heads).
  */
 typedef struct {
   int B, T, H, Hk, d;
