@@ -22,16 +22,18 @@ struct DecayArgs {
 };
 
 // One call's cut of the sequences: `segments` runs of `seg_len` tokens (whole
-// chunks; the last may be shorter), and the workspace's arrays. States are
-// [B * H, slots, nk, nv] fp32.
+// chunks; the last may be shorter), each of `parts_per` pieces of `piece_len`
+// tokens whose own states are computed separately (`pieces` in all), and the
+// workspace's arrays. States are [B * H, slots, nk, nv] fp32.
 struct DecaySplit {
   int segments = 1;
   int seg_len = 0;
-  int slots = 0;              // state slots per (batch, head)
+  int pieces = 1, parts_per = 1, piece_len = 0;
+  int slots = 0;              // state slots per (batch, head): pieces, backward + 1
   int parts = 1;              // partial sums of each boundary dot product
-  float* S = nullptr;         // slot p: the state entering segment p
+  float* S = nullptr;         // slot p: the state entering piece p
   float* D = nullptr;         // slot p: the gradient of that state (backward)
-  float* decay = nullptr;     // [B * H, segments] product of a segment's decays
+  float* decay = nullptr;     // [B * H, pieces] product of a piece's decays
   float* dots = nullptr;      // [B * H, slots, parts] partial <S_p, D_p>
   // Terms of the gate's gradient by token, [flows, B * H, T] (the parts add up):
   // what its row takes from before its block of 32 tokens, what its keys and values
@@ -43,6 +45,10 @@ struct DecaySplit {
   float* dq_part = nullptr;   // [B, T, H, nk] per-head gradients of shared q, k
   float* dk_part = nullptr;
   float* dg_part = nullptr;   // [B * H, segments] sums for a per-head decay
+  // slot of the state entering segment p (p = segments: leaving the last)
+  __host__ __device__ int slot_of(int p) const { return p < segments ? p * parts_per : pieces; }
+  // pieces whose own state is needed: up to the last segment's start, or to the end
+  __host__ __device__ int states(bool to_end) const { return to_end ? pieces : slot_of(segments - 1); }
 };
 
 // A log-decay at or below this clears the state: exp() of it is zero in fp32.
@@ -60,7 +66,7 @@ cudaError_t launch_decay_states_tc(const DecayArgs& a, const DecaySplit& sp, boo
                                    cudaStream_t stream);
 cudaError_t launch_decay_fwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream);
 cudaError_t launch_decay_bwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream);
-// Chains the segments' states (decay_chain.cu); backward also chains the
+// Chains the pieces' states (decay_chain.cu); backward also chains the
 // states' gradients and writes the boundary dot products.
 cudaError_t launch_decay_chain(const DecayArgs& a, const DecaySplit& sp, bool backward,
                                cudaStream_t stream);

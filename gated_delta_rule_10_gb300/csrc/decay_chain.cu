@@ -21,10 +21,10 @@ __device__ __forceinline__ float block_sum(float x, float* red) {
   return s;
 }
 
-// S_p = decay_{p-1} S_{p-1} + (segment p-1's own state), S_0 = h0; in place over
+// S_p = decay_{p-1} S_{p-1} + (piece p-1's own state), S_0 = h0; in place over
 // the slots, each thread carrying one float4 of the state along the chain (the
-// loads of the segments' own states do not wait for it). Backward: D_p =
-// decay_p D_{p+1} + (segment p's own gradient), D_P = dhT, and this block's part
+// loads of the pieces' own states do not wait for it). Backward: D_p =
+// decay_p D_{p+1} + (piece p's own gradient), D_P = dhT, and this block's part
 // of <S_p, D_p> for every p >= 1.
 template <bool BWD>
 __global__ void __launch_bounds__(kChainThreads) chain_kernel(const DecayArgs a,
@@ -33,13 +33,14 @@ __global__ void __launch_bounds__(kChainThreads) chain_kernel(const DecayArgs a,
   const int bh = blockIdx.y, el = (blockIdx.x * kChainThreads + threadIdx.x) * 4;
   const size_t st = static_cast<size_t>(a.nk) * a.nv;
   float4* S = reinterpret_cast<float4*>(sp.S + bh * sp.slots * st + el);
-  const float* decay = sp.decay + static_cast<size_t>(bh) * sp.segments;
+  const float* decay = sp.decay + static_cast<size_t>(bh) * sp.pieces;
   const size_t step = st / 4;
   float4 s = a.h0 ? *reinterpret_cast<const float4*>(a.h0 + bh * st + el)
                   : make_float4(0.f, 0.f, 0.f, 0.f);
   S[0] = s;
-#pragma unroll 4
-  for (int p = 1; p < sp.slots; ++p) {
+  const int states = sp.states(a.dhT != nullptr);
+#pragma unroll 8
+  for (int p = 1; p <= states; ++p) {
     const float4 x = S[p * step];
     const float d = decay[p - 1];
     s = make_float4(fmaf(d, s.x, x.x), fmaf(d, s.y, x.y), fmaf(d, s.z, x.z), fmaf(d, s.w, x.w));
@@ -49,14 +50,15 @@ __global__ void __launch_bounds__(kChainThreads) chain_kernel(const DecayArgs a,
   float4* D = reinterpret_cast<float4*>(sp.D + bh * sp.slots * st + el);
   float4 d = a.dhT ? *reinterpret_cast<const float4*>(a.dhT + bh * st + el)
                    : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = sp.segments; p >= 1; --p) {
-    if (p < sp.segments) {
+  for (int p = sp.pieces; p >= sp.slot_of(1); --p) {
+    if (p < sp.pieces) {
       const float4 x = D[p * step];
       const float f = decay[p];
       d = make_float4(fmaf(f, d.x, x.x), fmaf(f, d.y, x.y), fmaf(f, d.z, x.z), fmaf(f, d.w, x.w));
     }
     D[p * step] = d;
-    const float4 x = S[p * step];
+    // (the last state is not there where its gradient is zero)
+    const float4 x = p <= states ? S[p * step] : make_float4(0.f, 0.f, 0.f, 0.f);
     const float dot = block_sum<kChainThreads>(x.x * d.x + x.y * d.y + x.z * d.z + x.w * d.w, red);
     if (threadIdx.x == 0)
       sp.dots[(static_cast<size_t>(bh) * sp.slots + p) * sp.parts + blockIdx.x] = dot;
@@ -144,8 +146,8 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const DecayArgs
           c += sp.dots[(static_cast<size_t>(bh) * sp.slots + slot) * sp.parts + i];
       return c;
     };
-    float c = edge(seg + 1);
-    const float start = seg > 0 ? edge(seg) : first;
+    float c = edge(sp.slot_of(seg + 1));
+    const float start = seg > 0 ? edge(sp.slot_of(seg)) : first;
     int last = blocks - 1, run = 0;
     for (int blk = blocks - 1; blk >= 0; --blk) {
       const bool keep = s_keep[blk];

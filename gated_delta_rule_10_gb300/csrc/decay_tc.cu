@@ -53,7 +53,8 @@ struct Walk {
   void* out;                       // [B, T, H, nz] bf16, or
   float* part;                     // the same in fp32 (a head's part of a shared gradient)
   const float* start;              // first state; null: zero
-  size_t start_bh, start_seg;      // its elements between (batch, head)s and segments
+  size_t start_bh;                 // its elements between (batch, head)s
+  bool chained;                    // it is the slot of this segment's edge
   int row_step, col_step;          // its elements between rows (W) and columns (z)
   float* end;                      // last state [B * H, W, nz], or null
   const __nv_bfloat16* partner;    // FINE: rows whose dot product with the result is wanted
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     const bool mine = row < W;
     float R[64];
-    read_row(R, w.start && mine ? w.start + bh * w.start_bh + seg * w.start_seg +
+    const size_t edge = w.chained ? sp.slot_of(REV ? seg + 1 : seg) : 0;
+    read_row(R, w.start && mine ? w.start + bh * w.start_bh + edge * W * w.nz +
                                       static_cast<size_t>(row) * w.row_step +
                                       static_cast<size_t>(64 * slice) * w.col_step
                                 : nullptr,
@@ -471,11 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ states
 
-// A segment's own end state, S = sum over its tokens of decay k v^T (REV: the
+// A piece's own end state, S = sum over its tokens of decay k v^T (REV: the
 // gradient of its start state from its own read-outs, s sum of decay q dO^T,
 // chunks in reverse), 64 value columns per CTA: the P product alone, V' double
 // buffered so that a chunk is split while the previous one is multiplied.
-constexpr int kStThreads = 224;   // 128: V' and state; loads; products; gates
+constexpr int kStThreads = 352;   // 128: half of V' and state; 128: the other half; loads;
+                                  // products; gates
 constexpr int kStStages = 3;
 
 enum : uint32_t { sFull = 0, sEmpty = 3, sSplit = 6, sP = 8, sGates = 10, sGFree = 12, sEnd = 14,
@@ -500,9 +503,9 @@ __global__ void __launch_bounds__(kStThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slices = a.nv / 64, slice = blockIdx.x % slices;
-  const int seg = blockIdx.x / slices + (REV ? 1 : 0);   // segment 0's gradient is not needed
+  const int seg = blockIdx.x / slices + (REV ? sp.slot_of(1) : 0);   // (no gradient before)
   const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
-  const int t0 = seg * sp.seg_len, t1 = min(a.T, t0 + sp.seg_len);
+  const int t0 = seg * sp.piece_len, t1 = min(a.T, t0 + sp.piece_len);
   const int cnt = (t1 - t0 + kC - 1) / kC;
   auto at = [&](int n) { return t0 + (REV ? cnt - 1 - n : n) * kC; };
   auto bar = [&](uint32_t i) { return sb + L::oBar + 8 * i; };
@@ -513,10 +516,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
   auto gates = [&](int n) -> Gates& {
     return *reinterpret_cast<Gates*>(smem + L::oGates + (n & 1) * sizeof(Gates));
   };
-  if (warp == 5) tc::tmem_alloc(smem_u32(slot), 256);
+  if (warp == 9) tc::tmem_alloc(smem_u32(slot), 256);
   if (tid == 0) {
     for (uint32_t i = 0; i < kStBars; ++i)
-      tc::mbar_init(bar(i), (i >= sSplit && i < sP) || (i >= sGFree && i < sEnd) ? 4 : 1);   // warps
+      tc::mbar_init(bar(i), (i >= sSplit && i < sP) || (i >= sGFree && i < sEnd) ? 8 : 1);   // warps
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
@@ -531,26 +534,24 @@ __global__ void __launch_bounds__(kStThreads, 1)
   float* dst = (REV ? sp.D : sp.S) +
                (static_cast<size_t>(bh) * sp.slots + (REV ? seg : seg + 1)) * st + 64 * slice;
 
+  auto split = [&](int n, int half) {
+    if (!warp_wait(bar2(sGates, n), par(n), abort_flag) ||
+        !warp_wait(bar(sFull + n % kStStages), (n / kStStages) & 1, abort_flag))
+      return false;
+    const Gates& g = gates(n);
+    split_row(sb + (n % kStStages) * L::kStage + L::kWide, sb + L::oSplit + (n & 1) * 2 * kTile, row,
+              4 * half, REV ? g.head[row] : g.tail[row]);
+    tc::fence_proxy_async();
+    warp_arrive(bar2(sSplit, n));
+    return true;
+  };
   if (warp < 4) {
     float S[64];
     read_row(S, nullptr, 1);
     float prod = 1.f;
-    auto split = [&](int n) {
-      if (!warp_wait(bar2(sGates, n), par(n), abort_flag) ||
-          !warp_wait(bar(sFull + n % kStStages), (n / kStStages) & 1, abort_flag))
-        return false;
-      const Gates& g = gates(n);
-      split_row(sb + (n % kStStages) * L::kStage + L::kWide,
-                sb + L::oSplit + (n & 1) * 2 * kTile, row, 0, REV ? g.head[row] : g.tail[row]);
-      split_row(sb + (n % kStStages) * L::kStage + L::kWide,
-                sb + L::oSplit + (n & 1) * 2 * kTile, row, 4, REV ? g.head[row] : g.tail[row]);
-      tc::fence_proxy_async();
-      warp_arrive(bar2(sSplit, n));
-      return true;
-    };
-    bool ok = split(0);
+    bool ok = split(0, 0);
     for (int n = 0; ok && n < cnt; ++n) {
-      if (n + 1 < cnt) ok = split(n + 1);
+      if (n + 1 < cnt) ok = split(n + 1, 0);
       if (ok) ok = warp_wait(bar2(sP, n), par(n), abort_flag);
       if (!ok) break;
       tc::fence_after_sync();
@@ -562,10 +563,16 @@ __global__ void __launch_bounds__(kStThreads, 1)
     }
     if (ok) {
       if (mine) write_row(S, REV ? a.scale : 1.f, dst + static_cast<size_t>(row) * a.nv);
-      if (!REV && tid == 0 && slice == 0)
-        sp.decay[static_cast<size_t>(bh) * sp.segments + seg] = prod;
+      if (tid == 0 && slice == 0)   // (a piece of both walks: the same value twice)
+        sp.decay[static_cast<size_t>(bh) * sp.pieces + seg] = prod;
     }
-  } else if (warp == 4) {
+  } else if (warp < 8) {
+    for (int n = 0; n < cnt; ++n) {
+      if (n >= 2 && !warp_wait(bar2(sP, n), par(n - 2), abort_flag)) break;
+      if (!split(n, 1)) break;
+      warp_arrive(bar2(sGFree, n));
+    }
+  } else if (warp == 8) {
     if (lane == 0) {
       int issued = 0;
       for (int n = 0; n < cnt; ++n) {
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
       for (int n = max(0, issued - kStStages); n < issued; ++n)
         tc::mbar_wait(bar(sFull + n % kStStages), (n / kStStages) & 1);
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     const uint32_t go = lane == 0;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     constexpr uint32_t idP = tc::idesc_bf16(128, 128, 1, 1);
@@ -623,7 +630,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   if (*abort_flag)   // a bounded wait gave up: the state, and all that follows, reads NaN
     for (int i = tid; i < NK * 64; i += kStThreads)
       dst[static_cast<size_t>(i / 64) * a.nv + i % 64] = __int_as_float(0x7fffffff);
-  if (warp == 5) tc::tmem_dealloc(tmem, 256);
+  if (warp == 9) tc::tmem_dealloc(tmem, 256);
 }
 
 // ------------------------------------------------------------------ pairs
@@ -883,10 +890,10 @@ Walk from(const DecayArgs& a, const DecaySplit& sp, bool grad, bool transposed) 
   w.start = grad ? a.dhT : a.h0;
   w.start_bh = st;
   if (sp.segments > 1) {
-    w.start = grad ? sp.D + st : sp.S;   // segment p ends with D_{p+1}
+    w.start = grad ? sp.D : sp.S;
     w.start_bh = sp.slots * st;
-    w.start_seg = st;
   }
+  w.chained = sp.segments > 1;
   w.row_step = transposed ? 1 : a.nv;
   w.col_step = transposed ? a.nv : 1;
   return w;
@@ -903,7 +910,7 @@ cudaError_t states(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream
     return cudaErrorInvalidValue;
   const cudaError_t err = opt_in(decay_states_tc<NK, REV>, L::launch);
   if (err != cudaSuccess) return err;
-  const int segs = REV ? sp.segments - 1 : sp.slots - 1;
+  const int segs = REV ? sp.pieces - sp.slot_of(1) : sp.states(a.dhT != nullptr);
   decay_states_tc<NK, REV><<<dim3(segs * (a.nv / 64), a.B * a.H), kStThreads, L::launch, stream>>>(
       a, sp, tx, ty);
   return cudaGetLastError();
@@ -965,7 +972,7 @@ cudaError_t launch_decay_bwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaSt
 
 cudaError_t launch_decay_states_tc(const DecayArgs& a, const DecaySplit& sp, bool reverse,
                                    cudaStream_t stream) {
-  if ((reverse ? sp.segments : sp.slots) < 2) return cudaSuccess;
+  if ((reverse ? sp.pieces - sp.slot_of(1) : sp.states(a.dhT != nullptr)) < 1) return cudaSuccess;
   if (reverse)
     return a.nk == 64 ? states<64, true>(a, sp, stream) : states<128, true>(a, sp, stream);
   return a.nk == 64 ? states<64, false>(a, sp, stream) : states<128, false>(a, sp, stream);

@@ -193,13 +193,13 @@ struct Where {
   int b, h, bh, t0, t1;
   size_t tok;   // b * T
 };
-__device__ __forceinline__ Where where(const DecayArgs& a, const DecaySplit& sp, int seg) {
+__device__ __forceinline__ Where where(const DecayArgs& a, int len, int seg) {
   Where w;
   w.bh = blockIdx.y;
   w.b = w.bh / a.H;
   w.h = w.bh % a.H;
-  w.t0 = seg * sp.seg_len;
-  w.t1 = min(a.T, w.t0 + sp.seg_len);
+  w.t0 = seg * len;
+  w.t1 = min(a.T, w.t0 + len);
   w.tok = static_cast<size_t>(w.b) * a.T;
   return w;
 }
@@ -234,15 +234,15 @@ __device__ __forceinline__ void scale_rows(float* X, const float* f) {
   for (int i = threadIdx.x; i < kC * W; i += kThreads) X[(i / W) * (W + 4) + i % W] *= f[i / W];
 }
 
-// Local end state of every segment from a zero state (REV: the gradient of its
+// Local end state of every piece from a zero state (REV: the gradient of its
 // start state from a zero gradient at its end), and the product of its decays.
 template <int NK, int NV, bool REV, typename T>
 __global__ void __launch_bounds__(kThreads, 1) states_warp(const DecayArgs a, const DecaySplit sp) {
   extern __shared__ __align__(16) float sm[];
   float *S = sm, *X = S + NK * (NV + 4), *Y = X + kC * (NK + 4);
   __shared__ Gates gates;
-  const int seg = static_cast<int>(blockIdx.x) + (REV ? 1 : 0);   // segment 0's D is not needed
-  const Where w = where(a, sp, seg);
+  const int seg = static_cast<int>(blockIdx.x) + (REV ? sp.slot_of(1) : 0);   // (no D before)
+  const Where w = where(a, sp.piece_len, seg);
   const int hk = w.h / (a.H / a.Hk);
   load_state<NK, NV>(S, nullptr);
   float prod = 1.f;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_warp(const DecayArgs a, co
       dst[i] = a.scale * S[(i / NV) * (NV + 4) + i % NV];
   else
     store_state<NK, NV>(S, dst);
-  if (!REV && threadIdx.x == 0) sp.decay[static_cast<size_t>(w.bh) * sp.segments + seg] = prod;
+  if (threadIdx.x == 0) sp.decay[static_cast<size_t>(w.bh) * sp.pieces + seg] = prod;
 }
 
 template <int NK, int NV, typename T>
@@ -282,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_warp(const DecayArgs a, const
   float *S = sm, *Q = S + NK * (NV + 4), *K = Q + kC * (NK + 4), *V = K + kC * (NK + 4),
         *A = V + kC * (NV + 4);
   __shared__ Gates gates;
-  const Where w = where(a, sp, blockIdx.x);
+  const Where w = where(a, sp.seg_len, blockIdx.x);
   const int hk = w.h / (a.H / a.Hk);
   const float* start = sp.segments > 1
-                           ? sp.S + (static_cast<size_t>(w.bh) * sp.slots + blockIdx.x) * NK * NV
+                           ? sp.S + (static_cast<size_t>(w.bh) * sp.slots + sp.slot_of(blockIdx.x)) * NK * NV
                            : (a.h0 ? a.h0 + static_cast<size_t>(w.bh) * NK * NV : nullptr);
   load_state<NK, NV>(S, start);
   for (int t = w.t0; t < w.t1; t += kC) {
@@ -331,16 +331,16 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
         *O = V + kC * (NV + 4), *A = O + kC * (NV + 4);
   __shared__ Gates gates;
   __shared__ float flow[6][kC];
-  const Where w = where(a, sp, blockIdx.x);
+  const Where w = where(a, sp.seg_len, blockIdx.x);
   const int hk = w.h / (a.H / a.Hk);
   const bool rev = blockIdx.z == 1;
   const size_t st = static_cast<size_t>(NK) * NV;
   const float* start;
   if (!rev)
-    start = sp.segments > 1 ? sp.S + (static_cast<size_t>(w.bh) * sp.slots + blockIdx.x) * st
+    start = sp.segments > 1 ? sp.S + (static_cast<size_t>(w.bh) * sp.slots + sp.slot_of(blockIdx.x)) * st
                             : (a.h0 ? a.h0 + w.bh * st : nullptr);
   else
-    start = sp.segments > 1 ? sp.D + (static_cast<size_t>(w.bh) * sp.slots + blockIdx.x + 1) * st
+    start = sp.segments > 1 ? sp.D + (static_cast<size_t>(w.bh) * sp.slots + sp.slot_of(blockIdx.x + 1)) * st
                             : (a.dhT ? a.dhT + w.bh * st : nullptr);
   load_state<NK, NV>(S, start);
   const long long so = static_cast<long long>(a.H) * NV;
@@ -486,8 +486,8 @@ template <int NK, int NV, typename T>
 struct Warp {
   static cudaError_t states(const DecayArgs& a, const DecaySplit& sp, bool rev, cudaStream_t s) {
     const size_t smem = state(NK, NV) + tile(NK) + tile(NV);
-    return rev ? run(states_warp<NK, NV, true, T>, a, sp, sp.segments - 1, 1, smem, s)
-               : run(states_warp<NK, NV, false, T>, a, sp, sp.slots - 1, 1, smem, s);
+    return rev ? run(states_warp<NK, NV, true, T>, a, sp, sp.pieces - sp.slot_of(1), 1, smem, s)
+               : run(states_warp<NK, NV, false, T>, a, sp, sp.states(a.dhT != nullptr), 1, smem, s);
   }
   static cudaError_t fwd(const DecayArgs& a, const DecaySplit& sp, cudaStream_t s) {
     return run(fwd_warp<NK, NV, T>, a, sp, sp.segments, 1,
@@ -509,7 +509,7 @@ struct Warp {
 
 cudaError_t launch_decay_states_warp(const DecayArgs& a, const DecaySplit& sp, bool reverse,
                                      bool f32, cudaStream_t stream) {
-  if ((reverse ? sp.segments : sp.slots) < 2) return cudaSuccess;
+  if ((reverse ? sp.pieces - sp.slot_of(1) : sp.states(a.dhT != nullptr)) < 1) return cudaSuccess;
   return GDR_WIDTHS(states(a, sp, reverse, stream));
 }
 cudaError_t launch_decay_fwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,

@@ -59,11 +59,13 @@ gdr::DecayArgs decay_args(const gdr_decay_shape* s) {
 constexpr int kMinRun = 4;          // chunks per segment, at least
 constexpr int kMaxBwdRun = 4096;    // tokens per segment of the backward, at most
 
-// Segments of each sequence. A CTA walks one segment of a (batch, head), so few
-// sequences are cut until the CTAs fill the SMs (the backward has two CTAs per
-// segment); each cut costs a second read of k and v, so no further than that.
-// The backward also bounds a segment's tokens: the gate's gradient is a running
-// sum from the segment's end.
+// Segments of each sequence, and pieces of each segment. A CTA walks one segment of
+// a (batch, head, 64 columns), so few sequences are cut until the CTAs fill the
+// SMs; each cut costs a pass over k and v for the segments' own states, so no
+// further than that (1 x 65536 x 32 heads: two segments). That pass has one segment
+// less, and takes segments in pieces until it fills the SMs too (865 -> 710 us).
+// The backward also bounds a segment's tokens: what its gate gradient passes on
+// from block to block rounds (gate_grad_kernel), and its blocks are kept on chip.
 void cut(const gdr_decay_shape* s, bool backward, gdr::DecaySplit* sp) {
   const int chunk = s->dtype == GDR_BF16 ? 128 : 64;
   const int chunks = (s->T + chunk - 1) / chunk;
@@ -74,9 +76,30 @@ void cut(const gdr_decay_shape* s, bool backward, gdr::DecaySplit* sp) {
   if (backward && p < (s->T + kMaxBwdRun - 1) / kMaxBwdRun)
     p = (s->T + kMaxBwdRun - 1) / kMaxBwdRun;
   if (p < 1) p = 1;
-  const int per = static_cast<int>((chunks + p - 1) / p);
+  int per = static_cast<int>((chunks + p - 1) / p);
   sp->segments = (chunks + per - 1) / per;
+  long long q = 1;
+  if (sp->segments > 1) {
+    const long long busy = ctas * (sp->segments - 1);
+    q = kSms / busy;
+    if (q > per / kMinRun) q = per / kMinRun;
+    if (q < 1) q = 1;
+  }
+  const int piece = static_cast<int>((per + q - 1) / q);
+  per = static_cast<int>(piece * q);       // whole pieces
+  if (backward && per * chunk > kMaxBwdRun) {
+    per = piece * (kMaxBwdRun / chunk / piece);
+    if (per < 1) per = kMaxBwdRun / chunk;
+  }
+  sp->segments = (chunks + per - 1) / per;
+  sp->parts_per = per / piece;
+  sp->piece_len = piece * chunk;
   sp->seg_len = per * chunk;
+  sp->pieces = sp->segments > 1 ? (chunks + piece - 1) / piece : 1;
+  if (sp->segments == 1) {   // one piece, whose state only the backward needs
+    sp->parts_per = 1;
+    sp->piece_len = sp->seg_len;
+  }
   sp->parts = s->dk * s->dv / 1024;
 }
 
@@ -90,10 +113,10 @@ size_t lay_out(const gdr_decay_shape* s, bool backward, bool end_grad, char* bas
   };
   const size_t bh = static_cast<size_t>(s->B) * s->H, st = static_cast<size_t>(s->dk) * s->dv;
   const bool chain = sp->segments > 1 || (backward && end_grad);
-  sp->slots = sp->segments + (backward ? 1 : 0);
+  sp->slots = sp->pieces + (backward ? 1 : 0);
   if (chain) {
     take(&sp->S, bh * sp->slots * st);
-    take(&sp->decay, bh * sp->segments);
+    take(&sp->decay, bh * sp->pieces);
   }
   if (!backward) return at;
   if (chain) {
