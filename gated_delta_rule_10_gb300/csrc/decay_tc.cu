@@ -35,6 +35,8 @@
 // 40 us for the products of 4 x 4096 x 16 x 128 alone). Each tile is loaded
 // again as soon as its last reader is done, about one chunk's time ahead.
 // The two column halves of a head re-read x and y (from L2) and repeat A.
+#include <algorithm>
+
 #include "decay_tc.cuh"
 #include "tma.h"
 
@@ -42,8 +44,6 @@ namespace gdr {
 namespace {
 
 using namespace dtc;
-
-constexpr int kSmCount = 152;
 
 // ------------------------------------------------------------------ walk
 
@@ -93,19 +93,18 @@ struct WalkSmem {
   static constexpr uint32_t launch = bytes + 1024;   // room to align the base
 };
 
+// One CTA's walk over segment `seg` of (batch, head) `bh`, columns 64 slice .. + 63.
 template <int W, bool REV, bool FINE>
-__global__ void __launch_bounds__(kThreads, 1)
-    decay_walk_tc(const DecayArgs a, const DecaySplit sp, const Walk w,
-                  const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
-                  const __grid_constant__ CUtensorMap tz) {
+__device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& sp, const Walk& w,
+                                         const CUtensorMap* tx, const CUtensorMap* ty,
+                                         const CUtensorMap* tz, int seg, int slice, int bh) {
   using L = WalkSmem<W, FINE>;
   using C = Cols;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slices = w.nz / 64, slice = blockIdx.x % slices, seg = blockIdx.x / slices;
-  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+  const int b = bh / a.H, h = bh % a.H;
   const int t0 = seg * sp.seg_len, t1 = min(a.T, t0 + sp.seg_len);
   const int cnt = (t1 - t0 + kC - 1) / kC;
   const size_t tok = static_cast<size_t>(b) * a.T;
@@ -148,11 +147,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tma_load_4d(sb + base + (n & 1) * L::kWide + blk * kTile, m, 64 * blk,
                       h / (a.H / heads), at(n), b, bar(bXY, n));
   };
-  auto load_x = [&](int n) { load_wide(L::oX, &tx, w.x_heads, n); };
-  auto load_y = [&](int n) { load_wide(L::oY, &ty, w.y_heads, n); };
+  auto load_x = [&](int n) { load_wide(L::oX, tx, w.x_heads, n); };
+  auto load_y = [&](int n) { load_wide(L::oY, ty, w.y_heads, n); };
   auto load_z = [&](int n) {
     tc::mbar_arrive_expect_tx(bar(bZ, n), kTile);
-    tc::tma_load_4d(sb + L::oZ + zslot(n), &tz, 64 * slice, h / (a.H / w.z_heads), at(n), b,
+    tc::tma_load_4d(sb + L::oZ + zslot(n), tz, 64 * slice, h / (a.H / w.z_heads), at(n), b,
                     bar(bZ, n));
   };
   // half of the columns of this lane's token of Z'; its last reader is P(n - 1),
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 256)
       for (; nz < min(kAhead, cnt); ++nz) load_z(nz);
     auto soon = [&](int n) {   // one tile only: the next one comes into L2 meanwhile
-      if (n < cnt) tc::tma_prefetch_4d(&tz, 64 * slice, h / (a.H / w.z_heads), at(n), b);
+      if (n < cnt) tc::tma_prefetch_4d(tz, 64 * slice, h / (a.H / w.z_heads), at(n), b);
     };
     if (FINE && tid == 256) soon(1);
     __syncwarp();
@@ -471,6 +470,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 13) tc::tmem_dealloc(tmem, kCols);
 }
 
+template <int W>
+__global__ void __launch_bounds__(kThreads, 1)
+    decay_fwd_tc(const DecayArgs a, const DecaySplit sp, const Walk w,
+                 const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
+                 const __grid_constant__ CUtensorMap tz) {
+  const int slices = w.nz / 64;
+  walk_cta<W, false, false>(a, sp, w, &tx, &ty, &tz, blockIdx.x / slices, blockIdx.x % slices,
+                            blockIdx.y);
+}
+
 // ------------------------------------------------------------------ states
 
 // A piece's own end state, S = sum over its tokens of decay k v^T (REV: the
@@ -643,9 +652,9 @@ __global__ void __launch_bounds__(kStThreads, 1)
 // column sums are each a sum along one lane's columns; everything is fp32, as the
 // sums' differences need it. The blocks' factors come out of the sums:
 // from_t = row[t] sum_i (A . dA)_ti col[i].
-// Chunks are independent: persistent CTAs take every gridDim.x-th, and a chunk's
+// Chunks are independent: a CTA takes every ctas-th, and a chunk's
 // tiles are asked for as soon as the products of the last one are complete.
-constexpr int kPairThreads = 320;   // 128: rows; 128: columns; products and loads; gates
+// Warps 0-3: rows; 4-7: columns; 8: products and loads; 9: gates.
 
 enum : uint32_t { pFull = 0, pDone = 1, pFree = 2, pGates = 4, pGFree = 6, pEnd = 8, kPairBars = 9 };
 
@@ -659,10 +668,10 @@ struct PairSmem {
 };
 
 template <int NK, int NV>
-__global__ void __launch_bounds__(kPairThreads, 1)
-    decay_pairs_tc(const DecayArgs a, const DecaySplit sp, const __grid_constant__ CUtensorMap tq,
-                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                   const __grid_constant__ CUtensorMap to) {
+__device__ __forceinline__ void pairs_cta(const DecayArgs& a, const DecaySplit& sp,
+                                          const CUtensorMap* tq, const CUtensorMap* tk,
+                                          const CUtensorMap* tv, const CUtensorMap* to, int cta,
+                                          int ctas) {
   using L = PairSmem<NK, NV>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -670,10 +679,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunks = (a.T + kC - 1) / kC;
   const long long jobs = static_cast<long long>(a.B) * a.H * chunks;
-  const int cnt = static_cast<int>((jobs - blockIdx.x + gridDim.x - 1) / gridDim.x);
+  const int cnt = jobs > cta ? static_cast<int>((jobs - cta + ctas - 1) / ctas) : 0;
   // heads fastest: heads that share q and k, and rows of one batch, run together
   auto job = [&](int n, int& b, int& h, int& t) {
-    const long long j = blockIdx.x + static_cast<long long>(n) * gridDim.x;
+    const long long j = cta + static_cast<long long>(n) * ctas;
     h = static_cast<int>(j % a.H);
     const long long c = j / a.H;
     t = static_cast<int>(c % chunks) * kC;
@@ -775,13 +784,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tc::mbar_arrive_expect_tx(bar(pFull), 2 * (L::kK + L::kV));
 #pragma unroll
       for (int blk = 0; blk < NK / 64; ++blk) {
-        tc::tma_load_4d(sb + L::oQ + blk * kTile, &tq, 64 * blk, hk, t, b, bar(pFull));
-        tc::tma_load_4d(sb + L::oK + blk * kTile, &tk, 64 * blk, hk, t, b, bar(pFull));
+        tc::tma_load_4d(sb + L::oQ + blk * kTile, tq, 64 * blk, hk, t, b, bar(pFull));
+        tc::tma_load_4d(sb + L::oK + blk * kTile, tk, 64 * blk, hk, t, b, bar(pFull));
       }
 #pragma unroll
       for (int blk = 0; blk < NV / 64; ++blk) {
-        tc::tma_load_4d(sb + L::oV + blk * kTile, &tv, 64 * blk, h, t, b, bar(pFull));
-        tc::tma_load_4d(sb + L::oO + blk * kTile, &to, 64 * blk, h, t, b, bar(pFull));
+        tc::tma_load_4d(sb + L::oV + blk * kTile, tv, 64 * blk, h, t, b, bar(pFull));
+        tc::tma_load_4d(sb + L::oO + blk * kTile, to, 64 * blk, h, t, b, bar(pFull));
       }
     };
     int issued = 0;
@@ -814,7 +823,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     commit_if(go, bar(pEnd));
     tc::mbar_wait(bar(pEnd), 0);
     if (issued > 0) tc::mbar_wait(bar(pFull), (issued - 1) & 1);   // no copy may outlive the CTA
-  } else {
+  } else if (warp == 9) {
     float x[4], y[4];
     auto read = [&](float (&v)[4], int n) {
       int b, h, t;
@@ -838,11 +847,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int n = 0; n < cnt; ++n) {
       int b, h, t;
       job(n, b, h, t);
-      for (int i = tid; i < kC; i += kPairThreads)
+      for (int i = tid; i < kC; i += kThreads)
         if (t + i < a.T)
           sp.near[(static_cast<size_t>(b) * a.H + h) * a.T + t + i] = __int_as_float(0x7fffffff);
     }
   if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+// The whole backward: blockIdx.z 0: dq, 1: dk, 2: dv, from 3 on the pairs. They do
+// not depend on one another, so in one launch they fill each other's last wave (the
+// pairs come last, in CTAs of about four chunks), and with few sequences they run
+// side by side (2 x 777 x 4 heads: 118 -> 62 us).
+struct Walks {
+  Walk dq, dk, dv;
+};
+
+template <int NK, int NV>
+__global__ void __launch_bounds__(kThreads, 1)
+    decay_bwd_tc(const DecayArgs a, const DecaySplit sp, const Walks w,
+                 const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to) {
+  const int x = blockIdx.x, bh = blockIdx.y;
+  if (blockIdx.z >= 3) {
+    const int plane = gridDim.x * gridDim.y;
+    pairs_cta<NK, NV>(a, sp, &tq, &tk, &tv, &to,
+                      (blockIdx.z - 3) * plane + bh * gridDim.x + x, (gridDim.z - 3) * plane);
+    return;
+  }
+  const int slices = (blockIdx.z == 2 ? NV : NK) / 64;
+  if (x >= sp.segments * slices) return;   // the other width has more slices
+  if (blockIdx.z == 0)
+    walk_cta<NV, false, true>(a, sp, w.dq, &to, &tv, &tk, x / slices, x % slices, bh);
+  else if (blockIdx.z == 1)
+    walk_cta<NV, true, true>(a, sp, w.dk, &tv, &to, &tq, x / slices, x % slices, bh);
+  else
+    walk_cta<NK, true, false>(a, sp, w.dv, &tk, &tq, &to, x / slices, x % slices, bh);
 }
 
 template <class Kern>
@@ -860,26 +899,18 @@ bool map_of(CUtensorMap* m, const DecayArgs& a, const Rows& r) {
   return make_rows_tmap(m, r.p, a.B, a.T, r.heads, r.width, r.stride);
 }
 
-template <int W, bool REV, bool FINE>
-cudaError_t walk_w(const DecayArgs& a, const DecaySplit& sp, Walk w, const Rows& x, const Rows& y,
-                   const Rows& z, cudaStream_t stream) {
-  using L = WalkSmem<W, FINE>;
+template <int W>
+cudaError_t fwd(const DecayArgs& a, const DecaySplit& sp, const Walk& w, const Rows& q,
+                const Rows& k, const Rows& v, cudaStream_t stream) {
+  using L = WalkSmem<W, false>;
   static_assert(L::launch <= 232448, "shared memory budget of one CTA");
-  w.x_heads = x.heads; w.y_heads = y.heads; w.z_heads = z.heads; w.nz = z.width;
-  CUtensorMap tx, ty, tz;
-  if (!map_of(&tx, a, x) || !map_of(&ty, a, y) || !map_of(&tz, a, z)) return cudaErrorInvalidValue;
-  const cudaError_t err = opt_in(decay_walk_tc<W, REV, FINE>, L::launch);
+  CUtensorMap tq, tk, tv;
+  if (!map_of(&tq, a, q) || !map_of(&tk, a, k) || !map_of(&tv, a, v)) return cudaErrorInvalidValue;
+  const cudaError_t err = opt_in(decay_fwd_tc<W>, L::launch);
   if (err != cudaSuccess) return err;
-  decay_walk_tc<W, REV, FINE>
-      <<<dim3(sp.segments * (w.nz / 64), a.B * a.H), kThreads, L::launch, stream>>>(a, sp, w, tx,
-                                                                                     ty, tz);
+  decay_fwd_tc<W><<<dim3(sp.segments * (w.nz / 64), a.B * a.H), kThreads, L::launch, stream>>>(
+      a, sp, w, tq, tk, tv);
   return cudaGetLastError();
-}
-template <bool REV, bool FINE>
-cudaError_t walk(const DecayArgs& a, const DecaySplit& sp, const Walk& w, const Rows& x,
-                 const Rows& y, const Rows& z, cudaStream_t stream) {
-  return x.width == 64 ? walk_w<64, REV, FINE>(a, sp, w, x, y, z, stream)
-                       : walk_w<128, REV, FINE>(a, sp, w, x, y, z, stream);
 }
 
 // The walk's first state: S (or D), as rows of key channels or transposed, from
@@ -917,18 +948,23 @@ cudaError_t states(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream
 }
 
 template <int NK, int NV>
-cudaError_t pairs(const DecayArgs& a, const DecaySplit& sp, const Rows& q, const Rows& k,
-                  const Rows& v, const Rows& dO, cudaStream_t stream) {
-  using L = PairSmem<NK, NV>;
-  static_assert(L::launch <= 232448, "shared memory budget of one CTA");
+cudaError_t bwd(const DecayArgs& a, const DecaySplit& sp, const Walks& w, const Rows& q,
+                const Rows& k, const Rows& v, const Rows& dO, cudaStream_t stream) {
+  constexpr uint32_t la = WalkSmem<NV, true>::launch, lb = WalkSmem<NK, false>::launch,
+                     lc = PairSmem<NK, NV>::launch, lab = la > lb ? la : lb,
+                     bytes = lab > lc ? lab : lc;
+  static_assert(bytes <= 232448, "shared memory budget of one CTA");
   CUtensorMap tq, tk, tv, to;
   if (!map_of(&tq, a, q) || !map_of(&tk, a, k) || !map_of(&tv, a, v) || !map_of(&to, a, dO))
     return cudaErrorInvalidValue;
-  const cudaError_t err = opt_in(decay_pairs_tc<NK, NV>, L::launch);
+  const cudaError_t err = opt_in(decay_bwd_tc<NK, NV>, bytes);
   if (err != cudaSuccess) return err;
+  const int slices = (NK > NV ? NK : NV) / 64;
+  const long long ctas = static_cast<long long>(sp.segments) * slices * a.B * a.H;
   const long long jobs = static_cast<long long>(a.B) * a.H * ((a.T + kC - 1) / kC);
-  const unsigned grid = static_cast<unsigned>(jobs < kSmCount ? jobs : kSmCount);
-  decay_pairs_tc<NK, NV><<<grid, kPairThreads, L::launch, stream>>>(a, sp, tq, tk, tv, to);
+  const int planes = static_cast<int>(std::max(1LL, std::min(16LL, jobs / (4 * ctas))));
+  decay_bwd_tc<NK, NV><<<dim3(sp.segments * slices, a.B * a.H, 3 + planes), kThreads, bytes, stream>>>(
+      a, sp, w, tq, tk, tv, to);
   return cudaGetLastError();
 }
 
@@ -938,36 +974,45 @@ cudaError_t launch_decay_fwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaSt
   Walk w = from(a, sp, false, false);
   w.out = a.o;
   w.end = a.hT;
-  return walk<false, false>(a, sp, w, Rows{a.q, a.Hk, a.nk, a.sq}, Rows{a.k, a.Hk, a.nk, a.sk},
-                            Rows{a.v, a.H, a.nv, a.sv}, stream);
+  w.x_heads = w.y_heads = a.Hk;
+  w.z_heads = a.H;
+  w.nz = a.nv;
+  const Rows q{a.q, a.Hk, a.nk, a.sq}, k{a.k, a.Hk, a.nk, a.sk}, v{a.v, a.H, a.nv, a.sv};
+  return a.nk == 64 ? fwd<64>(a, sp, w, q, k, v, stream) : fwd<128>(a, sp, w, q, k, v, stream);
 }
 
 cudaError_t launch_decay_bwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream) {
   const Rows q{a.q, a.Hk, a.nk, a.sq}, k{a.k, a.Hk, a.nk, a.sk}, v{a.v, a.H, a.nv, a.sv},
       dO{a.dO, a.H, a.nv, static_cast<long long>(a.H) * a.nv};
-  Walk w = from(a, sp, false, true);
-  w.out = a.dq;
-  w.part = sp.dq_part;
-  w.partner = static_cast<const __nv_bfloat16*>(a.q);
-  w.partner_stride = a.sq;
-  w.flow = sp.from;
-  cudaError_t err = walk<false, true>(a, sp, w, dO, v, k, stream);
-  if (err != cudaSuccess) return err;
-  w = from(a, sp, true, true);
-  w.out = a.dk;
-  w.part = sp.dk_part;
-  w.partner = static_cast<const __nv_bfloat16*>(a.k);
-  w.partner_stride = a.sk;
-  w.flow = sp.to;
-  if ((err = walk<true, true>(a, sp, w, v, dO, q, stream)) != cudaSuccess) return err;
-  w = from(a, sp, true, false);
-  w.out = a.dv;
-  w.end = a.dh0;
-  if ((err = walk<true, false>(a, sp, w, k, q, dO, stream)) != cudaSuccess) return err;
-  return a.nk == 64 ? (a.nv == 64 ? pairs<64, 64>(a, sp, q, k, v, dO, stream)
-                                  : pairs<64, 128>(a, sp, q, k, v, dO, stream))
-                    : (a.nv == 64 ? pairs<128, 64>(a, sp, q, k, v, dO, stream)
-                                  : pairs<128, 128>(a, sp, q, k, v, dO, stream));
+  Walks w;
+  w.dq = from(a, sp, false, true);
+  w.dq.out = a.dq;
+  w.dq.part = sp.dq_part;
+  w.dq.partner = static_cast<const __nv_bfloat16*>(a.q);
+  w.dq.partner_stride = a.sq;
+  w.dq.flow = sp.from;
+  w.dk = from(a, sp, true, true);
+  w.dk.out = a.dk;
+  w.dk.part = sp.dk_part;
+  w.dk.partner = static_cast<const __nv_bfloat16*>(a.k);
+  w.dk.partner_stride = a.sk;
+  w.dk.flow = sp.to;
+  for (Walk* p : {&w.dq, &w.dk}) {   // dO, v, k and v, dO, q
+    p->x_heads = p->y_heads = a.H;
+    p->z_heads = a.Hk;
+    p->nz = a.nk;
+  }
+  w.dv = from(a, sp, true, false);   // k, q, dO
+  w.dv.out = a.dv;
+  w.dv.end = a.dh0;
+  w.dv.x_heads = w.dv.y_heads = a.Hk;
+  w.dv.z_heads = a.H;
+  w.dv.nz = a.nv;
+  if (a.nk == 64)
+    return a.nv == 64 ? bwd<64, 64>(a, sp, w, q, k, v, dO, stream)
+                      : bwd<64, 128>(a, sp, w, q, k, v, dO, stream);
+  return a.nv == 64 ? bwd<128, 64>(a, sp, w, q, k, v, dO, stream)
+                    : bwd<128, 128>(a, sp, w, q, k, v, dO, stream);
 }
 
 cudaError_t launch_decay_states_tc(const DecayArgs& a, const DecaySplit& sp, bool reverse,
