@@ -18,15 +18,17 @@
 //   A  = X Y^T                        (128 x 128, K = W)
 //   O1 = X R                          (128 x 64,  K = W)
 //   O2 = (A . D) Z                    (128 x 64,  K = 128, A . D from tensor memory)
-//   P  = Y^T [Z'hi | Z'lo]            (W x 128,   K = 128), Z' the decayed Z.
+//   P  = Y^T Z'                       (W x 64,    K = 128), Z' the decayed Z.
 // x, y and z go from TMA to the tensor cores as they are. A . D and the R of the
 // read-out are rounded to bf16 (the result is rounded to bf16 anyway); the decayed
-// Z' is split into two bf16 terms because it enters the fp32 state, whose error
-// would otherwise be bf16's. The two terms sit side by side, one N = 128 product.
+// Z' is split into three bf16 terms because it enters the fp32 state, whose error
+// would otherwise be bf16's. Two terms sit side by side in one N = 128 product, the
+// third is added to the second's columns. Z' is made for 64 tokens at a time, half
+// the space.
 //
 // FINE (dq and dk): the gate's gradient needs f_t (R^T x_t) . p_t in fp32, p the
-// partner row (q or k). R is then split into hi + lo for O1 as well, in the space
-// of the second z tile, and the read-out also writes that product.
+// partner row (q or k). R is then split into three terms for O1 as well, partly in
+// the space of the second z tile, and the read-out also writes that product.
 //
 // Only R_{n+1} <- R_n is a chain, and it holds no product: P of any chunk can be
 // ready before R is. A and O1 are issued by one warp, P and O2 by another: the
@@ -77,18 +79,22 @@ struct Cols {
 enum : uint32_t {   // mbarriers, each a pair for even and odd chunks
   bXY = 0, bZ = 2,                           // tiles landed
   bMA = 4, bMO1 = 6, bMO2 = 8, bMP = 10,     // products complete
-  bMask = 12, bSplit = 14, bState = 16, bFree = 18,
-  bGates = 20, bGFree = 24,                  // four each: a ring of four chunks' gates
-  bEnd = 28, kBars = 30
+  bMask = 12, bState = 16, bFree = 18,
+  bSplit = 14,                               // Z' of tokens 0..63, 64..127, every chunk
+  bGates = 20, bGFree = 24,                  // a ring of four (FINE: two) chunks' gates
+  bEnd = 28, bMP0 = 30,                      // (P of tokens 0..63 complete)
+  kBars = 32
 };
+
+constexpr uint32_t kHalf = kTile / 2;   // 64 rows of 64 bf16 columns
 
 template <int W, bool FINE>
 struct WalkSmem {
-  static constexpr uint32_t kWide = W / 64 * kTile, kZ = FINE ? 1 : 2;
+  static constexpr uint32_t kWide = W / 64 * kTile, kZ = FINE ? 1 : 2, kRing = FINE ? 2 : 4;
   static constexpr uint32_t oX = 0, oY = oX + 2 * kWide, oZ = oY + 2 * kWide,
-                            oSplit = oZ + kZ * kTile, oR = oSplit + 2 * kTile,
-                            kR = W * 128, oGates = oR + (FINE ? 2 : 1) * kR,
-                            oBar = oGates + 4 * sizeof(Gates), oSlot = oBar + 8 * kBars,
+                            oSplit = oZ + kZ * kTile, oR = oSplit + 3 * kHalf,
+                            kR = W * 128, oGates = oR + (FINE ? 3 : 1) * kR,
+                            oBar = oGates + kRing * sizeof(Gates), oSlot = oBar + 8 * kBars,
                             oAbort = oSlot + 4, bytes = oAbort + 12;
   static constexpr uint32_t launch = bytes + 1024;   // room to align the base
 };
@@ -111,12 +117,13 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
   auto at = [&](int n) { return t0 + (REV ? cnt - 1 - n : n) * kC; };   // chunk n's first token
   auto bar = [&](uint32_t i, int n) { return sb + L::oBar + 8 * (i + (n & 1)); };
   auto par = [](int n) { return static_cast<uint32_t>(n >> 1) & 1u; };
-  auto bar4 = [&](uint32_t i, int n) { return sb + L::oBar + 8 * (i + (n & 3)); };
-  auto par4 = [](int n) { return static_cast<uint32_t>(n >> 2) & 1u; };
+  constexpr int kRing = L::kRing;
+  auto bar4 = [&](uint32_t i, int n) { return sb + L::oBar + 8 * (i + (n & (kRing - 1))); };
+  auto par4 = [](int n) { return static_cast<uint32_t>(n / kRing) & 1u; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::oAbort);
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::oSlot);
   auto gates = [&](int n) -> Gates& {
-    return *reinterpret_cast<Gates*>(smem + L::oGates + (n & 3) * sizeof(Gates));
+    return *reinterpret_cast<Gates*>(smem + L::oGates + (n & (kRing - 1)) * sizeof(Gates));
   };
   auto zslot = [](int n) { return FINE ? 0u : static_cast<uint32_t>(n & 1) * kTile; };
 
@@ -154,17 +161,23 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     tc::tma_load_4d(sb + L::oZ + zslot(n), tz, 64 * slice, h / (a.H / w.z_heads), at(n), b,
                     bar(bZ, n));
   };
-  // half of the columns of this lane's token of Z'; its last reader is P(n - 1),
-  // whose completion the caller has waited for
+  // the state's and the read-out's 256 threads make Z' of tokens 64 half .. + 63, a
+  // quarter of a row each; its last reader is P of the tokens before
   auto split = [&](int n, int half) {
-    if (!warp_wait(bar4(bGates, n), par4(n), abort_flag) ||
-        !warp_wait(bar(bZ, n), par(n), abort_flag))
+    if (half == 0) {
+      if (!warp_wait(bar4(bGates, n), par4(n), abort_flag) ||
+          !warp_wait(bar(bZ, n), par(n), abort_flag) ||
+          (n > 0 && !warp_wait(bar(bMP, n - 1), par(n - 1), abort_flag)))
+        return false;
+    } else if (!warp_wait(sb + L::oBar + 8 * (bMP0 + (n & 1)), par(n), abort_flag)) {
       return false;
+    }
     const Gates& g = gates(n);
-    split_row(sb + L::oZ + zslot(n), sb + L::oSplit, row, 4 * half,
-              REV ? a.scale * g.head[row] : g.tail[row]);
+    const int to = tid & 63, r = 64 * half + to;
+    split_row(sb + L::oZ + zslot(n), sb + L::oSplit, kHalf, r, to, 2 * ((tid >> 6) & 3),
+              REV ? a.scale * g.head[r] : g.tail[r]);
     tc::fence_proxy_async();
-    warp_arrive(bar(bSplit, n));
+    warp_arrive(sb + L::oBar + 8 * (bSplit + half));
     return true;
   };
 
@@ -238,10 +251,10 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
                                       static_cast<size_t>(64 * slice) * w.col_step
                                 : nullptr,
              w.col_step);
-    if (mine) round_row<FINE>(smem + L::oR, L::kR, row, R);
+    if (mine) round_row<FINE>(sb + L::oR, L::kR, row, R);
     tc::fence_proxy_async();
     warp_arrive(bar(bState, 0));
-    bool ok = split(0, 0);
+    bool ok = split(0, 0) && split(0, 1);
     for (int n = 0; ok && n < cnt; ++n) {
       ok = warp_wait(bar(bMP, n), par(n), abort_flag);
       if (!ok) break;
@@ -263,9 +276,10 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
             nx = n + 3;
           }
           __syncwarp();
-          if (mine) round_row<FINE>(smem + L::oR, L::kR, row, R);
+          if (mine) round_row<FINE>(sb + L::oR, L::kR, row, R);
           tc::fence_proxy_async();
           warp_arrive(bar(bState, n + 1));
+          ok = split(n + 1, 1);
         }
       }
     }
@@ -291,7 +305,7 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     if (FINE && tid == 256) soon(1);
     __syncwarp();
     bool ok = true;
-    if (!FINE) ok = split(0, 1);
+    if (!FINE) ok = split(0, 0) && split(0, 1);
     for (int n = 0; ok && n < cnt; ++n) {
       const int t = at(n) + row;
       const bool live = t < t1;
@@ -303,9 +317,9 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
         for (int i = 0; i < 8; ++i)
           pr[i] = live ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
         // one z tile: its last reader O2(n - 1) was waited for below
-        ok = (n == 0 || warp_wait(bar(bMP, n - 1), par(n - 1), abort_flag)) && split(n, 1);
+        ok = split(n, 0) && split(n, 1);
       } else if (n + 1 < cnt) {
-        ok = warp_wait(bar(bMP, n), par(n), abort_flag) && split(n + 1, 1);
+        ok = split(n + 1, 0) && split(n + 1, 1);
       }
       ok = ok && warp_wait(bar(bMO1, n), par(n), abort_flag) &&
            warp_wait(bar(bMO2, n), par(n), abort_flag);
@@ -398,25 +412,35 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
           mma_if(go, tm + C::O1(n), dx + kmaj(k0), dR + rows(k0), idO, k0 > 0);
         if (FINE) {
 #pragma unroll 1
-          for (int k0 = 0; k0 < W; k0 += 16)
-            mma_if(go, tm + C::O1(n), dx + kmaj(k0), dR + (L::kR >> 4) + rows(k0), idO, 1);
+          for (int k0 = 0; k0 < 2 * W; k0 += 16)   // the other two terms
+            mma_if(go, tm + C::O1(n), dx + kmaj(k0 & (W - 1)), dR + (L::kR >> 4) + rows(k0), idO, 1);
         }
         commit_if(go, bar(bMO1, n));
       }
     } else {
       end += 8;
-      const uint64_t dSplit = tc::smem_desc(sb + L::oSplit, kTile, 1024);
+      const uint64_t dSplit = tc::smem_desc(sb + L::oSplit, kHalf, 1024);
+      const uint64_t dThird = tc::smem_desc(sb + L::oSplit + 2 * kHalf, 16, 1024);
+      constexpr uint32_t idT = tc::idesc_bf16(128, 64, 1, 1);
       for (int n = 0; n < cnt; ++n) {
-        // the state has added the last P before it made its half of this Z'
-        if (!warp_wait(bar(bSplit, n), par(n), abort_flag) ||
-            !warp_wait(bar(bXY, n), par(n), abort_flag))
-          break;
-        tc::fence_after_sync();
+        if (!warp_wait(bar(bXY, n), par(n), abort_flag)) break;
         const uint64_t dy = tc::smem_desc(sb + L::oY + (n & 1) * L::kWide, kTile, 1024);
+        bool ok = true;
 #pragma unroll 1
-        for (int k0 = 0; k0 < kC; k0 += 16)
-          mma_if(go, tm + C::P, dy + rows(k0), dSplit + rows(k0), idP, k0 > 0);
-        commit_if(go, bar(bMP, n));
+        for (int half = 0; half < 2; ++half) {
+          // (the state has added the last P before it made its part of this Z')
+          ok = warp_wait(sb + L::oBar + 8 * (bSplit + half), n & 1, abort_flag);
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int k0 = 0; k0 < 64; k0 += 16) {
+            const uint64_t y = dy + rows(64 * half + k0);
+            mma_if(go, tm + C::P, y, dSplit + rows(k0), idP, half + k0 > 0);
+            mma_if(go, tm + C::P + 64, y, dThird + rows(k0), idT, 1);
+          }
+          commit_if(go, half ? bar(bMP, n) : sb + L::oBar + 8 * (bMP0 + (n & 1)));
+        }
+        if (!ok) break;
         if (!warp_wait(bar(bMask, n), par(n), abort_flag)) break;
         tc::fence_after_sync();
         const uint64_t dz = tc::smem_desc(sb + L::oZ + zslot(n), 16, 1024);
@@ -431,7 +455,7 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     tc::mbar_wait(end, 0);
   } else {
     // ---------------------------------------------- gates: the two warps take every
-    // other chunk, up to four chunks ahead of the readers
+    // other chunk, up to a ring ahead of the readers
     float x[4], y[4];
     auto read = [&](float (&v)[4], int n) {
       read_gates(v, a, tok + at(n), h, min(kC, t1 - at(n)));
@@ -441,7 +465,7 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     for (int n = first; n < cnt; n += 2) {
       // the next values are on their way while these are used
       if (n + 2 < cnt) read(y, n + 2);
-      if (n >= 4 && !warp_wait(bar4(bGFree, n), par4(n - 4), abort_flag)) break;
+      if (n >= kRing && !warp_wait(bar4(bGFree, n), par4(n - kRing), abort_flag)) break;
       fill_gates<REV>(gates(n), x);
       warp_arrive(bar4(bGates, n));
 #pragma unroll
@@ -484,11 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // A piece's own end state, S = sum over its tokens of decay k v^T (REV: the
 // gradient of its start state from its own read-outs, s sum of decay q dO^T,
-// chunks in reverse), 64 value columns per CTA: the P product alone, V' double
-// buffered so that a chunk is split while the previous one is multiplied.
+// chunks in reverse), 64 value columns per CTA: the P product alone, V' (whole chunks)
+// double buffered so that a chunk is split while the previous one is multiplied.
 constexpr int kStThreads = 352;   // 128: half of V' and state; 128: the other half; loads;
                                   // products; gates
-constexpr int kStStages = 3;
+constexpr int kStStages = 2;
 
 enum : uint32_t { sFull = 0, sEmpty = 3, sSplit = 6, sP = 8, sGates = 10, sGFree = 12, sEnd = 14,
                   kStBars = 15 };
@@ -496,7 +520,7 @@ enum : uint32_t { sFull = 0, sEmpty = 3, sSplit = 6, sP = 8, sGates = 10, sGFree
 template <int NK>
 struct StSmem {
   static constexpr uint32_t kWide = NK / 64 * kTile, kStage = kWide + kTile;
-  static constexpr uint32_t oSplit = kStStages * kStage, oGates = oSplit + 4 * kTile,
+  static constexpr uint32_t oSplit = kStStages * kStage, oGates = oSplit + 6 * kTile,
                             oBar = oGates + 2 * sizeof(Gates), oSlot = oBar + 8 * kStBars + 4,
                             oAbort = oSlot + 4, bytes = oAbort + 8;
   static constexpr uint32_t launch = bytes + 1024;
@@ -548,8 +572,11 @@ __global__ void __launch_bounds__(kStThreads, 1)
         !warp_wait(bar(sFull + n % kStStages), (n / kStStages) & 1, abort_flag))
       return false;
     const Gates& g = gates(n);
-    split_row(sb + (n % kStStages) * L::kStage + L::kWide, sb + L::oSplit + (n & 1) * 2 * kTile, row,
-              4 * half, REV ? g.head[row] : g.tail[row]);
+    const float f = REV ? g.head[row] : g.tail[row];
+#pragma unroll 1
+    for (int c = 4 * half; c < 4 * half + 4; c += 2)
+      split_row(sb + (n % kStStages) * L::kStage + L::kWide, sb + L::oSplit + (n & 1) * 3 * kTile,
+                kTile, row, row, c, f);
     tc::fence_proxy_async();
     warp_arrive(bar2(sSplit, n));
     return true;
@@ -603,15 +630,20 @@ __global__ void __launch_bounds__(kStThreads, 1)
     const uint32_t go = lane == 0;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     constexpr uint32_t idP = tc::idesc_bf16(128, 128, 1, 1);
+    constexpr uint32_t idT = tc::idesc_bf16(128, 64, 1, 1);
     for (int n = 0; n < cnt; ++n) {
       // (the state has read this accumulator, chunk n - 2's, before it made this V')
       if (!warp_wait(bar2(sSplit, n), par(n), abort_flag)) break;
       tc::fence_after_sync();
       const uint64_t dx = tc::smem_desc(sb + (n % kStStages) * L::kStage, kTile, 1024);
-      const uint64_t dy = tc::smem_desc(sb + L::oSplit + (n & 1) * 2 * kTile, kTile, 1024);
-#pragma unroll
-      for (int k0 = 0; k0 < kC; k0 += 16)
-        mma_if(go, tm + (n & 1) * 128, dx + ((k0 * 128) >> 4), dy + ((k0 * 128) >> 4), idP, k0 > 0);
+      const uint64_t dy = tc::smem_desc(sb + L::oSplit + (n & 1) * 3 * kTile, kTile, 1024);
+      const uint64_t dt = tc::smem_desc(sb + L::oSplit + ((n & 1) * 3 + 2) * kTile, 16, 1024);
+#pragma unroll 1
+      for (int k0 = 0; k0 < kC; k0 += 16) {
+        const uint64_t at = (k0 * 128) >> 4;
+        mma_if(go, tm + (n & 1) * 128, dx + at, dy + at, idP, k0 > 0);
+        mma_if(go, tm + (n & 1) * 128 + 64, dx + at, dt + at, idT, 1);
+      }
       commit_if(go, bar2(sP, n));
       commit_if(go, bar(sEmpty + n % kStStages));
     }

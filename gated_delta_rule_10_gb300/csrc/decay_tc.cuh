@@ -239,59 +239,78 @@ __device__ __forceinline__ void sts4(uint32_t addr, const uint32_t (&u)[4]) {
                : "memory");
 }
 
-// Chunks c0 .. c0 + 3 (32 columns) of row `r` of a 128 x 64 bf16 tile times f,
-// as hi + lo bf16 tiles (kTile apart): together they hold the product to 2^-17,
-// so the fp32 state they feed keeps its precision.
-__device__ __forceinline__ void split_row(uint32_t src, uint32_t dst, int r, int c0, float f) {
-  const F2 ff = pack2(f, f), minus = pack2(-1.f, -1.f);
-#pragma unroll 1
-  for (int c = c0; c < c0 + 4; c += 2) {
-    const uint32_t off[2] = {static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)),
-                             static_cast<uint32_t>(r * 128 + (((c + 1) ^ (r & 7)) << 4))};
-    uint4 u[2];
-#pragma unroll
-    for (int p = 0; p < 2; ++p) u[p] = lds4(src + off[p]);
-    uint32_t hi[2][4], lo[2][4];
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const uint32_t w[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const F2 x = mul2(widen2(w[i]), ff);
-        hi[p][i] = round2(x);
-        lo[p][i] = round2(fma2(widen2(hi[p][i]), minus, x));
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      sts4(dst + off[p], hi[p]);
-      sts4(dst + kTile + off[p], lo[p]);
-    }
-  }
+// x in three bf16 terms (24 bits): hi, and what it leaves, and what that leaves.
+struct Terms {
+  uint32_t hi, mid, lo;
+};
+__device__ __forceinline__ Terms terms_of(F2 x) {
+  const F2 minus = pack2(-1.f, -1.f);
+  Terms t;
+  t.hi = round2(x);
+  x = fma2(widen2(t.hi), minus, x);
+  t.mid = round2(x);
+  t.lo = round2(fma2(widen2(t.mid), minus, x));
+  return t;
 }
 
-// 64 fp32 values as one row of a swizzled bf16 tile with 128-byte rows; with LO
-// also what the rounding left, as a second tile `lo` bytes on.
-template <bool LO>
-__device__ __forceinline__ void round_row(unsigned char* dst, uint32_t lo, int r,
-                                          const float (&x)[64]) {
-  const F2 minus = pack2(-1.f, -1.f);
+// Two chunks (16 columns from column 8 c) of row `r` of a tile with 64 bf16 columns,
+// times f, as rows `to` of three tiles `apart` bytes from one another: the fp32 state
+// they feed keeps fp32's precision. (Two terms leave 2.4e-6 of the state, which the
+// gate's gradient gathers over thousands of tokens.)
+__device__ __forceinline__ void split_row(uint32_t src, uint32_t dst, uint32_t apart, int r, int to,
+                                          int c, float f) {
+  const F2 ff = pack2(f, f);
+  uint4 u[2];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    unsigned char* d = dst + r * 128 + ((c ^ (r & 7)) << 4);
-    uint32_t hi[4], rest[4];
+  for (int p = 0; p < 2; ++p) u[p] = lds4(src + r * 128 + (((c + p) ^ (r & 7)) << 4));
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const uint32_t w[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
+    uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      hi[i] = pack_bf16x2(x[8 * c + 2 * i], x[8 * c + 2 * i + 1]);
-      if (LO)
-        rest[i] = round2(fma2(widen2(hi[i]), minus, pack2(x[8 * c + 2 * i], x[8 * c + 2 * i + 1])));
+      const Terms t = terms_of(mul2(widen2(w[i]), ff));
+      hi[i] = t.hi;
+      mid[i] = t.mid;
+      lo[i] = t.lo;
     }
-    *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if (LO) *reinterpret_cast<uint4*>(d + lo) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+    const uint32_t d = dst + to * 128 + (((c + p) ^ (to & 7)) << 4);
+    sts4(d, hi);
+    sts4(d + apart, mid);
+    sts4(d + 2 * apart, lo);
   }
 }
 
-// S = all * S + (hi + lo) from 128 accumulator columns [hi 64 | lo 64].
+// 64 fp32 values as one row of a swizzled bf16 tile with 128-byte rows; with ALL as
+// three tiles `apart` bytes from one another.
+template <bool ALL>
+__device__ __forceinline__ void round_row(uint32_t dst, uint32_t apart, int r,
+                                          const float (&x)[64]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t d = dst + r * 128 + ((c ^ (r & 7)) << 4);
+    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F2 v = pack2(x[8 * c + 2 * i], x[8 * c + 2 * i + 1]);
+      if (ALL) {
+        const Terms t = terms_of(v);
+        hi[i] = t.hi;
+        mid[i] = t.mid;
+        lo[i] = t.lo;
+      } else {
+        hi[i] = round2(v);
+      }
+    }
+    sts4(d, hi);
+    if (ALL) {
+      sts4(d + apart, mid);
+      sts4(d + 2 * apart, lo);
+    }
+  }
+}
+
+// S = all * S + (hi + rest) from 128 accumulator columns [hi 64 | the other terms 64].
 __device__ __forceinline__ void add_state(float (&S)[64], float all, uint32_t taddr) {
   const F2 g = pack2(all, all);
 #pragma unroll

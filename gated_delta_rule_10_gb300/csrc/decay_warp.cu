@@ -102,9 +102,14 @@ struct Acc {
         split_tf32(B.at(k + t + 4, c0 + n * 8 + g), bh[1], bl[1]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          mma_tf32(v[m][n], al[m], bh[0], bh[1]);
-          mma_tf32(v[m][n], ah[m], bl[0], bl[1]);
-          mma_tf32(v[m][n], ah[m], bh[0], bh[1]);
+          // the tensor cores truncate as they add: each step's products are added up
+          // by themselves, and to the sum with rounding
+          float p[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_tf32(p, al[m], bh[0], bh[1]);
+          mma_tf32(p, ah[m], bl[0], bl[1]);
+          mma_tf32(p, ah[m], bh[0], bh[1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[m][n][i] += p[i];
         }
       }
     }
