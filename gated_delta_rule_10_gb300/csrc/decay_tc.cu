@@ -21,14 +21,15 @@
 //   P  = Y^T Z'                       (W x 64,    K = 128), Z' the decayed Z.
 // x, y and z go from TMA to the tensor cores as they are. A . D and the R of the
 // read-out are rounded to bf16 (the result is rounded to bf16 anyway); the decayed
-// Z' is split into three bf16 terms because it enters the fp32 state, whose error
-// would otherwise be bf16's. Two terms sit side by side in one N = 128 product, the
-// third is added to the second's columns. Z' is made for 64 tokens at a time, half
-// the space.
+// Z' is split into two bf16 terms, side by side in one N = 128 product, because it
+// enters the fp32 state, whose error would otherwise be bf16's (1.7e-3; with two
+// terms 2.4e-6 of 64 bits).
 //
 // FINE (dq and dk): the gate's gradient needs f_t (R^T x_t) . p_t in fp32, p the
-// partner row (q or k). R is then split into three terms for O1 as well, partly in
-// the space of the second z tile, and the read-out also writes that product.
+// partner row (q or k), and sums of those differences over thousands of tokens. Two
+// terms are not enough there (2e-5 of a fixed decay's gradient at 1100 tokens): Z'
+// and, for O1, R take three each, which is all of fp32 (states 1e-7, gradient 1e-6),
+// for a fifth more time. Z' is then made for 64 tokens at a time, and z has one tile.
 //
 // Only R_{n+1} <- R_n is a chain, and it holds no product: P of any chunk can be
 // ready before R is. A and O1 are issued by one warp, P and O2 by another: the
@@ -64,7 +65,7 @@ struct Walk {
   float* flow;                     // [slices, B * H, T], that product
 };
 
-constexpr int kThreads = 512;   // 3 x 128: mask, state, read-out; products (2); gates (2)
+constexpr int kThreads = 512;   // 3 x 128: mask, state, read-out; products (2); gates; loads
 constexpr uint32_t kCols = 512;
 
 // Tensor-memory columns of chunk n: two buffers of A, whose columns 0..63 take
@@ -80,7 +81,7 @@ enum : uint32_t {   // mbarriers, each a pair for even and odd chunks
   bXY = 0, bZ = 2,                           // tiles landed
   bMA = 4, bMO1 = 6, bMO2 = 8, bMP = 10,     // products complete
   bMask = 12, bState = 16, bFree = 18,
-  bSplit = 14,                               // Z' of tokens 0..63, 64..127, every chunk
+  bSplit = 14,                               // (FINE: Z' of tokens 0..63 and 64..127)
   bGates = 20, bGFree = 24,                  // a ring of four (FINE: two) chunks' gates
   bEnd = 28, bMP0 = 30,                      // (P of tokens 0..63 complete)
   kBars = 32
@@ -92,7 +93,7 @@ template <int W, bool FINE>
 struct WalkSmem {
   static constexpr uint32_t kWide = W / 64 * kTile, kZ = FINE ? 1 : 2, kRing = FINE ? 2 : 4;
   static constexpr uint32_t oX = 0, oY = oX + 2 * kWide, oZ = oY + 2 * kWide,
-                            oSplit = oZ + kZ * kTile, oR = oSplit + 3 * kHalf,
+                            oSplit = oZ + kZ * kTile, oR = oSplit + (FINE ? 3 * kHalf : 2 * kTile),
                             kR = W * 128, oGates = oR + (FINE ? 3 : 1) * kR,
                             oBar = oGates + kRing * sizeof(Gates), oSlot = oBar + 8 * kBars,
                             oAbort = oSlot + 4, bytes = oAbort + 12;
@@ -145,8 +146,7 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
   const int quad = warp & 3, row = 32 * quad + lane;
   const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16);
 
-  // tiles of chunk n into their slots; the roles that see a slot's last reader
-  // finish ask for the next tile themselves (one lane)
+  // tiles of chunk n into their slots (one lane of the loading warp)
   auto load_wide = [&](uint32_t base, const CUtensorMap* m, int heads, int n) {
     tc::mbar_arrive_expect_tx(bar(bXY, n), L::kWide);
 #pragma unroll
@@ -161,23 +161,30 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     tc::tma_load_4d(sb + L::oZ + zslot(n), tz, 64 * slice, h / (a.H / w.z_heads), at(n), b,
                     bar(bZ, n));
   };
-  // the state's and the read-out's 256 threads make Z' of tokens 64 half .. + 63, a
-  // quarter of a row each; its last reader is P of the tokens before
+  // Z' by the state's and the read-out's 256 threads; its last reader is the P before.
+  // FINE: tokens 64 half .. + 63, a quarter of a row each. Else half the columns of
+  // this lane's token, the caller having waited for P(n - 1).
   auto split = [&](int n, int half) {
-    if (half == 0) {
+    if (!FINE || half == 0) {
       if (!warp_wait(bar4(bGates, n), par4(n), abort_flag) ||
           !warp_wait(bar(bZ, n), par(n), abort_flag) ||
-          (n > 0 && !warp_wait(bar(bMP, n - 1), par(n - 1), abort_flag)))
+          (FINE && n > 0 && !warp_wait(bar(bMP, n - 1), par(n - 1), abort_flag)))
         return false;
     } else if (!warp_wait(sb + L::oBar + 8 * (bMP0 + (n & 1)), par(n), abort_flag)) {
       return false;
     }
     const Gates& g = gates(n);
-    const int to = tid & 63, r = 64 * half + to;
-    split_row(sb + L::oZ + zslot(n), sb + L::oSplit, kHalf, r, to, 2 * ((tid >> 6) & 3),
-              REV ? a.scale * g.head[r] : g.tail[r]);
+    const int to = FINE ? tid & 63 : row, r = FINE ? 64 * half + to : row;
+    const float f = REV ? a.scale * g.head[r] : g.tail[r];
+    if (FINE) {
+      split_row<3>(sb + L::oZ + zslot(n), sb + L::oSplit, kHalf, r, to, 2 * ((tid >> 6) & 3), f);
+    } else {
+#pragma unroll 1
+      for (int c = 4 * half; c < 4 * half + 4; c += 2)
+        split_row<2>(sb + L::oZ + zslot(n), sb + L::oSplit, kTile, r, r, c, f);
+    }
     tc::fence_proxy_async();
-    warp_arrive(sb + L::oBar + 8 * (bSplit + half));
+    warp_arrive(sb + L::oBar + 8 * (bSplit + (FINE ? half : n & 1)));
     return true;
   };
 
@@ -236,13 +243,6 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
   } else if (warp < 8) {
     // ---------------------------------------------- the state, one row per lane, and
     // half of Z'
-    int nx = 0, ny = 0;   // (tid 128) tiles requested
-    if (tid == 128)
-      for (; nx < min(2, cnt); ++nx, ++ny) {
-        load_x(nx);
-        load_y(ny);
-      }
-    __syncwarp();
     const bool mine = row < W;
     float R[64];
     const size_t edge = w.chained ? sp.slot_of(REV ? seg + 1 : seg) : 0;
@@ -254,15 +254,10 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     if (mine) round_row<FINE>(sb + L::oR, L::kR, row, R);
     tc::fence_proxy_async();
     warp_arrive(bar(bState, 0));
-    bool ok = split(0, 0) && split(0, 1);
+    bool ok = split(0, 0) && (!FINE || split(0, 1));
     for (int n = 0; ok && n < cnt; ++n) {
       ok = warp_wait(bar(bMP, n), par(n), abort_flag);
       if (!ok) break;
-      if (tid == 128 && n + 2 < cnt && wait(bar(bMA, n), par(n), abort_flag)) {
-        load_y(n + 2);   // y's readers A(n) and P(n) are done
-        ny = n + 3;
-      }
-      __syncwarp();
       tc::fence_after_sync();
       const float all = gates(n).all;
       warp_arrive(bar4(bGFree, n));
@@ -271,41 +266,20 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
       if (n + 1 < cnt) {
         ok = split(n + 1, 0) && warp_wait(bar(bMO1, n), par(n), abort_flag);   // R_n has been read
         if (ok) {
-          if (tid == 128 && n + 2 < cnt) {
-            load_x(n + 2);
-            nx = n + 3;
-          }
-          __syncwarp();
           if (mine) round_row<FINE>(sb + L::oR, L::kR, row, R);
           tc::fence_proxy_async();
           warp_arrive(bar(bState, n + 1));
-          ok = split(n + 1, 1);
+          if (FINE) ok = split(n + 1, 1);
         }
       }
     }
     if (ok && mine && w.end && seg == (REV ? 0 : sp.segments - 1))
       write_row(R, 1.f, w.end + (static_cast<size_t>(bh) * W + row) * w.nz + 64 * slice);
-    // no copy may outlive the CTA, whatever gave up (x and y of a chunk share a
-    // barrier: a y left alone by an abort gets its x, so that it completes)
-    if (tid == 128) {
-      if (nx < ny) load_x(nx);
-      for (int n = max(0, ny - 2); n < ny; ++n) tc::mbar_wait(bar(bXY, n), par(n));
-    }
-    __syncwarp();
   } else if (warp < 12) {
     // ---------------------------------------------- read-out, one token per lane, and
     // the other half of Z'
-    constexpr int kAhead = FINE ? 1 : 2;
-    int nz = 0;   // (tid 256) tiles requested
-    if (tid == 256)
-      for (; nz < min(kAhead, cnt); ++nz) load_z(nz);
-    auto soon = [&](int n) {   // one tile only: the next one comes into L2 meanwhile
-      if (n < cnt) tc::tma_prefetch_4d(tz, 64 * slice, h / (a.H / w.z_heads), at(n), b);
-    };
-    if (FINE && tid == 256) soon(1);
-    __syncwarp();
     bool ok = true;
-    if (!FINE) ok = split(0, 0) && split(0, 1);
+    if (!FINE) ok = split(0, 1);
     for (int n = 0; ok && n < cnt; ++n) {
       const int t = at(n) + row;
       const bool live = t < t1;
@@ -319,17 +293,11 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
         // one z tile: its last reader O2(n - 1) was waited for below
         ok = split(n, 0) && split(n, 1);
       } else if (n + 1 < cnt) {
-        ok = split(n + 1, 0) && split(n + 1, 1);
+        ok = warp_wait(bar(bMP, n), par(n), abort_flag) && split(n + 1, 1);
       }
       ok = ok && warp_wait(bar(bMO1, n), par(n), abort_flag) &&
            warp_wait(bar(bMO2, n), par(n), abort_flag);
       if (!ok) break;
-      if (tid == 256 && n + kAhead < cnt) {   // z's readers, Z'(n) and O2(n), are done
-        load_z(n + kAhead);
-        nz = n + kAhead + 1;
-        if (FINE) soon(n + 2);
-      }
-      __syncwarp();
       tc::fence_after_sync();
       const float f = REV ? gates(n).tail[row] : a.scale * gates(n).head[row];
       warp_arrive(bar4(bGFree, n));
@@ -378,9 +346,6 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
       tc::fence_before_sync();
       warp_arrive(bar(bFree, n));
     }
-    if (tid == 256)
-      for (int n = max(0, nz - kAhead); n < nz; ++n) tc::mbar_wait(bar(bZ, n), par(n));
-    __syncwarp();
   } else if (warp < 14) {
     // ---------------------------------------------- products
     const uint32_t go = lane == 0;
@@ -419,28 +384,37 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
       }
     } else {
       end += 8;
-      const uint64_t dSplit = tc::smem_desc(sb + L::oSplit, kHalf, 1024);
+      const uint64_t dSplit = tc::smem_desc(sb + L::oSplit, FINE ? kHalf : kTile, 1024);
       const uint64_t dThird = tc::smem_desc(sb + L::oSplit + 2 * kHalf, 16, 1024);
       constexpr uint32_t idT = tc::idesc_bf16(128, 64, 1, 1);
       for (int n = 0; n < cnt; ++n) {
         if (!warp_wait(bar(bXY, n), par(n), abort_flag)) break;
         const uint64_t dy = tc::smem_desc(sb + L::oY + (n & 1) * L::kWide, kTile, 1024);
-        bool ok = true;
+        // (the state has added the last P before it made its part of this Z')
+        if constexpr (FINE) {
+          bool ok = true;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          // (the state has added the last P before it made its part of this Z')
-          ok = warp_wait(sb + L::oBar + 8 * (bSplit + half), n & 1, abort_flag);
+          for (int half = 0; half < 2; ++half) {
+            ok = warp_wait(sb + L::oBar + 8 * (bSplit + half), n & 1, abort_flag);
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int k0 = 0; k0 < 64; k0 += 16) {
+              const uint64_t y = dy + rows(64 * half + k0);
+              mma_if(go, tm + C::P, y, dSplit + rows(k0), idP, half + k0 > 0);
+              mma_if(go, tm + C::P + 64, y, dThird + rows(k0), idT, 1);
+            }
+            commit_if(go, half ? bar(bMP, n) : sb + L::oBar + 8 * (bMP0 + (n & 1)));
+          }
           if (!ok) break;
+        } else {
+          if (!warp_wait(bar(bSplit, n), par(n), abort_flag)) break;
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int k0 = 0; k0 < 64; k0 += 16) {
-            const uint64_t y = dy + rows(64 * half + k0);
-            mma_if(go, tm + C::P, y, dSplit + rows(k0), idP, half + k0 > 0);
-            mma_if(go, tm + C::P + 64, y, dThird + rows(k0), idT, 1);
-          }
-          commit_if(go, half ? bar(bMP, n) : sb + L::oBar + 8 * (bMP0 + (n & 1)));
+          for (int k0 = 0; k0 < kC; k0 += 16)
+            mma_if(go, tm + C::P, dy + rows(k0), dSplit + rows(k0), idP, k0 > 0);
+          commit_if(go, bar(bMP, n));
         }
-        if (!ok) break;
         if (!warp_wait(bar(bMask, n), par(n), abort_flag)) break;
         tc::fence_after_sync();
         const uint64_t dz = tc::smem_desc(sb + L::oZ + zslot(n), 16, 1024);
@@ -453,18 +427,51 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     // nothing may still be reading shared memory when the CTA goes
     commit_if(go, end);
     tc::mbar_wait(end, 0);
+  } else if (warp == 15) {
+    // ---------------------------------------------- loads: a slot is free once the last
+    // product that reads it is complete, seen here at once (left to the roles, a z
+    // tile was asked for a third of a chunk later and waited for)
+    if (lane == 0) {
+      constexpr int kAhead = FINE ? 1 : 2;   // z tiles
+      auto soon = [&](int n) {   // FINE: the z tile after the next comes into L2 meanwhile
+        if (FINE && n < cnt) tc::tma_prefetch_4d(tz, 64 * slice, h / (a.H / w.z_heads), at(n), b);
+      };
+      int nx = 0, ny = 0, nz = 0;   // tiles requested
+      for (; nx < min(2, cnt); ++nx, ++ny) {
+        load_x(nx);
+        load_y(ny);
+      }
+      for (; nz < min(kAhead, cnt); ++nz) load_z(nz);
+      soon(1);
+      for (int n = 0; n + kAhead < cnt; ++n) {
+        if (n + 2 < cnt) {
+          if (!wait(bar(bMO1, n), par(n), abort_flag)) break;   // (its warp issued A first)
+          load_x(nx++);
+          if (!wait(bar(bMP, n), par(n), abort_flag) || !wait(bar(bMA, n), par(n), abort_flag)) break;
+          load_y(ny++);
+        }
+        // O2(n) follows P(n), which waited for Z'(n): z's readers are done
+        if (!wait(bar(bMO2, n), par(n), abort_flag)) break;
+        load_z(nz++);
+        soon(n + 2);
+      }
+      // no copy may outlive the CTA, whatever gave up (x and y of a chunk share a
+      // barrier: an x left alone by an abort gets its y, so that it completes)
+      if (ny < nx) load_y(ny);
+      for (int n = max(0, nx - 2); n < nx; ++n) tc::mbar_wait(bar(bXY, n), par(n));
+      for (int n = max(0, nz - kAhead); n < nz; ++n) tc::mbar_wait(bar(bZ, n), par(n));
+    }
   } else {
-    // ---------------------------------------------- gates: the two warps take every
-    // other chunk, up to a ring ahead of the readers
+    // ---------------------------------------------- gates, up to a ring ahead of the
+    // readers
     float x[4], y[4];
     auto read = [&](float (&v)[4], int n) {
       read_gates(v, a, tok + at(n), h, min(kC, t1 - at(n)));
     };
-    const int first = warp - 14;
-    if (first < cnt) read(x, first);
-    for (int n = first; n < cnt; n += 2) {
+    read(x, 0);
+    for (int n = 0; n < cnt; ++n) {
       // the next values are on their way while these are used
-      if (n + 2 < cnt) read(y, n + 2);
+      if (n + 1 < cnt) read(y, n + 1);
       if (n >= kRing && !warp_wait(bar4(bGFree, n), par4(n - kRing), abort_flag)) break;
       fill_gates<REV>(gates(n), x);
       warp_arrive(bar4(bGates, n));
@@ -517,20 +524,20 @@ constexpr int kStStages = 2;
 enum : uint32_t { sFull = 0, sEmpty = 3, sSplit = 6, sP = 8, sGates = 10, sGFree = 12, sEnd = 14,
                   kStBars = 15 };
 
-template <int NK>
+template <int NK, int TERMS>
 struct StSmem {
   static constexpr uint32_t kWide = NK / 64 * kTile, kStage = kWide + kTile;
-  static constexpr uint32_t oSplit = kStStages * kStage, oGates = oSplit + 6 * kTile,
+  static constexpr uint32_t oSplit = kStStages * kStage, oGates = oSplit + 2 * TERMS * kTile,
                             oBar = oGates + 2 * sizeof(Gates), oSlot = oBar + 8 * kStBars + 4,
                             oAbort = oSlot + 4, bytes = oAbort + 8;
   static constexpr uint32_t launch = bytes + 1024;
 };
 
-template <int NK, bool REV>
+template <int NK, bool REV, int TERMS>
 __global__ void __launch_bounds__(kStThreads, 1)
     decay_states_tc(const DecayArgs a, const DecaySplit sp, const __grid_constant__ CUtensorMap tx,
                     const __grid_constant__ CUtensorMap ty) {
-  using L = StSmem<NK>;
+  using L = StSmem<NK, TERMS>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -575,8 +582,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
     const float f = REV ? g.head[row] : g.tail[row];
 #pragma unroll 1
     for (int c = 4 * half; c < 4 * half + 4; c += 2)
-      split_row(sb + (n % kStStages) * L::kStage + L::kWide, sb + L::oSplit + (n & 1) * 3 * kTile,
-                kTile, row, row, c, f);
+      split_row<TERMS>(sb + (n % kStStages) * L::kStage + L::kWide,
+                       sb + L::oSplit + (n & 1) * TERMS * kTile, kTile, row, row, c, f);
     tc::fence_proxy_async();
     warp_arrive(bar2(sSplit, n));
     return true;
@@ -636,13 +643,13 @@ __global__ void __launch_bounds__(kStThreads, 1)
       if (!warp_wait(bar2(sSplit, n), par(n), abort_flag)) break;
       tc::fence_after_sync();
       const uint64_t dx = tc::smem_desc(sb + (n % kStStages) * L::kStage, kTile, 1024);
-      const uint64_t dy = tc::smem_desc(sb + L::oSplit + (n & 1) * 3 * kTile, kTile, 1024);
-      const uint64_t dt = tc::smem_desc(sb + L::oSplit + ((n & 1) * 3 + 2) * kTile, 16, 1024);
+      const uint64_t dy = tc::smem_desc(sb + L::oSplit + (n & 1) * TERMS * kTile, kTile, 1024);
+      const uint64_t dt = tc::smem_desc(sb + L::oSplit + ((n & 1) * TERMS + 2) * kTile, 16, 1024);
 #pragma unroll 1
       for (int k0 = 0; k0 < kC; k0 += 16) {
         const uint64_t at = (k0 * 128) >> 4;
         mma_if(go, tm + (n & 1) * 128, dx + at, dy + at, idP, k0 > 0);
-        mma_if(go, tm + (n & 1) * 128 + 64, dx + at, dt + at, idT, 1);
+        if (TERMS == 3) mma_if(go, tm + (n & 1) * 128 + 64, dx + at, dt + at, idT, 1);
       }
       commit_if(go, bar2(sP, n));
       commit_if(go, bar(sEmpty + n % kStStages));
@@ -962,19 +969,19 @@ Walk from(const DecayArgs& a, const DecaySplit& sp, bool grad, bool transposed) 
   return w;
 }
 
-template <int NK, bool REV>
+template <int NK, bool REV, int TERMS>
 cudaError_t states(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream) {
-  using L = StSmem<NK>;
+  using L = StSmem<NK, TERMS>;
   static_assert(L::launch <= 232448, "shared memory budget of one CTA");
   const long long so = static_cast<long long>(a.H) * a.nv;
   CUtensorMap tx, ty;
   if (!make_rows_tmap(&tx, REV ? a.q : a.k, a.B, a.T, a.Hk, NK, REV ? a.sq : a.sk) ||
       !make_rows_tmap(&ty, REV ? a.dO : a.v, a.B, a.T, a.H, a.nv, REV ? so : a.sv))
     return cudaErrorInvalidValue;
-  const cudaError_t err = opt_in(decay_states_tc<NK, REV>, L::launch);
+  const cudaError_t err = opt_in(decay_states_tc<NK, REV, TERMS>, L::launch);
   if (err != cudaSuccess) return err;
   const int segs = REV ? sp.pieces - sp.slot_of(1) : sp.states(a.dhT != nullptr);
-  decay_states_tc<NK, REV><<<dim3(segs * (a.nv / 64), a.B * a.H), kStThreads, L::launch, stream>>>(
+  decay_states_tc<NK, REV, TERMS><<<dim3(segs * (a.nv / 64), a.B * a.H), kStThreads, L::launch, stream>>>(
       a, sp, tx, ty);
   return cudaGetLastError();
 }
@@ -1050,9 +1057,12 @@ cudaError_t launch_decay_bwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaSt
 cudaError_t launch_decay_states_tc(const DecayArgs& a, const DecaySplit& sp, bool reverse,
                                    cudaStream_t stream) {
   if ((reverse ? sp.pieces - sp.slot_of(1) : sp.states(a.dhT != nullptr)) < 1) return cudaSuccess;
+  // two terms for the forward, three where the gate's gradient comes from them (above)
   if (reverse)
-    return a.nk == 64 ? states<64, true>(a, sp, stream) : states<128, true>(a, sp, stream);
-  return a.nk == 64 ? states<64, false>(a, sp, stream) : states<128, false>(a, sp, stream);
+    return a.nk == 64 ? states<64, true, 3>(a, sp, stream) : states<128, true, 3>(a, sp, stream);
+  if (sp.D)
+    return a.nk == 64 ? states<64, false, 3>(a, sp, stream) : states<128, false, 3>(a, sp, stream);
+  return a.nk == 64 ? states<64, false, 2>(a, sp, stream) : states<128, false, 2>(a, sp, stream);
 }
 
 }  // namespace gdr

@@ -254,9 +254,9 @@ __device__ __forceinline__ Terms terms_of(F2 x) {
 }
 
 // Two chunks (16 columns from column 8 c) of row `r` of a tile with 64 bf16 columns,
-// times f, as rows `to` of three tiles `apart` bytes from one another: the fp32 state
-// they feed keeps fp32's precision. (Two terms leave 2.4e-6 of the state, which the
-// gate's gradient gathers over thousands of tokens.)
+// times f, as rows `to` of TERMS tiles `apart` bytes from one another: two leave
+// 2.4e-6 of the state they feed, three 1e-7.
+template <int TERMS>
 __device__ __forceinline__ void split_row(uint32_t src, uint32_t dst, uint32_t apart, int r, int to,
                                           int c, float f) {
   const F2 ff = pack2(f, f);
@@ -277,7 +277,7 @@ __device__ __forceinline__ void split_row(uint32_t src, uint32_t dst, uint32_t a
     const uint32_t d = dst + to * 128 + (((c + p) ^ (to & 7)) << 4);
     sts4(d, hi);
     sts4(d + apart, mid);
-    sts4(d + 2 * apart, lo);
+    if (TERMS == 3) sts4(d + 2 * apart, lo);
   }
 }
 
