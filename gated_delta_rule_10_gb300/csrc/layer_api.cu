@@ -56,14 +56,13 @@ gdr::DecayArgs decay_args(const gdr_decay_shape* s) {
   return a;
 }
 
-constexpr int kMinRun = 4;          // chunks per segment, at least
 constexpr int kMaxBwdRun = 4096;    // tokens per segment of the backward, at most
 
 // Segments of each sequence, and pieces of each segment. A CTA walks one segment of
 // a (batch, head, 64 columns), so few sequences are cut until the CTAs fill the
 // SMs; each cut costs a pass over k and v for the segments' own states, so no
 // further than that (1 x 65536 x 32 heads: two segments). That pass has one segment
-// less, and takes segments in pieces until it fills the SMs too (865 -> 710 us).
+// less, and takes segments in pieces until it fills the SMs too (864 -> 726 us).
 // The backward also bounds a segment's tokens: what its gate gradient passes on
 // from block to block rounds (gate_grad_kernel), and its blocks are kept on chip.
 void cut(const gdr_decay_shape* s, bool backward, gdr::DecaySplit* sp) {
@@ -72,7 +71,11 @@ void cut(const gdr_decay_shape* s, bool backward, gdr::DecaySplit* sp) {
   const long long ctas = static_cast<long long>(s->B) * s->H *
                          (s->dtype == GDR_BF16 ? s->dv / 64 : backward ? 2 : 1);
   long long p = kSms / ctas;
-  if (p > chunks / kMinRun) p = chunks / kMinRun;
+  // chunks per segment or piece, at least: a chunk takes ~2 us on the tensor cores,
+  // less than the launches that a cut adds, and ~10 us in fp32, more than those
+  // (1 x 257 x 2 heads x 64 in fp32: 63 us uncut, 31 us in five segments)
+  const int least = s->dtype == GDR_BF16 ? 4 : 1;
+  if (p > chunks / least) p = chunks / least;
   if (backward && p < (s->T + kMaxBwdRun - 1) / kMaxBwdRun)
     p = (s->T + kMaxBwdRun - 1) / kMaxBwdRun;
   if (p < 1) p = 1;
@@ -82,7 +85,7 @@ void cut(const gdr_decay_shape* s, bool backward, gdr::DecaySplit* sp) {
   if (sp->segments > 1) {
     const long long busy = ctas * (sp->segments - 1);
     q = kSms / busy;
-    if (q > per / kMinRun) q = per / kMinRun;
+    if (q > per / least) q = per / least;
     if (q < 1) q = 1;
   }
   const int piece = static_cast<int>((per + q - 1) / q);
