@@ -54,13 +54,11 @@ struct DecaySplit {
 // A log-decay at or below this clears the state: exp() of it is zero in fp32.
 constexpr float kDecayReset = -104.f;
 
-// Split-tf32 warp products (decay_warp.cu).
-cudaError_t launch_decay_states_warp(const DecayArgs& a, const DecaySplit& sp, bool reverse,
-                                     bool f32, cudaStream_t stream);
-cudaError_t launch_decay_fwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,
-                                  cudaStream_t stream);
-cudaError_t launch_decay_bwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,
-                                  cudaStream_t stream);
+// fp32 inputs: split-tf32 warp products, chunks of 64 tokens (decay_f32.cu).
+cudaError_t launch_decay_states_f32(const DecayArgs& a, const DecaySplit& sp, bool reverse,
+                                    cudaStream_t stream);
+cudaError_t launch_decay_fwd_f32(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream);
+cudaError_t launch_decay_bwd_f32(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream);
 // bf16 inputs on tcgen05, chunks of 128 tokens (decay_tc.cu).
 cudaError_t launch_decay_states_tc(const DecayArgs& a, const DecaySplit& sp, bool reverse,
                                    cudaStream_t stream);

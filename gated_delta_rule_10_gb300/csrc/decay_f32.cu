@@ -181,8 +181,8 @@ __device__ void load_gates(Gates& s, const DecayArgs& a, int b, int h, int t0, i
 }
 
 // Rows [t0, t0 + n) of one head into a 64 x W tile, zeros past n.
-template <int W, typename T>
-__device__ void load_tile(float* dst, const T* src, long long stride, int n) {
+template <int W>
+__device__ void load_tile(float* dst, const float* src, long long stride, int n) {
   constexpr int V = W / 8, LD = W + 4;
   for (int i = threadIdx.x; i < kC * V; i += kThreads) {
     const int r = i / V, c = i % V;
@@ -208,10 +208,9 @@ __device__ __forceinline__ Where where(const DecayArgs& a, int len, int seg) {
   w.tok = static_cast<size_t>(w.b) * a.T;
   return w;
 }
-template <typename T>
-__device__ __forceinline__ const T* rows_of(const void* p, const Where& w, int t,
+__device__ __forceinline__ const float* rows_of(const void* p, const Where& w, int t,
                                             long long stride, int head_off) {
-  return static_cast<const T*>(p) + static_cast<long long>(w.tok + t) * stride + head_off;
+  return static_cast<const float*>(p) + static_cast<long long>(w.tok + t) * stride + head_off;
 }
 
 template <int NK, int NV>
@@ -241,8 +240,8 @@ __device__ __forceinline__ void scale_rows(float* X, const float* f) {
 
 // Local end state of every piece from a zero state (REV: the gradient of its
 // start state from a zero gradient at its end), and the product of its decays.
-template <int NK, int NV, bool REV, typename T>
-__global__ void __launch_bounds__(kThreads, 1) states_warp(const DecayArgs a, const DecaySplit sp) {
+template <int NK, int NV, bool REV>
+__global__ void __launch_bounds__(kThreads, 1) states_f32(const DecayArgs a, const DecaySplit sp) {
   extern __shared__ __align__(16) float sm[];
   float *S = sm, *X = S + NK * (NV + 4), *Y = X + kC * (NK + 4);
   __shared__ Gates gates;
@@ -257,12 +256,12 @@ __global__ void __launch_bounds__(kThreads, 1) states_warp(const DecayArgs a, co
     __syncthreads();
     if (threadIdx.x < 32) load_gates(gates, a, w.b, w.h, t, n);
     if (REV) {
-      load_tile<NK>(X, rows_of<T>(a.q, w, t, a.sq, hk * NK), a.sq, n);
-      load_tile<NV>(Y, rows_of<T>(a.dO, w, t, static_cast<long long>(a.H) * NV, w.h * NV),
+      load_tile<NK>(X, rows_of(a.q, w, t, a.sq, hk * NK), a.sq, n);
+      load_tile<NV>(Y, rows_of(a.dO, w, t, static_cast<long long>(a.H) * NV, w.h * NV),
                     static_cast<long long>(a.H) * NV, n);
     } else {
-      load_tile<NK>(X, rows_of<T>(a.k, w, t, a.sk, hk * NK), a.sk, n);
-      load_tile<NV>(Y, rows_of<T>(a.v, w, t, a.sv, w.h * NV), a.sv, n);
+      load_tile<NK>(X, rows_of(a.k, w, t, a.sk, hk * NK), a.sk, n);
+      load_tile<NV>(Y, rows_of(a.v, w, t, a.sv, w.h * NV), a.sv, n);
     }
     __syncthreads();
     scale_rows<NV>(Y, REV ? gates.head : gates.tail);
@@ -281,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) states_warp(const DecayArgs a, co
   if (threadIdx.x == 0) sp.decay[static_cast<size_t>(w.bh) * sp.pieces + seg] = prod;
 }
 
-template <int NK, int NV, typename T>
-__global__ void __launch_bounds__(kThreads, 1) fwd_warp(const DecayArgs a, const DecaySplit sp) {
+template <int NK, int NV>
+__global__ void __launch_bounds__(kThreads, 1) fwd_f32(const DecayArgs a, const DecaySplit sp) {
   extern __shared__ __align__(16) float sm[];
   float *S = sm, *Q = S + NK * (NV + 4), *K = Q + kC * (NK + 4), *V = K + kC * (NK + 4),
         *A = V + kC * (NV + 4);
@@ -297,9 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_warp(const DecayArgs a, const
     const int n = min(kC, w.t1 - t);
     __syncthreads();
     if (threadIdx.x < 32) load_gates(gates, a, w.b, w.h, t, n);
-    load_tile<NK>(Q, rows_of<T>(a.q, w, t, a.sq, hk * NK), a.sq, n);
-    load_tile<NK>(K, rows_of<T>(a.k, w, t, a.sk, hk * NK), a.sk, n);
-    load_tile<NV>(V, rows_of<T>(a.v, w, t, a.sv, w.h * NV), a.sv, n);
+    load_tile<NK>(Q, rows_of(a.q, w, t, a.sq, hk * NK), a.sq, n);
+    load_tile<NK>(K, rows_of(a.k, w, t, a.sk, hk * NK), a.sk, n);
+    load_tile<NV>(V, rows_of(a.v, w, t, a.sv, w.h * NV), a.sv, n);
     __syncthreads();
     {
       Acc<kC, kC> s;
@@ -313,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_warp(const DecayArgs a, const
     o.each([&](int r, int, float& x) { x *= gates.head[r]; });
     __syncthreads();
     o.template mul<kC>(View{A, kC + 4, 1}, View{V, NV + 4, 1});
-    T* out = static_cast<T*>(a.o);
+    float* out = static_cast<float*>(a.o);
     o.each([&](int r, int c, float& x) {
-      if (r < n) out[((w.tok + t + r) * a.H + w.h) * NV + c] = static_cast<T>(a.scale * x);
+      if (r < n) out[((w.tok + t + r) * a.H + w.h) * NV + c] = a.scale * x;
     });
     __syncthreads();
     scale_rows<NV>(V, gates.tail);
@@ -329,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_warp(const DecayArgs a, const
 
 // blockIdx.z = 0: dq and the states' part of what comes from before, forward with
 // S. 1: dk, dv and the other terms, backward with D.
-template <int NK, int NV, typename T>
-__global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const DecaySplit sp) {
+template <int NK, int NV>
+__global__ void __launch_bounds__(kThreads, 1) bwd_f32(const DecayArgs a, const DecaySplit sp) {
   extern __shared__ __align__(16) float sm[];
   float *S = sm, *Q = S + NK * (NV + 4), *K = Q + kC * (NK + 4), *V = K + kC * (NK + 4),
         *O = V + kC * (NV + 4), *A = O + kC * (NV + 4);
@@ -350,19 +349,19 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
   load_state<NK, NV>(S, start);
   const long long so = static_cast<long long>(a.H) * NV;
   const int chunks = (w.t1 - w.t0 + kC - 1) / kC;
-  T* dq = static_cast<T*>(a.dq);
-  T* dk = static_cast<T*>(a.dk);
-  T* dv = static_cast<T*>(a.dv);
+  float* dq = static_cast<float*>(a.dq);
+  float* dk = static_cast<float*>(a.dk);
+  float* dv = static_cast<float*>(a.dv);
   const int wn = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
   for (int i = 0; i < chunks; ++i) {
     const int t = w.t0 + (rev ? chunks - 1 - i : i) * kC, n = min(kC, w.t1 - t);
     __syncthreads();
     if (threadIdx.x < 32) load_gates(gates, a, w.b, w.h, t, n);
     for (int j = threadIdx.x; j < 6 * kC; j += kThreads) flow[j / kC][j % kC] = 0.f;
-    load_tile<NK>(Q, rows_of<T>(a.q, w, t, a.sq, hk * NK), a.sq, n);
-    load_tile<NK>(K, rows_of<T>(a.k, w, t, a.sk, hk * NK), a.sk, n);
-    load_tile<NV>(V, rows_of<T>(a.v, w, t, a.sv, w.h * NV), a.sv, n);
-    load_tile<NV>(O, rows_of<T>(a.dO, w, t, so, w.h * NV), so, n);
+    load_tile<NK>(Q, rows_of(a.q, w, t, a.sq, hk * NK), a.sq, n);
+    load_tile<NK>(K, rows_of(a.k, w, t, a.sk, hk * NK), a.sk, n);
+    load_tile<NV>(V, rows_of(a.v, w, t, a.sv, w.h * NV), a.sv, n);
+    load_tile<NV>(O, rows_of(a.dO, w, t, so, w.h * NV), so, n);
     __syncthreads();
     Acc<kC, kC> dA;
     dA.zero();
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
         if (r >= n) return;
         const size_t at = ((w.tok + t + r) * a.H + w.h) * NK + c;
         if (sp.dq_part) sp.dq_part[at] = a.scale * x;
-        else dq[at] = static_cast<T>(a.scale * x);
+        else dq[at] = a.scale * x;
       });
       if (threadIdx.x < n)
         sp.from[static_cast<size_t>(w.bh) * a.T + t + threadIdx.x] =
@@ -417,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
     dvv.each([&](int r, int, float& x) { x *= gates.tail[r]; });
     dvv.template mul<kC>(View{A, 1, kC + 4}, View{O, NV + 4, 1});
     dvv.each([&](int r, int c, float& x) {
-      if (r < n) dv[((w.tok + t + r) * a.H + w.h) * NV + c] = static_cast<T>(x);
+      if (r < n) dv[((w.tok + t + r) * a.H + w.h) * NV + c] = x;
     });
     __syncthreads();
     // M = s * dA into A, then its row and column sums
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_warp(const DecayArgs a, const
       if (r >= n) return;
       const size_t at = ((w.tok + t + r) * a.H + w.h) * NK + c;
       if (sp.dk_part) sp.dk_part[at] = x;
-      else dk[at] = static_cast<T>(x);
+      else dk[at] = x;
     });
     if (threadIdx.x < n) {
       const int r = threadIdx.x;
@@ -487,42 +486,38 @@ cudaError_t run(Kern kern, const DecayArgs& a, const DecaySplit& sp, int segment
 constexpr size_t tile(int w) { return static_cast<size_t>(kC) * (w + 4) * 4; }
 constexpr size_t state(int nk, int nv) { return static_cast<size_t>(nk) * (nv + 4) * 4; }
 
-template <int NK, int NV, typename T>
-struct Warp {
+template <int NK, int NV>
+struct F32 {
   static cudaError_t states(const DecayArgs& a, const DecaySplit& sp, bool rev, cudaStream_t s) {
     const size_t smem = state(NK, NV) + tile(NK) + tile(NV);
-    return rev ? run(states_warp<NK, NV, true, T>, a, sp, sp.pieces - sp.slot_of(1), 1, smem, s)
-               : run(states_warp<NK, NV, false, T>, a, sp, sp.states(a.dhT != nullptr), 1, smem, s);
+    return rev ? run(states_f32<NK, NV, true>, a, sp, sp.pieces - sp.slot_of(1), 1, smem, s)
+               : run(states_f32<NK, NV, false>, a, sp, sp.states(a.dhT != nullptr), 1, smem, s);
   }
   static cudaError_t fwd(const DecayArgs& a, const DecaySplit& sp, cudaStream_t s) {
-    return run(fwd_warp<NK, NV, T>, a, sp, sp.segments, 1,
+    return run(fwd_f32<NK, NV>, a, sp, sp.segments, 1,
                state(NK, NV) + 2 * tile(NK) + tile(NV) + tile(kC), s);
   }
   static cudaError_t bwd(const DecayArgs& a, const DecaySplit& sp, cudaStream_t s) {
-    return run(bwd_warp<NK, NV, T>, a, sp, sp.segments, 2,
+    return run(bwd_f32<NK, NV>, a, sp, sp.segments, 2,
                state(NK, NV) + 2 * tile(NK) + 2 * tile(NV) + tile(kC), s);
   }
 };
 
 }  // namespace
 
-#define GDR_TYPE(nk_, nv_, call) \
-  (f32 ? Warp<nk_, nv_, float>::call : Warp<nk_, nv_, __nv_bfloat16>::call)
-#define GDR_WIDTHS(call)                                                  \
-  (a.nk == 64 ? (a.nv == 64 ? GDR_TYPE(64, 64, call) : GDR_TYPE(64, 128, call)) \
-              : (a.nv == 64 ? GDR_TYPE(128, 64, call) : GDR_TYPE(128, 128, call)))
+#define GDR_WIDTHS(call)                                               \
+  (a.nk == 64 ? (a.nv == 64 ? F32<64, 64>::call : F32<64, 128>::call)  \
+              : (a.nv == 64 ? F32<128, 64>::call : F32<128, 128>::call))
 
-cudaError_t launch_decay_states_warp(const DecayArgs& a, const DecaySplit& sp, bool reverse,
-                                     bool f32, cudaStream_t stream) {
+cudaError_t launch_decay_states_f32(const DecayArgs& a, const DecaySplit& sp, bool reverse,
+                                    cudaStream_t stream) {
   if ((reverse ? sp.pieces - sp.slot_of(1) : sp.states(a.dhT != nullptr)) < 1) return cudaSuccess;
   return GDR_WIDTHS(states(a, sp, reverse, stream));
 }
-cudaError_t launch_decay_fwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,
-                                  cudaStream_t stream) {
+cudaError_t launch_decay_fwd_f32(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream) {
   return GDR_WIDTHS(fwd(a, sp, stream));
 }
-cudaError_t launch_decay_bwd_warp(const DecayArgs& a, const DecaySplit& sp, bool f32,
-                                  cudaStream_t stream) {
+cudaError_t launch_decay_bwd_f32(const DecayArgs& a, const DecaySplit& sp, cudaStream_t stream) {
   return GDR_WIDTHS(bwd(a, sp, stream));
 }
 

@@ -200,12 +200,12 @@ gdr_status gdr_decay_chunk_fwd(const gdr_decay_shape* shape, const void* q, cons
   const cudaStream_t cs = stream_of(stream);
   cudaError_t err = cudaSuccess;
   if (sp.segments > 1) {
-    err = f32 ? gdr::launch_decay_states_warp(a, sp, false, f32, cs)
+    err = f32 ? gdr::launch_decay_states_f32(a, sp, false, cs)
               : gdr::launch_decay_states_tc(a, sp, false, cs);
     if (err == cudaSuccess) err = gdr::launch_decay_chain(a, sp, false, cs);
   }
   if (err == cudaSuccess)
-    err = f32 ? gdr::launch_decay_fwd_warp(a, sp, f32, cs) : gdr::launch_decay_fwd_tc(a, sp, cs);
+    err = f32 ? gdr::launch_decay_fwd_f32(a, sp, cs) : gdr::launch_decay_fwd_tc(a, sp, cs);
   return status_of(err);
 }
 
@@ -243,12 +243,12 @@ gdr_status gdr_decay_chunk_bwd(const gdr_decay_shape* shape, const void* q, cons
   cudaError_t err = cudaSuccess;
   if (sp.S) {
     for (int rev = 0; rev < 2 && err == cudaSuccess; ++rev)
-      err = f32 ? gdr::launch_decay_states_warp(a, sp, rev, f32, cs)
+      err = f32 ? gdr::launch_decay_states_f32(a, sp, rev, cs)
                 : gdr::launch_decay_states_tc(a, sp, rev, cs);
     if (err == cudaSuccess) err = gdr::launch_decay_chain(a, sp, true, cs);
   }
   if (err == cudaSuccess)
-    err = f32 ? gdr::launch_decay_bwd_warp(a, sp, f32, cs) : gdr::launch_decay_bwd_tc(a, sp, cs);
+    err = f32 ? gdr::launch_decay_bwd_f32(a, sp, cs) : gdr::launch_decay_bwd_tc(a, sp, cs);
   if (err == cudaSuccess) err = gdr::launch_decay_gate_grad(a, sp, f32, cs);
   return status_of(err);
 }
