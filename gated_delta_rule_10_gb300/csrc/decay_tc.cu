@@ -28,8 +28,13 @@
 // FINE (dq and dk): the gate's gradient needs f_t (R^T x_t) . p_t in fp32, p the
 // partner row (q or k), and sums of those differences over thousands of tokens. Two
 // terms are not enough there (2e-5 of a fixed decay's gradient at 1100 tokens): Z'
-// and, for O1, R take three each, which is all of fp32 (states 1e-7, gradient 1e-6),
-// for a fifth more time. Z' is then made for 64 tokens at a time, and z has one tile.
+// and, for O1, R take three each, which is all of fp32 (states 1e-7, gradient 1e-6).
+// A chunk then takes ~7000 cycles, against ~4000: shared memory has room for one tile
+// of z and Z' of 64 tokens at a time, so Z' is made by the mask's threads from rows of z
+// read ahead into registers (the state's threads, who round R meanwhile, were what the
+// rest waited for), the first term of R and the others sit side by side in one N = 128
+// product, and the result leaves through z's tile (396 -> 368 us for all gradients of
+// 4 x 4096 x 16 x 128).
 //
 // Only R_{n+1} <- R_n is a chain, and it holds no product: P of any chunk can be
 // ready before R is. A and O1 are issued by one warp, P and O2 by another: the
@@ -60,8 +65,8 @@ struct Walk {
   bool chained;                    // it is the slot of this segment's edge
   int row_step, col_step;          // its elements between rows (W) and columns (z)
   float* end;                      // last state [B * H, W, nz], or null
-  const __nv_bfloat16* partner;    // FINE: rows whose dot product with the result is wanted
-  long long partner_stride;
+  const __nv_bfloat16 *z, *partner;   // FINE: z itself, and the rows whose dot product with
+  long long z_stride, partner_stride;   // the result is wanted
   float* flow;                     // [slices, B * H, T], that product
 };
 
@@ -69,11 +74,13 @@ constexpr int kThreads = 512;   // 3 x 128: mask, state, read-out; products (2);
 constexpr uint32_t kCols = 512;
 
 // Tensor-memory columns of chunk n: two buffers of A, whose columns 0..63 take
-// A . D as bf16 and 64..127 O2 once A has been read, two of O1, and P.
+// A . D as bf16 and 64..127 O2 once A has been read, two of O1 (FINE: one, with 64
+// columns for the first term of R and 64 for the others), and P.
+template <bool FINE>
 struct Cols {
   __device__ static uint32_t A(int n) { return (n & 1) * 128; }
   __device__ static uint32_t O2(int n) { return A(n) + 64; }
-  __device__ static uint32_t O1(int n) { return 256 + (n & 1) * 64; }
+  __device__ static uint32_t O1(int n) { return 256 + (FINE ? 0 : (n & 1) * 64); }
   static constexpr uint32_t P = 384;
 };
 
@@ -84,7 +91,8 @@ enum : uint32_t {   // mbarriers, each a pair for even and odd chunks
   bSplit = 14,                               // (FINE: Z' of tokens 0..63 and 64..127)
   bGates = 20, bGFree = 24,                  // a ring of four (FINE: two) chunks' gates
   bEnd = 28, bMP0 = 30,                      // (P of tokens 0..63 complete)
-  kBars = 32
+  bAdd = 32,                                 // (FINE: P read)
+  kBars = 34
 };
 
 constexpr uint32_t kHalf = kTile / 2;   // 64 rows of 64 bf16 columns
@@ -104,9 +112,10 @@ struct WalkSmem {
 template <int W, bool REV, bool FINE>
 __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& sp, const Walk& w,
                                          const CUtensorMap* tx, const CUtensorMap* ty,
-                                         const CUtensorMap* tz, int seg, int slice, int bh) {
+                                         const CUtensorMap* tz, const CUtensorMap* tout, int seg,
+                                         int slice, int bh) {
   using L = WalkSmem<W, FINE>;
-  using C = Cols;
+  using C = Cols<FINE>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -127,13 +136,13 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     return *reinterpret_cast<Gates*>(smem + L::oGates + (n & (kRing - 1)) * sizeof(Gates));
   };
   auto zslot = [](int n) { return FINE ? 0u : static_cast<uint32_t>(n & 1) * kTile; };
-
   if (warp == 13) tc::tmem_alloc(smem_u32(slot), kCols);
   if (tid == 0) {
     for (uint32_t i = 0; i < kBars; ++i) {
       uint32_t count = i < bZ ? 2 : 1;   // x and y land on one barrier
-      if (i >= bMask && i < bGates) count = i == bSplit || i == bSplit + 1 ? 8 : 4;   // warps
+      if (i >= bMask && i < bGates) count = !FINE && (i == bSplit || i == bSplit + 1) ? 8 : 4;   // warps
       if (i >= bGFree && i < bEnd) count = 8;
+      if (i >= bAdd) count = 4;
       tc::mbar_init(sb + L::oBar + 8 * i, count);
     }
     *abort_flag = 0;
@@ -161,37 +170,63 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     tc::tma_load_4d(sb + L::oZ + zslot(n), tz, 64 * slice, h / (a.H / w.z_heads), at(n), b,
                     bar(bZ, n));
   };
-  // Z' by the state's and the read-out's 256 threads; its last reader is the P before.
-  // FINE: tokens 64 half .. + 63, a quarter of a row each. Else half the columns of
-  // this lane's token, the caller having waited for P(n - 1).
+  // Z' by the state's and the read-out's 256 threads, half the columns of this lane's
+  // token each, the caller having waited for P(n - 1), its last reader.
   auto split = [&](int n, int half) {
-    if (!FINE || half == 0) {
+    if (!warp_wait(bar4(bGates, n), par4(n), abort_flag) ||
+        !warp_wait(bar(bZ, n), par(n), abort_flag))
+      return false;
+    const Gates& g = gates(n);
+    const float f = REV ? a.scale * g.head[row] : g.tail[row];
+#pragma unroll 1
+    for (int c = 4 * half; c < 4 * half + 4; c += 2)
+      split_row<2>(sb + L::oZ + zslot(n), sb + L::oSplit, kTile, row, c, f);
+    tc::fence_proxy_async();
+    warp_arrive(bar(bSplit, n));
+    return true;
+  };
+  // FINE: by the mask's threads, tokens 64 half .. + 63, a quarter of a row at a time, from
+  // registers that were filled a half ahead (through the one z tile Z' would wait for the
+  // O2 before and a load).
+  uint4 zr[2][2];
+  auto fetch = [&](int n, int half, int set) {
+    const int t = at(n) + 64 * half + 32 * set + (tid >> 2);
+    const uint4* p = reinterpret_cast<const uint4*>(
+        w.z + static_cast<long long>(tok + t) * w.z_stride + (h / (a.H / w.z_heads)) * w.nz +
+        64 * slice + 16 * (tid & 3));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      zr[set][i] = n < cnt && t < t1 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+  };
+  auto split_half = [&](int n, int half) {
+    if (half == 0) {
       if (!warp_wait(bar4(bGates, n), par4(n), abort_flag) ||
-          !warp_wait(bar(bZ, n), par(n), abort_flag) ||
-          (FINE && n > 0 && !warp_wait(bar(bMP, n - 1), par(n - 1), abort_flag)))
+          (n > 0 && !warp_wait(bar(bMP, n - 1), par(n - 1), abort_flag)))
         return false;
     } else if (!warp_wait(sb + L::oBar + 8 * (bMP0 + (n & 1)), par(n), abort_flag)) {
       return false;
     }
     const Gates& g = gates(n);
-    const int to = FINE ? tid & 63 : row, r = FINE ? 64 * half + to : row;
-    const float f = REV ? a.scale * g.head[r] : g.tail[r];
-    if (FINE) {
-      split_row<3>(sb + L::oZ + zslot(n), sb + L::oSplit, kHalf, r, to, 2 * ((tid >> 6) & 3), f);
-    } else {
-#pragma unroll 1
-      for (int c = 4 * half; c < 4 * half + 4; c += 2)
-        split_row<2>(sb + L::oZ + zslot(n), sb + L::oSplit, kTile, r, r, c, f);
+#pragma unroll
+    for (int set = 0; set < 2; ++set) {
+      const int to = 32 * set + (tid >> 2), r = 64 * half + to;
+      split_pair<3>(zr[set], sb + L::oSplit, kHalf, to, 2 * (tid & 3),
+                    REV ? a.scale * g.head[r] : g.tail[r]);
+      fetch(n + half, half ^ 1, set);
     }
     tc::fence_proxy_async();
-    warp_arrive(sb + L::oBar + 8 * (bSplit + (FINE ? half : n & 1)));
+    warp_arrive(sb + L::oBar + 8 * (bSplit + half));
     return true;
   };
 
   if (warp < 4) {
     // ---------------------------------------------- A . D, one token per lane
+    if (FINE) {
+      fetch(0, 0, 0);
+      fetch(0, 0, 1);
+    }
     for (int n = 0; n < cnt; ++n) {
-      const bool ok = warp_wait(bar4(bGates, n), par4(n), abort_flag) &&
+      bool ok = warp_wait(bar4(bGates, n), par4(n), abort_flag) &&
                 warp_wait(bar(bMA, n), par(n), abort_flag);
       if (!ok) break;
       tc::fence_after_sync();
@@ -239,6 +274,11 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
       tc::tmem_st_wait();
       tc::fence_before_sync();
       warp_arrive(bar(bMask, n));
+      if (FINE) {
+#pragma unroll 1
+        for (int half = 0; ok && half < 2; ++half) ok = split_half(n, half);
+        if (!ok) break;
+      }
     }
   } else if (warp < 8) {
     // ---------------------------------------------- the state, one row per lane, and
@@ -251,26 +291,40 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
                                       static_cast<size_t>(64 * slice) * w.col_step
                                 : nullptr,
              w.col_step);
-    if (mine) round_row<FINE>(sb + L::oR, L::kR, row, R);
-    tc::fence_proxy_async();
-    warp_arrive(bar(bState, 0));
-    bool ok = split(0, 0) && (!FINE || split(0, 1));
-    for (int n = 0; ok && n < cnt; ++n) {
-      ok = warp_wait(bar(bMP, n), par(n), abort_flag);
-      if (!ok) break;
+    bool ok = true;
+    auto publish = [&](int n) {   // R as an operand of O1(n)
+      if (mine) round_row<FINE>(sb + L::oR, L::kR, row, R);
+      tc::fence_proxy_async();
+      warp_arrive(bar(bState, n));
+    };
+    auto add = [&](int n) {
+      if (!warp_wait(bar(bMP, n), par(n), abort_flag)) return false;
       tc::fence_after_sync();
       const float all = gates(n).all;
       warp_arrive(bar4(bGFree, n));
       if (mine || W == 128) add_state(R, all, tl + C::P);
       tc::fence_before_sync();
-      if (n + 1 < cnt) {
+      if (FINE) warp_arrive(bar(bAdd, n));
+      return true;
+    };
+    // (one copy of each step in the loops: the roles' code together is more than the
+    // instruction cache holds as it is)
+    if constexpr (FINE) {
+#pragma unroll 1
+      for (int n = 0; ok && n < cnt; ++n) {
+        if (n > 0) ok = warp_wait(bar(bMO1, n - 1), par(n - 1), abort_flag);   // has read R
+        if (!ok) break;
+        publish(n);
+        ok = add(n);
+      }
+    } else {
+      publish(0);
+      ok = split(0, 0);
+      for (int n = 0; ok && n < cnt; ++n) {
+        ok = add(n);
+        if (!ok || n + 1 == cnt) break;
         ok = split(n + 1, 0) && warp_wait(bar(bMO1, n), par(n), abort_flag);   // R_n has been read
-        if (ok) {
-          if (mine) round_row<FINE>(sb + L::oR, L::kR, row, R);
-          tc::fence_proxy_async();
-          warp_arrive(bar(bState, n + 1));
-          if (FINE) ok = split(n + 1, 1);
-        }
+        if (ok) publish(n + 1);
       }
     }
     if (ok && mine && w.end && seg == (REV ? 0 : sp.segments - 1))
@@ -285,13 +339,11 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
       const bool live = t < t1;
       uint4 pr[FINE ? 8 : 1];
       if (FINE) {   // the partner's row, on its way while the products run
-        const __nv_bfloat16* p = w.partner + static_cast<long long>(tok + t) * w.partner_stride +
-                                 (h / (a.H / w.z_heads)) * w.nz + 64 * slice;
+        const uint4* p = reinterpret_cast<const uint4*>(
+            w.partner + static_cast<long long>(tok + t) * w.partner_stride +
+            (h / (a.H / w.z_heads)) * w.nz + 64 * slice);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          pr[i] = live ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
-        // one z tile: its last reader O2(n - 1) was waited for below
-        ok = split(n, 0) && split(n, 1);
+        for (int i = 0; i < 8; ++i) pr[i] = live ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
       } else if (n + 1 < cnt) {
         ok = warp_wait(bar(bMP, n), par(n), abort_flag) && split(n + 1, 1);
       }
@@ -303,46 +355,77 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
       warp_arrive(bar4(bGFree, n));
       const F2 ff = pack2(f, f), ss = pack2(a.scale, a.scale);
       const size_t to = ((tok + t) * a.H + h) * static_cast<size_t>(w.nz) + 64 * slice;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w.out) + to);
+      // FINE: the row goes out through z's tile, which O2 has read last. Else it is stored
+      // from here, two lanes on 32 bytes of one row: what two rows' lanes hold is
+      // exchanged first (16 bytes to each of 32 rows take the SM twice as long, and z's or
+      // x's tile is asked for too soon to wait for a store: 70 -> 81 us)
+      const uint32_t tile = sb + L::oZ + row * 128;
+      const uint32_t odd = lane & 1;
+      const size_t pitch = static_cast<size_t>(a.H) * w.nz;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(w.out) + to - (odd ? pitch : 0) + 8 * odd;
+      const bool live0 = t - static_cast<int>(odd) < t1, live1 = t + 1 - static_cast<int>(odd) < t1;
       F2 dot = pack2(0.f, 0.f);
-      auto quarter = [&](int p, const uint4* q) {
+#pragma unroll 1
+      for (int p = 0; p < 4; ++p) {
         float x[16], z[16];
-        tmem_ld16x2(tl + C::O1(n) + 16 * p, tl + C::O2(n) + 16 * p, x, z);
+        if (FINE) {
+          tmem_ld16x2(tl + C::O1(n) + 16 * p, tl + C::O1(n) + 64 + 16 * p, x, z);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] += z[i];
+          tc::tmem_ld16(tl + C::O2(n) + 16 * p, z);
+        } else {
+          tmem_ld16x2(tl + C::O1(n) + 16 * p, tl + C::O2(n) + 16 * p, x, z);
+        }
         F2 y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           y[i] = fma2(ff, pack2(x[2 * i], x[2 * i + 1]),
                       mul2(ss, pack2(z[2 * i], z[2 * i + 1])));
         if (FINE) {
-          const uint32_t v[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+          const uint32_t v[8] = {pr[0].x, pr[0].y, pr[0].z, pr[0].w,
+                                 pr[1].x, pr[1].y, pr[1].z, pr[1].w};
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             dot = fma2(pack2(x[2 * i], x[2 * i + 1]), widen2(v[i]), dot);
+#pragma unroll
+          for (int i = 0; i < 6; ++i) pr[i] = pr[i + 2];   // (the loop stays rolled)
           if (w.part) {
             if (live) {
               ulonglong2* d = reinterpret_cast<ulonglong2*>(w.part + to + 16 * p);
 #pragma unroll
               for (int i = 0; i < 4; ++i) d[i] = make_ulonglong2(y[2 * i], y[2 * i + 1]);
             }
-            return;
+            continue;
           }
         }
-        if (live) {
-          dst[2 * p] = make_uint4(round2(y[0]), round2(y[1]), round2(y[2]), round2(y[3]));
-          dst[2 * p + 1] = make_uint4(round2(y[4]), round2(y[5]), round2(y[6]), round2(y[7]));
-        }
-      };
-      if constexpr (FINE) {
+        uint32_t u[2][4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) quarter(p, pr + 2 * p);
+        for (int i = 0; i < 8; ++i) u[i >> 2][i & 3] = round2(y[i]);
+        if (FINE) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) sts4(tile + (((2 * p + i) ^ (row & 7)) << 4), u[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? u[0][i] : u[1][i], 1);
+            u[0][i] = odd ? other : u[0][i];
+            u[1][i] = odd ? u[1][i] : other;
+          }
+          if (live0)
+            *reinterpret_cast<uint4*>(dst + 16 * p) =
+                make_uint4(u[0][0], u[0][1], u[0][2], u[0][3]);
+          if (live1)
+            *reinterpret_cast<uint4*>(dst + pitch + 16 * p) =
+                make_uint4(u[1][0], u[1][1], u[1][2], u[1][3]);
+        }
+      }
+      if (FINE) {
         float d0, d1;
         unpack2(dot, d0, d1);
         if (live)
           w.flow[(static_cast<size_t>(slice) * a.B * a.H + bh) * a.T + t] = f * (d0 + d1);
-      } else {
-#pragma unroll 1
-        for (int p = 0; p < 4; ++p) quarter(p, nullptr);
       }
+      if (FINE) tc::fence_proxy_async();
       tc::fence_before_sync();
       warp_arrive(bar(bFree, n));
     }
@@ -358,11 +441,11 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     auto rows = [](int k0) { return static_cast<uint64_t>(k0 * 128) >> 4; };
     uint32_t end = sb + L::oBar + 8 * bEnd;
     if (warp == 12) {
-      const uint64_t dR = tc::smem_desc(sb + L::oR, 16, 1024);
-      for (int n = 0; n < cnt; ++n) {
-        if (!warp_wait(bar(bXY, n), par(n), abort_flag)) break;
-        // the read-out of chunk n - 2 frees the buffers of A and O1
-        if (n >= 2 && !warp_wait(bar(bFree, n), par(n - 2), abort_flag)) break;
+      const uint64_t dR = tc::smem_desc(sb + L::oR, FINE ? L::kR : 16, 1024);
+      const uint64_t dR3 = tc::smem_desc(sb + L::oR + 2 * L::kR, 16, 1024);
+      constexpr uint32_t idR = tc::idesc_bf16(128, FINE ? 128 : 64, 0, 1);
+      auto products_a = [&](int n) {
+        if (!warp_wait(bar(bXY, n), par(n), abort_flag)) return false;
         tc::fence_after_sync();
         const uint64_t dx = tc::smem_desc(sb + L::oX + (n & 1) * L::kWide, 16, 1024);
         const uint64_t dy = tc::smem_desc(sb + L::oY + (n & 1) * L::kWide, 16, 1024);
@@ -370,15 +453,27 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
         for (int k0 = 0; k0 < W; k0 += 16)
           mma_if(go, tm + C::A(n), dx + kmaj(k0), dy + kmaj(k0), idA, k0 > 0);
         commit_if(go, bar(bMA, n));
+        return true;
+      };
+      for (int n = FINE ? -1 : 0; n < cnt; ++n) {
+        // the read-out frees the buffers of A and O1: of chunk n - 2 for this one's, or
+        // (FINE, the one buffer of O1 and the next chunk's A, which the longer way
+        // through the mask to Z' waits for) of chunk n - 1
+        const int freed = FINE ? n - 1 : n - 2;
+        if (freed >= 0 && !warp_wait(bar(bFree, freed), par(freed), abort_flag)) break;
+        if (FINE) {
+          if (n + 1 < cnt && !products_a(n + 1)) break;
+          if (n < 0) continue;
+        } else if (!products_a(n)) {
+          break;
+        }
         if (!warp_wait(bar(bState, n), par(n), abort_flag)) break;
         tc::fence_after_sync();
+        const uint64_t dx = tc::smem_desc(sb + L::oX + (n & 1) * L::kWide, 16, 1024);
 #pragma unroll 1
-        for (int k0 = 0; k0 < W; k0 += 16)
-          mma_if(go, tm + C::O1(n), dx + kmaj(k0), dR + rows(k0), idO, k0 > 0);
-        if (FINE) {
-#pragma unroll 1
-          for (int k0 = 0; k0 < 2 * W; k0 += 16)   // the other two terms
-            mma_if(go, tm + C::O1(n), dx + kmaj(k0 & (W - 1)), dR + (L::kR >> 4) + rows(k0), idO, 1);
+        for (int k0 = 0; k0 < W; k0 += 16) {
+          mma_if(go, tm + C::O1(n), dx + kmaj(k0), dR + rows(k0), idR, k0 > 0);
+          if (FINE) mma_if(go, tm + C::O1(n) + 64, dx + kmaj(k0), dR3 + rows(k0), idO, 1);
         }
         commit_if(go, bar(bMO1, n));
       }
@@ -396,6 +491,7 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             ok = warp_wait(sb + L::oBar + 8 * (bSplit + half), n & 1, abort_flag);
+            if (ok && half == 0 && n > 0) ok = warp_wait(bar(bAdd, n - 1), par(n - 1), abort_flag);
             if (!ok) break;
             tc::fence_after_sync();
 #pragma unroll 1
@@ -417,6 +513,7 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
         }
         if (!warp_wait(bar(bMask, n), par(n), abort_flag)) break;
         tc::fence_after_sync();
+        if (FINE && !warp_wait(bar(bZ, n), par(n), abort_flag)) break;
         const uint64_t dz = tc::smem_desc(sb + L::oZ + zslot(n), 16, 1024);
 #pragma unroll 1
         for (int k0 = 0; k0 < kC; k0 += 16)
@@ -433,28 +530,34 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     // tile was asked for a third of a chunk later and waited for)
     if (lane == 0) {
       constexpr int kAhead = FINE ? 1 : 2;   // z tiles
-      auto soon = [&](int n) {   // FINE: the z tile after the next comes into L2 meanwhile
-        if (FINE && n < cnt) tc::tma_prefetch_4d(tz, 64 * slice, h / (a.H / w.z_heads), at(n), b);
-      };
       int nx = 0, ny = 0, nz = 0;   // tiles requested
       for (; nx < min(2, cnt); ++nx, ++ny) {
         load_x(nx);
         load_y(ny);
       }
       for (; nz < min(kAhead, cnt); ++nz) load_z(nz);
-      soon(1);
-      for (int n = 0; n + kAhead < cnt; ++n) {
+      for (int n = 0; n < cnt; ++n) {
         if (n + 2 < cnt) {
           if (!wait(bar(bMO1, n), par(n), abort_flag)) break;   // (its warp issued A first)
           load_x(nx++);
           if (!wait(bar(bMP, n), par(n), abort_flag) || !wait(bar(bMA, n), par(n), abort_flag)) break;
           load_y(ny++);
         }
-        // O2(n) follows P(n), which waited for Z'(n): z's readers are done
-        if (!wait(bar(bMO2, n), par(n), abort_flag)) break;
-        load_z(nz++);
-        soon(n + 2);
+        if (FINE) {
+          // z's tile holds the result now; tokens past the sequence's end are not written
+          if (!wait(bar(bFree, n), par(n), abort_flag)) break;
+          if (!w.part) {
+            tc::tma_store_4d(tout, 64 * slice, h, at(n), b, sb + L::oZ);
+            tc::bulk_commit();
+            tc::bulk_wait_read<0>();
+          }
+        } else if (n + 2 < cnt) {
+          // O2(n) follows P(n), which waited for Z'(n): z's readers are done
+          if (!wait(bar(bMO2, n), par(n), abort_flag)) break;
+        }
+        if (n + kAhead < cnt) load_z(nz++);
       }
+      if (FINE) tc::bulk_wait_all<0>();
       // no copy may outlive the CTA, whatever gave up (x and y of a chunk share a
       // barrier: an x left alone by an abort gets its y, so that it completes)
       if (ny < nx) load_y(ny);
@@ -507,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
                  const __grid_constant__ CUtensorMap tz) {
   const int slices = w.nz / 64;
-  walk_cta<W, false, false>(a, sp, w, &tx, &ty, &tz, blockIdx.x / slices, blockIdx.x % slices,
+  walk_cta<W, false, false>(a, sp, w, &tx, &ty, &tz, nullptr, blockIdx.x / slices, blockIdx.x % slices,
                             blockIdx.y);
 }
 
@@ -583,7 +686,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
 #pragma unroll 1
     for (int c = 4 * half; c < 4 * half + 4; c += 2)
       split_row<TERMS>(sb + (n % kStStages) * L::kStage + L::kWide,
-                       sb + L::oSplit + (n & 1) * TERMS * kTile, kTile, row, row, c, f);
+                       sb + L::oSplit + (n & 1) * TERMS * kTile, kTile, row, c, f);
     tc::fence_proxy_async();
     warp_arrive(bar2(sSplit, n));
     return true;
@@ -905,7 +1008,8 @@ template <int NK, int NV>
 __global__ void __launch_bounds__(kThreads, 1)
     decay_bwd_tc(const DecayArgs a, const DecaySplit sp, const Walks w,
                  const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to) {
+                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+                 const __grid_constant__ CUtensorMap tdq, const __grid_constant__ CUtensorMap tdk) {
   const int x = blockIdx.x, bh = blockIdx.y;
   if (blockIdx.z >= 3) {
     const int plane = gridDim.x * gridDim.y;
@@ -916,11 +1020,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int slices = (blockIdx.z == 2 ? NV : NK) / 64;
   if (x >= sp.segments * slices) return;   // the other width has more slices
   if (blockIdx.z == 0)
-    walk_cta<NV, false, true>(a, sp, w.dq, &to, &tv, &tk, x / slices, x % slices, bh);
+    walk_cta<NV, false, true>(a, sp, w.dq, &to, &tv, &tk, &tdq, x / slices, x % slices, bh);
   else if (blockIdx.z == 1)
-    walk_cta<NV, true, true>(a, sp, w.dk, &tv, &to, &tq, x / slices, x % slices, bh);
+    walk_cta<NV, true, true>(a, sp, w.dk, &tv, &to, &tq, &tdk, x / slices, x % slices, bh);
   else
-    walk_cta<NK, true, false>(a, sp, w.dv, &tk, &tq, &to, x / slices, x % slices, bh);
+    walk_cta<NK, true, false>(a, sp, w.dv, &tk, &tq, &to, nullptr, x / slices, x % slices, bh);
 }
 
 template <class Kern>
@@ -993,8 +1097,10 @@ cudaError_t bwd(const DecayArgs& a, const DecaySplit& sp, const Walks& w, const 
                      lc = PairSmem<NK, NV>::launch, lab = la > lb ? la : lb,
                      bytes = lab > lc ? lab : lc;
   static_assert(bytes <= 232448, "shared memory budget of one CTA");
-  CUtensorMap tq, tk, tv, to;
-  if (!map_of(&tq, a, q) || !map_of(&tk, a, k) || !map_of(&tv, a, v) || !map_of(&to, a, dO))
+  CUtensorMap tq, tk, tv, to, tdq, tdk;
+  // (the maps of shared heads' gradients are not used: those leave as `part`)
+  if (!map_of(&tq, a, q) || !map_of(&tk, a, k) || !map_of(&tv, a, v) || !map_of(&to, a, dO) ||
+      !map_of(&tdq, a, {a.dq, a.Hk, NK, static_cast<long long>(a.Hk) * NK}) || !map_of(&tdk, a, {a.dk, a.Hk, NK, static_cast<long long>(a.Hk) * NK}))
     return cudaErrorInvalidValue;
   const cudaError_t err = opt_in(decay_bwd_tc<NK, NV>, bytes);
   if (err != cudaSuccess) return err;
@@ -1003,7 +1109,7 @@ cudaError_t bwd(const DecayArgs& a, const DecaySplit& sp, const Walks& w, const 
   const long long jobs = static_cast<long long>(a.B) * a.H * ((a.T + kC - 1) / kC);
   const int planes = static_cast<int>(std::max(1LL, std::min(16LL, jobs / (4 * ctas))));
   decay_bwd_tc<NK, NV><<<dim3(sp.segments * slices, a.B * a.H, 3 + planes), kThreads, bytes, stream>>>(
-      a, sp, w, tq, tk, tv, to);
+      a, sp, w, tq, tk, tv, to, tdq, tdk);
   return cudaGetLastError();
 }
 
@@ -1025,16 +1131,16 @@ cudaError_t launch_decay_bwd_tc(const DecayArgs& a, const DecaySplit& sp, cudaSt
       dO{a.dO, a.H, a.nv, static_cast<long long>(a.H) * a.nv};
   Walks w;
   w.dq = from(a, sp, false, true);
+  w.dk = from(a, sp, true, true);
   w.dq.out = a.dq;
   w.dq.part = sp.dq_part;
-  w.dq.partner = static_cast<const __nv_bfloat16*>(a.q);
-  w.dq.partner_stride = a.sq;
+  w.dq.z = w.dk.partner = static_cast<const __nv_bfloat16*>(a.k);
+  w.dq.z_stride = w.dk.partner_stride = a.sk;
+  w.dk.z = w.dq.partner = static_cast<const __nv_bfloat16*>(a.q);
+  w.dk.z_stride = w.dq.partner_stride = a.sq;
   w.dq.flow = sp.from;
-  w.dk = from(a, sp, true, true);
   w.dk.out = a.dk;
   w.dk.part = sp.dk_part;
-  w.dk.partner = static_cast<const __nv_bfloat16*>(a.k);
-  w.dk.partner_stride = a.sk;
   w.dk.flow = sp.to;
   for (Walk* p : {&w.dq, &w.dk}) {   // dO, v, k and v, dO, q
     p->x_heads = p->y_heads = a.H;

@@ -253,16 +253,13 @@ __device__ __forceinline__ Terms terms_of(F2 x) {
   return t;
 }
 
-// Two chunks (16 columns from column 8 c) of row `r` of a tile with 64 bf16 columns,
-// times f, as rows `to` of TERMS tiles `apart` bytes from one another: two leave
-// 2.4e-6 of the state they feed, three 1e-7.
+// Two pieces of 16 bytes (16 columns from column 8 c) times f, into row `r` of TERMS
+// tiles `apart` bytes from one another: two leave 2.4e-6 of the state they feed,
+// three 1e-7.
 template <int TERMS>
-__device__ __forceinline__ void split_row(uint32_t src, uint32_t dst, uint32_t apart, int r, int to,
-                                          int c, float f) {
+__device__ __forceinline__ void split_pair(const uint4 (&u)[2], uint32_t dst, uint32_t apart, int r,
+                                           int c, float f) {
   const F2 ff = pack2(f, f);
-  uint4 u[2];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) u[p] = lds4(src + r * 128 + (((c + p) ^ (r & 7)) << 4));
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const uint32_t w[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
@@ -274,11 +271,20 @@ __device__ __forceinline__ void split_row(uint32_t src, uint32_t dst, uint32_t a
       mid[i] = t.mid;
       lo[i] = t.lo;
     }
-    const uint32_t d = dst + to * 128 + (((c + p) ^ (to & 7)) << 4);
+    const uint32_t d = dst + r * 128 + (((c + p) ^ (r & 7)) << 4);
     sts4(d, hi);
     sts4(d + apart, mid);
     if (TERMS == 3) sts4(d + 2 * apart, lo);
   }
+}
+// The same from row `r` of a tile with 64 bf16 columns.
+template <int TERMS>
+__device__ __forceinline__ void split_row(uint32_t src, uint32_t dst, uint32_t apart, int r, int c,
+                                          float f) {
+  uint4 u[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) u[p] = lds4(src + r * 128 + (((c + p) ^ (r & 7)) << 4));
+  split_pair<TERMS>(u, dst, apart, r, c, f);
 }
 
 // 64 fp32 values as one row of a swizzled bf16 tile with 128-byte rows; with ALL as
