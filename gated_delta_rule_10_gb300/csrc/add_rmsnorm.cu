@@ -12,8 +12,8 @@
 // 512), at most kVec vectors of 8 columns per thread. The CTAs are persistent and
 // walk the rows; the next row's vectors are requested before the current row's
 // sums are taken, so that loads are in flight through the barriers and the stores
-// (without: 334 us, 0.83 of measured HBM, for 65536 x 4096 to 8 bits). The weight
-// stays in registers over all rows.
+// (without: 334 us; with: 295 us, 0.94 of measured HBM, for 65536 x 4096 to 8 bits).
+// The weight stays in registers over all rows.
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -168,9 +168,13 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 768 / threads
 
 // dx, and the weight's gradient of this CTA's rows as one row of `partial`. Each
 // thread keeps its columns' sums in registers over all its rows; the CTA's row
-// groups add theirs through shared memory at the end, in a fixed order.
+// groups add theirs through shared memory at the end, in a fixed order. 512 threads of
+// 128 registers an SM, which the grid counts on: with the ~150 that the compiler took by
+// itself a quarter of the CTAs ran as a second wave (59 -> 51 us, 0.78 of measured HBM,
+// for 16384 x 2048 bf16; ~5 of them are the second launch, which adds up the CTAs' rows).
 template <typename T, int TPR, int VEC>
-__global__ void __launch_bounds__(threads<TPR>()) add_rmsnorm_bwd_kernel(const AddNormBwdArgs a) {
+__global__ void __launch_bounds__(threads<TPR>(), 512 / threads<TPR>())
+    add_rmsnorm_bwd_kernel(const AddNormBwdArgs a) {
   constexpr int kThreads = threads<TPR>(), kRows = kThreads / TPR;
   __shared__ float2 red[2][16];
   __shared__ float sums[kRows > 1 ? kThreads * 8 : 1];
@@ -208,22 +212,22 @@ __global__ void __launch_bounds__(threads<TPR>()) add_rmsnorm_bwd_kernel(const A
   const long long r0 = static_cast<long long>(blockIdx.x) * kRows;
 #pragma unroll
   for (int k = 0; k < kDepth; ++k) fetch(buf[k], r0 + sub + k * step);
+  // (the row is widened once for its sums and once more for its output: as floats in
+  // between it would not leave 128 registers for four rows of 2048 columns in flight)
   auto work = [&](Row& f, long long row, int parity) {
     const bool live = row < a.rows;
-    float x[VEC][8], dy[VEC][8], d[VEC][8];
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      f.x[i].get(x[i]);
-      f.y[i].get(dy[i]);
-      f.d[i].get(d[i]);
+      float x[8], dy[8];
+      f.x[i].get(x);
+      f.y[i].get(dy);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        ss = fmaf(x[i][j], x[i][j], ss);
-        dot = fmaf(w[i][j] * dy[i][j], x[i][j], dot);
+        ss = fmaf(x[j], x[j], ss);
+        dot = fmaf(w[i][j] * dy[j], x[j], dot);
       }
     }
-    fetch(f, row + kDepth * step);
     row_sum<TPR>(ss, dot, red, parity);
     const float n = static_cast<float>(a.D);
     const float inv = rsqrtf(ss / n + a.eps);
@@ -232,13 +236,18 @@ __global__ void __launch_bounds__(threads<TPR>()) add_rmsnorm_bwd_kernel(const A
     for (int i = 0; i < VEC; ++i) {
       const int c = lane + i * TPR;
       if (!(live && c < nv)) continue;
+      float x[8], dy[8], d[8];
+      f.x[i].get(x);
+      f.y[i].get(dy);
+      f.d[i].get(d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dw[i][j] = fmaf(dy[i][j], x[i][j] * inv, dw[i][j]);
-        d[i][j] += inv * (w[i][j] * dy[i][j] - x[i][j] * m);
+        dw[i][j] = fmaf(dy[j], x[j] * inv, dw[i][j]);
+        d[j] += inv * (w[i][j] * dy[j] - x[j] * m);
       }
-      store8(static_cast<T*>(a.dx) + row * a.D + 8 * c, d[i]);
+      store8(static_cast<T*>(a.dx) + row * a.D + 8 * c, d);
     }
+    fetch(f, row + kDepth * step);
   };
   for (long long r = r0; r < a.rows; r += 2 * step) {
     work(buf[0], r + sub, 0);
