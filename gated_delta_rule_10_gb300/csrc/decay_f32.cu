@@ -124,7 +124,7 @@ struct Gates {
   float head[kC];         // e^{G_r}, 0 once a token of the chunk has cleared the state
   float tail[kC];         // e^{G_C - G_i}, 0 if a later token clears
   int cut[kC];            // last clearing token at or before r, -1: none
-  float all;              // e^{G_C}
+  float sum;              // G_C, minus infinity if a token clears
   __device__ __forceinline__ float between(int r, int i) const {
     return i <= r && i >= cut[r] ? expf((hi[r] - hi[i]) + (lo[r] - lo[i])) : 0.f;
   }
@@ -177,7 +177,7 @@ __device__ void load_gates(Gates& s, const DecayArgs& a, int b, int h, int t0, i
     s.head[r] = cut < 0 ? expf(static_cast<float>(G)) : 0.f;
     s.tail[r] = lt <= r ? expf(static_cast<float>(total - G)) : 0.f;
   }
-  if (lane == 0) s.all = lt < 0 ? expf(static_cast<float>(total)) : 0.f;
+  if (lane == 0) s.sum = lt < 0 ? static_cast<float>(total) : -INFINITY;
 }
 
 // Rows [t0, t0 + n) of one head into a 64 x W tile, zeros past n.
@@ -224,12 +224,13 @@ __device__ void store_state(const float* S, float* dst) {
     dst[i] = S[(i / NV) * (NV + 4) + i % NV];
 }
 
-// S = all * S + X^T Y over the chunk's tokens (X: 64 x NK, Y: 64 x NV, one of
+// S = e^sum S + X^T Y over the chunk's tokens (X: 64 x NK, Y: 64 x NV, one of
 // them scaled by the caller)
 template <int NK, int NV>
-__device__ __forceinline__ void update_state(float* S, float all, const float* X, const float* Y) {
+__device__ __forceinline__ void update_state(float* S, float sum, const float* X, const float* Y) {
   Acc<NK, NV> acc;
-  acc.each([&](int r, int c, float& x) { x = all * S[r * (NV + 4) + c]; });
+  const float d = decay_code(sum);
+  acc.each([&](int r, int c, float& x) { x = decayed(d, S[r * (NV + 4) + c], 0.f); });
   acc.template mul<kC>(View{X, 1, NK + 4}, View{Y, NV + 4, 1});
   acc.each([&](int r, int c, float& x) { S[r * (NV + 4) + c] = x; });
 }
@@ -239,7 +240,7 @@ __device__ __forceinline__ void scale_rows(float* X, const float* f) {
 }
 
 // Local end state of every piece from a zero state (REV: the gradient of its
-// start state from a zero gradient at its end), and the product of its decays.
+// start state from a zero gradient at its end), and its decay.
 template <int NK, int NV, bool REV>
 __global__ void __launch_bounds__(kThreads, 1) states_f32(const DecayArgs a, const DecaySplit sp) {
   extern __shared__ __align__(16) float sm[];
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_f32(const DecayArgs a, con
   const Where w = where(a, sp.piece_len, seg);
   const int hk = w.h / (a.H / a.Hk);
   load_state<NK, NV>(S, nullptr);
-  float prod = 1.f;
+  float sum = 0.f;
   const int chunks = (w.t1 - w.t0 + kC - 1) / kC;
   for (int i = 0; i < chunks; ++i) {
     const int t = w.t0 + (REV ? chunks - 1 - i : i) * kC, n = min(kC, w.t1 - t);
@@ -266,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) states_f32(const DecayArgs a, con
     __syncthreads();
     scale_rows<NV>(Y, REV ? gates.head : gates.tail);
     __syncthreads();
-    update_state<NK, NV>(S, gates.all, X, Y);
-    prod *= gates.all;
+    update_state<NK, NV>(S, gates.sum, X, Y);
+    sum += gates.sum;
   }
   __syncthreads();
   const int slot = REV ? seg : seg + 1;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_f32(const DecayArgs a, con
       dst[i] = a.scale * S[(i / NV) * (NV + 4) + i % NV];
   else
     store_state<NK, NV>(S, dst);
-  if (threadIdx.x == 0) sp.decay[static_cast<size_t>(w.bh) * sp.pieces + seg] = prod;
+  if (threadIdx.x == 0) sp.decay[static_cast<size_t>(w.bh) * sp.pieces + seg] = decay_code(sum);
 }
 
 template <int NK, int NV>
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_f32(const DecayArgs a, const 
     __syncthreads();
     scale_rows<NV>(V, gates.tail);
     __syncthreads();
-    update_state<NK, NV>(S, gates.all, K, V);
+    update_state<NK, NV>(S, gates.sum, K, V);
   }
   __syncthreads();
   if (a.hT && blockIdx.x == gridDim.x - 1)
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_f32(const DecayArgs a, const 
       __syncthreads();
       scale_rows<NV>(V, gates.tail);
       __syncthreads();
-      update_state<NK, NV>(S, gates.all, K, V);
+      update_state<NK, NV>(S, gates.sum, K, V);
       continue;
     }
     Acc<kC, kC> s;
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_f32(const DecayArgs a, const 
     __syncthreads();
     scale_rows<NV>(O, gates.head);
     __syncthreads();
-    update_state<NK, NV>(S, gates.all, Q, O);
+    update_state<NK, NV>(S, gates.sum, Q, O);
   }
   __syncthreads();
   if (rev && a.dh0 && blockIdx.x == 0) store_state<NK, NV>(S, a.dh0 + w.bh * st);

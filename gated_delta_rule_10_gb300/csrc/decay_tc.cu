@@ -694,23 +694,23 @@ __global__ void __launch_bounds__(kStThreads, 1)
   if (warp < 4) {
     float S[64];
     read_row(S, nullptr, 1);
-    float prod = 1.f;
+    float sum = 0.f;
     bool ok = split(0, 0);
     for (int n = 0; ok && n < cnt; ++n) {
       if (n + 1 < cnt) ok = split(n + 1, 0);
       if (ok) ok = warp_wait(bar2(sP, n), par(n), abort_flag);
       if (!ok) break;
       tc::fence_after_sync();
-      const float all = gates(n).all;
+      const float all = gates(n).all, add = gates(n).sum;
       warp_arrive(bar2(sGFree, n));
       if (mine || NK == 128) add_state(S, all, tl + (n & 1) * 128);
-      prod *= all;
+      sum += add;
       tc::fence_before_sync();
     }
     if (ok) {
       if (mine) write_row(S, REV ? a.scale : 1.f, dst + static_cast<size_t>(row) * a.nv);
       if (tid == 0 && slice == 0)   // (a piece of both walks: the same value twice)
-        sp.decay[static_cast<size_t>(bh) * sp.pieces + seg] = prod;
+        sp.decay[static_cast<size_t>(bh) * sp.pieces + seg] = decay_code(sum);
     }
   } else if (warp < 8) {
     for (int n = 0; n < cnt; ++n) {

@@ -27,8 +27,9 @@ struct Gates {
   float col[192];       // col[col_at(b) + i]: decay from after i through the end of block b-1
   float head[kC];       // decay from the chunk's start through r
   float tail[kC];       // decay from after i through the chunk's end
-  float all;            // decay of the whole chunk
-  float pad[3];
+  float sum;            // log of the whole chunk's decay
+  float all;            // that decay (decay_code)
+  float pad[2];
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -163,7 +164,10 @@ __device__ __forceinline__ void fill_gates(Gates& s, const float (&x)[4]) {
     s.tail[r] = exp_fast(e);
     pre += total[b];
   }
-  if (lane == 0) s.all = exp_fast(pre);
+  if (lane == 0) {
+    s.sum = pre;
+    s.all = decay_code(pre);
+  }
 }
 
 // Bounded mbarrier wait that also gives up once another role has aborted.
@@ -316,9 +320,11 @@ __device__ __forceinline__ void round_row(uint32_t dst, uint32_t apart, int r,
   }
 }
 
-// S = all * S + (hi + rest) from 128 accumulator columns [hi 64 | the other terms 64].
+// S = decay * S + (hi + rest), as decayed() does, two at a time, from 128 accumulator
+// columns [hi 64 | the other terms 64].
 __device__ __forceinline__ void add_state(float (&S)[64], float all, uint32_t taddr) {
-  const F2 g = pack2(all, all);
+  const float near = signbit(all) ? 1.f : 0.f;
+  const F2 g = pack2(all, all), c = pack2(near, near);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     float hi[16], lo[16];
@@ -326,7 +332,8 @@ __device__ __forceinline__ void add_state(float (&S)[64], float all, uint32_t ta
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
       float &a = S[16 * p + j], &b = S[16 * p + j + 1];
-      unpack2(fma2(g, pack2(a, b), add2(pack2(hi[j], hi[j + 1]), pack2(lo[j], lo[j + 1]))), a, b);
+      const F2 s = pack2(a, b), p2 = add2(pack2(hi[j], hi[j + 1]), pack2(lo[j], lo[j + 1]));
+      unpack2(fma2(g, s, fma2(c, s, p2)), a, b);
     }
   }
 }
