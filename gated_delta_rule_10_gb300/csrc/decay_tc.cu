@@ -43,6 +43,9 @@
 // 40 us for the products of 4 x 4096 x 16 x 128 alone). Each tile is loaded
 // again as soon as its last reader is done, about one chunk's time ahead.
 // The two column halves of a head re-read x and y (from L2) and repeat A.
+// Bound by shared memory: of the ~4000 cycles of a chunk its products' operands, the
+// tiles' arrival, Z', R and the results take ~3200. Forward of 4 x 4096 x 16 x 128:
+// 68 us, 0.6 of measured HBM bandwidth; 1 x 65536 x 32 x 128: 675 us with the states.
 #include <algorithm>
 
 #include "decay_tc.cuh"
@@ -619,7 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A piece's own end state, S = sum over its tokens of decay k v^T (REV: the
 // gradient of its start state from its own read-outs, s sum of decay q dO^T,
 // chunks in reverse), 64 value columns per CTA: the P product alone, V' (whole chunks)
-// double buffered so that a chunk is split while the previous one is multiplied.
+// double buffered so that a chunk is split while the previous one is multiplied. Bound,
+// like the walk, by shared memory (V' is read, written and multiplied from there): 180 us
+// for the first half of 1 x 65536 x 32 x 128 (537 MB), 22 us for 18 of 19 pieces of
+// 1 x 29999 x 4 x 128; a third term costs a tenth more.
 constexpr int kStThreads = 352;   // 128: half of V' and state; 128: the other half; loads;
                                   // products; gates
 constexpr int kStStages = 2;
@@ -796,7 +802,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
 // from_t = row[t] sum_i (A . dA)_ti col[i].
 // Chunks are independent: a CTA takes every ctas-th, and a chunk's
 // tiles are asked for as soon as the products of the last one are complete.
-// Warps 0-3: rows; 4-7: columns; 8: products and loads; 9: gates.
+// Warps 0-3: rows; 4-7: columns; 8: products and loads; 9: gates. As part of the
+// backward's launch it fills the last wave (4 x 4096 x 16 x 128: 348 us in all).
 
 enum : uint32_t { pFull = 0, pDone = 1, pFree = 2, pGates = 4, pGFree = 6, pEnd = 8, kPairBars = 9 };
 
@@ -999,7 +1006,11 @@ __device__ __forceinline__ void pairs_cta(const DecayArgs& a, const DecaySplit& 
 // The whole backward: blockIdx.z 0: dq, 1: dk, 2: dv, from 3 on the pairs. They do
 // not depend on one another, so in one launch they fill each other's last wave (the
 // pairs come last, in CTAs of about four chunks), and with few sequences they run
-// side by side (2 x 777 x 4 heads: 118 -> 62 us).
+// side by side (2 x 777 x 4 heads: 118 us as launches of their own, 62 as one).
+// 4 x 4096 x 16 x 128: 348 us, of which the products' minimum, with each operand read
+// once from shared memory, would be a third; what a chunk of dq or dk waits for is the
+// chain P -> state -> R in three terms -> O1 next to Z' for the next P, all of it through
+// the same shared memory.
 struct Walks {
   Walk dq, dk, dv;
 };

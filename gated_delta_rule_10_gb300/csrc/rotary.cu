@@ -8,7 +8,9 @@
 // Bound by HBM: every element is read and written once. A thread takes 8 pairs
 // (two 16-byte vectors of bf16) of kHeads heads of one token, q's and k's heads
 // alike, so that one read of the 8 cosines and sines serves them all and kHeads
-// pairs of loads are in flight.
+// pairs of loads are in flight: 44 us, 0.93 of measured HBM bandwidth, for
+// 4 x 4096 x (16 + 16) heads x 128 (one head a thread, CTAs of 256: 58 us). A few
+// tokens take as long as their launch.
 #include "rotary.h"
 #include "vec_io.cuh"
 

@@ -556,7 +556,11 @@ gdr_status gdr_rmsnorm_gate(long long rows, int dv, gdr_dtype dtype, const void*
  * (GDR_ERR_UNSUPPORTED beyond; gdr_decay_step: B * H < 2^31). Pointers are 16-byte
  * aligned (g and dg 4-byte) and strides multiples of 16 bytes. Outputs are dense
  * and overlap no input, except that h0 and hT may be one buffer, and so may dhT
- * and dh0. Non-finite inputs propagate.
+ * and dh0. A non-finite input reaches every row of its chunk (128 tokens, 64 in
+ * fp32), earlier ones among them, and through the state all later chunks: clearing
+ * the state multiplies it by zero. The state is fp32; for bf16 inputs what a chunk
+ * adds to it enters as two bf16 terms (16 bits, 2.4e-6 of a 64-bit state), and as
+ * three where the gradient of g is taken from it.
  */
 typedef struct {
   int B, T, H;        /* batch, tokens, heads of v and o                      */
