@@ -105,6 +105,34 @@ __global__ void __launch_bounds__(kChainThreads) chain_kernel(const DecayArgs a,
   }
 }
 
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  uint2 u = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+// Gradients of a q and k head shared by several heads: the sum of theirs, by CTAs
+// `cta` of `ctas`. It needs nothing of the gate's gradient and shares its launch
+// (2 x 777 x 4 heads: 65 us, as a launch of its own 68).
+template <typename T>
+__device__ __forceinline__ void shared_grad(const DecayArgs& a, const DecaySplit& sp, size_t cta,
+                                            size_t ctas) {
+  const int r = a.H / a.Hk, shift = a.nk == 64 ? 4 : 5;   // float4s of a head, log2
+  const size_t n4 = static_cast<size_t>(a.B) * a.T * a.Hk << shift;
+  for (size_t i = cta * blockDim.x + threadIdx.x; i < 2 * n4; i += ctas * blockDim.x) {
+    const bool key = i >= n4;
+    const size_t j = key ? i - n4 : i, head = j >> shift;   // token * Hk + shared head
+    const int c = static_cast<int>(j & ((1u << shift) - 1)) * 4;
+    const float* src = (key ? sp.dk_part : sp.dq_part) + head * r * a.nk + c;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int n = 0; n < r; ++n) {
+      const float4 x = *reinterpret_cast<const float4*>(src + static_cast<size_t>(n) * a.nk);
+      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    store4(static_cast<T*>(key ? a.dk : a.dq) + head * a.nk + c, s);
+  }
+}
+
 // The gate's gradient. With c the product <S, D> at a block's end (32 tokens),
 //   dg_t = c + sum over the block's j >= t of (from_j - to_j + near_j),
 //   <S, D> at its start = c - sum of to + sum of from.
@@ -121,8 +149,15 @@ constexpr int kMaxBlocks = 128;   // blocks per segment: 4096 tokens
 constexpr int kMaxFlows = 3;      // two column slices and the pairs
 constexpr int kGateThreads = 1024;
 
+template <typename T>
 __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const DecayArgs a,
                                                                   const DecaySplit sp) {
+  if (blockIdx.z > 0) {
+    const size_t plane = static_cast<size_t>(gridDim.x) * gridDim.y;
+    shared_grad<T>(a, sp, (blockIdx.z - 1) * plane + blockIdx.y * gridDim.x + blockIdx.x,
+                   (gridDim.z - 1) * plane);
+    return;
+  }
   constexpr int kWarps = kGateThreads / 32;
   constexpr int kMine = kMaxBlocks / kWarps;   // blocks per warp
   __shared__ float s_from[kMaxBlocks], s_to[kMaxBlocks], s_c[kMaxBlocks];
@@ -257,31 +292,6 @@ __global__ void __launch_bounds__(32) head_grad_kernel(const DecayArgs a, const 
   if (threadIdx.x == 0) a.dg[h] = s;
 }
 
-__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
-  uint2 u = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-  *reinterpret_cast<uint2*>(p) = u;
-}
-
-// Gradients of a q and k head shared by `r` heads: the sum of theirs.
-template <typename T>
-__global__ void __launch_bounds__(256) shared_grad_kernel(const DecayArgs a, const DecaySplit sp,
-                                                          size_t n4, int r) {
-  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n4) return;
-  const float* src = blockIdx.y ? sp.dk_part : sp.dq_part;
-  T* dst = static_cast<T*>(blockIdx.y ? a.dk : a.dq);
-  const int v = a.nk / 4;
-  const size_t head = i / v;      // token * Hk + shared head
-  const int c = static_cast<int>(i % v) * 4;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < r; ++j) {
-    const float4 x = *reinterpret_cast<const float4*>(src + (head * r + j) * a.nk + c);
-    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-  }
-  store4(dst + head * a.nk + c, s);
-}
-
 }  // namespace
 
 cudaError_t launch_decay_chain(const DecayArgs& a, const DecaySplit& sp, bool backward,
@@ -294,14 +304,15 @@ cudaError_t launch_decay_chain(const DecayArgs& a, const DecaySplit& sp, bool ba
 
 cudaError_t launch_decay_gate_grad(const DecayArgs& a, const DecaySplit& sp, bool f32,
                                    cudaStream_t stream) {
-  gate_grad_kernel<<<dim3(sp.segments, a.B * a.H), kGateThreads, 0, stream>>>(a, sp);
-  if (a.per_head) head_grad_kernel<<<a.H, 32, 0, stream>>>(a, sp);
-  if (sp.dq_part) {
-    const size_t n4 = static_cast<size_t>(a.B) * a.T * a.Hk * (a.nk / 4);
-    const dim3 grid(static_cast<unsigned>((n4 + 255) / 256), 2);
-    if (f32) shared_grad_kernel<float><<<grid, 256, 0, stream>>>(a, sp, n4, a.H / a.Hk);
-    else shared_grad_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, sp, n4, a.H / a.Hk);
+  dim3 grid(sp.segments, a.B * a.H, 1);
+  if (sp.dq_part) {   // two float4s a thread, up to 16 planes
+    const size_t work = static_cast<size_t>(a.B) * a.T * a.Hk * (a.nk / 4);
+    const size_t planes = work / (static_cast<size_t>(kGateThreads) * grid.x * grid.y) + 1;
+    grid.z += static_cast<unsigned>(planes < 16 ? planes : 16);
   }
+  if (f32) gate_grad_kernel<float><<<grid, kGateThreads, 0, stream>>>(a, sp);
+  else gate_grad_kernel<__nv_bfloat16><<<grid, kGateThreads, 0, stream>>>(a, sp);
+  if (a.per_head) head_grad_kernel<<<a.H, 32, 0, stream>>>(a, sp);
   return cudaGetLastError();
 }
 
