@@ -183,6 +183,18 @@ def test_attention_gate_gradient_over_thousands_of_tokens():
     assert off(got[:, :, pick], ref) <= GATE_TOL
 
 
+def test_attention_fixed_decays_with_memories_of_thousands_of_tokens():
+    """Fixed decays close to 1 in fp32: a chunk's decay is the same all along, so its
+    rounding must not add up over the ~90 chunks in memory. 2e-6: products kept to 2^-21,
+    and one rounding of 2^-24 a chunk, 90 of them at random 6e-7."""
+    x = attn_inputs(1, 6001, 8, 4, 64, 64, F32, seed=21, h0=True)
+    x["g"] = -1.0 / torch.linspace(3000.0, 23000.0, 8, device="cuda")
+    o, hT = run_fwd(x)
+    ro, rh = attn_oracle(x)
+    assert off(o, ro) <= 2e-6
+    assert off(hT, rh) <= 2e-6
+
+
 def test_attention_gradient_against_differences():
     """fp32, along a random direction: the loss's difference against <grad, d>. The
     second-order term (step^2) and the losses' rounding (1e-6 over the step) both
