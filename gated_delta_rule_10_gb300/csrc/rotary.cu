@@ -96,9 +96,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
 
 // cos and sin of position p times the j-th frequency, in fp64 and rounded once.
 // kind 0: base^(-2j/rot). 1: positions divided by `factor`. 2: the base raised so
-// that the lowest frequency is divided by `factor`. 3: frequencies that turn at
-// least `fast` times over `original` positions are kept, those below `slow` are
-// divided by `factor`, with a linear ramp in j between; cos and sin times `magnitude`.
+// that the lowest frequency is divided by `factor`. 3 (the by-parts interpolation of
+// "YaRN: Efficient Context Window Extension of Large Language Models", Peng et al.):
+// frequencies that turn at least `fast` times over `original` positions are kept,
+// those below `slow` are divided by `factor`, with a linear ramp in j between; cos and
+// sin times `magnitude`. The ramp may end past the last frequency (half - 1): where even
+// that one turns more than `slow` times, none is divided in full.
 __global__ void __launch_bounds__(kThreads) rotary_table_kernel(const RotaryTableArgs a) {
   const long long id = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int half = a.rot / 2;
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) rotary_table_kernel(const RotaryTabl
     };
     double lo = floor(at(a.fast)), hi = ceil(at(a.slow));
     lo = lo < 0.0 ? 0.0 : lo;
-    hi = hi > half - 1.0 ? half - 1.0 : hi;
+    hi = hi > n - 1.0 ? n - 1.0 : hi;
     double r = (j - lo) / (hi > lo ? hi - lo : 1e-3);
     r = r < 0.0 ? 0.0 : (r > 1.0 ? 1.0 : r);
     f = f * (1.0 - r) + f / a.factor * r;

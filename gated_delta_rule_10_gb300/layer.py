@@ -336,7 +336,7 @@ def rotary_table(length, rot, base=10000.0, *, scaling=None, factor=1.0, origina
     by factor), "base" (the base raised) or "ramp" (frequencies that turn ``fast``
     times over ``original_length`` kept, those that turn ``slow`` times divided by
     factor, a ramp between; cos and sin times ``magnitude``, by default
-    0.1 ln(factor) + 1).
+    0.1 ln(factor) + 1; both after "YaRN", Peng et al.).
     """
     if scaling not in _KINDS:
         raise ValueError("unknown scaling %r" % (scaling,))

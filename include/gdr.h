@@ -686,7 +686,9 @@ gdr_status gdr_rotary(const gdr_rotary_shape* shape, const void* q, const void* 
  *   GDR_ROPE_RAMP    frequencies that turn at least `fast` times over
  *                    original_length are kept, those that turn at most `slow`
  *                    times divided by factor, a linear ramp in j between (its ends
- *                    rounded outwards to whole j); cos and sin times magnitude
+ *                    rounded outwards to whole j and held within 0 and rot - 1, so
+ *                    that it may end past the last frequency; after "YaRN", Peng et
+ *                    al.); cos and sin times magnitude
  */
 enum { GDR_ROPE_NONE = 0, GDR_ROPE_LINEAR = 1, GDR_ROPE_BASE = 2, GDR_ROPE_RAMP = 3 };
 typedef struct {

@@ -100,7 +100,9 @@ def rotary_frequencies(rot, base, kind=None, factor=1.0, original=0, fast=32.0, 
     if kind == "ramp":
         # the j at which a frequency turns r times over `original` positions
         at = lambda r: rot * np.log(original / (2 * np.pi * r)) / (2 * np.log(base))  # noqa: E731
-        lo, hi = max(np.floor(at(fast)), 0.0), min(np.ceil(at(slow)), rot // 2 - 1.0)
+        # ends outwards to whole j, within 0 and rot - 1 (the YaRN paper's bounds: the ramp
+        # may end past the last frequency, rot / 2 - 1)
+        lo, hi = max(np.floor(at(fast)), 0.0), min(np.ceil(at(slow)), rot - 1.0)
         r = np.clip((j - lo) / (hi - lo if hi > lo else 1e-3), 0.0, 1.0)
         f = f * (1 - r) + f / factor * r
     return f
