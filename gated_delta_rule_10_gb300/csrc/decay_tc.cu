@@ -1068,17 +1068,15 @@ cudaError_t fwd(const DecayArgs& a, const DecaySplit& sp, const Walk& w, const R
 }
 
 // The walk's first state: S (or D), as rows of key channels or transposed, from
-// the segments' chain or the caller's.
+// the segments' chain or the caller's. D comes from the chain, which has copied dhT to
+// its last slot, whenever there is one: dhT may be dh0, which the dv walk writes while
+// the dk walk of the same launch reads its start.
 Walk from(const DecayArgs& a, const DecaySplit& sp, bool grad, bool transposed) {
   Walk w{};
   const size_t st = static_cast<size_t>(a.nk) * a.nv;
-  w.start = grad ? a.dhT : a.h0;
-  w.start_bh = st;
-  if (sp.segments > 1) {
-    w.start = grad ? sp.D : sp.S;
-    w.start_bh = sp.slots * st;
-  }
-  w.chained = sp.segments > 1;
+  w.chained = grad ? sp.D != nullptr : sp.segments > 1;
+  w.start = w.chained ? (grad ? sp.D : sp.S) : (grad ? nullptr : a.h0);
+  w.start_bh = w.chained ? sp.slots * st : st;
   w.row_step = transposed ? 1 : a.nv;
   w.col_step = transposed ? a.nv : 1;
   return w;

@@ -1,14 +1,54 @@
 """Edges of the layer operators on the GPU, against the float64 oracle
 (oracle/layer.py); the bars are those of test_layer_gpu.py unless a test says its own."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_10_gb300 as gdr
+from gated_delta_rule_10_gb300 import layer as wrappers
 from oracle import layer
-from test_layer_gpu import f64
+from test_layer_gpu import BF, F32, attn_inputs, f64, run_bwd
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ linear attention
+
+def backward_call(x, dhT, dh0):
+    """gdr_decay_chunk_bwd through the C ABI: dh0 (a tensor, or None) is the caller's."""
+    B, T, H, dv = x["v"].shape
+    Hk, dk = x["q"].shape[2:]
+    dt = x["q"].dtype
+    s = wrappers.DecayShape(B, T, H, Hk, dk, dv, gdr.GDR_BF16 if dt == BF else gdr.GDR_F32,
+                            int(x["g"].dim() == 1), x["scale"], 0, 0, 0)
+    out = {"q": torch.empty_like(x["q"]), "k": torch.empty_like(x["k"]),
+           "v": torch.empty_like(x["v"]), "g": torch.empty_like(x["g"])}
+    ws = torch.empty(gdr.decay_chunk_bwd_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = wrappers._lib().gdr_decay_chunk_bwd(
+        ctypes.byref(s), *(p(x[n]) for n in ("q", "k", "v", "g", "h0", "dO")), p(dhT),
+        *(p(out[n]) for n in ("q", "k", "v", "g")), p(dh0), p(ws), ws.numel(),
+        torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(2, 100, 3, 1, 64, 128), (3, 520, 64, 32, 128, 128),
+                                   (1, 1300, 2, 2, 128, 64)], ids=lambda s: "x".join(map(str, s)))
+def test_backward_with_the_state_gradients_in_one_buffer(shape, dtype):
+    """dhT and dh0 may be one buffer: the same bits as with two, uncut (one chunk, and
+    several with more (batch, head)s than SMs) and cut into segments."""
+    x = attn_inputs(*shape, dtype, seed=51, h0=True)
+    ref = run_bwd(x)
+    for _ in range(3):
+        both = x["dhT"].clone()
+        got = backward_call(x, both, both)
+        assert all(torch.equal(got[n], ref[n]) for n in got)
+        assert torch.equal(both, ref["h0"])
 
 
 # ------------------------------------------------------------------ rotary
