@@ -619,8 +619,11 @@ gdr_status gdr_decay_step(const gdr_decay_shape* shape, const void* q, const voi
  * x, residual, residual_out in dtype, weight [D] fp32, arithmetic in fp32.
  * gdr_add_rmsnorm writes y [rows,D] in dtype. gdr_add_rmsnorm_fp8 writes y in 8
  * bits (e4m3) with one fp32 scale for each 128 columns (the last block may be
- * shorter), scales [rows, ceil(D/128)]: scale = max |y| / 448 over the block, 1
- * for a block of zeros, and y = scale * (the 8-bit value) up to its rounding.
+ * shorter), scales [rows, ceil(D/128)]: scale = max |y| / 448 over the block, at
+ * least 2^-126, 1 for a block of zeros, and y = scale * (the 8-bit value) up to its
+ * rounding. The 8-bit value is y * (448 / max |y|), rounded twice in fp32 before its
+ * rounding to 8 bits, so that next to the middle between two 8-bit numbers it may
+ * be the other one than y / scale would give.
  * residual_out may be x or residual, and y (in dtype) x or residual when it is
  * not residual_out; other overlaps are not allowed. Pointers are 16-byte aligned
  * (scales 4-byte); D a multiple of 8, at most 8192, rows < 2^31

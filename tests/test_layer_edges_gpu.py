@@ -51,6 +51,29 @@ def test_backward_with_the_state_gradients_in_one_buffer(shape, dtype):
         assert torch.equal(both, ref["h0"])
 
 
+# ------------------------------------------------------------------ norm
+
+@pytest.mark.parametrize("D", [64, 256, 1000, 4096])
+def test_norm_to_8_bits_of_subnormal_blocks(D):
+    """Blocks whose max / 448 is subnormal, or zero to the nearest."""
+    x = torch.zeros(8, D, device="cuda")
+    for i, m in enumerate((1e-45, 3e-45, 2e-44, 1e-43, 9e-43, 1e-41, 1e-39, 1e-36)):
+        x[i, ::3] = m
+        x[i, 1::3] = -m / 3
+    w = torch.full((D,), 2.0 ** -10, device="cuda")
+    y, s, _ = gdr.add_rmsnorm_fp8(x, torch.zeros_like(x), w, 1e-6)
+    got = f64(y.float()) * np.repeat(f64(s), 128, axis=1)[:, :D]
+    ref = layer.add_rmsnorm(f64(x), f64(w), 1e-6)
+    # y is rounded to the subnormals' unit (a block that is then zero has scale 1); then
+    # half a step of a 3-bit mantissa, or of the smallest 8-bit numbers at the scale
+    unit = 2.0 ** -149
+    wide = np.maximum(layer.block_scales(ref) * (layer.block_scales(ref) < 1), 2.0 ** -126)
+    band = (2.0 ** -4 * (np.abs(ref) + unit) + 2.0 ** -10 * np.repeat(wide, 128, axis=1)[:, :D]) * \
+        (1 + 1e-4) + unit
+    assert (np.abs(got - ref) <= band).all()
+    assert (f64(s) >= 2.0 ** -126).all()
+
+
 # ------------------------------------------------------------------ rotary
 
 @pytest.mark.parametrize("rot,original", [(64, 65536), (64, 131072), (128, 131072)])
