@@ -811,7 +811,7 @@ template <int NK, int NV>
 struct PairSmem {
   static constexpr uint32_t kK = NK / 64 * kTile, kV = NV / 64 * kTile;
   static constexpr uint32_t oQ = 0, oK = kK, oV = 2 * kK, oO = oV + kV, oGates = oO + kV,
-                            oBar = oGates + 2 * sizeof(Gates), oSlot = oBar + 8 * kPairBars,
+                            oBar = oGates + 2 * sizeof(PairGates), oSlot = oBar + 8 * kPairBars,
                             oAbort = oSlot + 4, bytes = oAbort + 4;
   static constexpr uint32_t launch = bytes + 1024;
 };
@@ -842,8 +842,8 @@ __device__ __forceinline__ void pairs_cta(const DecayArgs& a, const DecaySplit& 
   auto par = [](int n) { return static_cast<uint32_t>(n >> 1) & 1u; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::oAbort);
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::oSlot);
-  auto gates = [&](int n) -> Gates& {
-    return *reinterpret_cast<Gates*>(smem + L::oGates + (n & 1) * sizeof(Gates));
+  auto gates = [&](int n) -> PairGates& {
+    return *reinterpret_cast<PairGates*>(smem + L::oGates + (n & 1) * sizeof(PairGates));
   };
   if (warp == 8) tc::tmem_alloc(smem_u32(slot), 512);
   if (tid == 0) {
@@ -873,8 +873,8 @@ __device__ __forceinline__ void pairs_cta(const DecayArgs& a, const DecaySplit& 
           !warp_wait(bar(pDone), n & 1, abort_flag))
         break;
       tc::fence_after_sync();
-      const Gates& g = gates(n);
-      const float lr = g.loc[row];
+      const PairGates& g = gates(n);
+      const float lr = g.loc[row], ll = g.low[row];
       const uint32_t mine = g.allow[row];
       float far_sum = 0.f, near_sum = 0.f;
 #pragma unroll 1
@@ -883,7 +883,7 @@ __device__ __forceinline__ void pairs_cta(const DecayArgs& a, const DecaySplit& 
         tc::tmem_ld32(ta + 32 * cb, x);
         tc::tmem_ld32(ta + 128 + 32 * cb, y);
         if (cb == quad) {
-          const float* f = g.loc + 32 * cb;
+          const float *f = g.loc + 32 * cb, *fl = g.low + 32 * cb;
           const uint32_t* m = g.allow + 32 * cb;
           float acc[2] = {0.f, 0.f};
 #pragma unroll
@@ -891,7 +891,8 @@ __device__ __forceinline__ void pairs_cta(const DecayArgs& a, const DecaySplit& 
             // rows: i < r reaches r; columns: r > i is reached by i
             const bool use = cols ? i > lane && (m[i] >> lane & 1u)
                                   : i < lane && (mine >> i & 1u);
-            const float d = exp2_fast(cols ? f[i] - lr : lr - f[i]);
+            const float e = (f[i] - lr) + (fl[i] - ll);
+            const float d = exp2_fast(cols ? e : -e);
             acc[i & 1] += use ? x[i] * y[i] * d : 0.f;
           }
           near_sum = acc[0] + acc[1];

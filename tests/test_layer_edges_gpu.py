@@ -9,7 +9,7 @@ import torch
 import gated_delta_rule_10_gb300 as gdr
 from gated_delta_rule_10_gb300 import layer as wrappers
 from oracle import layer
-from test_layer_gpu import BF, F32, attn_inputs, f64, run_bwd
+from test_layer_gpu import BF, F32, attn_inputs, check_bwd, check_fwd, f64, run_bwd
 
 pytestmark = pytest.mark.gpu
 
@@ -49,6 +49,19 @@ def test_backward_with_the_state_gradients_in_one_buffer(shape, dtype):
         got = backward_call(x, both, both)
         assert all(torch.equal(got[n], ref[n]) for n in got)
         assert torch.equal(both, ref["h0"])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("low,share", [(-103.9, 0.5), (-100.0, 0.1), (-60.0, 0.5), (-20.0, 0.5)])
+def test_attention_decays_that_all_but_clear(low, share, dtype):
+    """Tokens just above the clearing decay among slow ones: the sums of the log-decays
+    reach thousands, and the pairs between those tokens still decay by their own."""
+    x = attn_inputs(1, 300, 2, 2, 64, 128, dtype, seed=61, decay="slow", h0=True)
+    gen = torch.Generator(device="cuda").manual_seed(62)
+    at = torch.rand(1, 300, 2, generator=gen, device="cuda") < share
+    x["g"] = torch.where(at, torch.full_like(x["g"], low), x["g"] / 100)
+    check_fwd(x)
+    check_bwd(x)
 
 
 # ------------------------------------------------------------------ norm
