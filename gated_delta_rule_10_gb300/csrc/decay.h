@@ -35,6 +35,8 @@ struct DecaySplit {
   float* D = nullptr;         // slot p: the gradient of that state (backward)
   float* decay = nullptr;     // [B * H, pieces] a piece's decay (decay_code)
   float* dots = nullptr;      // [B * H, slots, parts] partial <S_p, D_p>
+  int firsts = 1;             // partial sums of the same product at the sequence's start,
+  float* first = nullptr;     // [B * H, firsts] <h0, D_0> from the walk that gives dk
   // Terms of the gate's gradient by token, [flows, B * H, T] (the parts add up):
   // what its row takes from before its block of 32 tokens, what its keys and values
   // give to after it, and [nears, B * H, T] the difference within the block.

@@ -141,7 +141,7 @@ __device__ __forceinline__ void shared_grad(const DecayArgs& a, const DecaySplit
 // is below 2^-30 passes nothing on (what crosses it is 2^-30 of <S, D>): c is then
 // its sum of to, and the start's its sum of from.
 // So c is known at both ends of every run of blocks between such blocks and the
-// segment's edges (from the states there). What the blocks' sums pass on, with
+// segment's edges (from the states there, and from the sequence's own start). What the blocks' sums pass on, with
 // rounding that gathers like a random walk, misses the far end by a little; the
 // miss is spread evenly over the run, which takes two thirds of the walk's variance
 // away. A clearing token's gradient is 0.
@@ -217,15 +217,6 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const DecayArgs
       s_keep[blk] = !(g < -20.8f);   // (NaN keeps)
     }
   }
-  // <S, D> where the sequence starts from a state
-  float first = 0.f;
-  const bool given = seg == 0 && a.h0;
-  if (given && a.dh0) {
-    const size_t st = static_cast<size_t>(a.nk) * a.nv;
-    for (size_t i = threadIdx.x; i < st; i += kGateThreads)
-      first = fmaf(a.h0[bh * st + i], a.dh0[bh * st + i], first);
-    first = block_sum<kGateThreads>(first, red);
-  }
   __syncthreads();
   if (threadIdx.x == 0) {
     auto edge = [&](int slot) {   // <S, D> at a segment's edge
@@ -236,7 +227,10 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const DecayArgs
       return c;
     };
     float c = edge(sp.slot_of(seg + 1));
-    const float start = seg > 0 ? edge(sp.slot_of(seg)) : first;
+    float start = 0.f;
+    if (seg > 0) start = edge(sp.slot_of(seg));
+    else if (a.h0)
+      for (int i = 0; i < sp.firsts; ++i) start += sp.first[bh * sp.firsts + i];
     int last = blocks - 1, run = 0;
     for (int blk = blocks - 1; blk >= 0; --blk) {
       const bool keep = s_keep[blk];
@@ -244,14 +238,11 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const DecayArgs
       s_c[blk] = keep ? c : e;
       s_run[blk] = keep ? run : kMaxBlocks;
       if (keep) c += f - e;
-      // a run's far end is a block that passes nothing, or the segment's start (not
-      // known where a given state's gradient was not asked for)
+      // a run's far end is a block that passes nothing, or the segment's start
       if (!keep || blk == 0) {
         const int steps = last - blk + (keep ? 1 : 0);
-        const bool known = !keep || !given || a.dh0;
         run_last[run] = last;
-        run_share[run] = known && steps > 0 ? (c - (keep ? start : e)) / static_cast<float>(steps)
-                                            : 0.f;
+        run_share[run] = steps > 0 ? (c - (keep ? start : e)) / static_cast<float>(steps) : 0.f;
         ++run;
       }
       if (!keep) {

@@ -474,7 +474,21 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_f32(const DecayArgs a, const 
     update_state<NK, NV>(S, gates.sum, Q, O);
   }
   __syncthreads();
-  if (rev && a.dh0 && blockIdx.x == 0) store_state<NK, NV>(S, a.dh0 + w.bh * st);
+  if (!rev || blockIdx.x != 0) return;
+  if (a.dh0) store_state<NK, NV>(S, a.dh0 + w.bh * st);
+  if (a.h0) {   // <h0, D> where the gate's gradient starts
+    float dot = 0.f;
+    for (int i = threadIdx.x; i < NK * NV; i += kThreads)
+      dot = fmaf(a.h0[w.bh * st + i], S[(i / NV) * (NV + 4) + i % NV], dot);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    if (lane == 0) flow[0][threadIdx.x >> 5] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < kThreads / 32; ++i) dot += flow[0][i];
+      sp.first[w.bh] = dot;
+    }
+  }
 }
 
 template <class Kern>

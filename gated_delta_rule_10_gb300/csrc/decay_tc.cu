@@ -332,6 +332,18 @@ __device__ __forceinline__ void walk_cta(const DecayArgs& a, const DecaySplit& s
     }
     if (ok && mine && w.end && seg == (REV ? 0 : sp.segments - 1))
       write_row(R, 1.f, w.end + (static_cast<size_t>(bh) * W + row) * w.nz + 64 * slice);
+    if constexpr (FINE && REV) {
+      // <h0, D> where the gate's gradient starts, from three terms (dh0 has two)
+      if (ok && mine && a.h0 && seg == 0) {
+        const float* s = a.h0 + (static_cast<size_t>(bh) * w.nz + 64 * slice) * W + row;
+        float dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) dot = fmaf(R[j], s[j * W], dot);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        if (lane == 0) sp.first[bh * sp.firsts + slice * (W / 32) + quad] = dot;
+      }
+    }
   } else if (warp < 12) {
     // ---------------------------------------------- read-out, one token per lane, and
     // the other half of Z'

@@ -129,6 +129,8 @@ size_t lay_out(const gdr_decay_shape* s, bool backward, bool end_grad, char* bas
   const bool tc = s->dtype == GDR_BF16;
   sp->flows = tc ? s->dk / 64 + 1 : 2;   // the states' parts (by column slice), and the pairs
   sp->nears = tc ? 2 : 1;                // rows, columns
+  sp->firsts = tc ? s->dk / 64 * (s->dv / 32) : 1;   // a warp of each column slice's
+  take(&sp->first, bh * sp->firsts);
   take(&sp->from, sp->flows * bh * s->T);
   take(&sp->to, sp->flows * bh * s->T);
   take(&sp->near, sp->nears * bh * s->T);

@@ -9,7 +9,8 @@ import torch
 import gated_delta_rule_10_gb300 as gdr
 from gated_delta_rule_10_gb300 import layer as wrappers
 from oracle import layer
-from test_layer_gpu import BF, F32, attn_inputs, check_bwd, check_fwd, f64, run_bwd
+from test_layer_gpu import (BF, F32, GATE_TOL, attn_grad_oracle, attn_inputs, check_bwd, check_fwd,
+                            f64, off, run_bwd)
 
 pytestmark = pytest.mark.gpu
 
@@ -49,6 +50,31 @@ def test_backward_with_the_state_gradients_in_one_buffer(shape, dtype):
         got = backward_call(x, both, both)
         assert all(torch.equal(got[n], ref[n]) for n in got)
         assert torch.equal(both, ref["h0"])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape,decay", [((1, 900, 2, 1, 64, 128), "slow"),
+                                         ((2, 130, 80, 40, 128, 64), "head"),
+                                         ((1, 200, 3, 3, 128, 128), "token")],
+                         ids=lambda c: c if isinstance(c, str) else "x".join(map(str, c)))
+def test_backward_without_the_state_gradient(shape, decay, dtype):
+    """The other gradients are the same bits whether or not that of h0 is asked for."""
+    x = attn_inputs(*shape, dtype, seed=52, decay=decay, h0=True)
+    ref = run_bwd(x)
+    got = backward_call(x, x["dhT"], None)
+    assert all(torch.equal(got[n], ref[n]) for n in got)
+
+
+@pytest.mark.parametrize("decay", ["slow", "fixed"])
+def test_gate_gradient_from_a_state_over_thousands_of_tokens(decay):
+    """One segment of 4096 tokens that starts from a state, as does the gate's gradient."""
+    x = attn_inputs(1, 4096, 152, 152, 64, 64, BF, seed=53, decay="slow", h0=True)
+    if decay == "fixed":
+        x["g"] = -1.0 / torch.linspace(2.0, 20000.0, 152, device="cuda")
+    got, pick = run_bwd(x)["g"], [0, 75, 151]
+    sub = {n: t[:, pick] if n in ("h0", "dhT") else t[..., pick] if n == "g" else t[:, :, pick]
+           if torch.is_tensor(t) else t for n, t in x.items()}
+    assert off(got[..., pick], attn_grad_oracle(sub)["g"]) <= GATE_TOL
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
