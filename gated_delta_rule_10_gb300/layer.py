@@ -156,6 +156,17 @@ def _new_or(t, name, shape, dtype, device):
     return t, False
 
 
+def _workspace_bytes(t, device):
+    """Bytes of a caller's workspace (None: 0), which the kernels write as it stands."""
+    if t is None:
+        return 0
+    if not t.is_cuda or t.device != device:
+        raise ValueError("workspace must be a CUDA tensor on %s" % (device,))
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def _decay_shape(q, k, v, g, scale):
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be [B, T, heads, d]")
@@ -209,8 +220,7 @@ def decay_chunk_fwd(q, k, v, g, h0=None, *, scale=None, output_final_state=True,
     if workspace is None and need:
         ws = workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _call("gdr_decay_chunk_fwd", dev, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-          _ptr(h0), _ptr(o), _ptr(hT), _ptr(workspace),
-          0 if workspace is None else workspace.numel() * workspace.element_size(),
+          _ptr(h0), _ptr(o), _ptr(hT), _ptr(workspace), _workspace_bytes(workspace, dev),
           _stream(stream, dev))
     _used_on(stream, dev, ws, o if new_o else None, hT if new_h else None)
     return o, hT
@@ -237,7 +247,7 @@ def decay_chunk_bwd(q, k, v, g, dO, h0=None, dhT=None, *, scale=None, workspace=
                                      device=dev)
     _call("gdr_decay_chunk_bwd", dev, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
           _ptr(h0), _ptr(dO), _ptr(dhT), *(_ptr(out[n]) for n in ("q", "k", "v", "g", "h0")),
-          _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, dev))
+          _ptr(workspace), _workspace_bytes(workspace, dev), _stream(stream, dev))
     _used_on(stream, dev, ws, *out.values())
     return out
 
@@ -322,8 +332,8 @@ def add_rmsnorm_bwd(dy, sum, weight, eps=1e-6, *, dres=None, dx=None, workspace=
             raise GdrError(st, "gdr_add_rmsnorm_bwd_workspace")
         ws = workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
     _call("gdr_add_rmsnorm_bwd", dev, rows, D, dt, _ptr(dy), _ptr(sum), _ptr(weight), float(eps),
-          _ptr(dres), _ptr(dx), _ptr(dw), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), _stream(stream, dev))
+          _ptr(dres), _ptr(dx), _ptr(dw), _ptr(workspace), _workspace_bytes(workspace, dev),
+          _stream(stream, dev))
     _used_on(stream, dev, ws, dw, dx if new_x else None)
     return dx, dw
 

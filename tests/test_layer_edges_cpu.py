@@ -2,7 +2,9 @@
 (oracle/layer.py) and the wrappers' checks."""
 import numpy as np
 import pytest
+import torch
 
+from gated_delta_rule_10_gb300 import layer as wrappers
 from oracle import layer
 
 LONG = [(64, 65536), (64, 131072), (128, 131072), (128, 4096), (32, 2 ** 20)]
@@ -36,3 +38,11 @@ def test_ramp_by_hand():
     f = layer.rotary_frequencies(64, 10000.0)
     r = layer.rotary_frequencies(64, 10000.0, "ramp", 4.0, 131072)
     assert r[31] / f[31] == pytest.approx(1 - 9 / 13 * 0.75)
+
+
+def test_a_workspace_elsewhere_is_refused():
+    """A caller's workspace is written by the kernels: it has to be the device's."""
+    dev = torch.device("cuda", 0)
+    assert wrappers._workspace_bytes(None, dev) == 0
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        wrappers._workspace_bytes(torch.empty(4096, dtype=torch.uint8), dev)

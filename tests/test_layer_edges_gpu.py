@@ -77,6 +77,31 @@ def test_gate_gradient_from_a_state_over_thousands_of_tokens(decay):
     assert off(got[..., pick], attn_grad_oracle(sub)["g"]) <= GATE_TOL
 
 
+def test_callers_workspaces():
+    """Large enough, of any type: the same bits; elsewhere, or with gaps: refused before
+    any launch, and too small by the library."""
+    x = attn_inputs(1, 700, 2, 1, 64, 64, BF, seed=54, h0=True)
+    dy, w = torch.randn(40, 256, device="cuda"), torch.ones(256, device="cuda")
+    y = attn_inputs(1, 1500, 2, 1, 64, 64, BF, seed=55)
+    calls = [lambda **k: gdr.decay_chunk_fwd(x["q"], x["k"], x["v"], x["g"], x["h0"], **k),   # none needed
+             lambda **k: gdr.decay_chunk_fwd(y["q"], y["k"], y["v"], y["g"], **k),
+             lambda **k: tuple(gdr.decay_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["dO"], x["h0"],
+                                                   x["dhT"], **k).values()),
+             lambda **k: gdr.add_rmsnorm_bwd(dy, dy, w, **k)]
+    n = 1 << 24
+    for call in calls:
+        for ws in (torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty(n // 4, device="cuda")):
+            assert all(torch.equal(a, b) for a, b in zip(call(), call(workspace=ws)))
+        with pytest.raises(ValueError, match="workspace"):
+            call(workspace=torch.empty(n, dtype=torch.uint8))
+        with pytest.raises(ValueError, match="contiguous"):
+            call(workspace=torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2])
+        if call is calls[0]:
+            continue
+        with pytest.raises(gdr.GdrError):
+            call(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("low,share", [(-103.9, 0.5), (-100.0, 0.1), (-60.0, 0.5), (-20.0, 0.5)])
 def test_attention_decays_that_all_but_clear(low, share, dtype):
