@@ -77,6 +77,24 @@ def test_gate_gradient_from_a_state_over_thousands_of_tokens(decay):
     assert off(got[..., pick], attn_grad_oracle(sub)["g"]) <= GATE_TOL
 
 
+def heads_of(x, pick):
+    """Those heads alone (q and k of their own)."""
+    r = x["v"].shape[2] // x["q"].shape[2]
+    at = {"q": [h // r for h in pick], "k": [h // r for h in pick]}
+    return {n: t if not torch.is_tensor(t) else t[:, pick] if n in ("h0", "dhT")
+            else t[..., pick] if n == "g" else t[:, :, at.get(n, pick)] for n, t in x.items()}
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_gate_gradient_of_fixed_decays_with_a_gradient_of_the_last_state(dtype):
+    """The last state's gradient is felt in the last tokens; what is rounded there must not
+    add up over the 4096 whose sum a fixed decay's gradient is."""
+    x = attn_inputs(1, 4096, 32, 32, 128, 128, dtype, seed=57, decay="head", h0=True)
+    pick = [0, 17, 31]
+    ref = attn_grad_oracle(heads_of(x, pick))["g"]
+    assert off(run_bwd(x)["g"][pick], ref) <= GATE_TOL
+
+
 def test_callers_workspaces():
     """Large enough, of any type: the same bits; elsewhere, or with gaps: refused before
     any launch, and too small by the library."""
