@@ -9,8 +9,8 @@ import torch
 import gated_delta_rule_10_gb300 as gdr
 from gated_delta_rule_10_gb300 import layer as wrappers
 from oracle import layer
-from test_layer_gpu import (BF, F32, GATE_TOL, attn_grad_oracle, attn_inputs, check_bwd, check_fwd,
-                            f64, off, run_bwd)
+from test_layer_gpu import (BF, F32, GATE_TOL, STATE_TOL, TOL, attn_grad_oracle, attn_inputs,
+                            attn_oracle, check_bwd, check_fwd, f64, off, run_bwd, run_fwd)
 
 pytestmark = pytest.mark.gpu
 
@@ -77,12 +77,80 @@ def test_gate_gradient_from_a_state_over_thousands_of_tokens(decay):
     assert off(got[..., pick], attn_grad_oracle(sub)["g"]) <= GATE_TOL
 
 
+def pieces(x, backward):
+    """The pieces of each sequence whose own states are computed, from the workspace's size:
+    the states are [B * H, pieces (backward: + 1, and twice), dk, dv] fp32, and everything
+    else but the backward's terms by token takes less than one more of them."""
+    B, T, H, dv = x["v"].shape
+    Hk, dk = x["q"].shape[2:]
+    bf = x["q"].dtype == BF
+    s = wrappers.DecayShape(B, T, H, Hk, dk, dv, gdr.GDR_BF16 if bf else gdr.GDR_F32,
+                            int(x["g"].dim() == 1), x["scale"], 0, 0, 0)
+    states = 4 * B * H * dk * dv
+    if not backward:
+        return gdr.decay_chunk_fwd_workspace_bytes(s) // states
+    planes = 2 * (dk // 64 + 1) + 2 if bf else 5
+    terms = 4 * B * H * T * (planes + (2 * dk if Hk != H else 0))
+    return (gdr.decay_chunk_bwd_workspace_bytes(s) - terms) // (2 * states) - 1
+
+
 def heads_of(x, pick):
     """Those heads alone (q and k of their own)."""
     r = x["v"].shape[2] // x["q"].shape[2]
     at = {"q": [h // r for h in pick], "k": [h // r for h in pick]}
     return {n: t if not torch.is_tensor(t) else t[:, pick] if n in ("h0", "dhT")
             else t[..., pick] if n == "g" else t[:, :, at.get(n, pick)] for n, t in x.items()}
+
+
+def check_heads(x, pick):
+    """check_fwd and check_bwd, of some heads; dq and dk where they are not shared."""
+    dt, sub = x["q"].dtype, heads_of(x, pick)
+    o, hT = run_fwd(x)
+    ro, rh = attn_oracle(sub)
+    assert off(o[:, :, pick], ro) <= TOL[dt]
+    assert off(hT[:, pick], rh) <= STATE_TOL
+    got, ref = run_bwd(x), attn_grad_oracle(sub)
+    for n in ("v",) if x["q"].shape[2] != x["v"].shape[2] else ("q", "k", "v"):
+        assert off(got[n][:, :, pick], ref[n]) <= TOL[dt], n
+    assert off(got["h0"][:, pick], ref["h0"]) <= STATE_TOL
+    assert off(got["g"][..., pick], ref["g"]) <= GATE_TOL
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("decay,clears", [("slow", ()), ("slow", (100, 511, 512, 640)), ("head", ())],
+                         ids=["slow", "clears", "head"])
+@pytest.mark.parametrize("shape", [(1, 1101, 3, 1, 64, 128), (2, 1090, 2, 2, 128, 64),
+                                   (1, 2050, 1, 1, 128, 128)], ids=lambda s: "x".join(map(str, s)))
+def test_segments_from_a_state(shape, decay, clears, dtype):
+    """Sequences cut into segments, from a given state and with a given gradient of the
+    last one."""
+    x = attn_inputs(*shape, dtype, seed=56, decay=decay, clears=clears, h0=True)
+    assert pieces(x, False) >= 2 and pieces(x, True) >= 2
+    check_fwd(x)
+    check_bwd(x)
+
+
+@pytest.mark.parametrize("states", [True, False], ids=["states", "zero"])
+@pytest.mark.parametrize("decay", ["slow", "head"])
+@pytest.mark.parametrize("dtype,T,H,Hk,backward", [(BF, 2100, 32, 32, True), (BF, 2100, 32, 8, True),
+                                                   (F32, 300, 64, 64, False),
+                                                   (F32, 300, 32, 32, True)])
+def test_segments_of_several_pieces(dtype, T, H, Hk, backward, decay, states):
+    """Segments whose own states are computed in several pieces: more pieces than there are
+    segments, of which no more than fill 152 SMs are made (a CTA each for the forward, for
+    64 columns of bf16; two in the fp32 backward)."""
+    x = attn_inputs(1, T, H, Hk, 128, 128, dtype, seed=57, decay=decay, h0=states)
+    ctas = H * (2 if dtype == BF or backward else 1)
+    assert pieces(x, backward) > 152 // ctas >= 2
+    check_heads(x, [0, H // 2 + 1, H - 1])
+
+
+def test_segments_of_a_long_backward_that_fills_the_gpu():
+    """More (batch, head)s than SMs: the forward runs uncut, the backward's segments end
+    after 4096 tokens all the same."""
+    x = attn_inputs(1, 4400, 160, 160, 64, 64, BF, seed=58, decay="slow", h0=True)
+    assert pieces(x, False) == 0 and pieces(x, True) >= 2
+    check_heads(x, [0, 79, 159])
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
