@@ -627,8 +627,11 @@ gdr_status gdr_decay_step(const gdr_decay_shape* shape, const void* q, const voi
  * residual_out may be x or residual, and y (in dtype) x or residual when it is
  * not residual_out; other overlaps are not allowed. Pointers are 16-byte aligned
  * (scales 4-byte); D a multiple of 8, at most 8192, rows < 2^31
- * (GDR_ERR_UNSUPPORTED beyond). rows = 0 launches nothing. A row with a
- * non-finite value gives NaN.
+ * (GDR_ERR_UNSUPPORTED beyond). rows = 0 launches nothing. A row with a NaN gives
+ * NaN throughout. One with an infinity gives what the formula does: NaN at that
+ * value (in 8 bits: in its block, scale among it) and zeros elsewhere. The sum of
+ * squares is taken in fp32 and must stay below 3.4e38: past it (some value above
+ * 1.8e19, or of 2e17 in every one of 8192 columns) a row of finite values gives zeros.
  */
 gdr_status gdr_add_rmsnorm(long long rows, int D, gdr_dtype dtype, const void* x,
                            const void* residual, const float* weight, float eps,

@@ -10,7 +10,8 @@ import gated_delta_rule_10_gb300 as gdr
 from gated_delta_rule_10_gb300 import layer as wrappers
 from oracle import layer
 from test_layer_gpu import (BF, F32, GATE_TOL, STATE_TOL, TOL, attn_grad_oracle, attn_inputs,
-                            attn_oracle, check_bwd, check_fwd, f64, off, run_bwd, run_fwd)
+                            attn_oracle, check_bwd, check_fwd, f64, near, norm_inputs, off,
+                            run_bwd, run_fwd)
 
 pytestmark = pytest.mark.gpu
 
@@ -222,6 +223,27 @@ def test_norm_to_8_bits_of_subnormal_blocks(D):
         (1 + 1e-4) + unit
     assert (np.abs(got - ref) <= band).all()
     assert (f64(s) >= 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_norm_of_rows_that_are_not_finite_or_overflow(dtype):
+    """NaN: the whole row. Infinity: NaN there (in 8 bits in its block), zeros elsewhere.
+    Finite values whose squares add up past fp32: zeros."""
+    D = 400
+    x, res, w = norm_inputs(5, D, dtype, 71)
+    x[1, 200], x[2, 200], x[3, 7] = torch.nan, torch.inf, 3e19
+    y, r = gdr.add_rmsnorm(x, res, w)
+    y8, s, r8 = gdr.add_rmsnorm_fp8(x, res, w)
+    assert torch.equal(r.isnan(), r8.isnan()) and torch.equal(r[2:], r8[2:])
+    a, b, c = f64(y), f64(y8.float()), f64(s)
+    assert np.isnan(a[1]).all() and np.isnan(b[1]).all() and np.isnan(c[1]).all()
+    other = np.arange(D) != 200
+    assert np.isnan(a[2, 200]) and (a[2, other] == 0).all()
+    block = np.arange(D) // 128 == 1
+    assert np.isnan(b[2, block]).all() and (b[2, ~block] == 0).all()
+    assert np.isnan(c[2, 1]) and (c[2, [0, 2, 3]] == 1).all()
+    assert (a[3] == 0).all() and (b[3] == 0).all() and (c[3] == 1).all()
+    near(y[[0, 4]], layer.add_rmsnorm(f64(r[[0, 4]]), f64(w), 1e-6), dtype)
 
 
 # ------------------------------------------------------------------ rotary
