@@ -43,9 +43,13 @@
 // 40 us for the products of 4 x 4096 x 16 x 128 alone). Each tile is loaded
 // again as soon as its last reader is done, about one chunk's time ahead.
 // The two column halves of a head re-read x and y (from L2) and repeat A.
-// Bound by shared memory: of the ~4000 cycles of a chunk its products' operands, the
-// tiles' arrival, Z', R and the results take ~3200. Forward of 4 x 4096 x 16 x 128:
-// 68 us, 0.6 of measured HBM bandwidth; 1 x 65536 x 32 x 128: 675 us with the states.
+// Forward of 4 x 4096 x 16 x 128: 68 us, 0.6 of measured HBM bandwidth; 1 x 65536 x 32 x
+// 128: 675 us with the states. No unit is near its rate there: of the busiest SM the
+// load/store pipe to shared memory is 0.45 busy, issue slots 0.48, tensor pipe 0.31 over
+// all SMs, DRAM 0.47; 24 of 152 SMs have no CTA. The ~4000 cycles of a chunk go to the
+// waits along its chains of roles, each a hand-over through an mbarrier and a read of
+// tensor or shared memory: of 8.2 warp cycles an instruction 2.9 are such waits, 1.3
+// fixed latencies and 0.8 instruction fetch (0.83 of the fetches hit).
 #include <algorithm>
 
 #include "decay_tc.cuh"
@@ -634,10 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A piece's own end state, S = sum over its tokens of decay k v^T (REV: the
 // gradient of its start state from its own read-outs, s sum of decay q dO^T,
 // chunks in reverse), 64 value columns per CTA: the P product alone, V' (whole chunks)
-// double buffered so that a chunk is split while the previous one is multiplied. Bound,
-// like the walk, by shared memory (V' is read, written and multiplied from there): 180 us
-// for the first half of 1 x 65536 x 32 x 128 (537 MB), 22 us for 18 of 19 pieces of
-// 1 x 29999 x 4 x 128; a third term costs a tenth more.
+// double buffered so that a chunk is split while the previous one is multiplied. 180 us
+// for the first half of 1 x 65536 x 32 x 128 (537 MB, 79 at the measured bandwidth), 22 us
+// for 18 of 19 pieces of 1 x 29999 x 4 x 128; a third term costs a tenth more. Each chunk
+// waits for its V' to be read, split and written back before its product, and the state
+// for that.
 constexpr int kStThreads = 352;   // 128: half of V' and state; 128: the other half; loads;
                                   // products; gates
 constexpr int kStStages = 2;
@@ -815,7 +820,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
 // Chunks are independent: a CTA takes every ctas-th, and a chunk's
 // tiles are asked for as soon as the products of the last one are complete.
 // Warps 0-3: rows; 4-7: columns; 8: products and loads; 9: gates. As part of the
-// backward's launch it fills the last wave (4 x 4096 x 16 x 128: 348 us in all).
+// backward's launch it fills the last wave (4 x 4096 x 16 x 128: 343 us in all).
 
 enum : uint32_t { pFull = 0, pDone = 1, pFree = 2, pGates = 4, pGFree = 6, pEnd = 8, kPairBars = 9 };
 
@@ -1020,10 +1025,11 @@ __device__ __forceinline__ void pairs_cta(const DecayArgs& a, const DecaySplit& 
 // not depend on one another, so in one launch they fill each other's last wave (the
 // pairs come last, in CTAs of about four chunks), and with few sequences they run
 // side by side (2 x 777 x 4 heads: 118 us as launches of their own, 62 as one).
-// 4 x 4096 x 16 x 128: 348 us, of which the products' minimum, with each operand read
-// once from shared memory, would be a third; what a chunk of dq or dk waits for is the
-// chain P -> state -> R in three terms -> O1 next to Z' for the next P, all of it through
-// the same shared memory.
+// 4 x 4096 x 16 x 128: 343 us. What a chunk of dq or dk waits for is the chain P -> state
+// -> R in three terms -> O1 next to Z' for the next P: issue slots are 0.37 busy, the
+// load/store pipe 0.44 on the busiest SM, the tensor pipe 0.29, DRAM 0.40; of 11 warp
+// cycles an instruction 4.4 are waits for a barrier or a read, 1.7 instruction fetch (0.78
+// of the fetches hit) and 1.2 fixed latencies.
 struct Walks {
   Walk dq, dk, dv;
 };

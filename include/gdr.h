@@ -558,9 +558,20 @@ gdr_status gdr_rmsnorm_gate(long long rows, int dv, gdr_dtype dtype, const void*
  * and overlap no input, except that h0 and hT may be one buffer, and so may dhT
  * and dh0. A non-finite input reaches every row of its chunk (128 tokens, 64 in
  * fp32), earlier ones among them, and through the state all later chunks: clearing
- * the state multiplies it by zero. The state is fp32; for bf16 inputs what a chunk
- * adds to it enters as two bf16 terms (16 bits, 2.4e-6 of a 64-bit state), and as
- * three where the gradient of g is taken from it.
+ * the state multiplies it by zero.
+ *
+ * Precision. All sums are fp32, and so is the state. With bf16 inputs the products'
+ * other operands are made up of bf16 terms:
+ *   - the decayed products of pairs (q k^T, dO v^T), and the states that o and dv are
+ *     read from: one term (2^-9). Their sum is rounded to bf16 once more, so that o, dq,
+ *     dk and dv are 2.35e-3 off 64 bits in the 2-norm (1.66e-3 for one rounding).
+ *   - what a chunk adds to the state of o or the gradient of dv: two terms, 2.4e-6 of
+ *     hT and dh0.
+ *   - the states that dq and dk are read from, and what is added to them: three terms
+ *     (24 bits), as the gradient of g comes from them: about 1e-6 of it.
+ * fp32 inputs are two tf32 terms (2^-21): o, the gradients and the states come to
+ * about 2e-7, the gradient of g to 1e-6. That gradient is made up of differences of
+ * sums over up to 4096 tokens: its error is relative to its norm, not to each token's.
  */
 typedef struct {
   int B, T, H;        /* batch, tokens, heads of v and o                      */
@@ -578,9 +589,8 @@ gdr_status gdr_decay_chunk_fwd_workspace(const gdr_decay_shape* shape, size_t* b
 
 /*
  * The chunked form over whole prompts: h0 [B,H,d_k,d_v] fp32 or NULL (zero), hT
- * the end state or NULL. o is rounded once to the dtype from fp32; the state is
- * fp32. workspace: at least gdr_decay_chunk_fwd_workspace() bytes, 16-byte
- * aligned; calls sharing one must be ordered on the stream.
+ * the end state or NULL. workspace: at least gdr_decay_chunk_fwd_workspace() bytes,
+ * 16-byte aligned; calls sharing one must be ordered on the stream.
  */
 gdr_status gdr_decay_chunk_fwd(const gdr_decay_shape* shape, const void* q, const void* k,
                                const void* v, const float* g, const float* h0, void* o,
