@@ -23,7 +23,9 @@
 // read-out are rounded to bf16 (the result is rounded to bf16 anyway); the decayed
 // Z' is split into two bf16 terms, side by side in one N = 128 product, because it
 // enters the fp32 state, whose error would otherwise be bf16's (1.7e-3; with two
-// terms 2.4e-6 of 64 bits).
+// terms 2.4e-6 of 64 bits). A third term would leave 1e-7 of hT and dh0; in this form of
+// the walk the forward of 4 x 4096 x 16 x 128 takes 87 us instead of 68 with one for half
+// of the tokens alone, for which there is room.
 //
 // FINE (dq and dk): the gate's gradient needs f_t (R^T x_t) . p_t in fp32, p the
 // partner row (q or k), and sums of those differences over thousands of tokens. Two

@@ -146,6 +146,12 @@ def test_segments_of_several_pieces(dtype, T, H, Hk, backward, decay, states):
     check_heads(x, [0, H // 2 + 1, H - 1])
 
 
+def test_a_training_batch():
+    """4 x 4096 x 16 heads x 128: one head of each sequence."""
+    x = attn_inputs(4, 4096, 16, 16, 128, 128, BF, seed=59, decay="slow", clears=(700, 2800))
+    check_heads(x, [11])
+
+
 def test_segments_of_a_long_backward_that_fills_the_gpu():
     """More (batch, head)s than SMs: the forward runs uncut, the backward's segments end
     after 4096 tokens all the same."""
