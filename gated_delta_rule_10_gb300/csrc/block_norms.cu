@@ -1,0 +1,373 @@
+// The norms after and before a block, with its gate and scale on the way into the residual:
+//   u = x rsqrt(mean_c x^2 + eps) wa,   r = round(res + scale sigmoid(gate) u),
+//   y = r rsqrt(mean_c r^2 + eps) wb,
+// and the gradients, for dy of y and dres of r: with nx = x rsqrt(..), nr = r rsqrt(..),
+//   dr = dres + rsqrt(mean r^2) (wb dy - nr mean_c(wb dy nr)),   dwb = sum_rows dy nr
+//   dgate = dr scale wa nx sg (1 - sg),   m = sum_rows dr sg nx: dscale = wa m, dwa = scale m
+//   dx = rsqrt(mean x^2) (t - nx mean_c(t nx)),  t = dr scale wa sg.
+// scale and wa enter as one product, rounded to fp32 once.
+//
+// Streams bound by HBM: every row is read once and stays in registers through its two
+// sums. A row is spread over TPR threads, at most kVec vectors of 8 columns each; the CTAs
+// are persistent, walk the rows and request the next row's vectors before the current
+// row's sums, so that loads are in flight through the barriers.
+#include "block_norms.h"
+
+#include <type_traits>
+
+#include "column_sum.cuh"
+#include "vec_io.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kVec = 2;          // 8-column vectors per thread, at most
+constexpr int kBwdCtas = 304;    // 2 x 152 SMs, of 256 threads: partial rows of the weights
+
+template <typename T>
+__device__ __forceinline__ float rounded(float x) {
+  return static_cast<float>(static_cast<T>(x));
+}
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
+
+// Sums of two values over the TPR threads of a row; `red` has a slot per warp, and
+// consecutive calls take different ones of its parts, so one barrier each is enough.
+template <int TPR>
+__device__ __forceinline__ void row_sum(float& x, float& y, float2 (&red)[16]) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, off);
+    y += __shfl_xor_sync(0xffffffffu, y, off);
+  }
+  if (TPR > 32) {
+    const int warp = threadIdx.x >> 5, first = warp & ~(TPR / 32 - 1);
+    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(x, y);
+    __syncthreads();
+    x = y = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) {
+      const float2 v = red[first + i];
+      x += v.x;
+      y += v.y;
+    }
+  }
+}
+
+template <int TPR>
+constexpr int threads() { return TPR > 32 ? TPR : 256; }
+
+// The columns' constants: post * scale and pre.
+template <int TPR, int VEC>
+__device__ __forceinline__ void load_weights(const float* post, const float* scale,
+                                             const float* pre, int lane, int nv,
+                                             float (&ws)[VEC][8], float (&wp)[VEC][8]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int c = lane + i * TPR;
+    float s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ws[i][j] = wp[i][j] = 0.f;
+      s[j] = 1.f;
+    }
+    if (c < nv) {
+      load8(post + 8 * c, ws[i]);
+      load8(pre + 8 * c, wp[i]);
+      if (scale) load8(scale + 8 * c, s);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ws[i][j] *= s[j];
+  }
+}
+
+template <typename T, int TPR, int VEC>
+__global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads<TPR>() : 1)
+    block_norms_kernel(const BlockNormsArgs a) {
+  constexpr int kRows = threads<TPR>() / TPR;
+  __shared__ float2 red[2][16];
+  const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int nv = a.D / 8;
+  float ws[VEC][8], wp[VEC][8];
+  Raw8<T> rx[VEC], rg[VEC], rr[VEC];
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int c = lane + i * TPR;
+      rg[i].zero();
+      if (row < a.rows && c < nv) {
+        rx[i].load(static_cast<const T*>(a.x) + row * a.D + 8 * c);
+        if (a.gate) rg[i].load(static_cast<const T*>(a.gate) + row * a.D + 8 * c);
+        rr[i].load(static_cast<const T*>(a.residual) + row * a.D + 8 * c);
+      } else {
+        rx[i].zero();
+        rr[i].zero();
+      }
+    }
+  };
+  const long long step = static_cast<long long>(gridDim.x) * kRows;
+  long long r0 = static_cast<long long>(blockIdx.x) * kRows;
+  fetch(r0 + sub);
+  load_weights<TPR, VEC>(a.post, a.scale, a.pre, lane, nv, ws, wp);
+  const float n = static_cast<float>(a.D);
+  for (; r0 < a.rows; r0 += step) {
+    const long long row = r0 + sub;
+    const bool live = row < a.rows;
+    float v[VEC][8], ss = 0.f, none = 0.f;
+    Raw8<T> kg[VEC], kr[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      rx[i].get(v[i]);
+      kg[i] = rg[i];
+      kr[i] = rr[i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    fetch(row + step);
+    row_sum<TPR>(ss, none, red[0]);
+    const float ix = rsqrtf(ss / n + a.eps);
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int c = lane + i * TPR;
+      float g[8], r[8];
+      kg[i].get(g);
+      kr[i].get(r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float u = v[i][j] * ix * ws[i][j];
+        if (a.gate) u *= sigmoid(g[j]);
+        v[i][j] = rounded<T>(r[j] + u);
+        ss = fmaf(v[i][j], v[i][j], ss);
+      }
+      if (live && c < nv) store8(static_cast<T*>(a.residual_out) + row * a.D + 8 * c, v[i]);
+    }
+    row_sum<TPR>(ss, none, red[1]);
+    const float ir = rsqrtf(ss / n + a.eps);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int c = lane + i * TPR;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * ir * wp[i][j];
+      if (live && c < nv) store8(static_cast<T*>(a.y) + row * a.D + 8 * c, v[i]);
+    }
+  }
+}
+
+// Each thread keeps its columns' sums in registers over all its rows; the CTA's row groups
+// add theirs at the end, in a fixed order, to one row of `partial` ([2, D]: m and dpre).
+template <typename T, int TPR, int VEC>
+__global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads<TPR>() : 1)
+    block_norms_bwd_kernel(const BlockNormsBwdArgs a) {
+  constexpr int kThreads = threads<TPR>(), kRows = kThreads / TPR;
+  __shared__ float2 red[2][16];
+  __shared__ float sums[kRows > 1 ? kThreads * 8 : 1];
+  const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int nv = a.D / 8;
+  float ws[VEC][8], wp[VEC][8], dm[VEC][8], dp[VEC][8];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dm[i][j] = dp[i][j] = 0.f;
+  struct Row {
+    Raw8<T> x[VEC], g[VEC], r[VEC], y[VEC], d[VEC];
+  } in;
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int c = lane + i * TPR;
+      in.d[i].zero();
+      in.g[i].zero();
+      if (row < a.rows && c < nv) {
+        in.r[i].load(static_cast<const T*>(a.sum) + row * a.D + 8 * c);
+        in.y[i].load(static_cast<const T*>(a.dy) + row * a.D + 8 * c);
+        if (a.dres) in.d[i].load(static_cast<const T*>(a.dres) + row * a.D + 8 * c);
+        in.x[i].load(static_cast<const T*>(a.x) + row * a.D + 8 * c);
+        if (a.gate) in.g[i].load(static_cast<const T*>(a.gate) + row * a.D + 8 * c);
+      } else {
+        in.r[i].zero();
+        in.y[i].zero();
+        in.x[i].zero();
+      }
+    }
+  };
+  const long long step = static_cast<long long>(gridDim.x) * kRows;
+  fetch(static_cast<long long>(blockIdx.x) * kRows + sub);
+  load_weights<TPR, VEC>(a.post, a.scale, a.pre, lane, nv, ws, wp);
+  const float n = static_cast<float>(a.D);
+  for (long long r0 = static_cast<long long>(blockIdx.x) * kRows; r0 < a.rows; r0 += step) {
+    const long long row = r0 + sub;
+    const bool live = row < a.rows;
+    const Row cur = in;
+    float ss = 0.f, dot = 0.f, xx = 0.f, none = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      float r[8], dy[8];
+      cur.r[i].get(r);
+      cur.y[i].get(dy);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ss = fmaf(r[j], r[j], ss);
+        dot = fmaf(wp[i][j] * dy[j], r[j], dot);
+      }
+    }
+    fetch(row + step);
+    row_sum<TPR>(ss, dot, red[0]);
+    const float ir = rsqrtf(ss / n + a.eps);
+    const float mr = ir * ir * (dot / n);
+    dot = 0.f;
+    float dr[VEC][8];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int c = lane + i * TPR;
+      float r[8], dy[8], x[8], g[8];
+      cur.r[i].get(r);
+      cur.y[i].get(dy);
+      cur.x[i].get(x);
+      cur.g[i].get(g);
+      cur.d[i].get(dr[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dp[i][j] = fmaf(dy[j], r[j] * ir, dp[i][j]);
+        dr[i][j] += ir * (wp[i][j] * dy[j] - r[j] * mr);
+        float t = dr[i][j] * ws[i][j];
+        if (a.gate) t *= sigmoid(g[j]);
+        xx = fmaf(x[j], x[j], xx);
+        dot = fmaf(t, x[j], dot);
+      }
+      if (live && c < nv) store8(static_cast<T*>(a.dresidual) + row * a.D + 8 * c, dr[i]);
+    }
+    row_sum<TPR>(xx, dot, red[1]);
+    (void)none;
+    const float ix = rsqrtf(xx / n + a.eps);
+    const float mx = ix * ix * (dot / n);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int c = lane + i * TPR;
+      float x[8], g[8], dx[8], dg[8];
+      cur.x[i].get(x);
+      cur.g[i].get(g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float sg = a.gate ? sigmoid(g[j]) : 1.f;
+        const float nx = x[j] * ix, t = dr[i][j] * ws[i][j] * sg;
+        dm[i][j] = fmaf(dr[i][j] * sg, nx, dm[i][j]);
+        dg[j] = t * nx * (1.f - sg);
+        dx[j] = ix * (t - x[j] * mx);
+      }
+      if (!(live && c < nv)) continue;
+      store8(static_cast<T*>(a.dx) + row * a.D + 8 * c, dx);
+      if (a.gate) store8(static_cast<T*>(a.dgate) + row * a.D + 8 * c, dg);
+    }
+  }
+#pragma unroll
+  for (int part = 0; part < 2; ++part)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int c = lane + i * TPR;
+      float s[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = part ? dp[i][j] : dm[i][j];
+      if constexpr (kRows > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[threadIdx.x * 8 + j] = s[j];
+        __syncthreads();
+        if (sub == 0)
+          for (int r = 1; r < kRows; ++r)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] += sums[(r * TPR + lane) * 8 + j];
+      }
+      if (sub == 0 && c < nv) {
+        float4* p = reinterpret_cast<float4*>(
+            a.partial + (static_cast<size_t>(blockIdx.x) * 2 + part) * a.D + 8 * c);
+        p[0] = make_float4(s[0], s[1], s[2], s[3]);
+        p[1] = make_float4(s[4], s[5], s[6], s[7]);
+      }
+    }
+}
+
+__global__ void __launch_bounds__(1024) block_weights_kernel(const BlockNormsBwdArgs a, int rows) {
+  column_sum(a.partial, rows, 2 * a.D, [&](int i, float s) {
+    if (i >= a.D) {
+      a.dpre[i - a.D] = s;
+    } else {
+      a.dpost[i] = a.scale ? s * a.scale[i] : s;
+      if (a.scale) a.dscale[i] = s * a.post[i];
+    }
+  });
+}
+
+// Threads per row and vectors per thread for a row of D columns.
+template <class F>
+cudaError_t by_width(int D, F f) {
+  const int nv = D / 8;
+  using std::integral_constant;
+  if (nv <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (nv <= 64) return f(integral_constant<int, 32>{}, integral_constant<int, kVec>{});
+  if (nv <= 128) return f(integral_constant<int, 64>{}, integral_constant<int, kVec>{});
+  if (nv <= 256) return f(integral_constant<int, 128>{}, integral_constant<int, kVec>{});
+  if (nv <= 512) return f(integral_constant<int, 256>{}, integral_constant<int, kVec>{});
+  return f(integral_constant<int, 512>{}, integral_constant<int, kVec>{});
+}
+
+int ctas(long long rows, int per_cta, int most) {
+  const long long want = (rows + per_cta - 1) / per_cta;
+  return static_cast<int>(want < most ? want : most);
+}
+
+// CTAs of a kernel that all SMs hold at once, asked for once per device.
+template <auto Kern>
+int resident(int threads) {
+  constexpr int kMaxDevices = 64;
+  static int held[kMaxDevices] = {};
+  int dev = 0, sms = 0, per = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 1;
+  if (held[dev] == 0 &&
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kern, threads, 0) == cudaSuccess)
+    held[dev] = sms * per;
+  return held[dev] > 0 ? held[dev] : 1;
+}
+
+template <typename T>
+cudaError_t fwd(const BlockNormsArgs& a, cudaStream_t stream) {
+  return by_width(a.D, [&](auto tpr, auto vec) {
+    constexpr int kThreads = threads<tpr>(), kRows = kThreads / tpr;
+    const int grid = ctas(a.rows, kRows, resident<block_norms_kernel<T, tpr, vec>>(kThreads));
+    block_norms_kernel<T, tpr, vec><<<grid, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+template <typename T>
+cudaError_t bwd(const BlockNormsBwdArgs& a, cudaStream_t stream) {
+  return by_width(a.D, [&](auto tpr, auto vec) {
+    constexpr int kThreads = threads<tpr>(), kRows = kThreads / tpr;
+    const int grid = ctas(a.rows, kRows, kBwdCtas * 256 / kThreads);
+    block_norms_bwd_kernel<T, tpr, vec><<<grid, kThreads, 0, stream>>>(a);
+    block_weights_kernel<<<(2 * a.D + 31) / 32, 1024, 0, stream>>>(a, grid);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace
+
+size_t block_norms_bwd_workspace_bytes(long long rows, int D) {
+  size_t bytes = 0;
+  by_width(D, [&](auto tpr, auto) {
+    constexpr int kThreads = threads<tpr>(), kRows = kThreads / tpr;
+    bytes = static_cast<size_t>(ctas(rows, kRows, kBwdCtas * 256 / kThreads)) * 2 * D *
+            sizeof(float);
+    return cudaSuccess;
+  });
+  return bytes;
+}
+
+cudaError_t launch_block_norms(const BlockNormsArgs& a, bool f32, cudaStream_t stream) {
+  return f32 ? fwd<float>(a, stream) : fwd<__nv_bfloat16>(a, stream);
+}
+cudaError_t launch_block_norms_bwd(const BlockNormsBwdArgs& a, bool f32, cudaStream_t stream) {
+  return f32 ? bwd<float>(a, stream) : bwd<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace gdr

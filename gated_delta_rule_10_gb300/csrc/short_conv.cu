@@ -1,0 +1,421 @@
+// Short causal convolution: one filter of K taps (2 to 4) for each channel,
+//   s_t = bias + sum_{j<K} w[K-1-j] x_{t-j},   y = s sigmoid(s) or s,
+// with taps that stop at a document's first token, and its gradients
+//   ds = dy act'(s),  dx_t = sum_j w[K-1-j] ds_{t+j},  dw[K-1-j] = sum_t ds_t x_{t-j}.
+//
+// Streams bound by HBM: a thread walks a run of consecutive tokens of 8 channels (a 16-byte
+// vector of bf16; the backward 4, for its sums) with the last K - 1 inputs in registers,
+// so that a token is read once per run plus K - 1 rows before it, and loads of several
+// tokens are in flight. Neighbouring threads have neighbouring channels.
+#include <type_traits>
+
+#include "column_sum.cuh"
+#include "short_conv.h"
+#include "vec_io.cuh"
+
+namespace gdr {
+namespace {
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
+
+// V elements as they are in memory (V = 4 or 8).
+template <typename T, int V>
+struct Raw {
+  static constexpr int kWords = V * sizeof(T) / 4;
+  uint32_t u[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 2) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+      u[0] = q.x;
+      u[1] = q.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        u[4 * i] = q.x;
+        u[4 * i + 1] = q.y;
+        u[4 * i + 2] = q.z;
+        u[4 * i + 3] = q.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kWords == 2) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] =
+            make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) u[i] = 0u;
+  }
+  __device__ __forceinline__ void get(float (&x)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = __uint_as_float(u[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&x)[V]) {   // one rounding
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[i] = __float_as_uint(x[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) u[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    }
+  }
+};
+
+template <int K, int V>
+__device__ __forceinline__ void load_filter(const ConvArgs& a, int c, float (&w)[K][V],
+                                            float (&bias)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][i] = __ldg(a.weight + static_cast<long long>(c + i) * K + k);
+    bias[i] = a.bias ? __ldg(a.bias + c + i) : 0.f;
+  }
+}
+
+// Row t of the sequence, t >= -(K - 1): the state's rows come before token 0.
+template <typename T, int K, int V>
+__device__ __forceinline__ void load_row(const ConvArgs& a, int b, int t, int c, Raw<T, V>& r) {
+  if (t >= 0)
+    r.load(static_cast<const T*>(a.x) + (static_cast<long long>(b) * a.T + t) * a.xs + c);
+  else if (a.state)
+    r.load(static_cast<const T*>(a.state) + (static_cast<long long>(b) * (K - 1) + K - 1 + t) * a.D + c);
+  else
+    r.zero();
+}
+
+// How many tokens behind token t are of its document, at most K - 1 (the state counts as
+// the same one).
+template <int K>
+__device__ __forceinline__ int reach(const unsigned char* starts, int t) {
+  int r = 0;
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j)
+    if (r == j && !(t - j >= 0 && starts[t - j])) r = j + 1;
+  return r;
+}
+
+constexpr int kFwdThreads = 128;
+constexpr int kAhead = 4;          // tokens requested together
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs a, int run,
+                                                                 int runs, long long total) {
+  constexpr int V = 8;
+  const long long id = static_cast<long long>(blockIdx.x) * kFwdThreads + threadIdx.x;
+  if (id >= total) return;
+  const int nv = a.D / V;
+  const int c = static_cast<int>(id % nv) * V;
+  const long long rest = id / nv;
+  const int t0 = static_cast<int>(rest % runs) * run, b = static_cast<int>(rest / runs);
+  const int t1 = min(t0 + run, a.T);
+  const unsigned char* starts = a.starts ? a.starts + static_cast<long long>(b) * a.T : nullptr;
+  const T* x = static_cast<const T*>(a.x) + static_cast<long long>(b) * a.T * a.xs + c;
+  T* y = static_cast<T*>(a.y) + static_cast<long long>(b) * a.T * a.D + c;
+  float w[K][V], bias[V], prev[K - 1][V];    // prev[j]: the row j + 1 tokens back
+  Raw<T, V> raw[kAhead];
+  load_filter<K, V>(a, c, w, bias);
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) load_row<T, K, V>(a, b, t0 - 1 - j, c, raw[j]);
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) raw[j].get(prev[j]);
+  if (starts && t0 > 0) {      // the run's first token may be in the middle of a document
+    const int r = reach<K>(starts, t0 - 1);
+#pragma unroll
+    for (int j = 1; j < K - 1; ++j)
+      if (j > r)
+#pragma unroll
+        for (int i = 0; i < V; ++i) prev[j][i] = 0.f;
+  }
+  for (int t = t0; t < t1; t += kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (t + k < t1) raw[k].load(x + static_cast<long long>(t + k) * a.xs);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (t + k >= t1) break;
+      if (starts && starts[t + k])
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) prev[j][i] = 0.f;
+      float v[V], s[V];
+      raw[k].get(v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[i] = fmaf(w[K - 1][i], v[i], bias[i]);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) s[i] = fmaf(w[K - 2 - j][i], prev[j][i], s[i]);
+        if (a.silu) s[i] *= sigmoid(s[i]);
+      }
+      store8(y + static_cast<long long>(t + k) * a.D, s);
+#pragma unroll
+      for (int j = K - 2; j > 0; --j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) prev[j][i] = prev[j - 1][i];
+#pragma unroll
+      for (int i = 0; i < V; ++i) prev[0][i] = v[i];
+    }
+  }
+  if (t1 == a.T && a.state_out) {     // prev is the last rows, zeros behind a start
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      Raw<T, V> r;
+      r.put(prev[j]);
+      r.store(static_cast<T*>(a.state_out) +
+              (static_cast<long long>(b) * (K - 1) + K - 2 - j) * a.D + c);
+    }
+  }
+}
+
+// Gradients: a warp has 128 channels (4 a thread) of one run of tokens, a CTA kRuns
+// neighbouring runs, whose filter gradients it adds up in a fixed order to one row of
+// `partial` ([K + 1, D], the last row the bias's); column_sum adds those rows. A run walks
+// K - 1 tokens past its end for what they pass back.
+constexpr int kRuns = 8;
+constexpr int kBwdThreads = 32 * kRuns;
+constexpr int kBwdRun = 32;
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kBwdThreads) short_conv_bwd_kernel(const ConvArgs a, int groups,
+                                                                     int slices) {
+  constexpr int V = 4;
+  __shared__ float sums[kRuns][K + 1][32 * V];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int slice = blockIdx.x % slices, c = (slice * 32 + lane) * V;
+  const int rest = blockIdx.x / slices, b = rest / groups, group = rest % groups;
+  const int t0 = (group * kRuns + warp) * kBwdRun, t1 = min(t0 + kBwdRun, a.T);
+  float dw[K + 1][V];
+#pragma unroll
+  for (int k = 0; k <= K; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[k][i] = 0.f;
+  if (c < a.D && t0 < a.T) {
+    const unsigned char* starts = a.starts ? a.starts + static_cast<long long>(b) * a.T : nullptr;
+    const T* dyp = static_cast<const T*>(a.dy) + static_cast<long long>(b) * a.T * a.D + c;
+    T* dxp = static_cast<T*>(a.dx) + static_cast<long long>(b) * a.T * a.D + c;
+    T* dst = a.dstate ? static_cast<T*>(a.dstate) + static_cast<long long>(b) * (K - 1) * a.D + c
+                      : nullptr;
+    float w[K][V], bias[V], prev[K - 1][V], acc[K][V];   // acc[j]: dx of the token j back
+    load_filter<K, V>(a, c, w, bias);
+    Raw<T, V> rx[kAhead], ry[kAhead];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) load_row<T, K, V>(a, b, t0 - 1 - j, c, rx[j]);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) rx[j].get(prev[j]);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
+    // tokens behind the current one that are of its document, up to K - 1
+    int back = K - 2;
+    if (starts && t0 > 0) back = reach<K>(starts, t0 - 1);
+    // a finished row: of this run's tokens, or the state's before the first
+    auto emit = [&](int e, const float (&v)[V]) {
+      Raw<T, V> r;
+      r.put(v);
+      if (e >= t0)
+        r.store(dxp + static_cast<long long>(e) * a.D);
+      else if (t0 == 0 && dst)
+        r.store(dst + static_cast<long long>(K - 1 + e) * a.D);
+    };
+    const int stop = min(t1 + K - 1, a.T);
+    for (int t = t0; t < stop; t += kAhead) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (t + k < stop) {
+          rx[k].load(static_cast<const T*>(a.x) + (static_cast<long long>(b) * a.T + t + k) * a.xs + c);
+          ry[k].load(dyp + static_cast<long long>(t + k) * a.D);
+        }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int now = t + k;
+        if (now >= stop) break;
+        back = min(back + 1, K - 1);
+        if (starts && starts[now]) back = 0;
+        float v[V], g[V];
+        rx[k].get(v);
+        ry[k].get(g);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+          if (j + 1 > back)
+#pragma unroll
+            for (int i = 0; i < V; ++i) prev[j][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (a.silu) {
+            float s = fmaf(w[K - 1][i], v[i], bias[i]);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) s = fmaf(w[K - 2 - j][i], prev[j][i], s);
+            const float sg = sigmoid(s);
+            // where sigmoid is zero, s may be -inf and the slope is still zero
+            g[i] *= sg * (1.f + (sg > 0.f ? s * (1.f - sg) : 0.f));
+          }
+          acc[0][i] = fmaf(w[K - 1][i], g[i], acc[0][i]);
+#pragma unroll
+          for (int j = 1; j < K; ++j)
+            if (j <= back) acc[j][i] = fmaf(w[K - 1 - j][i], g[i], acc[j][i]);
+          if (now < t1) {
+            dw[K - 1][i] = fmaf(g[i], v[i], dw[K - 1][i]);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) dw[K - 2 - j][i] = fmaf(g[i], prev[j][i], dw[K - 2 - j][i]);
+            dw[K][i] += g[i];
+          }
+        }
+        emit(now - (K - 1), acc[K - 1]);
+#pragma unroll
+        for (int j = K - 1; j > 0; --j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[j][i] = acc[j - 1][i];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[0][i] = 0.f;
+#pragma unroll
+        for (int j = K - 2; j > 0; --j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) prev[j][i] = prev[j - 1][i];
+#pragma unroll
+        for (int i = 0; i < V; ++i) prev[0][i] = v[i];
+      }
+    }
+    if (stop == a.T) {   // what is behind the last token comes from the state's gradient
+#pragma unroll
+      for (int j = 1; j < K; ++j) {
+        const int e = a.T - j;
+        if (a.dstate_out && j - 1 <= back) {
+          Raw<T, V> r;
+          float g[V];
+          r.load(static_cast<const T*>(a.dstate_out) +
+                 (static_cast<long long>(b) * (K - 1) + K - 1 - j) * a.D + c);
+          r.get(g);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[j][i] += g[i];
+        }
+        if (e < t1) emit(e, acc[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k <= K; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[warp][k][lane * V + i] = dw[k][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < (K + 1) * 32 * V; i += kBwdThreads) {
+    const int k = i / (32 * V), j = i % (32 * V), d = slice * 32 * V + j;
+    float s = sums[0][k][j];
+#pragma unroll
+    for (int r = 1; r < kRuns; ++r) s += sums[r][k][j];
+    if (d < a.D) a.partial[(static_cast<size_t>(rest) * (K + 1) + k) * a.D + d] = s;
+  }
+}
+
+__global__ void __launch_bounds__(1024) filter_grad_kernel(const ConvArgs a, int rows) {
+  column_sum(a.partial, rows, (a.K + 1) * a.D, [&](int i, float s) {
+    const int k = i / a.D, d = i % a.D;
+    if (k < a.K)
+      a.dweight[static_cast<long long>(d) * a.K + k] = s;
+    else if (a.dbias)
+      a.dbias[d] = s;
+  });
+}
+
+// One token of each sequence: a thread has 8 channels of one.
+template <typename T, int K>
+__global__ void __launch_bounds__(kFwdThreads) short_conv_step_kernel(const ConvArgs a,
+                                                                      long long total) {
+  constexpr int V = 8;
+  const long long id = static_cast<long long>(blockIdx.x) * kFwdThreads + threadIdx.x;
+  if (id >= total) return;
+  const int nv = a.D / V, c = static_cast<int>(id % nv) * V;
+  const long long b = id / nv;
+  T* st = static_cast<T*>(a.state_out) + b * (K - 1) * a.D + c;
+  Raw<T, V> r[K];
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) r[k].load(st + static_cast<long long>(k) * a.D);
+  r[K - 1].load(static_cast<const T*>(a.x) + b * a.xs + c);
+  float w[K][V], s[V];
+  load_filter<K, V>(a, c, w, s);
+#pragma unroll
+  for (int k = K - 1; k >= 0; --k) {
+    float v[V];
+    r[k].get(v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = fmaf(w[k][i], v[i], s[i]);
+  }
+  if (a.silu)
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] *= sigmoid(s[i]);
+  store8(static_cast<T*>(a.y) + b * a.D + c, s);
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) r[k + 1].store(st + static_cast<long long>(k) * a.D);
+}
+
+template <class F>
+cudaError_t by_taps(int K, bool f32, F f) {
+  using std::integral_constant;
+  auto typed = [&](auto k) { return f32 ? f(float{}, k) : f(__nv_bfloat16{}, k); };
+  if (K == 2) return typed(integral_constant<int, 2>{});
+  if (K == 3) return typed(integral_constant<int, 3>{});
+  return typed(integral_constant<int, 4>{});
+}
+
+// The CTAs' rows of partial sums: one for each batch row and kRuns runs.
+int bwd_groups(int T) { return (T + kRuns * kBwdRun - 1) / (kRuns * kBwdRun); }
+
+}  // namespace
+
+size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int K) {
+  return static_cast<size_t>(B) * bwd_groups(T) * (K + 1) * D * sizeof(float);
+}
+
+cudaError_t launch_short_conv(const ConvArgs& a, bool f32, cudaStream_t stream) {
+  // runs of 32 tokens where those fill the GPU's threads, else short ones
+  const long long vecs = static_cast<long long>(a.B) * (a.D / 8);
+  const int run = vecs * ((a.T + 31) / 32) >= 152 * 1024 ? 32 : 8;
+  const int runs = (a.T + run - 1) / run;
+  const long long total = vecs * runs, grid = (total + kFwdThreads - 1) / kFwdThreads;
+  if (grid > 2147483647LL) return cudaErrorInvalidValue;
+  return by_taps(a.K, f32, [&](auto t, auto k) {
+    short_conv_kernel<decltype(t), k><<<static_cast<unsigned>(grid), kFwdThreads, 0, stream>>>(
+        a, run, runs, total);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_short_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t stream) {
+  const int groups = bwd_groups(a.T), slices = (a.D + 127) / 128;
+  const long long grid = static_cast<long long>(slices) * a.B * groups;
+  if (grid > 2147483647LL) return cudaErrorInvalidValue;
+  return by_taps(a.K, f32, [&](auto t, auto k) {
+    short_conv_bwd_kernel<decltype(t), k>
+        <<<static_cast<unsigned>(grid), kBwdThreads, 0, stream>>>(a, groups, slices);
+    filter_grad_kernel<<<((a.K + 1) * a.D + 31) / 32, 1024, 0, stream>>>(a, a.B * groups);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_short_conv_step(const ConvArgs& a, bool f32, cudaStream_t stream) {
+  const long long total = static_cast<long long>(a.B) * (a.D / 8);
+  const long long grid = (total + kFwdThreads - 1) / kFwdThreads;
+  if (grid > 2147483647LL) return cudaErrorInvalidValue;
+  return by_taps(a.K, f32, [&](auto t, auto k) {
+    short_conv_step_kernel<decltype(t), k>
+        <<<static_cast<unsigned>(grid), kFwdThreads, 0, stream>>>(a, total);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace gdr

@@ -717,6 +717,154 @@ typedef struct {
 gdr_status gdr_rotary_table(int length, int rot, double base, const gdr_rotary_scaling* scaling,
                             float* cos_table, float* sin_table, gdr_stream_t stream);
 
+/*
+ * Short causal convolution over the tokens, one filter of K taps for each channel (the
+ * stage between a layer's input projection and q, k and v: Gated DeltaNet-2 notes,
+ * overall framework; LLMs from scratch ch. 11, section 11.3):
+ *
+ *   s_t = bias + sum_{j<K} weight[:, K-1-j] (.) x_{t-j},   y = s sigmoid(s) with silu, else s.
+ *
+ * x [B,T,D] in dtype, consecutive tokens x_stride elements apart (0: dense), batch rows T
+ * tokens apart; weight [D,K] and bias [D] fp32 (bias may be NULL: zero). Before the first
+ * token come the K - 1 rows of state [B,K-1,D] in dtype (NULL: zeros), and state_out (may
+ * be NULL) receives the last K - 1 rows, from which a next call continues. `starts` [B,T]
+ * bytes (may be NULL): a token with a nonzero byte begins a document, whose taps do not
+ * reach behind it; rows of state_out that are of an earlier document are zeros. y and
+ * every gradient are dense.
+ *
+ * Sizes: K from 2 to 4; D a multiple of 8, at most 2^20; T up to 2^30, B up to 65535.
+ * Pointers are 16-byte aligned (starts any), x_stride a multiple of 16 bytes. Arithmetic
+ * is fp32, rounded once. Outputs overlap no input (state_out not state either). A value
+ * that is not finite reaches its own and the next K - 1 tokens of its document.
+ */
+typedef struct {
+  int B, T, D, K;
+  int dtype;            /* gdr_dtype of x, y, the states and their gradients */
+  int silu;             /* nonzero: the activation */
+  long long x_stride;   /* elements between tokens, 0: dense */
+} gdr_conv_shape;
+
+gdr_status gdr_short_conv_fwd(const gdr_conv_shape* shape, const void* x, const float* weight,
+                              const float* bias, const unsigned char* starts, const void* state,
+                              void* y, void* state_out, gdr_stream_t stream);
+
+/*
+ * Gradients of L = <dy, y> + <dstate_out, state_out> (dstate_out may be NULL: zero): dx
+ * [B,T,D] and dstate [B,K-1,D] (may be NULL) in dtype, dweight [D,K] and dbias [D] (may
+ * be NULL) fp32. workspace: at least gdr_short_conv_bwd_workspace() bytes, 16-byte
+ * aligned; calls sharing one must be ordered. No sum uses atomics.
+ */
+gdr_status gdr_short_conv_bwd_workspace(const gdr_conv_shape* shape, size_t* bytes);
+gdr_status gdr_short_conv_bwd(const gdr_conv_shape* shape, const void* x, const float* weight,
+                              const float* bias, const unsigned char* starts, const void* state,
+                              const void* dy, const void* dstate_out, void* dx, float* dweight,
+                              float* dbias, void* dstate, void* workspace, size_t ws_bytes,
+                              gdr_stream_t stream);
+
+/* One token of each of B sequences (T = 1): x [B,D] (rows x_stride apart), state [B,K-1,D]
+ * is read and moved on by one row in place, y [B,D]. */
+gdr_status gdr_short_conv_step(const gdr_conv_shape* shape, const void* x, const float* weight,
+                               const float* bias, void* state, void* y, gdr_stream_t stream);
+
+/*
+ * State space recurrence with a decay for each token, channel and state: N states for each
+ * of D channels, which do not mix,
+ *
+ *   u_t = softplus(dt_t + dt_bias)       (softplus nonzero; else dt_t + dt_bias)
+ *   h_t[d,n] = exp(u_t[d] A[d,n]) h_{t-1}[d,n] + u_t[d] x_t[d] Bm_t[g,n]
+ *   y_t[d] = (sum_n Cm_t[g,n] h_t[d,n] + skip[d] x_t[d]) * z_t[d] sigmoid(z_t[d])
+ *
+ * with g = d / (D / G): Bm and Cm are shared by the D / G channels of a group. skip, dt_bias
+ * and z may be NULL (no such term, zero, no gate). Where the decays of a head are one number
+ * this is gdr_decay_chunk_fwd, with larger states; here every channel has its own.
+ *
+ * x, dt, z [B,T,D] and Bm, Cm [B,T,G,N] in dtype, A [D,N], skip, dt_bias [D] fp32; consecutive
+ * tokens of the former are their stride's elements apart (0: dense), batch rows T tokens
+ * apart, so that parts of one projection are taken as they are. h0 [B,D,N] fp32 or NULL
+ * (zero), hT the end state or NULL; starts as above: a start clears the state before its
+ * token. y is dense. h0 and hT may be one buffer; other outputs overlap no input.
+ *
+ * Sizes: N in {8, 16, 32, 64}; D / G a multiple of 8, D up to 2^20; T up to 2^30, B up to
+ * 65535. Pointers are 16-byte aligned (starts any), strides multiples of 16 bytes. A is
+ * finite and usually negative. The state, the decays and every sum are fp32; y is rounded
+ * once. A value that is not finite reaches the later tokens of its document and channel (a
+ * group's channels, from Bm), in the gradients also the earlier ones.
+ */
+typedef struct {
+  int B, T, D, G, N;
+  int dtype;            /* gdr_dtype of x, dt, z, Bm, Cm, y and their gradients */
+  int softplus;
+  long long x_stride, dt_stride, z_stride, b_stride, c_stride; /* elements, 0: dense */
+} gdr_state_space_shape;
+
+/* Device workspace bytes of gdr_state_space_fwd (0 where B * D * N fills the GPU; otherwise
+ * the sequences are cut into segments whose states it holds). */
+gdr_status gdr_state_space_fwd_workspace(const gdr_state_space_shape* shape, size_t* bytes);
+gdr_status gdr_state_space_fwd(const gdr_state_space_shape* shape, const void* x, const void* dt,
+                               const float* A, const void* Bm, const void* Cm, const float* skip,
+                               const void* z, const float* dt_bias, const unsigned char* starts,
+                               const float* h0, void* y, float* hT, void* workspace,
+                               size_t ws_bytes, gdr_stream_t stream);
+
+/*
+ * Gradients of L = <dy, y> + <dhT, hT> (dy dense; dhT [B,D,N] fp32 or NULL: zero): dx, ddt, dz
+ * [B,T,D] and dBm, dCm [B,T,G,N] in dtype, dA [D,N], dskip, ddt_bias [D] and dh0 [B,D,N] fp32.
+ * dskip, dz and ddt_bias are needed with skip, z and dt_bias and else not written; dh0 may be
+ * NULL. dhT and dh0 may be one buffer. workspace: at least gdr_state_space_bwd_workspace()
+ * bytes, 16-byte aligned (the states at every 16th token among them: D * N * 4 bytes each).
+ * No sum uses atomics.
+ */
+gdr_status gdr_state_space_bwd_workspace(const gdr_state_space_shape* shape, size_t* bytes);
+gdr_status gdr_state_space_bwd(const gdr_state_space_shape* shape, const void* x, const void* dt,
+                               const float* A, const void* Bm, const void* Cm, const float* skip,
+                               const void* z, const float* dt_bias, const unsigned char* starts,
+                               const float* h0, const void* dy, const float* dhT, void* dx,
+                               void* ddt, float* dA, void* dBm, void* dCm, float* dskip, void* dz,
+                               float* ddt_bias, float* dh0, void* workspace, size_t ws_bytes,
+                               gdr_stream_t stream);
+
+/* One token of each of B sequences (T = 1): state [B,D,N] fp32 is read as h_{t-1} and
+ * overwritten with h_t; the strides are those between sequences. */
+gdr_status gdr_state_space_step(const gdr_state_space_shape* shape, const void* x, const void* dt,
+                                const float* A, const void* Bm, const void* Cm, const float* skip,
+                                const void* z, const float* dt_bias, float* state, void* y,
+                                gdr_stream_t stream);
+
+/*
+ * The norms after and before a block, with the block's gate and scale on its way into the
+ * residual, over `rows` dense rows of D columns:
+ *
+ *   u = x / sqrt(mean_c x^2 + eps) * post_weight            (after the block whose output is x)
+ *   residual_out = residual + scale (.) sigmoid(gate) (.) u   (rounded to dtype)
+ *   y = residual_out / sqrt(mean_c residual_out^2 + eps) * pre_weight    (before the next)
+ *
+ * x, gate, residual, residual_out, y in dtype; post_weight, scale, pre_weight [D] fp32;
+ * gate and scale may be NULL (ones). Arithmetic is fp32. residual_out may be x, gate or
+ * residual, and y any of them that is not residual_out; other overlaps are not allowed.
+ * Pointers are 16-byte aligned; D a multiple of 8, at most 8192, rows < 2^31
+ * (GDR_ERR_UNSUPPORTED beyond). rows = 0 launches nothing. The sums of squares must stay
+ * below 3.4e38, and rows that are not finite give what gdr_add_rmsnorm's do.
+ */
+gdr_status gdr_block_norms(long long rows, int D, gdr_dtype dtype, const void* x, const void* gate,
+                           const void* residual, const float* post_weight, const float* scale,
+                           const float* pre_weight, float eps, void* residual_out, void* y,
+                           gdr_stream_t stream);
+
+/*
+ * Gradients of gdr_block_norms for dy of y and dres of residual_out (in dtype; dres may be
+ * NULL). sum is the forward's residual_out. dx, dgate (with gate), dresidual [rows,D] in
+ * dtype; dpost, dscale (with scale), dpre [D] fp32. dx, dgate and dresidual may be any of
+ * the inputs of their kind (each a different one). workspace: at least
+ * gdr_block_norms_bwd_workspace() bytes, 16-byte aligned. No sum uses atomics.
+ */
+gdr_status gdr_block_norms_bwd_workspace(long long rows, int D, size_t* bytes);
+gdr_status gdr_block_norms_bwd(long long rows, int D, gdr_dtype dtype, const void* dy,
+                               const void* dres, const void* x, const void* gate, const void* sum,
+                               const float* post_weight, const float* scale,
+                               const float* pre_weight, float eps, void* dx, void* dgate,
+                               void* dresidual, float* dpost, float* dscale, float* dpre,
+                               void* workspace, size_t ws_bytes, gdr_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* gdr_status_string(gdr_status status);
 
