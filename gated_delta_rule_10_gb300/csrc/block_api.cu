@@ -91,15 +91,17 @@ double waves(long long n) {
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
   const int tile = backward ? gdr::kSpaceTile : 32;
   const int tiles = (s->T + tile - 1) / tile, each = s->D / s->G;
-  const int channels = gdr::space_channels(s->N, backward);
+  const int channels = backward ? gdr::space_bwd_channels(s->N) : gdr::space_channels(s->N);
   sp->blocks = (each + channels - 1) / channels;
   const long long ctas = static_cast<long long>(s->B) * s->G * sp->blocks;
   double best = 0.0;
   int per = tiles;
   for (int n = 1; n <= 64 && n <= tiles; ++n) {
     const int len = (tiles + n - 1) / n, segments = (tiles + len - 1) / len;
-    double cost = waves(ctas * segments) * len;
-    if (segments > 1) cost += (backward ? 0.05 * waves(ctas * segments) : 0.7 * waves(ctas * (segments - 1))) * len + 2.0;
+    // (a CTA's start and end take as long as a tile)
+    double cost = waves(ctas * segments) * (len + 1.0);
+    if (segments > 1)
+      cost += backward ? 1.0 : 0.7 * waves(ctas * (segments - 1)) * (len + 1.0) + 2.0;
     if (n == 1 || cost < best) {
       best = cost;
       per = len;
@@ -232,7 +234,10 @@ gdr_status gdr_state_space_fwd(const gdr_state_space_shape* shape, const void* x
   a.starts = starts; a.h0 = h0; a.y = y; a.hT = hT;
   const bool f32 = shape->dtype == GDR_F32;
   cudaError_t err = cudaSuccess;
-  if (sp.segments > 1) err = gdr::launch_space_states(a, sp, f32, stream_of(stream));
+  if (sp.segments > 1) {
+    err = gdr::launch_space_states(a, sp, f32, stream_of(stream));
+    if (err == cudaSuccess) err = gdr::launch_space_chain(a, sp, false, stream_of(stream));
+  }
   if (err == cudaSuccess) err = gdr::launch_space_walk(a, sp, f32, stream_of(stream));
   return status_of(err);
 }
@@ -274,6 +279,7 @@ gdr_status gdr_state_space_bwd(const gdr_state_space_shape* shape, const void* x
   a.ddt_bias = ddt_bias; a.dh0 = dh0;
   const bool f32 = shape->dtype == GDR_F32;
   cudaError_t err = gdr::launch_space_bwd_states(a, sp, f32, stream_of(stream));
+  if (err == cudaSuccess) err = gdr::launch_space_chain(a, sp, true, stream_of(stream));
   if (err == cudaSuccess) err = gdr::launch_space_bwd(a, sp, f32, stream_of(stream));
   return status_of(err);
 }

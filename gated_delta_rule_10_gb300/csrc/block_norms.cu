@@ -8,7 +8,7 @@
 // scale and wa enter as one product, rounded to fp32 once.
 //
 // Streams bound by HBM: every row is read once and stays in registers through its two
-// sums. A row is spread over TPR threads, at most kVec vectors of 8 columns each; the CTAs
+// sums. A row is spread over TPR threads, one or two vectors of 8 columns each; the CTAs
 // are persistent, walk the rows and request the next row's vectors before the current
 // row's sums, so that loads are in flight through the barriers.
 #include "block_norms.h"
@@ -16,19 +16,18 @@
 #include <type_traits>
 
 #include "column_sum.cuh"
+#include "pair.cuh"
 #include "vec_io.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kVec = 2;          // 8-column vectors per thread, at most
 constexpr int kBwdCtas = 304;    // 2 x 152 SMs, of 256 threads: partial rows of the weights
 
 template <typename T>
 __device__ __forceinline__ float rounded(float x) {
   return static_cast<float>(static_cast<T>(x));
 }
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
 
 // Sums of two values over the TPR threads of a row; `red` has a slot per warp, and
 // consecutive calls take different ones of its parts, so one barrier each is enough.
@@ -297,17 +296,21 @@ __global__ void __launch_bounds__(1024) block_weights_kernel(const BlockNormsBwd
   });
 }
 
-// Threads per row and vectors per thread for a row of D columns.
-template <class F>
+// Threads per row and vectors per thread for a row of D columns. Two vectors a thread where
+// registers allow: fewer threads wait for a row's sums (forward, 65536 x 4096 bf16: 551 us
+// with one). The backward has five inputs and two sums a column (16384 x 2048: 255 us with
+// two, which spill).
+template <int VEC, class F>
 cudaError_t by_width(int D, F f) {
   const int nv = D / 8;
   using std::integral_constant;
   if (nv <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  if (nv <= 64) return f(integral_constant<int, 32>{}, integral_constant<int, kVec>{});
-  if (nv <= 128) return f(integral_constant<int, 64>{}, integral_constant<int, kVec>{});
-  if (nv <= 256) return f(integral_constant<int, 128>{}, integral_constant<int, kVec>{});
-  if (nv <= 512) return f(integral_constant<int, 256>{}, integral_constant<int, kVec>{});
-  return f(integral_constant<int, 512>{}, integral_constant<int, kVec>{});
+  if (nv <= 32 * VEC) return f(integral_constant<int, 32>{}, integral_constant<int, VEC>{});
+  if (nv <= 64 * VEC) return f(integral_constant<int, 64>{}, integral_constant<int, VEC>{});
+  if (nv <= 128 * VEC) return f(integral_constant<int, 128>{}, integral_constant<int, VEC>{});
+  if (nv <= 256 * VEC) return f(integral_constant<int, 256>{}, integral_constant<int, VEC>{});
+  if (nv <= 512 * VEC) return f(integral_constant<int, 512>{}, integral_constant<int, VEC>{});
+  return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
 }
 
 int ctas(long long rows, int per_cta, int most) {
@@ -331,7 +334,7 @@ int resident(int threads) {
 
 template <typename T>
 cudaError_t fwd(const BlockNormsArgs& a, cudaStream_t stream) {
-  return by_width(a.D, [&](auto tpr, auto vec) {
+  return by_width<2>(a.D, [&](auto tpr, auto vec) {
     constexpr int kThreads = threads<tpr>(), kRows = kThreads / tpr;
     const int grid = ctas(a.rows, kRows, resident<block_norms_kernel<T, tpr, vec>>(kThreads));
     block_norms_kernel<T, tpr, vec><<<grid, kThreads, 0, stream>>>(a);
@@ -341,7 +344,7 @@ cudaError_t fwd(const BlockNormsArgs& a, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t bwd(const BlockNormsBwdArgs& a, cudaStream_t stream) {
-  return by_width(a.D, [&](auto tpr, auto vec) {
+  return by_width<1>(a.D, [&](auto tpr, auto vec) {
     constexpr int kThreads = threads<tpr>(), kRows = kThreads / tpr;
     const int grid = ctas(a.rows, kRows, kBwdCtas * 256 / kThreads);
     block_norms_bwd_kernel<T, tpr, vec><<<grid, kThreads, 0, stream>>>(a);
@@ -354,7 +357,7 @@ cudaError_t bwd(const BlockNormsBwdArgs& a, cudaStream_t stream) {
 
 size_t block_norms_bwd_workspace_bytes(long long rows, int D) {
   size_t bytes = 0;
-  by_width(D, [&](auto tpr, auto) {
+  by_width<1>(D, [&](auto tpr, auto) {
     constexpr int kThreads = threads<tpr>(), kRows = kThreads / tpr;
     bytes = static_cast<size_t>(ctas(rows, kRows, kBwdCtas * 256 / kThreads)) * 2 * D *
             sizeof(float);

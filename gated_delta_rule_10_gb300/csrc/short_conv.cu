@@ -10,13 +10,12 @@
 #include <type_traits>
 
 #include "column_sum.cuh"
+#include "pair.cuh"
 #include "short_conv.h"
 #include "vec_io.cuh"
 
 namespace gdr {
 namespace {
-
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
 
 // V elements as they are in memory (V = 4 or 8).
 template <typename T, int V>
@@ -65,6 +64,18 @@ struct Raw {
       }
     }
   }
+  __device__ __forceinline__ void get(f32x2 (&x)[V / 2]) const {
+    float f[V];
+    get(f);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) x[i] = pair(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ __forceinline__ void put(const f32x2 (&x)[V / 2]) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) split(x[i], f[2 * i], f[2 * i + 1]);
+    put(f);
+  }
   __device__ __forceinline__ void put(const float (&x)[V]) {   // one rounding
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -76,14 +87,24 @@ struct Raw {
   }
 };
 
+// The filter of V channels, as pairs of channels.
 template <int K, int V>
-__device__ __forceinline__ void load_filter(const ConvArgs& a, int c, float (&w)[K][V],
-                                            float (&bias)[V]) {
+__device__ __forceinline__ void load_filter(const ConvArgs& a, int c, f32x2 (&w)[K][V / 2],
+                                            f32x2 (&bias)[V / 2]) {
+  float f[V * K], g[V];     // V * K consecutive floats
+  const float4* p = reinterpret_cast<const float4*>(a.weight + static_cast<long long>(c) * K);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+  for (int i = 0; i < V * K / 4; ++i) {
+    const float4 v = __ldg(p + i);
+    f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+  }
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k][i] = __ldg(a.weight + static_cast<long long>(c + i) * K + k);
-    bias[i] = a.bias ? __ldg(a.bias + c + i) : 0.f;
+  for (int i = 0; i < V; ++i) g[i] = a.bias ? __ldg(a.bias + c + i) : 0.f;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][i] = pair(f[2 * i * K + k], f[(2 * i + 1) * K + k]);
+    bias[i] = pair(g[2 * i], g[2 * i + 1]);
   }
 }
 
@@ -110,12 +131,12 @@ __device__ __forceinline__ int reach(const unsigned char* starts, int t) {
 }
 
 constexpr int kFwdThreads = 128;
-constexpr int kAhead = 4;          // tokens requested together
+constexpr int kBatch = 8;          // tokens requested together, one batch ahead
 
 template <typename T, int K>
 __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs a, int run,
                                                                  int runs, long long total) {
-  constexpr int V = 8;
+  constexpr int V = 4, H = V / 2;
   const long long id = static_cast<long long>(blockIdx.x) * kFwdThreads + threadIdx.x;
   if (id >= total) return;
   const int nv = a.D / V;
@@ -126,50 +147,68 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
   const unsigned char* starts = a.starts ? a.starts + static_cast<long long>(b) * a.T : nullptr;
   const T* x = static_cast<const T*>(a.x) + static_cast<long long>(b) * a.T * a.xs + c;
   T* y = static_cast<T*>(a.y) + static_cast<long long>(b) * a.T * a.D + c;
-  float w[K][V], bias[V], prev[K - 1][V];    // prev[j]: the row j + 1 tokens back
-  Raw<T, V> raw[kAhead];
+  f32x2 w[K][H], bias[H], prev[K - 1][H];    // prev[j]: the row j + 1 tokens back
+  struct Batch {
+    Raw<T, V> x[kBatch];
+    unsigned starts;
+  } cur;
+  auto fetch = [&](Batch& f, int t) {
+    f.starts = 0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (t + k < t1) {
+        f.x[k].load(x + static_cast<long long>(t + k) * a.xs);
+        if (starts) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
+      }
+  };
+  fetch(cur, t0);
   load_filter<K, V>(a, c, w, bias);
+  {
+    Raw<T, V> r[K - 1];
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) load_row<T, K, V>(a, b, t0 - 1 - j, c, raw[j]);
+    for (int j = 0; j < K - 1; ++j) load_row<T, K, V>(a, b, t0 - 1 - j, c, r[j]);
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) raw[j].get(prev[j]);
+    for (int j = 0; j < K - 1; ++j) r[j].get(prev[j]);
+  }
   if (starts && t0 > 0) {      // the run's first token may be in the middle of a document
     const int r = reach<K>(starts, t0 - 1);
 #pragma unroll
     for (int j = 1; j < K - 1; ++j)
       if (j > r)
 #pragma unroll
-        for (int i = 0; i < V; ++i) prev[j][i] = 0.f;
+        for (int i = 0; i < H; ++i) prev[j][i] = 0;
   }
-  for (int t = t0; t < t1; t += kAhead) {
+  for (int t = t0; t < t1; t += kBatch) {
+    Batch next;
+    fetch(next, t + kBatch);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (t + k < t1) raw[k].load(x + static_cast<long long>(t + k) * a.xs);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    for (int k = 0; k < kBatch; ++k) {
       if (t + k >= t1) break;
-      if (starts && starts[t + k])
+      if ((cur.starts >> k) & 1)
 #pragma unroll
         for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-          for (int i = 0; i < V; ++i) prev[j][i] = 0.f;
-      float v[V], s[V];
-      raw[k].get(v);
+          for (int i = 0; i < H; ++i) prev[j][i] = 0;
+      f32x2 v[H], s[H];
+      cur.x[k].get(v);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s[i] = fmaf(w[K - 1][i], v[i], bias[i]);
+      for (int i = 0; i < H; ++i) {
+        s[i] = fma2(w[K - 1][i], v[i], bias[i]);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) s[i] = fmaf(w[K - 2 - j][i], prev[j][i], s[i]);
-        if (a.silu) s[i] *= sigmoid(s[i]);
+        for (int j = 0; j < K - 1; ++j) s[i] = fma2(w[K - 2 - j][i], prev[j][i], s[i]);
+        if (a.silu) s[i] = mul2(s[i], sigmoid2(s[i]));
       }
-      store8(y + static_cast<long long>(t + k) * a.D, s);
+      Raw<T, V> out;
+      out.put(s);
+      out.store(y + static_cast<long long>(t + k) * a.D);
 #pragma unroll
       for (int j = K - 2; j > 0; --j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) prev[j][i] = prev[j - 1][i];
+        for (int i = 0; i < H; ++i) prev[j][i] = prev[j - 1][i];
 #pragma unroll
-      for (int i = 0; i < V; ++i) prev[0][i] = v[i];
+      for (int i = 0; i < H; ++i) prev[0][i] = v[i];
     }
+    cur = next;
   }
   if (t1 == a.T && a.state_out) {     // prev is the last rows, zeros behind a start
 #pragma unroll
@@ -189,43 +228,63 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
 constexpr int kRuns = 8;
 constexpr int kBwdThreads = 32 * kRuns;
 constexpr int kBwdRun = 32;
+constexpr int kBwdBatch = 4;
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kBwdThreads) short_conv_bwd_kernel(const ConvArgs a, int groups,
-                                                                     int slices) {
-  constexpr int V = 4;
-  __shared__ float sums[kRuns][K + 1][32 * V];
+__global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
+    short_conv_bwd_kernel(const ConvArgs a, int groups, int slices) {
+  constexpr int V = 4, H = V / 2;
+  __shared__ __align__(16) float sums[kRuns][K + 1][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slice = blockIdx.x % slices, c = (slice * 32 + lane) * V;
   const int rest = blockIdx.x / slices, b = rest / groups, group = rest % groups;
   const int t0 = (group * kRuns + warp) * kBwdRun, t1 = min(t0 + kBwdRun, a.T);
-  float dw[K + 1][V];
+  f32x2 dw[K + 1][H];
 #pragma unroll
   for (int k = 0; k <= K; ++k)
 #pragma unroll
-    for (int i = 0; i < V; ++i) dw[k][i] = 0.f;
+    for (int i = 0; i < H; ++i) dw[k][i] = 0;
   if (c < a.D && t0 < a.T) {
     const unsigned char* starts = a.starts ? a.starts + static_cast<long long>(b) * a.T : nullptr;
+    const T* xp = static_cast<const T*>(a.x) + static_cast<long long>(b) * a.T * a.xs + c;
     const T* dyp = static_cast<const T*>(a.dy) + static_cast<long long>(b) * a.T * a.D + c;
     T* dxp = static_cast<T*>(a.dx) + static_cast<long long>(b) * a.T * a.D + c;
     T* dst = a.dstate ? static_cast<T*>(a.dstate) + static_cast<long long>(b) * (K - 1) * a.D + c
                       : nullptr;
-    float w[K][V], bias[V], prev[K - 1][V], acc[K][V];   // acc[j]: dx of the token j back
+    const int stop = min(t1 + K - 1, a.T);
+    f32x2 w[K][H], bias[H], prev[K - 1][H], acc[K][H];   // acc[j]: dx of the token j back
+    struct Batch {
+      Raw<T, V> x[kBwdBatch], y[kBwdBatch];
+      unsigned starts;
+    } cur;
+    auto fetch = [&](Batch& f, int t) {
+      f.starts = 0;
+#pragma unroll
+      for (int k = 0; k < kBwdBatch; ++k)
+        if (t + k < stop) {
+          f.x[k].load(xp + static_cast<long long>(t + k) * a.xs);
+          f.y[k].load(dyp + static_cast<long long>(t + k) * a.D);
+          if (starts) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
+        }
+    };
+    fetch(cur, t0);
     load_filter<K, V>(a, c, w, bias);
-    Raw<T, V> rx[kAhead], ry[kAhead];
+    {
+      Raw<T, V> r[K - 1];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) load_row<T, K, V>(a, b, t0 - 1 - j, c, rx[j]);
+      for (int j = 0; j < K - 1; ++j) load_row<T, K, V>(a, b, t0 - 1 - j, c, r[j]);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) rx[j].get(prev[j]);
+      for (int j = 0; j < K - 1; ++j) r[j].get(prev[j]);
+    }
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
+      for (int i = 0; i < H; ++i) acc[j][i] = 0;
     // tokens behind the current one that are of its document, up to K - 1
     int back = K - 2;
     if (starts && t0 > 0) back = reach<K>(starts, t0 - 1);
     // a finished row: of this run's tokens, or the state's before the first
-    auto emit = [&](int e, const float (&v)[V]) {
+    auto emit = [&](int e, const f32x2 (&v)[H]) {
       Raw<T, V> r;
       r.put(v);
       if (e >= t0)
@@ -233,63 +292,66 @@ __global__ void __launch_bounds__(kBwdThreads) short_conv_bwd_kernel(const ConvA
       else if (t0 == 0 && dst)
         r.store(dst + static_cast<long long>(K - 1 + e) * a.D);
     };
-    const int stop = min(t1 + K - 1, a.T);
-    for (int t = t0; t < stop; t += kAhead) {
+    for (int t = t0; t < stop; t += kBwdBatch) {
+      Batch next;
+      fetch(next, t + kBwdBatch);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (t + k < stop) {
-          rx[k].load(static_cast<const T*>(a.x) + (static_cast<long long>(b) * a.T + t + k) * a.xs + c);
-          ry[k].load(dyp + static_cast<long long>(t + k) * a.D);
-        }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < kBwdBatch; ++k) {
         const int now = t + k;
         if (now >= stop) break;
         back = min(back + 1, K - 1);
-        if (starts && starts[now]) back = 0;
-        float v[V], g[V];
-        rx[k].get(v);
-        ry[k].get(g);
+        if ((cur.starts >> k) & 1) back = 0;
+        f32x2 v[H], g[H];
+        cur.x[k].get(v);
+        cur.y[k].get(g);
+        if (back < K - 1)
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j)
-          if (j + 1 > back)
+          for (int j = 0; j < K - 1; ++j)
+            if (j + 1 > back)
 #pragma unroll
-            for (int i = 0; i < V; ++i) prev[j][i] = 0.f;
+              for (int i = 0; i < H; ++i) prev[j][i] = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < H; ++i) {
           if (a.silu) {
-            float s = fmaf(w[K - 1][i], v[i], bias[i]);
+            f32x2 s = fma2(w[K - 1][i], v[i], bias[i]);
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) s = fmaf(w[K - 2 - j][i], prev[j][i], s);
-            const float sg = sigmoid(s);
-            // where sigmoid is zero, s may be -inf and the slope is still zero
-            g[i] *= sg * (1.f + (sg > 0.f ? s * (1.f - sg) : 0.f));
+            for (int j = 0; j < K - 1; ++j) s = fma2(w[K - 2 - j][i], prev[j][i], s);
+            // sg (1 + s (1 - sg)) = sg + (s sg) (1 - sg)
+            const f32x2 sg = sigmoid2(s), one = both(1.f);
+            const f32x2 slope = fma2(mul2(s, sg), fma2(sg, both(-1.f), one), sg);
+            g[i] = mul2(g[i], slope);
           }
-          acc[0][i] = fmaf(w[K - 1][i], g[i], acc[0][i]);
-#pragma unroll
-          for (int j = 1; j < K; ++j)
-            if (j <= back) acc[j][i] = fmaf(w[K - 1 - j][i], g[i], acc[j][i]);
-          if (now < t1) {
-            dw[K - 1][i] = fmaf(g[i], v[i], dw[K - 1][i]);
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) dw[K - 2 - j][i] = fmaf(g[i], prev[j][i], dw[K - 2 - j][i]);
-            dw[K][i] += g[i];
-          }
+          acc[0][i] = fma2(w[K - 1][i], g[i], acc[0][i]);
         }
+#pragma unroll
+        for (int j = 1; j < K; ++j)
+          if (j <= back)
+#pragma unroll
+            for (int i = 0; i < H; ++i) acc[j][i] = fma2(w[K - 1 - j][i], g[i], acc[j][i]);
+        if (now < t1)
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            dw[K - 1][i] = fma2(g[i], v[i], dw[K - 1][i]);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+              dw[K - 2 - j][i] = fma2(g[i], prev[j][i], dw[K - 2 - j][i]);
+            dw[K][i] = add2(dw[K][i], g[i]);
+          }
         emit(now - (K - 1), acc[K - 1]);
 #pragma unroll
         for (int j = K - 1; j > 0; --j)
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[j][i] = acc[j - 1][i];
+          for (int i = 0; i < H; ++i) acc[j][i] = acc[j - 1][i];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[0][i] = 0.f;
+        for (int i = 0; i < H; ++i) acc[0][i] = 0;
 #pragma unroll
         for (int j = K - 2; j > 0; --j)
 #pragma unroll
-          for (int i = 0; i < V; ++i) prev[j][i] = prev[j - 1][i];
+          for (int i = 0; i < H; ++i) prev[j][i] = prev[j - 1][i];
 #pragma unroll
-        for (int i = 0; i < V; ++i) prev[0][i] = v[i];
+        for (int i = 0; i < H; ++i) prev[0][i] = v[i];
       }
+      cur = next;
     }
     if (stop == a.T) {   // what is behind the last token comes from the state's gradient
 #pragma unroll
@@ -297,21 +359,24 @@ __global__ void __launch_bounds__(kBwdThreads) short_conv_bwd_kernel(const ConvA
         const int e = a.T - j;
         if (a.dstate_out && j - 1 <= back) {
           Raw<T, V> r;
-          float g[V];
+          f32x2 g[H];
           r.load(static_cast<const T*>(a.dstate_out) +
                  (static_cast<long long>(b) * (K - 1) + K - 1 - j) * a.D + c);
           r.get(g);
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[j][i] += g[i];
+          for (int i = 0; i < H; ++i) acc[j][i] = add2(acc[j][i], g[i]);
         }
         if (e < t1) emit(e, acc[j]);
       }
     }
   }
 #pragma unroll
-  for (int k = 0; k <= K; ++k)
+  for (int k = 0; k <= K; ++k) {
+    float f[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sums[warp][k][lane * V + i] = dw[k][i];
+    for (int i = 0; i < H; ++i) split(dw[k][i], f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<float4*>(&sums[warp][k][lane * V]) = make_float4(f[0], f[1], f[2], f[3]);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < (K + 1) * 32 * V; i += kBwdThreads) {
     const int k = i / (32 * V), j = i % (32 * V), d = slice * 32 * V + j;
@@ -346,19 +411,21 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_step_kernel(const Conv
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) r[k].load(st + static_cast<long long>(k) * a.D);
   r[K - 1].load(static_cast<const T*>(a.x) + b * a.xs + c);
-  float w[K][V], s[V];
+  f32x2 w[K][V / 2], s[V / 2];
   load_filter<K, V>(a, c, w, s);
 #pragma unroll
   for (int k = K - 1; k >= 0; --k) {
-    float v[V];
+    f32x2 v[V / 2];
     r[k].get(v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = fmaf(w[k][i], v[i], s[i]);
+    for (int i = 0; i < V / 2; ++i) s[i] = fma2(w[k][i], v[i], s[i]);
   }
   if (a.silu)
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] *= sigmoid(s[i]);
-  store8(static_cast<T*>(a.y) + b * a.D + c, s);
+    for (int i = 0; i < V / 2; ++i) s[i] = mul2(s[i], sigmoid2(s[i]));
+  Raw<T, V> out;
+  out.put(s);
+  out.store(static_cast<T*>(a.y) + b * a.D + c);
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) r[k + 1].store(st + static_cast<long long>(k) * a.D);
 }
@@ -382,9 +449,10 @@ size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int K) {
 }
 
 cudaError_t launch_short_conv(const ConvArgs& a, bool f32, cudaStream_t stream) {
-  // runs of 32 tokens where those fill the GPU's threads, else short ones
-  const long long vecs = static_cast<long long>(a.B) * (a.D / 8);
-  const int run = vecs * ((a.T + 31) / 32) >= 152 * 1024 ? 32 : 8;
+  // long runs where those fill the GPU's threads, else short ones
+  const long long vecs = static_cast<long long>(a.B) * (a.D / 4);
+  int run = 64;
+  while (run > 8 && vecs * ((a.T + run - 1) / run) < 152 * 2048) run /= 2;
   const int runs = (a.T + run - 1) / run;
   const long long total = vecs * runs, grid = (total + kFwdThreads - 1) / kFwdThreads;
   if (grid > 2147483647LL) return cudaErrorInvalidValue;

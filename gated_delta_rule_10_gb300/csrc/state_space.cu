@@ -7,15 +7,18 @@
 // channel. What bounds it is the exponential unit and the fp32 pipe; multiply-adds run two
 // to an instruction.
 //
-// A thread holds 8 states of one channel and walks the tokens in order; N / 8 neighbouring
-// lanes share a channel and add their parts of y. A tile of tokens is staged in shared
-// memory as (u, u x) for each channel and B, C in fp32; the next tile's loads are in flight
-// during the walk. The thread that writes a place's (u, u x) is the one that takes y from
-// there, so that two barriers a tile are enough.
+// A thread holds 8 states of two channels and walks the tokens in order; N / 8 neighbouring
+// lanes share the channels and add their parts of y. (With one channel a thread, every B and
+// C read from shared memory served half as many states, and that was the bound.) A tile of
+// tokens is staged in shared memory as u and u x for each channel and B, C in fp32; the next
+// tile's inputs are copied to shared memory meanwhile, without registers (prefetched in
+// registers, the kernel had four warps a scheduler at most and waited for half of its
+// time). A thread stages what it has copied itself, and takes y from where it has staged u, so
+// that two barriers a tile are enough.
 //
 // Few sequences are cut into segments until the CTAs fill the SMs: a first launch walks all
-// but the last one from zero for their end states and sums of u; a segment's CTA then
-// chains those before it (exp(A sum u) is a whole segment's decay).
+// but the last one from zero for their end states and sums of u, a second chains them
+// (exp(A sum u) is a whole segment's decay).
 #include <type_traits>
 
 #include "state_space.cuh"
@@ -23,36 +26,40 @@
 namespace gdr {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kStates = 8;        // states of a thread
+constexpr int kThreads = 128;
+constexpr int kStates = 8;        // states of a thread, of each of its channels
+constexpr int kOwn = 2;           // channels of a thread
 
 template <int N>
 struct Layout {
-  static constexpr int kLanes = N / kStates;              // lanes of a channel
-  static constexpr int kChannels = kThreads / kLanes;     // channels of a CTA
-  static constexpr int kTile = N == 8 ? 16 : 32;          // tokens of a tile
-  static constexpr int kVecs = kTile * kChannels / 8;     // vectors of 8 channels in a tile
+  static constexpr int kLanes = N / kStates;                     // lanes of a channel
+  static constexpr int kChannels = kOwn * kThreads / kLanes;     // channels of a CTA
+  static constexpr int kTile = N < 32 ? N : 32;                  // tokens of a tile
+  static constexpr int kVecs = kTile * kChannels / 8;            // vectors of 8 channels in a tile
   static constexpr int kPer = (kVecs + kThreads - 1) / kThreads;
-  static constexpr int kBcVecs = 2 * kTile * N / 8;       // vectors of B and C
+  static constexpr int kBcVecs = 2 * kTile * N / 8;              // vectors of B and C
   static constexpr int kBcPer = (kBcVecs + kThreads - 1) / kThreads;
 };
 
-template <int N>
+template <typename T, int N>
 struct __align__(16) Shared {
-  float2 ug[Layout<N>::kTile][Layout<N>::kChannels];
-  float bc[2][Layout<N>::kTile][N];
-  float bias[Layout<N>::kChannels], skip[Layout<N>::kChannels];
+  using L = Layout<N>;
+  float u[L::kTile][L::kChannels], g[L::kTile][L::kChannels];    // u (then y), u x
+  float bc[2][L::kTile][N];
+  T x[2][L::kTile][L::kChannels], dt[L::kTile][L::kChannels], z[2][L::kTile][L::kChannels];
+  T raw_bc[2][L::kTile][N];
+  float bias[L::kChannels], skip[L::kChannels];
   unsigned starts[4];
 };
 
 // WALK: y and the end state, from the segment's start state. Else: the segment's own end
 // state (segment 0's from h0), its sum of u and whether a document starts in it.
 template <typename T, int N, bool WALK>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 2)
     space_kernel(const SpaceArgs a, const SpaceSplit sp) {
   using L = Layout<N>;
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  Shared<N>& sm = *reinterpret_cast<Shared<N>*>(raw_smem);
+  Shared<T, N>& sm = *reinterpret_cast<Shared<T, N>*>(raw_smem);
   const int tid = threadIdx.x;
   const Channels ch(a, L::kChannels, blockIdx.x);
   const int seg = blockIdx.y, b = blockIdx.z;
@@ -60,31 +67,27 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   const long long row0 = static_cast<long long>(b) * a.T;
 
   // this thread's states
-  const int c = ch.first + tid / L::kLanes, n0 = (tid % L::kLanes) * kStates;
-  const bool live = c < ch.end;
-  f32x2 A2[kStates / 2], h[kStates / 2];
-  float usum = 0.f;
+  const int lane = tid % L::kLanes, ci = kOwn * (tid / L::kLanes), c = ch.first + ci;
+  const int n0 = lane * kStates;
+  const bool live = c < ch.end;      // channels come in eights
+  f32x2 A2[kOwn][kStates / 2], h[kOwn][kStates / 2];
+  f32x2 usum = 0;                    // of the two channels
   const size_t state = static_cast<size_t>(a.D) * N;
-  const size_t own = static_cast<size_t>(c) * N + n0;     // in a [D, N] array
-  {
+  const float* from = nullptr;
+  if (WALK && sp.segments > 1)
+    from = sp.h + (static_cast<size_t>(b) * sp.segments + seg) * state;
+  else if (seg == 0)
+    from = a.h0 ? a.h0 + b * state : nullptr;
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    const size_t own = static_cast<size_t>(c + o) * N + n0;     // in a [D, N] array
     float A[kStates], v[kStates];
 #pragma unroll
     for (int i = 0; i < kStates; ++i) A[i] = v[i] = 0.f;
     if (live) {
       load8(a.A + own, A);
-#pragma unroll
-      for (int i = 0; i < kStates; ++i) A[i] *= kLog2e;
-      if (WALK && sp.segments > 1) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float Aq[4] = {A[4 * q], A[4 * q + 1], A[4 * q + 2], A[4 * q + 3]};
-          float hq[4];
-          chain_states(a, sp, b, seg, c, n0 + 4 * q, Aq, hq);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[4 * q + i] = hq[i];
-        }
-      } else if (seg == 0 && a.h0) {
-        const float4* p = reinterpret_cast<const float4*>(a.h0 + b * state + own);
+      if (from) {
+        const float4* p = reinterpret_cast<const float4*>(from + own);
         const float4 lo = p[0], hi = p[1];
         v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
         v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
@@ -94,8 +97,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     }
 #pragma unroll
     for (int i = 0; i < kStates / 2; ++i) {
-      A2[i] = pair(A[2 * i], A[2 * i + 1]);
-      h[i] = pair(v[2 * i], v[2 * i + 1]);
+      A2[o][i] = pair(A[2 * i] * kLog2e, A[2 * i + 1] * kLog2e);
+      h[o][i] = pair(v[2 * i], v[2 * i + 1]);
     }
   }
   for (int i = tid; i < L::kChannels; i += kThreads) {
@@ -104,126 +107,171 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     sm.skip[i] = a.skip && d < ch.end ? a.skip[d] : 0.f;
   }
 
-  Raw8<T> rx[L::kPer], rdt[L::kPer], rz[L::kPer], rbc[L::kBcPer];
   bool mark = false;
-  // requests a tile: x and dt, B and C, the starts
-  auto fetch = [&](int t0) {
+  // copies a tile's inputs: x, dt and z, B and C; `k` of two places for what the tile's end needs
+  auto fetch = [&](int t0, int k) {
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kThreads, t = t0 + v / (L::kChannels / 8);
-      const int d = ch.first + 8 * (v % (L::kChannels / 8));
-      if (v < L::kVecs && t < t_end && d < ch.end) {
-        rx[i].load(static_cast<const T*>(a.x) + (row0 + t) * a.xs + d);
-        rdt[i].load(static_cast<const T*>(a.dt) + (row0 + t) * a.dts + d);
+      const int v = tid + i * kThreads, t = v / (L::kChannels / 8), d = 8 * (v % (L::kChannels / 8));
+      if (v < L::kVecs && t0 + t < t_end && ch.first + d < ch.end) {
+        const long long row = row0 + t0 + t;
+        copy8(&sm.x[k][t][d], static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
+        copy8(&sm.dt[t][d], static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
+        if (WALK && a.z)
+          copy8(&sm.z[k][t][d], static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
       }
     }
 #pragma unroll
     for (int i = 0; i < L::kBcPer; ++i) {
       const int v = tid + i * kThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
-      const int t = t0 + w / (N / 8), n = 8 * (w % (N / 8));
-      rbc[i].zero();
-      if (v < (WALK ? L::kBcVecs : L::kBcVecs / 2) && t < t_end)
-        rbc[i].load((which ? static_cast<const T*>(a.Cm) + (row0 + t) * a.cs
-                           : static_cast<const T*>(a.Bm) + (row0 + t) * a.bs) +
-                    ch.group * N + n);
+      const int t = w / (N / 8), n = 8 * (w % (N / 8));
+      if (v < (WALK ? L::kBcVecs : L::kBcVecs / 2) && t0 + t < t_end)
+        copy8(&sm.raw_bc[which][t][n],
+              (which ? static_cast<const T*>(a.Cm) + (row0 + t0 + t) * a.cs
+                     : static_cast<const T*>(a.Bm) + (row0 + t0 + t) * a.bs) +
+                  ch.group * N + n);
     }
     mark = a.starts && tid < L::kTile && t0 + tid < t_end && a.starts[row0 + t0 + tid] != 0;
   };
-  // and writes it to shared memory
-  auto stage = [&](int t0) {
+  // what this thread has copied, as the walk reads it
+  auto stage = [&](int t0, int k) {
+    copies_done();
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kThreads, t = v / (L::kChannels / 8);
-      const int d = 8 * (v % (L::kChannels / 8));
+      const int v = tid + i * kThreads, t = v / (L::kChannels / 8), d = 8 * (v % (L::kChannels / 8));
       if (v >= L::kVecs) break;
-      float x[8], u[8];
+      f32x2 x[4], u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = u[j] = 0;
       if (t0 + t < t_end && ch.first + d < ch.end) {
-        rx[i].get(x);
-        rdt[i].get(u);
+        f32x2 bias[4];
+        read8(&sm.x[k][t][d], x);
+        read8(&sm.dt[t][d], u);
+        read8(&sm.bias[d], bias);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u[j] += sm.bias[d + j];
-          if (a.softplus) u[j] = softplus(u[j]);
+        for (int j = 0; j < 4; ++j) {
+          u[j] = add2(u[j], bias[j]);
+          if (a.softplus) u[j] = softplus2(u[j]);
+          x[j] = mul2(u[j], x[j]);
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = u[j] = 0.f;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4*>(&sm.ug[t][d + 2 * j]) =
-            make_float4(u[2 * j], u[2 * j] * x[2 * j], u[2 * j + 1], u[2 * j + 1] * x[2 * j + 1]);
+      write8(&sm.u[t][d], u);
+      write8(&sm.g[t][d], x);
     }
 #pragma unroll
     for (int i = 0; i < L::kBcPer; ++i) {
       const int v = tid + i * kThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
+      const int t = w / (N / 8), n = 8 * (w % (N / 8));
       if (v >= (WALK ? L::kBcVecs : L::kBcVecs / 2)) break;
-      float x[8];
-      rbc[i].get(x);
-      float4* p = reinterpret_cast<float4*>(&sm.bc[which][w / (N / 8)][8 * (w % (N / 8))]);
-      p[0] = make_float4(x[0], x[1], x[2], x[3]);
-      p[1] = make_float4(x[4], x[5], x[6], x[7]);
+      f32x2 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = 0;
+      if (t0 + t < t_end) read8(&sm.raw_bc[which][t][n], x);
+      write8(&sm.bc[which][t][n], x);
     }
     const unsigned m = __ballot_sync(0xffffffffu, mark);
     if (tid == 0) sm.starts[0] = m;
   };
 
   int cleared = 0;
-  // one token; FIRST: it may begin a document
-  auto token = [&](int t, bool first) {
-    const float2 ug = sm.ug[t][tid / L::kLanes];
+  // one token, which may be a document's first: this thread's parts of its channels' y
+  auto token = [&](int t, bool first, float (&y)[kOwn]) {
+    const float2 u = *reinterpret_cast<const float2*>(&sm.u[t][ci]);
+    const float2 g = *reinterpret_cast<const float2*>(&sm.g[t][ci]);
     if (first) {
 #pragma unroll
-      for (int i = 0; i < kStates / 2; ++i) h[i] = pair(0.f, 0.f);
+      for (int o = 0; o < kOwn; ++o)
+#pragma unroll
+        for (int i = 0; i < kStates / 2; ++i) h[o][i] = 0;
     }
-    if (!WALK) usum += ug.x;
-    const f32x2 u2 = pair(ug.x, ug.x), g2 = pair(ug.y, ug.y);
+    if (!WALK) usum = add2(usum, pair(u.x, u.y));
+    const f32x2 u2[kOwn] = {both(u.x), both(u.y)}, g2[kOwn] = {both(g.x), both(g.y)};
     const ulonglong2* B = reinterpret_cast<const ulonglong2*>(&sm.bc[0][t][n0]);
     const ulonglong2* C = reinterpret_cast<const ulonglong2*>(&sm.bc[1][t][n0]);
-    f32x2 y = pair(0.f, 0.f);
+    f32x2 part[kOwn][2];
 #pragma unroll
     for (int q = 0; q < kStates / 4; ++q) {
       const ulonglong2 bq = B[q];
-      h[2 * q] = fma2(exp2_pair(mul2(A2[2 * q], u2)), h[2 * q], mul2(g2, bq.x));
-      h[2 * q + 1] = fma2(exp2_pair(mul2(A2[2 * q + 1], u2)), h[2 * q + 1], mul2(g2, bq.y));
-      if (WALK) {
-        const ulonglong2 cq = C[q];
-        y = fma2(cq.x, h[2 * q], y);
-        y = fma2(cq.y, h[2 * q + 1], y);
+      ulonglong2 cq;
+      if (WALK) cq = C[q];
+#pragma unroll
+      for (int o = 0; o < kOwn; ++o) {
+        h[o][2 * q] = fma2(exp2_pair(mul2(A2[o][2 * q], u2[o])), h[o][2 * q], mul2(g2[o], bq.x));
+        h[o][2 * q + 1] =
+            fma2(exp2_pair(mul2(A2[o][2 * q + 1], u2[o])), h[o][2 * q + 1], mul2(g2[o], bq.y));
+        if (WALK) {
+          part[o][0] = q ? fma2(cq.x, h[o][2 * q], part[o][0]) : mul2(cq.x, h[o][2 * q]);
+          part[o][1] = q ? fma2(cq.y, h[o][2 * q + 1], part[o][1]) : mul2(cq.y, h[o][2 * q + 1]);
+        }
       }
     }
-    if (WALK) {
-      float s = sum2(y);
+    if (WALK)
 #pragma unroll
-      for (int off = 1; off < L::kLanes; off *= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
-      if (tid % L::kLanes == 0) sm.ug[t][tid / L::kLanes].x = s;
+      for (int o = 0; o < kOwn; ++o) y[o] = sum2(add2(part[o][0], part[o][1]));
+  };
+  // y of four tokens: summed over the channels' lanes by halves, each lane going on with half
+  // of the sums (one of the channels, then half of the tokens). Written behind all four,
+  // whose loads would else wait for one another.
+  auto put = [&](int t, float (&y)[4][kOwn]) {
+    if constexpr (L::kLanes == 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) sm.u[t + k][ci + o] = y[k][o];
+    } else {
+      const bool odd = lane & 1;
+      float r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        r[k] = (odd ? y[k][1] : y[k][0]) +
+               __shfl_xor_sync(0xffffffffu, odd ? y[k][0] : y[k][1], 1);
+      if constexpr (L::kLanes == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sm.u[t + k][ci + lane] = r[k];
+      } else {
+        const bool up = lane & 2;
+        float q[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          q[j] = (up ? r[2 * j + 1] : r[2 * j]) +
+                 __shfl_xor_sync(0xffffffffu, up ? r[2 * j] : r[2 * j + 1], 2);
+        if constexpr (L::kLanes == 4) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) sm.u[t + 2 * j + up][ci + odd] = q[j];
+        } else {
+          const bool far = lane & 4;
+          const float v = (far ? q[1] : q[0]) + __shfl_xor_sync(0xffffffffu, far ? q[0] : q[1], 4);
+          sm.u[t + 2 * far + up][ci + odd] = v;
+        }
+      }
     }
   };
 
-  fetch(t_begin);
+  fetch(t_begin, 0);
   __syncthreads();
-  stage(t_begin);
+  stage(t_begin, 0);
   __syncthreads();
-  for (int t0 = t_begin; t0 < t_end; t0 += L::kTile) {
-    Raw8<T> cx[L::kPer];
-#pragma unroll
-    for (int i = 0; i < L::kPer; ++i) cx[i] = rx[i];
-    if (WALK && a.z)
-#pragma unroll
-      for (int i = 0; i < L::kPer; ++i) {
-        const int v = tid + i * kThreads, t = t0 + v / (L::kChannels / 8);
-        const int d = ch.first + 8 * (v % (L::kChannels / 8));
-        if (v < L::kVecs && t < t_end && d < ch.end)
-          rz[i].load(static_cast<const T*>(a.z) + (row0 + t) * a.zs + d);
-      }
-    fetch(t0 + L::kTile);
+  int k = 0;      // the tile's place
+  for (int t0 = t_begin; t0 < t_end; t0 += L::kTile, k ^= 1) {
+    fetch(t0 + L::kTile, k ^ 1);
     const int nt = min(L::kTile, t_end - t0);
     const unsigned starts = sm.starts[0];
+    // (tokens behind the end have u = B = C = 0 and leave the states as they are)
     if (starts == 0 && nt == L::kTile) {
-#pragma unroll 4
-      for (int t = 0; t < L::kTile; ++t) token(t, false);
+#pragma unroll 2
+      for (int t = 0; t < L::kTile; t += 4) {
+        float y[4][kOwn];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) token(t + k, false, y[k]);
+        if (WALK) put(t, y);
+      }
     } else {
-      for (int t = 0; t < nt; ++t) token(t, (starts >> t) & 1);
+      for (int t = 0; t < nt; t += 4) {
+        float y[4][kOwn];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) token(t + k, (starts >> (t + k)) & 1, y[k]);
+        if (WALK) put(t, y);
+      }
       cleared |= starts != 0;
     }
     __syncthreads();
@@ -233,20 +281,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         const int v = tid + i * kThreads, t = v / (L::kChannels / 8);
         const int d = 8 * (v % (L::kChannels / 8));
         if (v >= L::kVecs || t0 + t >= t_end || ch.first + d >= ch.end) continue;
-        float x[8], z[8], y[8];
-        cx[i].get(x);
-        if (a.z) rz[i].get(z);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          y[j] = sm.ug[t][d + j].x;
-          if (a.skip) y[j] = fmaf(sm.skip[d + j], x[j], y[j]);
-          if (a.z) y[j] *= silu(z[j]);
+        f32x2 x[4], z[4], skip[4], y[4];
+        read8(&sm.u[t][d], y);
+        if (a.skip) {
+          read8(&sm.x[k][t][d], x);
+          read8(&sm.skip[d], skip);
         }
-        store8(static_cast<T*>(a.y) + (row0 + t0 + t) * a.D + ch.first + d, y);
+        if (a.z) read8(&sm.z[k][t][d], z);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (a.skip) y[j] = fma2(skip[j], x[j], y[j]);
+          if (a.z) y[j] = mul2(y[j], mul2(z[j], sigmoid2(z[j])));
+        }
+        store_pairs(static_cast<T*>(a.y) + (row0 + t0 + t) * a.D + ch.first + d, y);
       }
     }
     if (t0 + L::kTile < t_end) {
-      stage(t0 + L::kTile);
+      stage(t0 + L::kTile, k ^ 1);
       __syncthreads();
     }
   }
@@ -256,25 +307,78 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     if (seg == sp.segments - 1 && a.hT) out = a.hT + b * state;
   } else {
     out = sp.h + (static_cast<size_t>(b) * sp.segments + seg + 1) * state;
-    if (live && n0 == 0) sp.total[(static_cast<size_t>(b) * sp.segments + seg) * a.D + c] = usum;
+    if (live && n0 == 0)
+      *reinterpret_cast<f32x2*>(sp.total + (static_cast<size_t>(b) * sp.segments + seg) * a.D + c) =
+          usum;
     if (blockIdx.x == 0 && tid == 0) sp.cleared[b * sp.segments + seg] = cleared;
   }
   if (out && live) {
-    float v[kStates];
 #pragma unroll
-    for (int i = 0; i < kStates / 2; ++i) split(h[i], v[2 * i], v[2 * i + 1]);
-    float4* p = reinterpret_cast<float4*>(out + own);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int o = 0; o < kOwn; ++o) {
+      ulonglong2* p = reinterpret_cast<ulonglong2*>(out + static_cast<size_t>(c + o) * N + n0);
+      p[0] = make_ulonglong2(h[o][0], h[o][1]);
+      p[1] = make_ulonglong2(h[o][2], h[o][3]);
+    }
+  }
+}
+
+constexpr int kFlatThreads = 256;    // of the kernels below
+
+// The start states of the segments, chained: slot s of `sp.h` from what segment s - 1 alone
+// adds (for slots 0 and 1 whole already), in place; and with `blockIdx.y` the gradients that
+// reach the segments' ends, from the last one on. A segment's decay is exp(A sum u), none of
+// a state passes a document's start. Four states a thread; loads of kBatch segments at once.
+__global__ void __launch_bounds__(kFlatThreads) space_chain_kernel(const SpaceArgs a,
+                                                               const SpaceSplit sp) {
+  constexpr int kBatch = 8;
+  const long long id = static_cast<long long>(blockIdx.x) * kFlatThreads + threadIdx.x;
+  const long long state = static_cast<long long>(a.D) * a.N;
+  if (id >= a.B * state / 4) return;
+  const int b = static_cast<int>(id / (state / 4)), S = sp.segments;
+  const long long own = id % (state / 4) * 4;
+  const int d = static_cast<int>(own / a.N);
+  const bool back = blockIdx.y == 1;
+  const float4 A = *reinterpret_cast<const float4*>(a.A + own);
+  const float A2[4] = {A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e};
+  float* slots = (back ? sp.e : sp.h) + static_cast<long long>(b) * S * state + own;
+  // step i: slot(i) <- slot(i) + decay of segment(i) * slot(i - 1)
+  auto slot = [&](int i) { return back ? S - 2 - i : 1 + i; };
+  auto segment = [&](int i) { return back ? S - 1 - i : i; };
+  const int steps = S - 1;
+  float4 v = *reinterpret_cast<const float4*>(slots + slot(0) * state);
+  for (int i = 1; i < steps; i += kBatch) {
+    float4 w[kBatch];
+    float u[kBatch];
+    int gone[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i + k < steps) {
+        w[k] = *reinterpret_cast<const float4*>(slots + slot(i + k) * state);
+        u[k] = sp.total[(static_cast<long long>(b) * S + segment(i + k)) * a.D + d];
+        gone[k] = sp.cleared[b * S + segment(i + k)];
+      }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i + k < steps) {
+        if (gone[k]) {
+          v = w[k];
+        } else {
+          v.x = fmaf(exp2_fast(A2[0] * u[k]), v.x, w[k].x);
+          v.y = fmaf(exp2_fast(A2[1] * u[k]), v.y, w[k].y);
+          v.z = fmaf(exp2_fast(A2[2] * u[k]), v.z, w[k].z);
+          v.w = fmaf(exp2_fast(A2[3] * u[k]), v.w, w[k].w);
+        }
+        *reinterpret_cast<float4*>(slots + slot(i + k) * state) = v;
+      }
   }
 }
 
 // One token of each sequence: the states are read and written once. A thread has four
 // states of a channel, N / 4 neighbouring lanes a channel.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) space_step_kernel(const SpaceArgs a, long long total) {
+__global__ void __launch_bounds__(kFlatThreads) space_step_kernel(const SpaceArgs a, long long total) {
   constexpr int kLanes = N / 4;
-  const long long id = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  const long long id = static_cast<long long>(blockIdx.x) * kFlatThreads + threadIdx.x;
   const bool live = id < total;
   const long long bd = live ? id / kLanes : 0;
   const int d = static_cast<int>(bd % a.D), n = static_cast<int>(id % kLanes) * 4;
@@ -324,7 +428,7 @@ template <bool WALK>
 cudaError_t launch(const SpaceArgs& a, const SpaceSplit& sp, int segments, bool f32,
                    cudaStream_t stream) {
   return by_states(a.N, f32, [&](auto t, auto n) {
-    constexpr int kBytes = static_cast<int>(sizeof(Shared<n>));
+    constexpr int kBytes = static_cast<int>(sizeof(Shared<decltype(t), n>));
     auto* kern = space_kernel<decltype(t), n, WALK>;
     const cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
@@ -337,6 +441,7 @@ cudaError_t launch(const SpaceArgs& a, const SpaceSplit& sp, int segments, bool 
 
 }  // namespace
 
+int space_channels(int N) { return kOwn * kThreads / (N / kStates); }
 cudaError_t launch_space_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                 cudaStream_t stream) {
   return launch<false>(a, sp, sp.segments - 1, f32, stream);
@@ -345,13 +450,23 @@ cudaError_t launch_space_walk(const SpaceArgs& a, const SpaceSplit& sp, bool f32
                               cudaStream_t stream) {
   return launch<true>(a, sp, sp.segments, f32, stream);
 }
+cudaError_t launch_space_chain(const SpaceArgs& a, const SpaceSplit& sp, bool backward,
+                               cudaStream_t stream) {
+  if (sp.segments < 3) return cudaSuccess;     // nothing to add
+  const long long total = static_cast<long long>(a.B) * a.D * (a.N / 4);
+  const long long grid = (total + kFlatThreads - 1) / kFlatThreads;
+  if (grid > 2147483647LL) return cudaErrorInvalidValue;
+  space_chain_kernel<<<dim3(static_cast<unsigned>(grid), backward ? 2 : 1), kFlatThreads, 0, stream>>>(
+      a, sp);
+  return cudaGetLastError();
+}
 cudaError_t launch_space_step(const SpaceArgs& a, bool f32, cudaStream_t stream) {
   const long long total = static_cast<long long>(a.B) * a.D * (a.N / 4);
-  const long long grid = (total + kThreads - 1) / kThreads;
+  const long long grid = (total + kFlatThreads - 1) / kFlatThreads;
   if (grid > 2147483647LL) return cudaErrorInvalidValue;
   return by_states(a.N, f32, [&](auto t, auto n) {
     space_step_kernel<decltype(t), n>
-        <<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a, total);
+        <<<static_cast<unsigned>(grid), kFlatThreads, 0, stream>>>(a, total);
     return cudaGetLastError();
   });
 }

@@ -1,92 +1,84 @@
-// Device helpers of the state space recurrence's kernels: pairs of fp32 in one register
-// pair, exponentials, the step size and its slope, and the channels of a CTA.
+// Device helpers of the state space recurrence's kernels: the step size and the channels of
+// a CTA.
 #pragma once
 
+#include "pair.cuh"
 #include "state_space.h"
 #include "vec_io.cuh"
 
 namespace gdr {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// Two fp32 numbers handled by one instruction.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split(f32x2 v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float sum2(f32x2 v) {
-  float lo, hi;
-  split(v, lo, hi);
-  return lo + hi;
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ f32x2 exp2_pair(f32x2 v) {
-  float lo, hi;
-  split(v, lo, hi);
-  return pair(exp2_fast(lo), exp2_fast(hi));
-}
-
-__device__ __forceinline__ float sigmoid(float x) {
-  return __fdividef(1.f, 1.f + exp2_fast(-kLog2e * x));
-}
-// x sigmoid(x) and its slope
-__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
-__device__ __forceinline__ float silu_slope(float x) {
-  const float s = sigmoid(x);
-  return s * fmaf(x, 1.f - s, 1.f);
-}
-
-// e^v for v <= 0 to about 2^-22 of it: the product with log2(e) keeps what its rounding
-// leaves (v = -7 would lose three bits by it).
-__device__ __forceinline__ float exp_kept(float v) {
-  const float hi = v * kLog2e;
-  // log2(e) - kLog2e = 1.925963e-8
-  const float lo = fmaf(v, 1.9259630e-8f, fmaf(v, kLog2e, -hi));
-  const float e = exp2_fast(hi);
-  return v > -104.f ? fmaf(e, lo * 0.6931471805599453f, e) : 0.f;
-}
-
 // log(1 + e^v) = max(v, 0) + log(1 + q), q = e^-|v| in (0, 1], and with s = q / (2 + q)
-// log(1 + q) = 2 atanh(s) = 2 (s + s^3 / 3 + s^5 / 5 + ...), s <= 1/3: nine terms leave
-// 1e-9 of it, and small steps keep all their digits (1 + q would not).
+// log(1 + q) = 2 atanh(s) = 2 (s + s^3 / 3 + s^5 / 5 + ...), s <= 1/3: six terms leave
+// 1.4e-7 of it, and small steps keep all their digits (1 + q would not). q is 2^(-|v| log2 e)
+// times 1 + what the product's rounding leaves of |v| (at v = -7 three bits).
+__device__ __forceinline__ f32x2 softplus2(f32x2 v) {
+  constexpr float kLn2 = 0.6931471805599453f;
+  float v0, v1, r0, r1;
+  split(v, v0, v1);
+  // (q is zero from -88 on, and the bound keeps infinities out of the products)
+  const f32x2 n = pair(fmaxf(-fabsf(v0), -120.f), fmaxf(-fabsf(v1), -120.f));
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r0) : "f"(v0));
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r1) : "f"(v1));
+  const f32x2 e = mul2(n, both(kLog2e));
+  f32x2 q = exp2_pair(e);
+  q = fma2(q, fma2(e, both(-kLn2), n), q);
+  float d0, d1;
+  split(add2(q, both(2.f)), d0, d1);
+  const f32x2 s = mul2(q, pair(rcp_fast(d0), rcp_fast(d1))), s2 = mul2(s, s);
+  f32x2 p = fma2(s2, both(2.f / 11.f), both(2.f / 9.f));
+  p = fma2(p, s2, both(2.f / 7.f));
+  p = fma2(p, s2, both(2.f / 5.f));
+  p = fma2(p, s2, both(2.f / 3.f));
+  p = fma2(p, s2, both(2.f));
+  return fma2(p, s, pair(r0, r1));
+}
 __device__ __forceinline__ float softplus(float v) {
-  const float q = exp_kept(-fabsf(v));
-  const float s = __fdividef(q, 2.f + q), s2 = s * s;
-  float p = 2.f / 17.f;
-  p = fmaf(p, s2, 2.f / 15.f);
-  p = fmaf(p, s2, 2.f / 13.f);
-  p = fmaf(p, s2, 2.f / 11.f);
-  p = fmaf(p, s2, 2.f / 9.f);
-  p = fmaf(p, s2, 2.f / 7.f);
-  p = fmaf(p, s2, 2.f / 5.f);
-  p = fmaf(p, s2, 2.f / 3.f);
-  p = fmaf(p, s2, 2.f);
-  return v != v ? v : fmaf(p, s, v > 0.f ? v : 0.f);
+  float lo, hi;
+  split(softplus2(both(v)), lo, hi);
+  return lo;
+}
+
+// 16 bytes from global to shared memory, and the wait for all of a thread's copies.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copies_done() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+// 8 elements of T, in 16-byte pieces.
+template <typename T>
+__device__ __forceinline__ void copy8(T* to, const T* from) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+    copy16(reinterpret_cast<uint4*>(to) + i, reinterpret_cast<const uint4*>(from) + i);
+}
+template <typename T>
+__device__ __forceinline__ void read8(const T* p, f32x2 (&x)[4]) {   // from shared memory
+  if constexpr (sizeof(T) == 4) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0];
+    const ulonglong2 b = reinterpret_cast<const ulonglong2*>(p)[1];
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+}
+__device__ __forceinline__ void write8(float* p, const f32x2 (&x)[4]) {   // to shared memory
+  reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(x[0], x[1]);
+  reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(x[2], x[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const f32x2 (&x)[4]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split(x[i], f[2 * i], f[2 * i + 1]);
+  store8(p, f);
 }
 
 // The channels of a CTA: `width` at most, all of one group.
@@ -99,26 +91,5 @@ struct Channels {
     end = min(first + width, (group + 1) * each);
   }
 };
-
-// The state entering segment s, states [d * N + n, + 4) of batch row b, from the slots of
-// `sp.h` (see there): what the segments before it leave, chained.
-__device__ __forceinline__ void chain_states(const SpaceArgs& a, const SpaceSplit& sp, int b, int s,
-                                             int d, int n, const float (&A2)[4], float (&h)[4]) {
-  const size_t state = static_cast<size_t>(a.D) * a.N;
-  const float* slot = sp.h + static_cast<size_t>(b) * sp.segments * state +
-                      static_cast<size_t>(d) * a.N + n;
-  const int from = s == 0 ? 0 : 1;
-  const float4 v = *reinterpret_cast<const float4*>(slot + from * state);
-  h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
-  for (int i = 2; i <= s; ++i) {
-    const float u = sp.total[(static_cast<size_t>(b) * sp.segments + i - 1) * a.D + d];
-    const bool cleared = sp.cleared[b * sp.segments + i - 1] != 0;
-    const float4 w = *reinterpret_cast<const float4*>(slot + i * state);
-    const float add[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      h[j] = cleared ? add[j] : fmaf(exp2_fast(A2[j] * u), h[j], add[j]);
-  }
-}
 
 }  // namespace gdr

@@ -27,12 +27,13 @@ struct SpaceSplit {
   int seg_len = 0;
   int tiles = 0;              // backward: tiles of kSpaceTile tokens in a sequence
   int blocks = 1;             // backward: CTAs over the channels (dBm's and dCm's partial sums)
-  // slot 0: h0; slot 1: the state behind segment 0; slot s > 1: what segment s - 1 alone adds
+  // slot 0: h0; slot 1: the state behind segment 0; slot s > 1: what segment s - 1 alone adds,
+  // after the chain the state entering segment s
   float* h = nullptr;         // [B, segments, D, N]
   float* total = nullptr;     // [B, segments, D] a segment's sum of u
   int* cleared = nullptr;     // [B, segments] nonzero: a document starts in it
   // backward: slot S - 1: dhT; slot s < S - 1: the gradient that segment s + 1 passes on
-  // (alone; the last segment's with dhT's)
+  // (alone; the last segment's with dhT's), after the chain all that enters segment s
   float* e = nullptr;         // [B, segments, D, N]
   float* kept = nullptr;      // [B, tiles, D, N] a segment's own state entering each tile
   float* kept_sum = nullptr;  // [B, tiles, D] the segment's sum of u up to there
@@ -42,9 +43,12 @@ struct SpaceSplit {
   float* bc_part = nullptr;   // [blocks, B, T, 2, N] of dBm and dCm
 };
 
-int space_channels(int N, bool backward);   // channels per CTA
+int space_channels(int N);       // channels of a CTA: forward, backward
+int space_bwd_channels(int N);
 cudaError_t launch_space_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                 cudaStream_t stream);
+cudaError_t launch_space_chain(const SpaceArgs& a, const SpaceSplit& sp, bool backward,
+                               cudaStream_t stream);
 cudaError_t launch_space_walk(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                               cudaStream_t stream);
 cudaError_t launch_space_bwd_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,

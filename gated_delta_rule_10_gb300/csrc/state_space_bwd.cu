@@ -28,48 +28,53 @@ namespace {
 
 // ------------------------------------------------------------------ states
 
-constexpr int kThreads = 256;
-constexpr int kStates = 8;        // states of a thread
+constexpr int kThreads = 128;
+constexpr int kStates = 8;        // states of a thread, of each of its channels
+constexpr int kOwn = 2;           // channels of a thread
 
 template <int N>
 struct PreLayout {
   static constexpr int kLanes = N / kStates;
-  static constexpr int kChannels = kThreads / kLanes;
-  static constexpr int kTile = kSpaceTile;
+  static constexpr int kChannels = kOwn * kThreads / kLanes;
+  static constexpr int kTile = N == 8 ? 8 : kSpaceTile;      // tokens staged together
   static constexpr int kVecs = kTile * kChannels / 8;
   static constexpr int kPer = (kVecs + kThreads - 1) / kThreads;
   static constexpr int kBcVecs = 2 * kTile * N / 8;
   static constexpr int kBcPer = (kBcVecs + kThreads - 1) / kThreads;
 };
 
-template <int N>
+template <typename T, int N>
 struct __align__(16) PreShared {
-  float u[PreLayout<N>::kTile][PreLayout<N>::kChannels];
-  float g[PreLayout<N>::kTile][PreLayout<N>::kChannels];
-  float p[PreLayout<N>::kTile][PreLayout<N>::kChannels];
-  float bc[2][PreLayout<N>::kTile][N];
-  float bias[PreLayout<N>::kChannels];
+  using L = PreLayout<N>;
+  float u[L::kTile][L::kChannels], g[L::kTile][L::kChannels], p[L::kTile][L::kChannels];
+  float bc[2][L::kTile][N];
+  T x[L::kTile][L::kChannels], dt[L::kTile][L::kChannels];
+  T z[L::kTile][L::kChannels], dy[L::kTile][L::kChannels];
+  T raw_bc[2][L::kTile][N];
+  float bias[L::kChannels];
   unsigned starts[4];
 };
 
 // CUT: there are several segments, which need the gradients that they pass back.
 template <typename T, int N, bool CUT>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
     space_bwd_states_kernel(const SpaceArgs a, const SpaceSplit sp) {
   using L = PreLayout<N>;
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  PreShared<N>& sm = *reinterpret_cast<PreShared<N>*>(raw_smem);
+  PreShared<T, N>& sm = *reinterpret_cast<PreShared<T, N>*>(raw_smem);
   const int tid = threadIdx.x;
   const Channels ch(a, L::kChannels, blockIdx.x);
   const int seg = blockIdx.y, b = blockIdx.z;
   const int t_begin = seg * sp.seg_len, t_end = min(t_begin + sp.seg_len, a.T);
   const long long row0 = static_cast<long long>(b) * a.T;
-  const int ci = tid / L::kLanes, c = ch.first + ci, n0 = (tid % L::kLanes) * kStates;
-  const bool live = c < ch.end;
-  const size_t state = static_cast<size_t>(a.D) * N, own = static_cast<size_t>(c) * N + n0;
-  f32x2 A2[kStates / 2], h[kStates / 2], P[kStates / 2], e[kStates / 2];
-  float usum = 0.f;
-  {
+  const int ci = kOwn * (tid / L::kLanes), c = ch.first + ci, n0 = (tid % L::kLanes) * kStates;
+  const bool live = c < ch.end;      // channels come in eights
+  const size_t state = static_cast<size_t>(a.D) * N;
+  f32x2 A2[kOwn][kStates / 2], h[kOwn][kStates / 2], P[kOwn][kStates / 2], e[kOwn][kStates / 2];
+  f32x2 usum = 0;                    // of the two channels
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    const size_t own = static_cast<size_t>(c + o) * N + n0;
     float A[kStates], v[kStates];
 #pragma unroll
     for (int i = 0; i < kStates; ++i) A[i] = v[i] = 0.f;
@@ -79,129 +84,137 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     }
 #pragma unroll
     for (int i = 0; i < kStates / 2; ++i) {
-      A2[i] = pair(A[2 * i] * kLog2e, A[2 * i + 1] * kLog2e);
-      h[i] = pair(v[2 * i], v[2 * i + 1]);
-      P[i] = pair(1.f, 1.f);
-      e[i] = pair(0.f, 0.f);
+      A2[o][i] = pair(A[2 * i] * kLog2e, A[2 * i + 1] * kLog2e);
+      h[o][i] = pair(v[2 * i], v[2 * i + 1]);
+      P[o][i] = both(1.f);
+      e[o][i] = 0;
     }
   }
   for (int i = tid; i < L::kChannels; i += kThreads)
     sm.bias[i] = a.dt_bias && ch.first + i < ch.end ? a.dt_bias[ch.first + i] : 0.f;
 
-  Raw8<T> rx[L::kPer], rdt[L::kPer], rz[L::kPer], ry[L::kPer], rbc[L::kBcPer];
   bool mark = false;
   constexpr int kBc = CUT ? L::kBcVecs : L::kBcVecs / 2;
+  // copies a tile's inputs
   auto fetch = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kThreads, t = t0 + v / (L::kChannels / 8);
-      const int d = ch.first + 8 * (v % (L::kChannels / 8));
-      if (v < L::kVecs && t < t_end && d < ch.end) {
-        rx[i].load(static_cast<const T*>(a.x) + (row0 + t) * a.xs + d);
-        rdt[i].load(static_cast<const T*>(a.dt) + (row0 + t) * a.dts + d);
+      const int v = tid + i * kThreads, t = v / (L::kChannels / 8), d = 8 * (v % (L::kChannels / 8));
+      if (v < L::kVecs && t0 + t < t_end && ch.first + d < ch.end) {
+        const long long row = row0 + t0 + t;
+        copy8(&sm.x[t][d], static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
+        copy8(&sm.dt[t][d], static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
         if (CUT) {
-          ry[i].load(static_cast<const T*>(a.dy) + (row0 + t) * a.D + d);
-          if (a.z) rz[i].load(static_cast<const T*>(a.z) + (row0 + t) * a.zs + d);
+          copy8(&sm.dy[t][d], static_cast<const T*>(a.dy) + row * a.D + ch.first + d);
+          if (a.z) copy8(&sm.z[t][d], static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < L::kBcPer; ++i) {
       const int v = tid + i * kThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
-      const int t = t0 + w / (N / 8), n = 8 * (w % (N / 8));
-      rbc[i].zero();
-      if (v < kBc && t < t_end)
-        rbc[i].load((which ? static_cast<const T*>(a.Cm) + (row0 + t) * a.cs
-                           : static_cast<const T*>(a.Bm) + (row0 + t) * a.bs) +
-                    ch.group * N + n);
+      const int t = w / (N / 8), n = 8 * (w % (N / 8));
+      if (v < kBc && t0 + t < t_end)
+        copy8(&sm.raw_bc[which][t][n],
+              (which ? static_cast<const T*>(a.Cm) + (row0 + t0 + t) * a.cs
+                     : static_cast<const T*>(a.Bm) + (row0 + t0 + t) * a.bs) +
+                  ch.group * N + n);
     }
     mark = a.starts && tid < L::kTile && t0 + tid < t_end && a.starts[row0 + t0 + tid] != 0;
   };
+  // what this thread has copied, as the walk reads it
   auto stage = [&](int t0) {
+    copies_done();
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kThreads, t = v / (L::kChannels / 8);
-      const int d = 8 * (v % (L::kChannels / 8));
+      const int v = tid + i * kThreads, t = v / (L::kChannels / 8), d = 8 * (v % (L::kChannels / 8));
       if (v >= L::kVecs) break;
-      float x[8], u[8], p[8];
+      f32x2 x[4], u[4], p[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = u[j] = p[j] = 0.f;
+      for (int j = 0; j < 4; ++j) x[j] = u[j] = p[j] = 0;
       if (t0 + t < t_end && ch.first + d < ch.end) {
-        rx[i].get(x);
-        rdt[i].get(u);
-        float z[8];
-        if (CUT) ry[i].get(p);
-        if (CUT && a.z) rz[i].get(z);
+        f32x2 bias[4], z[4];
+        read8(&sm.x[t][d], x);
+        read8(&sm.dt[t][d], u);
+        read8(&sm.bias[d], bias);
+        if (CUT) read8(&sm.dy[t][d], p);
+        if (CUT && a.z) read8(&sm.z[t][d], z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u[j] += sm.bias[d + j];
-          if (a.softplus) u[j] = softplus(u[j]);
-          x[j] *= u[j];
-          if (CUT && a.z) p[j] *= silu(z[j]);
+        for (int j = 0; j < 4; ++j) {
+          u[j] = add2(u[j], bias[j]);
+          if (a.softplus) u[j] = softplus2(u[j]);
+          x[j] = mul2(u[j], x[j]);
+          if (CUT && a.z) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
         }
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<float4*>(&sm.u[t][d + 4 * j]) =
-            make_float4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
-        *reinterpret_cast<float4*>(&sm.g[t][d + 4 * j]) =
-            make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-        if (CUT)
-          *reinterpret_cast<float4*>(&sm.p[t][d + 4 * j]) =
-              make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-      }
+      write8(&sm.u[t][d], u);
+      write8(&sm.g[t][d], x);
+      if (CUT) write8(&sm.p[t][d], p);
     }
 #pragma unroll
     for (int i = 0; i < L::kBcPer; ++i) {
       const int v = tid + i * kThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
+      const int t = w / (N / 8), n = 8 * (w % (N / 8));
       if (v >= kBc) break;
-      float x[8];
-      rbc[i].get(x);
-      float4* p = reinterpret_cast<float4*>(&sm.bc[which][w / (N / 8)][8 * (w % (N / 8))]);
-      p[0] = make_float4(x[0], x[1], x[2], x[3]);
-      p[1] = make_float4(x[4], x[5], x[6], x[7]);
+      f32x2 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = 0;
+      if (t0 + t < t_end) read8(&sm.raw_bc[which][t][n], x);
+      write8(&sm.bc[which][t][n], x);
     }
     const unsigned m = __ballot_sync(0xffffffffu, mark);
     if (tid == 0) sm.starts[0] = m;
   };
-  auto put = [&](float* out, const f32x2 (&v)[kStates / 2]) {
-    float f[kStates];
+  auto put = [&](float* out, const f32x2 (&v)[kOwn][kStates / 2]) {
 #pragma unroll
-    for (int i = 0; i < kStates / 2; ++i) split(v[i], f[2 * i], f[2 * i + 1]);
-    reinterpret_cast<float4*>(out + own)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(out + own)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    for (int o = 0; o < kOwn; ++o) {
+      ulonglong2* p = reinterpret_cast<ulonglong2*>(out + static_cast<size_t>(c + o) * N + n0);
+      p[0] = make_ulonglong2(v[o][0], v[o][1]);
+      p[1] = make_ulonglong2(v[o][2], v[o][3]);
+    }
   };
 
   bool cleared = false;     // a document starts in what has been walked of the segment
-  auto token = [&](int t, bool first) {
-    const float u = sm.u[t][ci], g = sm.g[t][ci];
+  // one token, which may be a document's first; `back`: with what it passes back (nothing
+  // from a document that starts in the segment)
+  auto token = [&](int t, bool first, bool back) {
+    const float2 u = *reinterpret_cast<const float2*>(&sm.u[t][ci]);
+    const float2 g = *reinterpret_cast<const float2*>(&sm.g[t][ci]);
     if (first) {
       cleared = true;
+      back = false;
 #pragma unroll
-      for (int i = 0; i < kStates / 2; ++i) h[i] = P[i] = pair(0.f, 0.f);
+      for (int o = 0; o < kOwn; ++o)
+#pragma unroll
+        for (int i = 0; i < kStates / 2; ++i) h[o][i] = P[o][i] = 0;
     }
-    usum += u;
-    const f32x2 u2 = pair(u, u), g2 = pair(g, g);
-    f32x2 p2;
-    if (CUT) {
-      const float p = sm.p[t][ci];
-      p2 = pair(p, p);
+    usum = add2(usum, pair(u.x, u.y));
+    const f32x2 u2[kOwn] = {both(u.x), both(u.y)}, g2[kOwn] = {both(g.x), both(g.y)};
+    f32x2 p2[kOwn];
+    if (back) {
+      const float2 p = *reinterpret_cast<const float2*>(&sm.p[t][ci]);
+      p2[0] = both(p.x);
+      p2[1] = both(p.y);
     }
     const ulonglong2* B = reinterpret_cast<const ulonglong2*>(&sm.bc[0][t][n0]);
     const ulonglong2* C = reinterpret_cast<const ulonglong2*>(&sm.bc[1][t][n0]);
 #pragma unroll
     for (int q = 0; q < kStates / 4; ++q) {
       const ulonglong2 bq = B[q];
-      const f32x2 a0 = exp2_pair(mul2(A2[2 * q], u2)), a1 = exp2_pair(mul2(A2[2 * q + 1], u2));
-      h[2 * q] = fma2(a0, h[2 * q], mul2(g2, bq.x));
-      h[2 * q + 1] = fma2(a1, h[2 * q + 1], mul2(g2, bq.y));
-      if (CUT && !cleared) {
-        const ulonglong2 cq = C[q];
-        P[2 * q] = mul2(P[2 * q], a0);
-        P[2 * q + 1] = mul2(P[2 * q + 1], a1);
-        e[2 * q] = fma2(P[2 * q], mul2(cq.x, p2), e[2 * q]);
-        e[2 * q + 1] = fma2(P[2 * q + 1], mul2(cq.y, p2), e[2 * q + 1]);
-      }
+      ulonglong2 cq;
+      if (back) cq = C[q];
+#pragma unroll
+      for (int o = 0; o < kOwn; ++o)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int i = 2 * q + j;
+          const f32x2 d = exp2_pair(mul2(A2[o][i], u2[o]));
+          h[o][i] = fma2(d, h[o][i], mul2(g2[o], j ? bq.y : bq.x));
+          if (back) {
+            P[o][i] = mul2(P[o][i], d);
+            e[o][i] = fma2(P[o][i], mul2(j ? cq.y : cq.x, p2[o]), e[o][i]);
+          }
+        }
     }
   };
 
@@ -211,19 +224,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   __syncthreads();
   for (int t0 = t_begin; t0 < t_end; t0 += L::kTile) {
     fetch(t0 + L::kTile);
-    const size_t tile = static_cast<size_t>(b) * sp.tiles + t0 / L::kTile;
-    if (live) {
-      put(sp.kept + tile * state, h);
-      if (n0 == 0) sp.kept_sum[tile * a.D + c] = usum;
+    if (t0 % kSpaceTile == 0) {
+      const size_t tile = static_cast<size_t>(b) * sp.tiles + t0 / kSpaceTile;
+      if (live) {
+        put(sp.kept + tile * state, h);
+        if (n0 == 0) *reinterpret_cast<f32x2*>(sp.kept_sum + tile * a.D + c) = usum;
+      }
+      if (blockIdx.x == 0 && tid == 0) sp.kept_clear[tile] = cleared;
     }
-    if (blockIdx.x == 0 && tid == 0) sp.kept_clear[tile] = cleared;
     const int nt = min(L::kTile, t_end - t0);
     const unsigned starts = sm.starts[0];
     if (starts == 0 && nt == L::kTile) {
+      if (CUT && !cleared) {
+#pragma unroll 2
+        for (int t = 0; t < L::kTile; ++t) token(t, false, true);
+      } else {
 #pragma unroll 4
-      for (int t = 0; t < L::kTile; ++t) token(t, false);
+        for (int t = 0; t < L::kTile; ++t) token(t, false, false);
+      }
     } else {
-      for (int t = 0; t < nt; ++t) token(t, (starts >> t) & 1);
+      for (int t = 0; t < nt; ++t) token(t, (starts >> t) & 1, CUT && !cleared);
     }
     __syncthreads();
     if (t0 + L::kTile < t_end) {
@@ -237,17 +257,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   if (live) {
     if (!last) {
       put(sp.h + (at + 1) * state, h);
-      if (n0 == 0) sp.total[at * a.D + c] = usum;
+      if (n0 == 0) *reinterpret_cast<f32x2*>(sp.total + at * a.D + c) = usum;
     } else {
-      float v[kStates];
+      f32x2 d[kOwn][kStates / 2];
 #pragma unroll
-      for (int i = 0; i < kStates; ++i) v[i] = 0.f;
-      if (a.dhT) load8(a.dhT + b * state + own, v);
-      f32x2 d[kStates / 2];
+      for (int o = 0; o < kOwn; ++o) {
+        float v[kStates];
 #pragma unroll
-      for (int i = 0; i < kStates / 2; ++i) {
-        d[i] = pair(v[2 * i], v[2 * i + 1]);
-        if (!cleared) e[i] = fma2(P[i], d[i], e[i]);
+        for (int i = 0; i < kStates; ++i) v[i] = 0.f;
+        if (a.dhT) load8(a.dhT + b * state + static_cast<size_t>(c + o) * N + n0, v);
+#pragma unroll
+        for (int i = 0; i < kStates / 2; ++i) {
+          d[o][i] = pair(v[2 * i], v[2 * i + 1]);
+          if (!cleared) e[o][i] = fma2(P[o][i], d[o][i], e[o][i]);
+        }
       }
       put(sp.e + at * state, d);
     }
@@ -267,51 +290,91 @@ template <int N>
 struct BwdLayout {
   static constexpr int kStateLanes = N / 4, kChannelLanes = 32 / kStateLanes;
   static constexpr int kWarpChannels = 4 * kChannelLanes, kChannels = kWarps * kWarpChannels;
-  static constexpr int kStateMask = (kStateLanes - 1) & 3;       // orders of the channels
-  static constexpr int kChannelMask = (kChannelLanes - 1) & 3;   // orders of the states
+  static constexpr int kOrders = kChannelLanes < 4 ? kChannelLanes : 4;   // of the states
   static constexpr int kVecs = kTile * kChannels / 8;
   static constexpr int kPer = (kVecs + kBwdThreads - 1) / kBwdThreads;
   static constexpr int kBcVecs = 2 * kTile * N / 8;
+  static constexpr int kBcPer = (kBcVecs + kBwdThreads - 1) / kBwdThreads;
   static constexpr int kRow = kChannels / 8;                     // vectors of a token
   static constexpr int kOrder = kTile * N + N;                   // floats of one order of B or C
+  static constexpr int kSums = (kChannels + kBwdThreads - 1) / kBwdThreads;
 };
 
-template <int N>
+template <typename T, int N, bool Z>
 struct __align__(16) BwdShared {
   using L = BwdLayout<N>;
+  // u; u x, then q; p, then C h; sum A w, then ddt
   float u[kTile][L::kChannels], g[kTile][L::kChannels], p[kTile][L::kChannels];
-  float q[kTile][L::kChannels], r[kTile][L::kChannels], y[kTile][L::kChannels];
-  float b[4][L::kOrder], c[4][L::kOrder];
-  float4 h[kTile / kSub][4][kBwdThreads];
+  float r[kTile][L::kChannels];
+  float b[L::kOrders][L::kOrder], c[L::kOrders][L::kOrder];
+  ulonglong2 h[kTile / kSub][4][kBwdThreads];
   float dbc[kWarps][kTile][2 * N];
-  float sums[kBwdThreads][17];        // dskip and ddt_bias of a thread's 8 channels
+  float px[kBwdThreads][8];           // dskip of a thread's 8 channels
+  // copies for the next tile: inputs, and the kept states
+  float4 kept[4][kBwdThreads];
+  T x[kTile][L::kChannels], dt[kTile][L::kChannels], dy[kTile][L::kChannels];
+  T z[Z ? kTile : 1][L::kChannels];
+  T bc[2][kTile][N];
   float bias[L::kChannels], skip[L::kChannels];
   unsigned starts[4];
 };
 
 // v[i] -> v[i ^ mask]
-template <typename V>
-__device__ __forceinline__ void reorder(V (&v)[4], int mask) {
+__device__ __forceinline__ void reorder(float (&v)[4], int mask) {
   if (mask & 1) {
-    V s = v[0]; v[0] = v[1]; v[1] = s;
+    float s = v[0]; v[0] = v[1]; v[1] = s;
     s = v[2]; v[2] = v[3]; v[3] = s;
   }
   if (mask & 2) {
-    V s = v[0]; v[0] = v[2]; v[2] = s;
+    float s = v[0]; v[0] = v[2]; v[2] = s;
     s = v[1]; v[1] = v[3]; v[3] = s;
+  }
+}
+// A thread's states: pairs of channels, in its order of the states.
+using Items = f32x2[2][4];
+__device__ __forceinline__ void to_items(const float4 (&in)[4], int order, Items& out) {
+  float v[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i][0] = in[i].x; v[i][1] = in[i].y; v[i][2] = in[i].z; v[i][3] = in[i].w;
+    reorder(v[i], order);
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[p][j] = pair(v[2 * p][j], v[2 * p + 1][j]);
+}
+__device__ __forceinline__ void from_items(const Items& in, int order, float4 (&out)[4]) {
+  float v[4][4];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split(in[p][j], v[2 * p][j], v[2 * p + 1][j]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    reorder(v[i], order);
+    out[i] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
   }
 }
 
 __device__ __forceinline__ float pass(float x, int lanes) {
   return __shfl_xor_sync(0xffffffffu, x, lanes);
 }
+// 8 elements read from global memory as pairs.
+template <typename T>
+__device__ __forceinline__ void raw_pairs(const Raw8<T>& r, f32x2 (&x)[4]) {
+  float f[8];
+  r.get(f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pair(f[2 * i], f[2 * i + 1]);
+}
 
 template <typename T, int N, bool Z>
-__global__ void __launch_bounds__(kBwdThreads, 2)
+__global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
     space_bwd_kernel(const SpaceArgs a, const SpaceSplit sp) {
   using L = BwdLayout<N>;
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  BwdShared<N>& sm = *reinterpret_cast<BwdShared<N>*>(raw_smem);
+  BwdShared<T, N, Z>& sm = *reinterpret_cast<BwdShared<T, N, Z>*>(raw_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sl = lane % L::kStateLanes, cl = lane / L::kStateLanes;
   const Channels ch(a, L::kChannels, blockIdx.x);
@@ -319,116 +382,140 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   const int t_begin = seg * sp.seg_len, t_end = min(t_begin + sp.seg_len, a.T);
   const long long row0 = static_cast<long long>(b) * a.T;
   const size_t state = static_cast<size_t>(a.D) * N;
-  const int n0 = 4 * sl;
-  const int cx = sl & L::kStateMask, nx = cl & L::kChannelMask;   // this lane's orders
-  const int cbase = warp * L::kWarpChannels + 4 * cl;             // of the CTA's channels
+  const int n0 = 4 * sl, nx = cl & (L::kOrders - 1);     // states n0 + (j ^ nx)
+  const int swap = sl & 1;                               // channels 2 (p ^ swap) + 0, 1
+  const int cbase = warp * L::kWarpChannels + 4 * cl;    // of the CTA's channels
+  const int c0 = cbase + 2 * swap, c1 = cbase + 2 * (swap ^ 1);
+  const bool live = ch.first + cbase < ch.end;           // channels come in eights
   const float* Border = sm.b[nx];
   const float* Corder = sm.c[nx];
+  // place of channel i (of four) in a [D, N] array
+  auto place = [&](int i) {
+    return static_cast<size_t>(ch.first + (i < 2 ? c0 : c1) + (i & 1)) * N + n0;
+  };
+  auto load_items = [&](const float* from, Items& out) {
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = live && from ? *reinterpret_cast<const float4*>(from + place(i))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    to_items(v, nx, out);
+  };
 
-  // [channel i: ch.first + cbase + (i ^ cx)][state j: n0 + (j ^ nx)]
-  f32x2 A2[4][2], dA[4][2], E[4][2];
-  float hs[4][4];      // the state entering the segment
+  Items A2, dA, E, hs;       // hs: the state entering the segment
   const bool from_start = seg == 0;
+  load_items(a.A, A2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int d = ch.first + cbase + (i ^ cx);
-    float A[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < 2; ++p)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) hs[i][j] = 0.f;
-    if (d < ch.end) {
-      const size_t own = static_cast<size_t>(d) * N + n0;
-      const float4 A4 = __ldg(reinterpret_cast<const float4*>(a.A + own));
-      A[0] = A4.x * kLog2e; A[1] = A4.y * kLog2e; A[2] = A4.z * kLog2e; A[3] = A4.w * kLog2e;
-      if (!from_start) chain_states(a, sp, b, seg, d, n0, A, hs[i]);
-      // the gradient entering the segment from behind
-      const float* from = nullptr;
-      int k = sp.segments - 1;
-      if (sp.segments == 1)
-        from = a.dhT ? a.dhT + b * state + own : nullptr;
-      else {
-        if (seg < k) --k;
-        from = sp.e + (static_cast<size_t>(b) * sp.segments + k) * state + own;
-      }
-      if (from) {
-        const float4 f = *reinterpret_cast<const float4*>(from);
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-      }
-      for (; k > seg; --k) {     // through segment k
-        const size_t at = static_cast<size_t>(b) * sp.segments + k;
-        const float u = sp.total[at * a.D + d];
-        const bool cleared = sp.cleared[at] != 0;
-        const float4 f = *reinterpret_cast<const float4*>(sp.e + (at - 1) * state + own);
-        const float add[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = cleared ? add[j] : fmaf(exp2_fast(A[j] * u), v[j], add[j]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      A2[p][j] = mul2(A2[p][j], both(kLog2e));
+      dA[p][j] = 0;
     }
-    reorder(A, nx);
-    reorder(v, nx);
-    reorder(hs[i], nx);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      A2[i][j] = pair(A[2 * j], A[2 * j + 1]);
-      E[i][j] = pair(v[2 * j], v[2 * j + 1]);
-      dA[i][j] = pair(0.f, 0.f);
-    }
-  }
+  const size_t at = static_cast<size_t>(b) * sp.segments + seg;
+  load_items(from_start ? nullptr : sp.h + at * state, hs);
+  // the gradient entering the segment from behind
+  load_items(sp.segments > 1 ? sp.e + at * state : a.dhT ? a.dhT + b * state : nullptr, E);
   for (int i = tid; i < L::kChannels; i += kBwdThreads) {
     const int d = ch.first + i;
     sm.bias[i] = a.dt_bias && d < ch.end ? a.dt_bias[d] : 0.f;
     sm.skip[i] = a.skip && d < ch.end ? a.skip[d] : 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sm.sums[tid][i] = 0.f;
-  __syncthreads();
+  for (int i = 0; i < 8; ++i) sm.px[tid][i] = 0.f;
+  float dbias[L::kSums];
+#pragma unroll
+  for (int i = 0; i < L::kSums; ++i) dbias[i] = 0.f;
 
-  for (int t0 = (t_end - 1) / kTile * kTile; t0 >= t_begin; t0 -= kTile) {
+  bool mark = false;
+  float ksum[4] = {0.f, 0.f, 0.f, 0.f};      // sums of u up to the tile, of this thread's channels
+  bool kclear = false;
+  // copies a tile's inputs and the state entering it
+  auto fetch = [&](int t0) {
     const int nt = min(kTile, t_end - t0);
-    // (u, u x, p) of the tile, B and C in all orders
+#pragma unroll
+    for (int i = 0; i < L::kPer; ++i) {
+      const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
+      if (v < L::kVecs && t < nt && ch.first + d < ch.end) {
+        const long long row = row0 + t0 + t;
+        copy8(&sm.x[t][d], static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
+        copy8(&sm.dt[t][d], static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
+        copy8(&sm.dy[t][d], static_cast<const T*>(a.dy) + row * a.D + ch.first + d);
+        if (Z) copy8(&sm.z[t][d], static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < L::kBcPer; ++i) {
+      const int v = tid + i * kBwdThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
+      const int t = w / (N / 8), n = 8 * (w % (N / 8));
+      if (v < L::kBcVecs && t < nt)
+        copy8(&sm.bc[which][t][n],
+              (which ? static_cast<const T*>(a.Cm) + (row0 + t0 + t) * a.cs
+                     : static_cast<const T*>(a.Bm) + (row0 + t0 + t) * a.bs) +
+                  ch.group * N + n);
+    }
+    const size_t tile = static_cast<size_t>(b) * sp.tiles + t0 / kTile;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) copy16(&sm.kept[i][tid], sp.kept + tile * state + place(i));
+      if (!from_start) {
+        const float2 s0 = *reinterpret_cast<const float2*>(sp.kept_sum + tile * a.D + ch.first + c0);
+        const float2 s1 = *reinterpret_cast<const float2*>(sp.kept_sum + tile * a.D + ch.first + c1);
+        ksum[0] = s0.x; ksum[1] = s0.y; ksum[2] = s1.x; ksum[3] = s1.y;
+      }
+    }
+    kclear = sp.kept_clear[tile] != 0;
+    mark = a.starts && tid < nt && a.starts[row0 + t0 + tid] != 0;
+  };
+
+  const int t_last = (t_end - 1) / kTile * kTile;
+  fetch(t_last);
+  __syncthreads();
+  for (int t0 = t_last; t0 >= t_begin; t0 -= kTile) {
+    const int nt = min(kTile, t_end - t0);
+    copies_done();
+    // u, u x and p of what this thread has copied
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
       const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
       if (v >= L::kVecs) break;
-      float x[8], u[8], p[8];
+      f32x2 x[4], u[4], p[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = u[j] = p[j] = 0.f;
+      for (int j = 0; j < 4; ++j) x[j] = u[j] = p[j] = 0;
       if (t < nt && ch.first + d < ch.end) {
-        const long long row = row0 + t0 + t;
-        load8(static_cast<const T*>(a.x) + row * a.xs + ch.first + d, x);
-        load8(static_cast<const T*>(a.dt) + row * a.dts + ch.first + d, u);
-        load8(static_cast<const T*>(a.dy) + row * a.D + ch.first + d, p);
-        float z[8];
-        if (Z) load8(static_cast<const T*>(a.z) + row * a.zs + ch.first + d, z);
+        f32x2 bias[4], z[4];
+        read8(&sm.x[t][d], x);
+        read8(&sm.dt[t][d], u);
+        read8(&sm.dy[t][d], p);
+        if (Z) read8(&sm.z[Z ? t : 0][d], z);
+        read8(&sm.bias[d], bias);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u[j] += sm.bias[d + j];
-          if (a.softplus) u[j] = softplus(u[j]);
-          x[j] *= u[j];
-          if (Z) p[j] *= silu(z[j]);
+        for (int j = 0; j < 4; ++j) {
+          u[j] = add2(u[j], bias[j]);
+          if (a.softplus) u[j] = softplus2(u[j]);
+          x[j] = mul2(u[j], x[j]);
+          if (Z) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
         }
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<float4*>(&sm.u[t][d + 4 * j]) =
-            make_float4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
-        *reinterpret_cast<float4*>(&sm.g[t][d + 4 * j]) =
-            make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-        *reinterpret_cast<float4*>(&sm.p[t][d + 4 * j]) =
-            make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-      }
+      write8(&sm.u[t][d], u);
+      write8(&sm.g[t][d], x);
+      write8(&sm.p[t][d], p);
     }
-    for (int v = tid; v < L::kBcVecs; v += kBwdThreads) {
-      const int which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
+    // B and C in all orders
+#pragma unroll
+    for (int i = 0; i < L::kBcPer; ++i) {
+      const int v = tid + i * kBwdThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
       const int t = w / (N / 8), n = 8 * (w % (N / 8));
+      if (v >= L::kBcVecs) break;
+      f32x2 y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = 0;
+      if (t < nt) read8(&sm.bc[which][t][n], y);
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.f;
-      if (t < nt)
-        load8((which ? static_cast<const T*>(a.Cm) + (row0 + t0 + t) * a.cs
-                     : static_cast<const T*>(a.Bm) + (row0 + t0 + t) * a.bs) + ch.group * N + n, x);
+      for (int j = 0; j < 4; ++j) split(y[j], x[2 * j], x[2 * j + 1]);
 #pragma unroll
-      for (int o = 0; o < 4; ++o)
+      for (int o = 0; o < L::kOrders; ++o)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           *reinterpret_cast<float4*>((which ? sm.c[o] : sm.b[o]) + t * N + n + 4 * j) =
@@ -436,150 +523,163 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
                           x[4 * j + (3 ^ o)]);
     }
     {
-      const bool mark = a.starts && tid < nt && a.starts[row0 + t0 + tid] != 0;
       const unsigned m = __ballot_sync(0xffffffffu, mark);
       if (tid == 0) sm.starts[0] = m;
     }
-    // the tile's first state
-    f32x2 h[4][2];
-    const size_t tile = static_cast<size_t>(b) * sp.tiles + t0 / kTile;
+    // the tile's first state: the segment's own, and what is left of the one that enters it
+    Items h;
+    {
+      float4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = ch.first + cbase + (i ^ cx);
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (d < ch.end) {
-        const float4 f = *reinterpret_cast<const float4*>(sp.kept + tile * state +
-                                                          static_cast<size_t>(d) * N + n0);
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-        reorder(v, nx);
-        if (!from_start && sp.kept_clear[tile] == 0) {
-          const float u = sp.kept_sum[tile * a.D + d];
+      for (int i = 0; i < 4; ++i)
+        v[i] = live ? sm.kept[i][tid] : make_float4(0.f, 0.f, 0.f, 0.f);
+      to_items(v, nx, h);
+      if (!from_start && !kclear) {
+        const f32x2 k2[2] = {pair(ksum[0], ksum[1]), pair(ksum[2], ksum[3])};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float lo, hi;
-            split(A2[i][j], lo, hi);
-            v[2 * j] = fmaf(exp2_fast(lo * u), hs[i][2 * j], v[2 * j]);
-            v[2 * j + 1] = fmaf(exp2_fast(hi * u), hs[i][2 * j + 1], v[2 * j + 1]);
-          }
-        }
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            h[p][j] = fma2(exp2_pair(mul2(A2[p][j], k2[p])), hs[p][j], h[p][j]);
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) h[i][j] = pair(v[2 * j], v[2 * j + 1]);
     }
     __syncthreads();
+    if (t0 > t_begin) fetch(t0 - kTile);
     const unsigned starts = sm.starts[0];
 
     // forward through the tile, a state kept every kSub tokens
     const int subs = (nt + kSub - 1) / kSub;
     for (int s = 0; s < subs; ++s) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float4 f;
-        split(h[i][0], f.x, f.y);
-        split(h[i][1], f.z, f.w);
-        sm.h[s][i][tid] = f;
-      }
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          sm.h[s][2 * p + j][tid] = make_ulonglong2(h[p][2 * j], h[p][2 * j + 1]);
       if (s + 1 == subs) break;
 #pragma unroll
       for (int k = 0; k < kSub; ++k) {
         const int t = s * kSub + k;
         if ((starts >> t) & 1) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[i][0] = h[i][1] = pair(0.f, 0.f);
-        }
-        const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(Border + t * N + n0);
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = sm.u[t][cbase + (i ^ cx)], g = sm.g[t][cbase + (i ^ cx)];
-          const f32x2 u2 = pair(u, u), g2 = pair(g, g);
-          h[i][0] = fma2(exp2_pair(mul2(A2[i][0], u2)), h[i][0], mul2(g2, B.x));
-          h[i][1] = fma2(exp2_pair(mul2(A2[i][1], u2)), h[i][1], mul2(g2, B.y));
+            for (int j = 0; j < 4; ++j) h[p][j] = 0;
         }
+        const float4 B = *reinterpret_cast<const float4*>(Border + t * N + n0);
+        const f32x2 b2[4] = {both(B.x), both(B.y), both(B.z), both(B.w)};
+        const f32x2 u[2] = {*reinterpret_cast<const f32x2*>(&sm.u[t][c0]),
+                            *reinterpret_cast<const f32x2*>(&sm.u[t][c1])};
+        const f32x2 g[2] = {*reinterpret_cast<const f32x2*>(&sm.g[t][c0]),
+                            *reinterpret_cast<const f32x2*>(&sm.g[t][c1])};
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            h[p][j] = fma2(exp2_pair(mul2(A2[p][j], u[p])), h[p][j], mul2(g[p], b2[j]));
       }
     }
     // and back
     for (int s = subs - 1; s >= 0; --s) {
-      f32x2 da[kSub][4][2], ah[kSub][4][2];     // decays, decayed states
+      Items da[kSub], ah[kSub];     // decays, decayed states
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 f = sm.h[s][i][tid];
-        h[i][0] = pair(f.x, f.y);
-        h[i][1] = pair(f.z, f.w);
-      }
-      // tokens behind the end have u = u x = p = B = C = 0: they change nothing
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const ulonglong2 v = sm.h[s][2 * p + j][tid];
+          h[p][2 * j] = v.x;
+          h[p][2 * j + 1] = v.y;
+        }
+      // (tokens behind the end have u = u x = p = B = C = 0: they change nothing)
 #pragma unroll
       for (int k = 0; k < kSub; ++k) {
         const int t = s * kSub + k;
-        const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(Border + t * N + n0);
-        const bool first = (starts >> t) & 1;
+        const float4 B = *reinterpret_cast<const float4*>(Border + t * N + n0);
+        const f32x2 b2[4] = {both(B.x), both(B.y), both(B.z), both(B.w)};
+        const f32x2 u[2] = {*reinterpret_cast<const f32x2*>(&sm.u[t][c0]),
+                            *reinterpret_cast<const f32x2*>(&sm.u[t][c1])};
+        const f32x2 g[2] = {*reinterpret_cast<const f32x2*>(&sm.g[t][c0]),
+                            *reinterpret_cast<const f32x2*>(&sm.g[t][c1])};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = sm.u[t][cbase + (i ^ cx)], g = sm.g[t][cbase + (i ^ cx)];
-          const f32x2 u2 = pair(u, u), g2 = pair(g, g);
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            da[k][i][j] = exp2_pair(mul2(A2[i][j], u2));
-            ah[k][i][j] = mul2(da[k][i][j], h[i][j]);
-            if (first) ah[k][i][j] = pair(0.f, 0.f);
-            h[i][j] = fma2(g2, j ? B.y : B.x, ah[k][i][j]);
+          for (int j = 0; j < 4; ++j) {
+            da[k][p][j] = exp2_pair(mul2(A2[p][j], u[p]));
+            ah[k][p][j] = mul2(da[k][p][j], h[p][j]);
+            h[p][j] = fma2(g[p], b2[j], ah[k][p][j]);
           }
+        if ((starts >> t) & 1) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              ah[k][p][j] = 0;
+              h[p][j] = mul2(g[p], b2[j]);
+            }
         }
       }
 #pragma unroll
       for (int k = kSub - 1; k >= 0; --k) {
         const int t = s * kSub + k;
-        const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(Border + t * N + n0);
-        const ulonglong2 C = *reinterpret_cast<const ulonglong2*>(Corder + t * N + n0);
-        f32x2 db[2], dc[2];
-        float q[4], r[4], y[4];
-        db[0] = db[1] = dc[0] = dc[1] = pair(0.f, 0.f);
-        const bool first = (starts >> t) & 1;
+        const float4 B = *reinterpret_cast<const float4*>(Border + t * N + n0);
+        const float4 C = *reinterpret_cast<const float4*>(Corder + t * N + n0);
+        const f32x2 b2[4] = {both(B.x), both(B.y), both(B.z), both(B.w)};
+        const f32x2 cc[4] = {both(C.x), both(C.y), both(C.z), both(C.w)};
+        f32x2 db[4], dc[4], q[2], r[2], y[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = cbase + (i ^ cx);
-          const float u = sm.u[t][at], g = sm.g[t][at], p = sm.p[t][at];
-          const f32x2 u2 = pair(u, u), g2 = pair(g, g), p2 = pair(p, p);
-          f32x2 qq = pair(0.f, 0.f), rr = qq, yy = qq;
+        for (int p = 0; p < 2; ++p) {
+          const int c = p ? c1 : c0;
+          const f32x2 u = *reinterpret_cast<const f32x2*>(&sm.u[t][c]);
+          const f32x2 g = *reinterpret_cast<const f32x2*>(&sm.g[t][c]);
+          const f32x2 pp = *reinterpret_cast<const f32x2*>(&sm.p[t][c]);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const f32x2 Bj = j ? B.y : B.x, Cj = j ? C.y : C.x;
-            const f32x2 e = fma2(Cj, p2, E[i][j]);
-            const f32x2 ht = fma2(g2, Bj, ah[k][i][j]);
-            const f32x2 w = mul2(e, ah[k][i][j]);
-            db[j] = fma2(g2, e, db[j]);
-            dc[j] = fma2(p2, ht, dc[j]);
-            qq = fma2(Bj, e, qq);
-            rr = fma2(A2[i][j], w, rr);
-            dA[i][j] = fma2(u2, w, dA[i][j]);
-            if (Z) yy = fma2(Cj, ht, yy);
-            E[i][j] = mul2(da[k][i][j], e);
-            if (first) E[i][j] = pair(0.f, 0.f);
+          for (int j = 0; j < 4; ++j) {
+            const f32x2 ahk = ah[k][p][j];
+            const f32x2 e = fma2(cc[j], pp, E[p][j]);
+            const f32x2 ht = fma2(g, b2[j], ahk);
+            const f32x2 w = mul2(e, ahk);
+            db[j] = p ? fma2(g, e, db[j]) : mul2(g, e);
+            dc[j] = p ? fma2(pp, ht, dc[j]) : mul2(pp, ht);
+            q[p] = j ? fma2(b2[j], e, q[p]) : mul2(b2[j], e);
+            r[p] = j ? fma2(A2[p][j], w, r[p]) : mul2(A2[p][j], w);
+            if (Z) y[p] = j ? fma2(cc[j], ht, y[p]) : mul2(cc[j], ht);
+            dA[p][j] = fma2(u, w, dA[p][j]);
+            E[p][j] = mul2(da[k][p][j], e);
           }
-          q[i] = sum2(qq);
-          r[i] = sum2(rr);
-          if (Z) y[i] = sum2(yy);
+        }
+        if ((starts >> t) & 1) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) E[p][j] = 0;
         }
         // over the state lanes: by halves over the 4 channels, then whole
-        auto over_states = [&](float (&v)[4], float* out) {
-          v[0] += pass(v[1], 1);
-          v[2] += pass(v[3], 1);
-          if constexpr (L::kStateLanes >= 4) v[0] += pass(v[2], 2);
-          if constexpr (L::kStateLanes >= 8) v[0] += pass(v[0], 4);
-          if constexpr (L::kStateLanes >= 16) v[0] += pass(v[0], 8);
-          if (sl < 4) {
-            out[cbase + cx] = v[0];
-            if (L::kStateLanes == 2) out[cbase + (2 ^ cx)] = v[2];
+        auto over_states = [&](const f32x2 (&v)[2], float* out) {
+          float lo, hi, lo1, hi1;
+          split(v[0], lo, hi);
+          split(v[1], lo1, hi1);
+          lo += pass(lo1, 1);
+          hi += pass(hi1, 1);
+          if constexpr (L::kStateLanes == 2) {
+            *reinterpret_cast<float2*>(out + c0) = make_float2(lo, hi);
+          } else {
+            const bool up = sl & 2;
+            float keep = up ? hi : lo;
+            keep += pass(up ? lo : hi, 2);
+            if constexpr (L::kStateLanes >= 8) keep += pass(keep, 4);
+            if constexpr (L::kStateLanes >= 16) keep += pass(keep, 8);
+            if (sl < 4) out[c0 + up] = keep;
           }
         };
-        over_states(q, sm.q[t]);
+        over_states(q, sm.g[t]);
         over_states(r, sm.r[t]);
-        if (Z) over_states(y, sm.y[t]);
+        if (Z) over_states(y, sm.p[t]);
         // over the channel lanes
         float vb[4], vc[4];
-        split(db[0], vb[0], vb[1]);
-        split(db[1], vb[2], vb[3]);
-        split(dc[0], vc[0], vc[1]);
-        split(dc[1], vc[2], vc[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          vb[j] = sum2(db[j]);
+          vc[j] = sum2(dc[j]);
+        }
         constexpr int kStep = L::kStateLanes;     // lanes to the next channel lane
         vb[0] += pass(vb[1], kStep);
         vb[2] += pass(vb[3], kStep);
@@ -608,41 +708,68 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
         }
       }
     }
-    __syncthreads();
 
-    // the tile's outputs
+    // the tile's outputs; the inputs once more, as the next tile's are on their way
+    Raw8<T> rx[L::kPer], rdt[L::kPer], ry[L::kPer], rz[L::kPer];
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
       const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
       if (v >= L::kVecs || t >= nt || ch.first + d >= ch.end) continue;
       const long long row = row0 + t0 + t;
-      const size_t out = static_cast<size_t>(row) * a.D + ch.first + d;
-      float x[8], raw[8], dy[8], z[8], dx[8], ddt[8], dz[8];
-      load8(static_cast<const T*>(a.x) + row * a.xs + ch.first + d, x);
-      load8(static_cast<const T*>(a.dt) + row * a.dts + ch.first + d, raw);
-      if (Z) {
-        load8(static_cast<const T*>(a.dy) + row * a.D + ch.first + d, dy);
-        load8(static_cast<const T*>(a.z) + row * a.zs + ch.first + d, z);
-      }
+      rx[i].load(static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
+      rdt[i].load(static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
+      ry[i].load(static_cast<const T*>(a.dy) + row * a.D + ch.first + d);
+      if (Z) rz[i].load(static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
+    }
+    __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float q = sm.q[t][d + j], p = sm.p[t][d + j], sk = sm.skip[d + j];
-        dx[j] = sm.u[t][d + j] * q;
-        if (a.skip) dx[j] = fmaf(sk, p, dx[j]);
-        // A2 is log2(e) A
-        ddt[j] = fmaf(x[j], q, sm.r[t][d + j] * (1.f / kLog2e));
-        if (a.softplus) ddt[j] *= sigmoid(raw[j] + sm.bias[d + j]);
-        if (Z) {
-          float y = sm.y[t][d + j];
-          if (a.skip) y = fmaf(sk, x[j], y);
-          dz[j] = dy[j] * y * silu_slope(z[j]);
+    for (int i = 0; i < L::kPer; ++i) {
+      const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
+      if (v >= L::kVecs || t >= nt || ch.first + d >= ch.end) continue;
+      const size_t out = static_cast<size_t>(row0 + t0 + t) * a.D + ch.first + d;
+      const f32x2 one = both(1.f), minus = both(-1.f);
+      f32x2 x[4], q[4], w[4], p[4], skip[4];
+      raw_pairs(rx[i], x);
+      raw_pairs(ry[i], p);
+      read8(&sm.g[t][d], q);
+      read8(&sm.skip[d], skip);
+      if (Z) {
+        f32x2 z[4], y[4], dz[4];
+        raw_pairs(rz[i], z);
+        read8(&sm.p[t][d], y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // silu = z sg, its slope sg (1 + z (1 - sg)) = sg + silu (1 - sg)
+          const f32x2 sg = sigmoid2(z[j]), act = mul2(z[j], sg);
+          if (a.skip) y[j] = fma2(skip[j], x[j], y[j]);
+          dz[j] = mul2(mul2(p[j], y[j]), fma2(act, fma2(sg, minus, one), sg));
+          p[j] = mul2(p[j], act);
         }
-        sm.sums[tid][j] = fmaf(p, x[j], sm.sums[tid][j]);
-        sm.sums[tid][8 + j] += ddt[j];
+        store_pairs(static_cast<T*>(a.dz) + out, dz);
       }
-      store8(static_cast<T*>(a.dx) + out, dx);
-      store8(static_cast<T*>(a.ddt) + out, ddt);
-      if (Z) store8(static_cast<T*>(a.dz) + out, dz);
+      f32x2 bias[4], u[4], dt[4], dx[4];
+      raw_pairs(rdt[i], dt);
+      read8(&sm.bias[d], bias);
+      read8(&sm.u[t][d], u);
+      read8(&sm.r[t][d], w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dx[j] = mul2(u[j], q[j]);
+        if (a.skip) dx[j] = fma2(skip[j], p[j], dx[j]);
+        // (A2 is log2(e) A)
+        w[j] = fma2(x[j], q[j], mul2(w[j], both(1.f / kLog2e)));
+        if (a.softplus) w[j] = mul2(w[j], sigmoid2(add2(dt[j], bias[j])));
+      }
+      store_pairs(static_cast<T*>(a.dx) + out, dx);
+      store_pairs(static_cast<T*>(a.ddt) + out, w);
+      if (a.dt_bias) write8(&sm.r[t][d], w);
+      if (a.skip) {
+        f32x2 sum[4];
+        read8(sm.px[tid], sum);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = fma2(p[j], x[j], sum[j]);
+        write8(sm.px[tid], sum);
+      }
     }
     const int blocks = gridDim.x / a.G, block = blockIdx.x % blocks;
     for (int i = tid; i < nt * 2 * N; i += kBwdThreads) {
@@ -654,32 +781,38 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
                  j] = s;
     }
     __syncthreads();
-  }
-
-  const size_t part = static_cast<size_t>(b) * sp.segments + seg;
+    if (a.dt_bias) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int d = ch.first + cbase + (i ^ cx);
-    if (d >= ch.end) continue;
-    const size_t own = static_cast<size_t>(d) * N + n0;
-    float v[4];
-    split(dA[i][0], v[0], v[1]);
-    split(dA[i][1], v[2], v[3]);
-    reorder(v, nx);
-    *reinterpret_cast<float4*>(sp.dA_part + part * state + own) = make_float4(v[0], v[1], v[2], v[3]);
-    if (seg == 0 && a.dh0) {
-      split(E[i][0], v[0], v[1]);
-      split(E[i][1], v[2], v[3]);
-      reorder(v, nx);
-      *reinterpret_cast<float4*>(a.dh0 + b * state + own) = make_float4(v[0], v[1], v[2], v[3]);
+      for (int i = 0; i < L::kSums; ++i) {
+        const int d = tid + i * kBwdThreads;
+        if (d < L::kChannels)
+          for (int t = 0; t < nt; ++t) dbias[i] += sm.r[t][d];
+      }
     }
   }
-  // dskip and ddt_bias: threads kRow apart have the same channels
-  for (int i = tid; i < 2 * L::kChannels; i += kBwdThreads) {
-    const int which = i / L::kChannels, d = i % L::kChannels;
+
+  // (places of channels past the group's end are not written)
+  if (live) {
+    float4 v[4];
+    from_items(dA, nx, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(sp.dA_part + at * state + place(i)) = v[i];
+    if (from_start && a.dh0) {
+      from_items(E, nx, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(a.dh0 + b * state + place(i)) = v[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < L::kSums; ++i) {
+    const int d = tid + i * kBwdThreads;
+    if (d >= L::kChannels || ch.first + d >= ch.end) continue;
+    // dskip: threads kRow apart have the same channels
     float s = 0.f;
-    for (int k = d / 8; k < kBwdThreads; k += L::kRow) s += sm.sums[k][8 * which + d % 8];
-    if (ch.first + d < ch.end) sp.d_part[(part * 2 + which) * a.D + ch.first + d] = s;
+    for (int k = d / 8; k < kBwdThreads; k += L::kRow) s += sm.px[k][d % 8];
+    sp.d_part[at * 2 * a.D + ch.first + d] = s;
+    sp.d_part[(at * 2 + 1) * a.D + ch.first + d] = dbias[i];
   }
 }
 
@@ -733,14 +866,12 @@ int blocks_of(const SpaceArgs& a, int channels) {
 
 }  // namespace
 
-int space_channels(int N, bool backward) {
-  return backward ? kWarps * 4 * 32 / (N / 4) : kThreads / (N / kStates);
-}
+int space_bwd_channels(int N) { return kWarps * 4 * 32 / (N / 4); }
 
 cudaError_t launch_space_bwd_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                     cudaStream_t stream) {
   return by_states(a.N, f32, [&](auto t, auto n) {
-    constexpr int kBytes = static_cast<int>(sizeof(PreShared<n>));
+    constexpr int kBytes = static_cast<int>(sizeof(PreShared<decltype(t), n>));
     auto* kern = sp.segments > 1 ? space_bwd_states_kernel<decltype(t), n, true>
                                  : space_bwd_states_kernel<decltype(t), n, false>;
     const cudaError_t err =
@@ -755,8 +886,9 @@ cudaError_t launch_space_bwd_states(const SpaceArgs& a, const SpaceSplit& sp, bo
 cudaError_t launch_space_bwd(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                              cudaStream_t stream) {
   const cudaError_t err = by_states(a.N, f32, [&](auto t, auto n) {
-    constexpr int kBytes = static_cast<int>(sizeof(BwdShared<n>));
     auto* kern = a.z ? space_bwd_kernel<decltype(t), n, true> : space_bwd_kernel<decltype(t), n, false>;
+    const int kBytes = static_cast<int>(a.z ? sizeof(BwdShared<decltype(t), n, true>)
+                                            : sizeof(BwdShared<decltype(t), n, false>));
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
