@@ -77,31 +77,40 @@ gdr::SpaceArgs space_args(const gdr_state_space_shape* s) {
   return a;
 }
 
-// Time of n CTAs of one length, as a part of what two on every SM take: one alone on an
-// SM runs faster than two, by less than half.
-double waves(long long n) {
-  const long long rest = n % (2 * kSms);
-  return static_cast<double>(n / (2 * kSms)) + (rest == 0 ? 0.0 : rest <= kSms ? 0.6 : 1.0);
+// Time of n CTAs of equal length, `most` of which an SM holds at once: one takes `first`, each
+// further one beside it `next` more.
+double waves(long long n, int most, double first, double next) {
+  const long long full = n / (kSms * most), rest = (n % (kSms * most) + kSms - 1) / kSms;
+  return full * (first + next * (most - 1)) + (rest ? first + next * (rest - 1) : 0.0);
 }
 
 // Segments of each sequence. A CTA walks one segment of a batch row's channels, so few
-// sequences are cut until the CTAs fill the SMs. The forward pays for a cut with a walk
-// over all segments but the last for their end states (0.7 of the other walk's time); the
-// backward makes that walk for its kept states anyway.
+// sequences are cut until the CTAs fill the SMs.
+// Forward: uncut, a CTA has half the channels, and needs no other launch; a cut costs a walk
+// over all segments but the last for their end states (0.65 of the other walk's time), and the
+// chain. Times of a token (us, bf16): uncut 0.084 and 0.062 (a CTA alone on its SM; a second
+// one beside it), cut 0.31 and 0.12. (4 x 4096 x 4096 channels x 16: 598 us uncut, 565 in 38
+// segments, 590 in 14; 1 x 65536 x 2048: 5510, 1133, 1867.)
+// The backward walks forward for its kept states anyway; a segment costs a CTA's start, about
+// as long as a tile (4 x 4096 x 2048 x 16: 1132 us in 4 segments, 997 in 9, 974 in 19).
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
   const int tile = backward ? gdr::kSpaceTile : 32;
   const int tiles = (s->T + tile - 1) / tile, each = s->D / s->G;
-  const int channels = backward ? gdr::space_bwd_channels(s->N) : gdr::space_channels(s->N);
-  sp->blocks = (each + channels - 1) / channels;
-  const long long ctas = static_cast<long long>(s->B) * s->G * sp->blocks;
+  auto blocks = [&](int channels) { return (each + channels - 1) / channels; };
+  sp->blocks = blocks(backward ? gdr::space_bwd_channels(s->N) : gdr::space_channels(s->N, false));
+  const long long rows = static_cast<long long>(s->B) * s->G, ctas = rows * sp->blocks;
   double best = 0.0;
   int per = tiles;
-  for (int n = 1; n <= 64 && n <= tiles; ++n) {
+  for (int n = 1; n <= 128 && n <= tiles; ++n) {
     const int len = (tiles + n - 1) / n, segments = (tiles + len - 1) / len;
-    // (a CTA's start and end take as long as a tile)
-    double cost = waves(ctas * segments) * (len + 1.0);
-    if (segments > 1)
-      cost += backward ? 1.0 : 0.7 * waves(ctas * (segments - 1)) * (len + 1.0) + 2.0;
+    double cost;
+    if (backward)
+      cost = waves(ctas * segments, 2, 0.7, 0.3) * (len + 1.0);
+    else if (segments == 1)
+      cost = waves(rows * blocks(gdr::space_channels(s->N, true)), 2, 0.084, 0.062) * s->T;
+    else
+      cost = (waves(ctas * segments, 5, 0.31, 0.12) + 0.65 * waves(ctas * (segments - 1), 5, 0.31, 0.12)) *
+                 (len + 1.0) * tile + 25.0;
     if (n == 1 || cost < best) {
       best = cost;
       per = len;

@@ -7,7 +7,7 @@
 // channel. What bounds it is the exponential unit and the fp32 pipe; multiply-adds run two
 // to an instruction.
 //
-// A thread holds 8 states of two channels and walks the tokens in order; N / 8 neighbouring
+// Cut into segments, a thread holds 8 states of two channels and walks the tokens in order; N / 8 neighbouring
 // lanes share the channels and add their parts of y. (With one channel a thread, every B and
 // C read from shared memory served half as many states, and that was the bound.) A tile of
 // tokens is staged in shared memory as u and u x for each channel and B, C in fp32; the next
@@ -26,24 +26,24 @@
 namespace gdr {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kStates = 8;        // states of a thread, of each of its channels
-constexpr int kOwn = 2;           // channels of a thread
-
-template <int N>
+// NARROW: a thread has 4 states of one channel instead of 8 of two.
+template <int N, bool NARROW>
 struct Layout {
+  static constexpr int kThreads = NARROW ? 256 : 128;
+  static constexpr int kOwn = NARROW ? 1 : 2;                    // channels of a thread
+  static constexpr int kStates = NARROW ? 4 : 8;                 // states of each
   static constexpr int kLanes = N / kStates;                     // lanes of a channel
   static constexpr int kChannels = kOwn * kThreads / kLanes;     // channels of a CTA
-  static constexpr int kTile = N < 32 ? N : 32;                  // tokens of a tile
+  static constexpr int kTile = NARROW || N > 16 ? 32 : N;        // tokens of a tile
   static constexpr int kVecs = kTile * kChannels / 8;            // vectors of 8 channels in a tile
   static constexpr int kPer = (kVecs + kThreads - 1) / kThreads;
   static constexpr int kBcVecs = 2 * kTile * N / 8;              // vectors of B and C
   static constexpr int kBcPer = (kBcVecs + kThreads - 1) / kThreads;
 };
 
-template <typename T, int N>
+template <typename T, int N, bool NARROW>
 struct __align__(16) Shared {
-  using L = Layout<N>;
+  using L = Layout<N, NARROW>;
   float u[L::kTile][L::kChannels], g[L::kTile][L::kChannels];    // u (then y), u x
   float bc[2][L::kTile][N];
   T x[2][L::kTile][L::kChannels], dt[L::kTile][L::kChannels], z[2][L::kTile][L::kChannels];
@@ -54,12 +54,13 @@ struct __align__(16) Shared {
 
 // WALK: y and the end state, from the segment's start state. Else: the segment's own end
 // state (segment 0's from h0), its sum of u and whether a document starts in it.
-template <typename T, int N, bool WALK>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 2)
+template <typename T, int N, bool NARROW, bool WALK>
+__global__ void __launch_bounds__(NARROW ? 256 : 128, (sizeof(T) == 2 ? 5 : 2) / (NARROW ? 2 : 1))
     space_kernel(const SpaceArgs a, const SpaceSplit sp) {
-  using L = Layout<N>;
+  using L = Layout<N, NARROW>;
+  constexpr int kThreads = L::kThreads, kOwn = L::kOwn, kStates = L::kStates;
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  Shared<T, N>& sm = *reinterpret_cast<Shared<T, N>*>(raw_smem);
+  Shared<T, N, NARROW>& sm = *reinterpret_cast<Shared<T, N, NARROW>*>(raw_smem);
   const int tid = threadIdx.x;
   const Channels ch(a, L::kChannels, blockIdx.x);
   const int seg = blockIdx.y, b = blockIdx.z;
@@ -81,24 +82,29 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 2)
 #pragma unroll
   for (int o = 0; o < kOwn; ++o) {
     const size_t own = static_cast<size_t>(c + o) * N + n0;     // in a [D, N] array
-    float A[kStates], v[kStates];
+    f32x2 A[kStates / 2], v[kStates / 2];
 #pragma unroll
-    for (int i = 0; i < kStates; ++i) A[i] = v[i] = 0.f;
+    for (int i = 0; i < kStates / 2; ++i) A[i] = v[i] = 0;
     if (live) {
-      load8(a.A + own, A);
-      if (from) {
-        const float4* p = reinterpret_cast<const float4*>(from + own);
-        const float4 lo = p[0], hi = p[1];
-        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+#pragma unroll
+      for (int i = 0; i < kStates / 4; ++i) {
+        const ulonglong2 q = __ldg(reinterpret_cast<const ulonglong2*>(a.A + own) + i);
+        A[2 * i] = q.x;
+        A[2 * i + 1] = q.y;
+        if (from) {
+          const ulonglong2 w = reinterpret_cast<const ulonglong2*>(from + own)[i];
+          v[2 * i] = w.x;
+          v[2 * i + 1] = w.y;
+        }
+        if (!WALK && seg == 0)
+          reinterpret_cast<ulonglong2*>(sp.h + static_cast<size_t>(b) * sp.segments * state + own)[i] =
+              make_ulonglong2(v[2 * i], v[2 * i + 1]);
       }
-      if (!WALK && seg == 0)
-        store8(sp.h + static_cast<size_t>(b) * sp.segments * state + own, v);
     }
 #pragma unroll
     for (int i = 0; i < kStates / 2; ++i) {
-      A2[o][i] = pair(A[2 * i] * kLog2e, A[2 * i + 1] * kLog2e);
-      h[o][i] = pair(v[2 * i], v[2 * i + 1]);
+      A2[o][i] = mul2(A[i], both(kLog2e));
+      h[o][i] = v[i];
     }
   }
   for (int i = tid; i < L::kChannels; i += kThreads) {
@@ -176,19 +182,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 2)
   int cleared = 0;
   // one token, which may be a document's first: this thread's parts of its channels' y
   auto token = [&](int t, bool first, float (&y)[kOwn]) {
-    const float2 u = *reinterpret_cast<const float2*>(&sm.u[t][ci]);
-    const float2 g = *reinterpret_cast<const float2*>(&sm.g[t][ci]);
+    float u[kOwn], g[kOwn];
+    if constexpr (kOwn == 2) {
+      const float2 v = *reinterpret_cast<const float2*>(&sm.u[t][ci]);
+      const float2 w = *reinterpret_cast<const float2*>(&sm.g[t][ci]);
+      u[0] = v.x; u[1] = v.y; g[0] = w.x; g[1] = w.y;
+      if (!WALK) usum = add2(usum, pair(v.x, v.y));
+    } else {
+      u[0] = sm.u[t][ci];
+      g[0] = sm.g[t][ci];
+      if (!WALK) usum = add2(usum, pair(u[0], 0.f));
+    }
     if (first) {
 #pragma unroll
       for (int o = 0; o < kOwn; ++o)
 #pragma unroll
         for (int i = 0; i < kStates / 2; ++i) h[o][i] = 0;
     }
-    if (!WALK) usum = add2(usum, pair(u.x, u.y));
-    const f32x2 u2[kOwn] = {both(u.x), both(u.y)}, g2[kOwn] = {both(g.x), both(g.y)};
     const ulonglong2* B = reinterpret_cast<const ulonglong2*>(&sm.bc[0][t][n0]);
     const ulonglong2* C = reinterpret_cast<const ulonglong2*>(&sm.bc[1][t][n0]);
-    f32x2 part[kOwn][2];
+    f32x2 part[kOwn];
 #pragma unroll
     for (int q = 0; q < kStates / 4; ++q) {
       const ulonglong2 bq = B[q];
@@ -196,52 +209,58 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 2)
       if (WALK) cq = C[q];
 #pragma unroll
       for (int o = 0; o < kOwn; ++o) {
-        h[o][2 * q] = fma2(exp2_pair(mul2(A2[o][2 * q], u2[o])), h[o][2 * q], mul2(g2[o], bq.x));
-        h[o][2 * q + 1] =
-            fma2(exp2_pair(mul2(A2[o][2 * q + 1], u2[o])), h[o][2 * q + 1], mul2(g2[o], bq.y));
-        if (WALK) {
-          part[o][0] = q ? fma2(cq.x, h[o][2 * q], part[o][0]) : mul2(cq.x, h[o][2 * q]);
-          part[o][1] = q ? fma2(cq.y, h[o][2 * q + 1], part[o][1]) : mul2(cq.y, h[o][2 * q + 1]);
-        }
+        const f32x2 u2 = both(u[o]), g2 = both(g[o]);
+        f32x2& h0 = h[o][2 * q];
+        f32x2& h1 = h[o][2 * q + 1];
+        h0 = fma2(exp2_pair(mul2(A2[o][2 * q], u2)), h0, mul2(g2, bq.x));
+        h1 = fma2(exp2_pair(mul2(A2[o][2 * q + 1], u2)), h1, mul2(g2, bq.y));
+        if (WALK) part[o] = fma2(cq.y, h1, q ? fma2(cq.x, h0, part[o]) : mul2(cq.x, h0));
       }
     }
     if (WALK)
 #pragma unroll
-      for (int o = 0; o < kOwn; ++o) y[o] = sum2(add2(part[o][0], part[o][1]));
+      for (int o = 0; o < kOwn; ++o) y[o] = sum2(part[o]);
   };
   // y of four tokens: summed over the channels' lanes by halves, each lane going on with half
-  // of the sums (one of the channels, then half of the tokens). Written behind all four,
-  // whose loads would else wait for one another.
-  auto put = [&](int t, float (&y)[4][kOwn]) {
+  // of the sums (one of two channels, half of the tokens). Written behind all four, whose
+  // loads would else wait for one another.
+  auto put = [&](int t, const float (&y)[4][kOwn]) {
+    // `n` sums, of which lanes apart by `bit` keep every other one: index 2 i + (lane & bit)
+    auto halve = [&](auto n, const float* in, int bit, float* out) {
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        const bool up = lane & bit;
+        out[i] = (up ? in[2 * i + 1] : in[2 * i]) +
+                 __shfl_xor_sync(0xffffffffu, up ? in[2 * i] : in[2 * i + 1], bit);
+      }
+    };
+    using std::integral_constant;
     if constexpr (L::kLanes == 1) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int o = 0; o < kOwn; ++o) sm.u[t + k][ci + o] = y[k][o];
     } else {
-      const bool odd = lane & 1;
-      float r[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        r[k] = (odd ? y[k][1] : y[k][0]) +
-               __shfl_xor_sync(0xffffffffu, odd ? y[k][0] : y[k][1], 1);
+      constexpr int kAll = 4 * kOwn;           // 8 or 4 sums, the channels fastest
+      float r[kAll / 2], q[kAll / 4 > 0 ? kAll / 4 : 1], v[1];
+      halve(integral_constant<int, kAll>{}, &y[0][0], 1, r);
+      const int b0 = lane & 1, b1 = (lane >> 1) & 1, b2 = (lane >> 2) & 1;
+      auto at = [&](int i) -> float& { return sm.u[t + i / kOwn][ci + i % kOwn]; };
       if constexpr (L::kLanes == 2) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sm.u[t + k][ci + lane] = r[k];
+        for (int i = 0; i < kAll / 2; ++i) at(2 * i + b0) = r[i];
       } else {
-        const bool up = lane & 2;
-        float q[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          q[j] = (up ? r[2 * j + 1] : r[2 * j]) +
-                 __shfl_xor_sync(0xffffffffu, up ? r[2 * j] : r[2 * j + 1], 2);
+        halve(integral_constant<int, kAll / 2>{}, r, 2, q);
         if constexpr (L::kLanes == 4) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) sm.u[t + 2 * j + up][ci + odd] = q[j];
-        } else {
-          const bool far = lane & 4;
-          const float v = (far ? q[1] : q[0]) + __shfl_xor_sync(0xffffffffu, far ? q[0] : q[1], 4);
-          sm.u[t + 2 * far + up][ci + odd] = v;
+          for (int i = 0; i < kAll / 4; ++i) at(4 * i + 2 * b1 + b0) = q[i];
+        } else if constexpr (kAll == 8) {      // 8 lanes of two channels
+          halve(integral_constant<int, 2>{}, q, 4, v);
+          at(4 * b2 + 2 * b1 + b0) = v[0];
+        } else {                               // 8 or 16 lanes of one: whole
+          v[0] = q[0] + __shfl_xor_sync(0xffffffffu, q[0], 4);
+          if constexpr (L::kLanes == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8);
+          if (lane < 4) at(2 * b1 + b0) = v[0];
         }
       }
     }
@@ -307,17 +326,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 2)
     if (seg == sp.segments - 1 && a.hT) out = a.hT + b * state;
   } else {
     out = sp.h + (static_cast<size_t>(b) * sp.segments + seg + 1) * state;
-    if (live && n0 == 0)
-      *reinterpret_cast<f32x2*>(sp.total + (static_cast<size_t>(b) * sp.segments + seg) * a.D + c) =
-          usum;
+    float u0, u1;
+    split(usum, u0, u1);
+    float* total = sp.total + (static_cast<size_t>(b) * sp.segments + seg) * a.D + c;
+    if (live && n0 == 0) {
+      total[0] = u0;
+      if (kOwn == 2) total[1] = u1;
+    }
     if (blockIdx.x == 0 && tid == 0) sp.cleared[b * sp.segments + seg] = cleared;
   }
   if (out && live) {
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) {
       ulonglong2* p = reinterpret_cast<ulonglong2*>(out + static_cast<size_t>(c + o) * N + n0);
-      p[0] = make_ulonglong2(h[o][0], h[o][1]);
-      p[1] = make_ulonglong2(h[o][2], h[o][3]);
+#pragma unroll
+      for (int i = 0; i < kStates / 4; ++i) p[i] = make_ulonglong2(h[o][2 * i], h[o][2 * i + 1]);
     }
   }
 }
@@ -424,31 +447,35 @@ cudaError_t by_states(int N, bool f32, F f) {
   return typed(integral_constant<int, 64>{});
 }
 
-template <bool WALK>
-cudaError_t launch(const SpaceArgs& a, const SpaceSplit& sp, int segments, bool f32,
-                   cudaStream_t stream) {
+template <bool NARROW, bool WALK>
+cudaError_t launch_as(const SpaceArgs& a, const SpaceSplit& sp, int segments, bool f32,
+                      cudaStream_t stream) {
   return by_states(a.N, f32, [&](auto t, auto n) {
-    constexpr int kBytes = static_cast<int>(sizeof(Shared<decltype(t), n>));
-    auto* kern = space_kernel<decltype(t), n, WALK>;
+    using L = Layout<n, NARROW>;
+    constexpr int kBytes = static_cast<int>(sizeof(Shared<decltype(t), n, NARROW>));
+    auto* kern = space_kernel<decltype(t), n, NARROW, WALK>;
     const cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (err != cudaSuccess) return err;
-    const int each = a.D / a.G, per = (each + Layout<n>::kChannels - 1) / Layout<n>::kChannels;
-    kern<<<dim3(a.G * per, segments, a.B), kThreads, kBytes, stream>>>(a, sp);
+    const int each = a.D / a.G, per = (each + L::kChannels - 1) / L::kChannels;
+    kern<<<dim3(a.G * per, segments, a.B), L::kThreads, kBytes, stream>>>(a, sp);
     return cudaGetLastError();
   });
 }
 
 }  // namespace
 
-int space_channels(int N) { return kOwn * kThreads / (N / kStates); }
+int space_channels(int N, bool narrow) {
+  return narrow ? 256 / (N / 4) : 2 * 128 / (N / 8);
+}
 cudaError_t launch_space_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                 cudaStream_t stream) {
-  return launch<false>(a, sp, sp.segments - 1, f32, stream);
+  return launch_as<false, false>(a, sp, sp.segments - 1, f32, stream);
 }
 cudaError_t launch_space_walk(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                               cudaStream_t stream) {
-  return launch<true>(a, sp, sp.segments, f32, stream);
+  return sp.segments == 1 ? launch_as<true, true>(a, sp, 1, f32, stream)
+                          : launch_as<false, true>(a, sp, sp.segments, f32, stream);
 }
 cudaError_t launch_space_chain(const SpaceArgs& a, const SpaceSplit& sp, bool backward,
                                cudaStream_t stream) {

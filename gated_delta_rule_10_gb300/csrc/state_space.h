@@ -43,7 +43,7 @@ struct SpaceSplit {
   float* bc_part = nullptr;   // [blocks, B, T, 2, N] of dBm and dCm
 };
 
-int space_channels(int N);       // channels of a CTA: forward, backward
+int space_channels(int N, bool narrow);   // channels of a CTA: forward, backward
 int space_bwd_channels(int N);
 cudaError_t launch_space_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                 cudaStream_t stream);
