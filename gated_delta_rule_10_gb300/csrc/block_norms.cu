@@ -29,6 +29,22 @@ __device__ __forceinline__ float rounded(float x) {
   return static_cast<float>(static_cast<T>(x));
 }
 
+// 8 elements as pairs, and back with one rounding.
+template <typename T>
+__device__ __forceinline__ void pairs(const Raw8<T>& r, f32x2 (&x)[4]) {
+  float f[8];
+  r.get(f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const f32x2 (&x)[4]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split(x[i], f[2 * i], f[2 * i + 1]);
+  store8(p, f);
+}
+
 // Sums of two values over the TPR threads of a row; `red` has a slot per warp, and
 // consecutive calls take different ones of its parts, so one barrier each is enough.
 template <int TPR>
@@ -162,11 +178,11 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
   __shared__ float sums[kRows > 1 ? kThreads * 8 : 1];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int nv = a.D / 8;
-  float ws[VEC][8], wp[VEC][8], dm[VEC][8], dp[VEC][8];
+  f32x2 ws[VEC][4], wp[VEC][4], dm[VEC][4], dp[VEC][4];
 #pragma unroll
   for (int i = 0; i < VEC; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dm[i][j] = dp[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) dm[i][j] = dp[i][j] = 0;
   struct Row {
     Raw8<T> x[VEC], g[VEC], r[VEC], y[VEC], d[VEC];
   } in;
@@ -191,71 +207,80 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
   };
   const long long step = static_cast<long long>(gridDim.x) * kRows;
   fetch(static_cast<long long>(blockIdx.x) * kRows + sub);
-  load_weights<TPR, VEC>(a.post, a.scale, a.pre, lane, nv, ws, wp);
+  {
+    float s[VEC][8], p[VEC][8];
+    load_weights<TPR, VEC>(a.post, a.scale, a.pre, lane, nv, s, p);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ws[i][j] = pair(s[i][2 * j], s[i][2 * j + 1]);
+        wp[i][j] = pair(p[i][2 * j], p[i][2 * j + 1]);
+      }
+  }
   const float n = static_cast<float>(a.D);
   for (long long r0 = static_cast<long long>(blockIdx.x) * kRows; r0 < a.rows; r0 += step) {
     const long long row = r0 + sub;
     const bool live = row < a.rows;
     const Row cur = in;
-    float ss = 0.f, dot = 0.f, xx = 0.f, none = 0.f;
+    f32x2 ss = 0, dot = 0, xx = 0;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      float r[8], dy[8];
-      cur.r[i].get(r);
-      cur.y[i].get(dy);
+      f32x2 r[4], dy[4];
+      pairs(cur.r[i], r);
+      pairs(cur.y[i], dy);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss = fmaf(r[j], r[j], ss);
-        dot = fmaf(wp[i][j] * dy[j], r[j], dot);
+      for (int j = 0; j < 4; ++j) {
+        ss = fma2(r[j], r[j], ss);
+        dot = fma2(mul2(wp[i][j], dy[j]), r[j], dot);
       }
     }
     fetch(row + step);
-    row_sum<TPR>(ss, dot, red[0]);
-    const float ir = rsqrtf(ss / n + a.eps);
-    const float mr = ir * ir * (dot / n);
-    dot = 0.f;
-    float dr[VEC][8];
+    float s0 = sum2(ss), s1 = sum2(dot);
+    row_sum<TPR>(s0, s1, red[0]);
+    const float ir = rsqrtf(s0 / n + a.eps);
+    const f32x2 ir2 = both(ir), mr = both(-ir * ir * (s1 / n));
+    dot = 0;
+    f32x2 dr[VEC][4], sg[VEC][4];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int c = lane + i * TPR;
-      float r[8], dy[8], x[8], g[8];
-      cur.r[i].get(r);
-      cur.y[i].get(dy);
-      cur.x[i].get(x);
-      cur.g[i].get(g);
-      cur.d[i].get(dr[i]);
+      f32x2 r[4], dy[4], x[4], g[4];
+      pairs(cur.r[i], r);
+      pairs(cur.y[i], dy);
+      pairs(cur.x[i], x);
+      pairs(cur.g[i], g);
+      pairs(cur.d[i], dr[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dp[i][j] = fmaf(dy[j], r[j] * ir, dp[i][j]);
-        dr[i][j] += ir * (wp[i][j] * dy[j] - r[j] * mr);
-        float t = dr[i][j] * ws[i][j];
-        if (a.gate) t *= sigmoid(g[j]);
-        xx = fmaf(x[j], x[j], xx);
-        dot = fmaf(t, x[j], dot);
+      for (int j = 0; j < 4; ++j) {
+        dp[i][j] = fma2(dy[j], mul2(r[j], ir2), dp[i][j]);
+        dr[i][j] = fma2(ir2, fma2(wp[i][j], dy[j], mul2(r[j], mr)), dr[i][j]);
+        sg[i][j] = a.gate ? sigmoid2(g[j]) : both(1.f);
+        xx = fma2(x[j], x[j], xx);
+        dot = fma2(mul2(mul2(dr[i][j], ws[i][j]), sg[i][j]), x[j], dot);
       }
-      if (live && c < nv) store8(static_cast<T*>(a.dresidual) + row * a.D + 8 * c, dr[i]);
+      if (live && c < nv) store_pairs(static_cast<T*>(a.dresidual) + row * a.D + 8 * c, dr[i]);
     }
-    row_sum<TPR>(xx, dot, red[1]);
-    (void)none;
-    const float ix = rsqrtf(xx / n + a.eps);
-    const float mx = ix * ix * (dot / n);
+    s0 = sum2(xx);
+    s1 = sum2(dot);
+    row_sum<TPR>(s0, s1, red[1]);
+    const float ix = rsqrtf(s0 / n + a.eps);
+    const f32x2 ix2 = both(ix), mx = both(-ix * ix * (s1 / n));
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int c = lane + i * TPR;
-      float x[8], g[8], dx[8], dg[8];
-      cur.x[i].get(x);
-      cur.g[i].get(g);
+      f32x2 x[4], dx[4], dg[4];
+      pairs(cur.x[i], x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float sg = a.gate ? sigmoid(g[j]) : 1.f;
-        const float nx = x[j] * ix, t = dr[i][j] * ws[i][j] * sg;
-        dm[i][j] = fmaf(dr[i][j] * sg, nx, dm[i][j]);
-        dg[j] = t * nx * (1.f - sg);
-        dx[j] = ix * (t - x[j] * mx);
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 nx = mul2(x[j], ix2), d = mul2(dr[i][j], sg[i][j]), t = mul2(d, ws[i][j]);
+        dm[i][j] = fma2(d, nx, dm[i][j]);
+        dg[j] = mul2(mul2(t, nx), fma2(sg[i][j], both(-1.f), both(1.f)));
+        dx[j] = mul2(ix2, fma2(x[j], mx, t));
       }
       if (!(live && c < nv)) continue;
-      store8(static_cast<T*>(a.dx) + row * a.D + 8 * c, dx);
-      if (a.gate) store8(static_cast<T*>(a.dgate) + row * a.D + 8 * c, dg);
+      store_pairs(static_cast<T*>(a.dx) + row * a.D + 8 * c, dx);
+      if (a.gate) store_pairs(static_cast<T*>(a.dgate) + row * a.D + 8 * c, dg);
     }
   }
 #pragma unroll
@@ -265,7 +290,7 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
       const int c = lane + i * TPR;
       float s[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = part ? dp[i][j] : dm[i][j];
+      for (int j = 0; j < 4; ++j) split(part ? dp[i][j] : dm[i][j], s[2 * j], s[2 * j + 1]);
       if constexpr (kRows > 1) {
         __syncthreads();
 #pragma unroll

@@ -151,17 +151,26 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
   struct Batch {
     Raw<T, V> x[kBatch];
     unsigned starts;
-  } cur;
+  } even, odd;
+  const T* xp = x + static_cast<long long>(t0) * a.xs;     // the next batch's
   auto fetch = [&](Batch& f, int t) {
     f.starts = 0;
+    if (t + kBatch <= t1) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      if (t + k < t1) {
-        f.x[k].load(x + static_cast<long long>(t + k) * a.xs);
-        if (starts) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
-      }
+      for (int k = 0; k < kBatch; ++k, xp += a.xs) f.x[k].load(xp);
+      if (starts)
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k, xp += a.xs)
+        if (t + k < t1) {
+          f.x[k].load(xp);
+          if (starts) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
+        }
+    }
   };
-  fetch(cur, t0);
+  fetch(even, t0);
   load_filter<K, V>(a, c, w, bias);
   {
     Raw<T, V> r[K - 1];
@@ -178,37 +187,50 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
 #pragma unroll
         for (int i = 0; i < H; ++i) prev[j][i] = 0;
   }
-  for (int t = t0; t < t1; t += kBatch) {
-    Batch next;
-    fetch(next, t + kBatch);
+  T* yp = y + static_cast<long long>(t0) * a.D;
+  auto token = [&](const Raw<T, V>& raw) {
+    f32x2 v[H], s[H];
+    raw.get(v);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (t + k >= t1) break;
-      if ((cur.starts >> k) & 1)
+    for (int i = 0; i < H; ++i) {
+      s[i] = fma2(w[K - 1][i], v[i], bias[i]);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-          for (int i = 0; i < H; ++i) prev[j][i] = 0;
-      f32x2 v[H], s[H];
-      cur.x[k].get(v);
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        s[i] = fma2(w[K - 1][i], v[i], bias[i]);
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) s[i] = fma2(w[K - 2 - j][i], prev[j][i], s[i]);
-        if (a.silu) s[i] = mul2(s[i], sigmoid2(s[i]));
-      }
-      Raw<T, V> out;
-      out.put(s);
-      out.store(y + static_cast<long long>(t + k) * a.D);
-#pragma unroll
-      for (int j = K - 2; j > 0; --j)
-#pragma unroll
-        for (int i = 0; i < H; ++i) prev[j][i] = prev[j - 1][i];
-#pragma unroll
-      for (int i = 0; i < H; ++i) prev[0][i] = v[i];
+      for (int j = 0; j < K - 1; ++j) s[i] = fma2(w[K - 2 - j][i], prev[j][i], s[i]);
+      if (a.silu) s[i] = mul2(s[i], sigmoid2(s[i]));
     }
-    cur = next;
+    Raw<T, V> out;
+    out.put(s);
+    out.store(yp);
+    yp += a.D;
+#pragma unroll
+    for (int j = K - 2; j > 0; --j)
+#pragma unroll
+      for (int i = 0; i < H; ++i) prev[j][i] = prev[j - 1][i];
+#pragma unroll
+    for (int i = 0; i < H; ++i) prev[0][i] = v[i];
+  };
+  auto tokens = [&](const Batch& f, int t) {
+    if (t + kBatch <= t1 && f.starts == 0) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) token(f.x[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (t + k >= t1) break;
+        if ((f.starts >> k) & 1)
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < H; ++i) prev[j][i] = 0;
+        token(f.x[k]);
+      }
+    }
+  };
+  for (int t = t0; t < t1; t += 2 * kBatch) {
+    fetch(odd, t + kBatch);
+    tokens(even, t);
+    fetch(even, t + 2 * kBatch);
+    tokens(odd, t + kBatch);
   }
   if (t1 == a.T && a.state_out) {     // prev is the last rows, zeros behind a start
 #pragma unroll
@@ -227,18 +249,17 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
 // K - 1 tokens past its end for what they pass back.
 constexpr int kRuns = 8;
 constexpr int kBwdThreads = 32 * kRuns;
-constexpr int kBwdRun = 32;
 constexpr int kBwdBatch = 4;
 
 template <typename T, int K>
 __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
-    short_conv_bwd_kernel(const ConvArgs a, int groups, int slices) {
+    short_conv_bwd_kernel(const ConvArgs a, int run, int groups, int slices) {
   constexpr int V = 4, H = V / 2;
   __shared__ __align__(16) float sums[kRuns][K + 1][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slice = blockIdx.x % slices, c = (slice * 32 + lane) * V;
   const int rest = blockIdx.x / slices, b = rest / groups, group = rest % groups;
-  const int t0 = (group * kRuns + warp) * kBwdRun, t1 = min(t0 + kBwdRun, a.T);
+  const int t0 = (group * kRuns + warp) * run, t1 = min(t0 + run, a.T);
   f32x2 dw[K + 1][H];
 #pragma unroll
   for (int k = 0; k <= K; ++k)
@@ -252,22 +273,35 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
     T* dst = a.dstate ? static_cast<T*>(a.dstate) + static_cast<long long>(b) * (K - 1) * a.D + c
                       : nullptr;
     const int stop = min(t1 + K - 1, a.T);
-    f32x2 w[K][H], bias[H], prev[K - 1][H], acc[K][H];   // acc[j]: dx of the token j back
+    f32x2 w[K][H], bias[H], prev[K - 1][H], acc[K][H];   // acc[j]: dx of the token j back (j > 0)
     struct Batch {
       Raw<T, V> x[kBwdBatch], y[kBwdBatch];
       unsigned starts;
-    } cur;
+    } even, odd;
+    const T* xf = xp + static_cast<long long>(t0) * a.xs;     // the next batch's
+    const T* yf = dyp + static_cast<long long>(t0) * a.D;
     auto fetch = [&](Batch& f, int t) {
       f.starts = 0;
+      if (t + kBwdBatch <= stop) {
 #pragma unroll
-      for (int k = 0; k < kBwdBatch; ++k)
-        if (t + k < stop) {
-          f.x[k].load(xp + static_cast<long long>(t + k) * a.xs);
-          f.y[k].load(dyp + static_cast<long long>(t + k) * a.D);
-          if (starts) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
+        for (int k = 0; k < kBwdBatch; ++k, xf += a.xs, yf += a.D) {
+          f.x[k].load(xf);
+          f.y[k].load(yf);
         }
+        if (starts)
+#pragma unroll
+          for (int k = 0; k < kBwdBatch; ++k) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
+      } else {
+#pragma unroll
+        for (int k = 0; k < kBwdBatch; ++k, xf += a.xs, yf += a.D)
+          if (t + k < stop) {
+            f.x[k].load(xf);
+            f.y[k].load(yf);
+            if (starts) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
+          }
+      }
     };
-    fetch(cur, t0);
+    fetch(even, t0);
     load_filter<K, V>(a, c, w, bias);
     {
       Raw<T, V> r[K - 1];
@@ -283,6 +317,8 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
     // tokens behind the current one that are of its document, up to K - 1
     int back = K - 2;
     if (starts && t0 > 0) back = reach<K>(starts, t0 - 1);
+    // rows of dx are finished K - 1 tokens later; where the current token's goes
+    T* dxo = dxp + (static_cast<long long>(t0) - (K - 1)) * a.D;
     // a finished row: of this run's tokens, or the state's before the first
     auto emit = [&](int e, const f32x2 (&v)[H]) {
       Raw<T, V> r;
@@ -292,66 +328,88 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
       else if (t0 == 0 && dst)
         r.store(dst + static_cast<long long>(K - 1 + e) * a.D);
     };
-    for (int t = t0; t < stop; t += kBwdBatch) {
-      Batch next;
-      fetch(next, t + kBwdBatch);
+    // one token; INNER: of the run, with K - 1 others of its document and the run behind it
+    auto token = [&](const Raw<T, V>& raw_x, const Raw<T, V>& raw_y, int now, auto inner) {
+      constexpr bool INNER = decltype(inner)::value;
+      f32x2 v[H], g[H];
+      raw_x.get(v);
+      raw_y.get(g);
+      if (!INNER && back < K - 1)
 #pragma unroll
-      for (int k = 0; k < kBwdBatch; ++k) {
-        const int now = t + k;
-        if (now >= stop) break;
-        back = min(back + 1, K - 1);
-        if ((cur.starts >> k) & 1) back = 0;
-        f32x2 v[H], g[H];
-        cur.x[k].get(v);
-        cur.y[k].get(g);
-        if (back < K - 1)
+        for (int j = 0; j < K - 1; ++j)
+          if (j + 1 > back)
 #pragma unroll
-          for (int j = 0; j < K - 1; ++j)
-            if (j + 1 > back)
+            for (int i = 0; i < H; ++i) prev[j][i] = 0;
 #pragma unroll
-              for (int i = 0; i < H; ++i) prev[j][i] = 0;
+      for (int i = 0; i < H; ++i) {
+        if (a.silu) {
+          f32x2 s = fma2(w[K - 1][i], v[i], bias[i]);
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) s = fma2(w[K - 2 - j][i], prev[j][i], s);
+          // sg (1 + s (1 - sg)) = sg + (s sg) (1 - sg)
+          const f32x2 sg = sigmoid2(s), one = both(1.f);
+          const f32x2 slope = fma2(mul2(s, sg), fma2(sg, both(-1.f), one), sg);
+          g[i] = mul2(g[i], slope);
+        }
+      }
+#pragma unroll
+      for (int j = 1; j < K; ++j)
+        if (INNER || j <= back)
+#pragma unroll
+          for (int i = 0; i < H; ++i) acc[j][i] = fma2(w[K - 1 - j][i], g[i], acc[j][i]);
+      if (INNER || now < t1)
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-          if (a.silu) {
-            f32x2 s = fma2(w[K - 1][i], v[i], bias[i]);
+          dw[K - 1][i] = fma2(g[i], v[i], dw[K - 1][i]);
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) s = fma2(w[K - 2 - j][i], prev[j][i], s);
-            // sg (1 + s (1 - sg)) = sg + (s sg) (1 - sg)
-            const f32x2 sg = sigmoid2(s), one = both(1.f);
-            const f32x2 slope = fma2(mul2(s, sg), fma2(sg, both(-1.f), one), sg);
-            g[i] = mul2(g[i], slope);
-          }
-          acc[0][i] = fma2(w[K - 1][i], g[i], acc[0][i]);
+          for (int j = 0; j < K - 1; ++j)
+            dw[K - 2 - j][i] = fma2(g[i], prev[j][i], dw[K - 2 - j][i]);
+          dw[K][i] = add2(dw[K][i], g[i]);
         }
-#pragma unroll
-        for (int j = 1; j < K; ++j)
-          if (j <= back)
-#pragma unroll
-            for (int i = 0; i < H; ++i) acc[j][i] = fma2(w[K - 1 - j][i], g[i], acc[j][i]);
-        if (now < t1)
-#pragma unroll
-          for (int i = 0; i < H; ++i) {
-            dw[K - 1][i] = fma2(g[i], v[i], dw[K - 1][i]);
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j)
-              dw[K - 2 - j][i] = fma2(g[i], prev[j][i], dw[K - 2 - j][i]);
-            dw[K][i] = add2(dw[K][i], g[i]);
-          }
+      if (INNER) {
+        Raw<T, V> r;
+        r.put(acc[K - 1]);
+        r.store(dxo);
+      } else {
         emit(now - (K - 1), acc[K - 1]);
-#pragma unroll
-        for (int j = K - 1; j > 0; --j)
-#pragma unroll
-          for (int i = 0; i < H; ++i) acc[j][i] = acc[j - 1][i];
-#pragma unroll
-        for (int i = 0; i < H; ++i) acc[0][i] = 0;
-#pragma unroll
-        for (int j = K - 2; j > 0; --j)
-#pragma unroll
-          for (int i = 0; i < H; ++i) prev[j][i] = prev[j - 1][i];
-#pragma unroll
-        for (int i = 0; i < H; ++i) prev[0][i] = v[i];
       }
-      cur = next;
+      dxo += a.D;
+#pragma unroll
+      for (int j = K - 1; j > 1; --j)
+#pragma unroll
+        for (int i = 0; i < H; ++i) acc[j][i] = acc[j - 1][i];
+#pragma unroll
+      for (int i = 0; i < H; ++i) acc[1][i] = mul2(w[K - 1][i], g[i]);
+#pragma unroll
+      for (int j = K - 2; j > 0; --j)
+#pragma unroll
+        for (int i = 0; i < H; ++i) prev[j][i] = prev[j - 1][i];
+#pragma unroll
+      for (int i = 0; i < H; ++i) prev[0][i] = v[i];
+    };
+    auto tokens = [&](Batch& f, int t) {
+      if (f.starts == 0 && back == K - 1 && t - (K - 1) >= t0 && t + kBwdBatch <= t1) {
+#pragma unroll
+        for (int k = 0; k < kBwdBatch; ++k) token(f.x[k], f.y[k], t + k, std::true_type{});
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < kBwdBatch && t + k < stop; ++k) {
+          back = (f.starts >> k) & 1 ? 0 : min(back + 1, K - 1);
+          // (a register array has no address: the batch moves on instead)
+          token(f.x[0], f.y[0], t + k, std::false_type{});
+#pragma unroll
+          for (int i = 0; i + 1 < kBwdBatch; ++i) {
+            f.x[i] = f.x[i + 1];
+            f.y[i] = f.y[i + 1];
+          }
+        }
+      }
+    };
+    for (int t = t0; t < stop; t += 2 * kBwdBatch) {
+      fetch(odd, t + kBwdBatch);
+      tokens(even, t);
+      fetch(even, t + 2 * kBwdBatch);
+      tokens(odd, t + kBwdBatch);
     }
     if (stop == a.T) {   // what is behind the last token comes from the state's gradient
 #pragma unroll
@@ -439,13 +497,21 @@ cudaError_t by_taps(int K, bool f32, F f) {
   return typed(integral_constant<int, 4>{});
 }
 
-// The CTAs' rows of partial sums: one for each batch row and kRuns runs.
-int bwd_groups(int T) { return (T + kRuns * kBwdRun - 1) / (kRuns * kBwdRun); }
+// Tokens of a run of the backward: 64 where that fills the SMs with two CTAs each, else fewer
+// (4 x 4096 x 4096 bf16: 118 us with 64, 133 with 32), and the CTAs' rows of partial sums,
+// one for each batch row and kRuns runs.
+int bwd_groups(int T, int run) { return (T + kRuns * run - 1) / (kRuns * run); }
+int bwd_run(int B, int T, int D) {
+  const long long slices = static_cast<long long>((D + 127) / 128) * B;
+  int run = 64;
+  while (run > 8 && slices * bwd_groups(T, run) < 2 * 152) run /= 2;
+  return run;
+}
 
 }  // namespace
 
 size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int K) {
-  return static_cast<size_t>(B) * bwd_groups(T) * (K + 1) * D * sizeof(float);
+  return static_cast<size_t>(B) * bwd_groups(T, bwd_run(B, T, D)) * (K + 1) * D * sizeof(float);
 }
 
 cudaError_t launch_short_conv(const ConvArgs& a, bool f32, cudaStream_t stream) {
@@ -464,12 +530,12 @@ cudaError_t launch_short_conv(const ConvArgs& a, bool f32, cudaStream_t stream) 
 }
 
 cudaError_t launch_short_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t stream) {
-  const int groups = bwd_groups(a.T), slices = (a.D + 127) / 128;
+  const int run = bwd_run(a.B, a.T, a.D), groups = bwd_groups(a.T, run), slices = (a.D + 127) / 128;
   const long long grid = static_cast<long long>(slices) * a.B * groups;
   if (grid > 2147483647LL) return cudaErrorInvalidValue;
   return by_taps(a.K, f32, [&](auto t, auto k) {
     short_conv_bwd_kernel<decltype(t), k>
-        <<<static_cast<unsigned>(grid), kBwdThreads, 0, stream>>>(a, groups, slices);
+        <<<static_cast<unsigned>(grid), kBwdThreads, 0, stream>>>(a, run, groups, slices);
     filter_grad_kernel<<<((a.K + 1) * a.D + 31) / 32, 1024, 0, stream>>>(a, a.B * groups);
     return cudaGetLastError();
   });
