@@ -8,11 +8,10 @@ import ctypes
 
 import torch
 
-from ._binding import GdrError, _vp, lib
-from .layer import (_call, _check, _dtype, _f32, _int, _ll, _new_or, _ptr, _stream, _sz, _used_on,
-                    _workspace_bytes)
+from ._binding import GDR_BF16, GDR_F32, GdrError, _check as _check_slow, _vp, lib
+from .layer import _f32, _int, _ll, _ptr, _sz, _used_on, _workspace_bytes
 
-F32 = torch.float32
+F32, BF16 = torch.float32, torch.bfloat16
 
 
 class ConvShape(ctypes.Structure):
@@ -65,17 +64,66 @@ def _bytes(name, *args):
     return n.value
 
 
+# A decode step makes these calls once per layer: as in ``layer``, the common case of each
+# helper is a few attribute reads.
+
 def _run(name, device, *args):
-    if _fns is None:
-        _lib()
-    _call(name, device, *args)
+    fn = getattr(_fns or _lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st:
+        raise GdrError(st, name)
+
+
+def _dtype(t):
+    """The library's number of the type of `t`, an operator's main input on the GPU."""
+    dt = t.dtype
+    if dt is not BF16 and dt is not F32:
+        raise ValueError("expected bf16 or fp32, got %s" % dt)
+    if not t.is_cuda:
+        raise ValueError("x must be a CUDA tensor, got one on %s" % t.device)
+    return GDR_BF16 if dt is BF16 else GDR_F32
+
+
+def _check(t, name, dtype, device, shape):
+    """A contiguous tensor like this on `device` (a GPU), or None."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and
+                     t.is_contiguous()):
+        return
+    _check_slow(t, name, dtype, device, shape)
+
+
+def _new_or(t, name, like, dtype=None, shape=None):
+    """`t` as the caller gave it, or a new tensor like `like`; and whether it is new."""
+    if t is None:
+        if shape is None:
+            return torch.empty_like(like, memory_format=torch.contiguous_format), True
+        return torch.empty(shape, dtype=dtype, device=like.device), True
+    if shape is None:
+        return _given(t, name, like), False
+    _check(t, name, dtype, like.device, shape)
+    return t, False
+
+
+def _given(t, name, like):
+    """A caller's output, to be as `like`."""
+    _check(t, name, like.dtype, like.device, like.shape)
+    return t
+
+
+def _stream(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(t, name, dtype, device, shape):
     """Checks a tensor [B, T, ...] ([N, ...] for single tokens) whose tokens are dense
     inside and evenly spaced; returns elements per token (0: dense)."""
-    if t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape and \
-            t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return 0
     if not t.is_cuda or t.device != device:
         raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
@@ -119,11 +167,11 @@ def _starts(t, device, shape):
 def _conv_shape(x, weight, bias, silu, lead):
     if x.dim() != lead + 1 or weight.dim() != 2:
         raise ValueError("x must be [%s, D] and weight [D, K]" % ("B, T" if lead == 2 else "N"))
-    shape = tuple(x.shape)
+    shape = x.shape
     D, K = weight.shape
-    dev, dt = x.device, _dtype(x)
     if shape[-1] != D:
         raise ValueError("weight has %d channels, x %d" % (D, shape[-1]))
+    dev, dt = x.device, _dtype(x)
     _check(weight, "weight", F32, dev, (D, K))
     _check(bias, "bias", F32, dev, (D,))
     return ConvShape(shape[0], shape[1] if lead == 2 else 1, D, K, dt, int(bool(silu)),
@@ -150,10 +198,10 @@ def short_conv_fwd(x, weight, bias=None, state=None, *, starts=None, silu=True,
     edge = (s.B, s.K - 1, s.D)
     _check(state, "state", dt, dev, edge)
     _starts(starts, dev, (s.B, s.T))
-    y, new_y = _new_or(y, "y", tuple(x.shape), dt, dev)
+    y, new_y = _new_or(y, "y", x)
     new_s = False
     if state_out is not None or output_final_state:
-        state_out, new_s = _new_or(state_out, "state_out", edge, dt, dev)
+        state_out, new_s = _new_or(state_out, "state_out", x, dt, edge)
     _run("gdr_short_conv_fwd", dev, ctypes.byref(s), _ptr(x), _ptr(weight), _ptr(bias),
          _ptr(starts), _ptr(state), _ptr(y), _ptr(state_out), _stream(stream, dev))
     _used_on(stream, dev, y if new_y else None, state_out if new_s else None)
@@ -169,7 +217,7 @@ def short_conv_bwd(dy, x, weight, bias=None, state=None, dstate=None, *, starts=
     edge = (s.B, s.K - 1, s.D)
     _check(state, "state", dt, dev, edge)
     _check(dstate, "dstate", dt, dev, edge)
-    _check(dy, "dy", dt, dev, tuple(x.shape))
+    _check(dy, "dy", dt, dev, x.shape)
     _starts(starts, dev, (s.B, s.T))
     out = {"x": torch.empty(x.shape, dtype=dt, device=dev),
            "weight": torch.empty(weight.shape, dtype=F32, device=dev),
@@ -191,15 +239,17 @@ def short_conv_step(x, weight, bias, state, *, silu=True, y=None, stream=None):
     """One token of each sequence (``gdr_short_conv_step``): x [N, D], state [N, K-1, D],
     moved on by one row in place. Returns y [N, D]."""
     s = _conv_shape(x, weight, bias, silu, 1)
-    dev, dt = x.device, x.dtype
+    dev = x.device
     if state is None:
         raise ValueError("state is needed")
-    _check(state, "state", dt, dev, (s.B, s.K - 1, s.D))
-    y, new_y = _new_or(y, "y", tuple(x.shape), dt, dev)
-    _run("gdr_short_conv_step", dev, ctypes.byref(s), _ptr(x), _ptr(weight), _ptr(bias),
-         _ptr(state), _ptr(y), _stream(stream, dev))
-    _used_on(stream, dev, y if new_y else None)
-    return y
+    _check(state, "state", x.dtype, dev, (s.B, s.K - 1, s.D))
+    out = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else \
+        _given(y, "y", x)
+    _run("gdr_short_conv_step", dev, ctypes.byref(s), x.data_ptr(), weight.data_ptr(), _ptr(bias),
+         state.data_ptr(), out.data_ptr(), _stream(stream, dev))
+    if y is None and stream is not None:
+        _used_on(stream, dev, out)
+    return out
 
 
 # ------------------------------------------------------------------ state space recurrence
@@ -250,10 +300,10 @@ def state_space_fwd(x, dt, A, B, C, h0=None, *, skip=None, z=None, dt_bias=None,
     dev = x.device
     _check(h0, "h0", F32, dev, (s.B, s.D, s.N))
     _starts(starts, dev, (s.B, s.T))
-    y, new_y = _new_or(y, "y", tuple(x.shape), x.dtype, dev)
+    y, new_y = _new_or(y, "y", x)
     new_h = False
     if hT is not None or output_final_state:
-        hT, new_h = _new_or(hT, "hT", (s.B, s.D, s.N), F32, dev)
+        hT, new_h = _new_or(hT, "hT", x, F32, (s.B, s.D, s.N))
     ws = None
     need = state_space_fwd_workspace_bytes(s)
     if workspace is None and need:
@@ -274,7 +324,7 @@ def state_space_bwd(dy, x, dt, A, B, C, h0=None, dhT=None, *, skip=None, z=None,
     dev, t = x.device, x.dtype
     _check(h0, "h0", F32, dev, (s.B, s.D, s.N))
     _check(dhT, "dhT", F32, dev, (s.B, s.D, s.N))
-    _check(dy, "dy", t, dev, tuple(x.shape))
+    _check(dy, "dy", t, dev, x.shape)
     _starts(starts, dev, (s.B, s.T))
     new = lambda like, d: None if like is None else torch.empty(like.shape, dtype=d, device=dev)  # noqa: E731
     out = {"x": new(x, t), "dt": new(dt, t), "A": new(A, F32), "B": new(B, t), "C": new(C, t),
@@ -301,24 +351,31 @@ def state_space_step(x, dt, A, B, C, state, *, skip=None, z=None, dt_bias=None, 
     if state is None:
         raise ValueError("state is needed")
     _check(state, "state", F32, dev, (s.B, s.D, s.N))
-    y, new_y = _new_or(y, "y", tuple(x.shape), x.dtype, dev)
-    _run("gdr_state_space_step", dev, ctypes.byref(s), _ptr(x), _ptr(dt), _ptr(A), _ptr(B),
-         _ptr(C), _ptr(skip), _ptr(z), _ptr(dt_bias), _ptr(state), _ptr(y), _stream(stream, dev))
-    _used_on(stream, dev, y if new_y else None)
-    return y
+    out = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else \
+        _given(y, "y", x)
+    _run("gdr_state_space_step", dev, ctypes.byref(s), x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+         B.data_ptr(), C.data_ptr(), _ptr(skip), _ptr(z), _ptr(dt_bias), state.data_ptr(),
+         out.data_ptr(), _stream(stream, dev))
+    if y is None and stream is not None:
+        _used_on(stream, dev, out)
+    return out
 
 
 # ------------------------------------------------------------------ norms around a block
 
 def _norms_inputs(x, gate, post_weight, scale, pre_weight):
-    D = x.shape[-1]
-    shape, dev = tuple(x.shape), x.device
     dt = _dtype(x)
-    _check(x, "x", x.dtype, dev, shape)
-    _check(gate, "gate", x.dtype, dev, shape)
-    _check(post_weight, "post_weight", F32, dev, (D,))
-    _check(scale, "scale", F32, dev, (D,))
-    _check(pre_weight, "pre_weight", F32, dev, (D,))
+    shape, dev = x.shape, x.device
+    D = shape[-1]
+    flat = (D,)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if gate is not None:
+        _check(gate, "gate", x.dtype, dev, shape)
+    _check(post_weight, "post_weight", F32, dev, flat)
+    if scale is not None:
+        _check(scale, "scale", F32, dev, flat)
+    _check(pre_weight, "pre_weight", F32, dev, flat)
     return x.numel() // D if D else 0, D, dt
 
 
@@ -332,16 +389,17 @@ def block_norms(x, residual, post_weight, pre_weight, eps=1e-6, *, gate=None, sc
     may be residual, x or gate itself (in place), ``out`` another of them.
     """
     rows, D, dt = _norms_inputs(x, gate, post_weight, scale, pre_weight)
-    shape, dev = tuple(x.shape), x.device
-    _check(residual, "residual", x.dtype, dev, shape)
-    y, new_y = _new_or(out, "out", shape, x.dtype, dev)
-    r, new_r = _new_or(residual_out, "residual_out", shape, x.dtype, dev)
+    dev = x.device
+    _check(residual, "residual", x.dtype, dev, x.shape)
+    y = torch.empty_like(x) if out is None else _given(out, "out", x)
+    r = torch.empty_like(x) if residual_out is None else _given(residual_out, "residual_out", x)
     if rows and y.data_ptr() == r.data_ptr():
         raise ValueError("out and residual_out must be apart")
-    _run("gdr_block_norms", dev, rows, D, dt, _ptr(x), _ptr(gate), _ptr(residual),
-         _ptr(post_weight), _ptr(scale), _ptr(pre_weight), float(eps), _ptr(r), _ptr(y),
-         _stream(stream, dev))
-    _used_on(stream, dev, y if new_y else None, r if new_r else None)
+    _run("gdr_block_norms", dev, rows, D, dt, x.data_ptr(), _ptr(gate), residual.data_ptr(),
+         post_weight.data_ptr(), _ptr(scale), pre_weight.data_ptr(), float(eps), r.data_ptr(),
+         y.data_ptr(), _stream(stream, dev))
+    if stream is not None:
+        _used_on(stream, dev, y if out is None else None, r if residual_out is None else None)
     return y, r
 
 
@@ -351,7 +409,7 @@ def block_norms_bwd(dy, x, sum, post_weight, pre_weight, eps=1e-6, *, gate=None,
     r = ``sum``. A dict with x, residual, gate (their dtype) and post_weight, pre_weight,
     scale (fp32; as post, pre, scale); gate and scale are None where they were not given."""
     rows, D, dt = _norms_inputs(x, gate, post_weight, scale, pre_weight)
-    shape, dev, t = tuple(x.shape), x.device, x.dtype
+    shape, dev, t = x.shape, x.device, x.dtype
     for v, name in ((dy, "dy"), (sum, "sum"), (dres, "dres")):
         _check(v, name, t, dev, shape)
     wide = lambda on: torch.empty(shape, dtype=t, device=dev) if on else None  # noqa: E731

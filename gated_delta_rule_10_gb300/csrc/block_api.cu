@@ -89,8 +89,9 @@ double waves(long long n, int most, double first, double next) {
 // Forward: uncut, a CTA has half the channels, and needs no other launch; a cut costs a walk
 // over all segments but the last for their end states (0.65 of the other walk's time), and the
 // chain. Times of a token (us, bf16): uncut 0.084 and 0.062 (a CTA alone on its SM; a second
-// one beside it), cut 0.31 and 0.12. (4 x 4096 x 4096 channels x 16: 598 us uncut, 565 in 38
-// segments, 590 in 14; 1 x 65536 x 2048: 5510, 1133, 1867.)
+// one beside it), cut 0.17 and 0.066, and a third of a tile for a CTA's start. (4 x 4096 x
+// 4096 channels x 16: 598 us uncut, 565 in 32 segments, 590 in 13; 1 x 65536 x 2048: 5510
+// uncut, 1133 in 38, 1867 in 14.)
 // The backward walks forward for its kept states anyway; a segment costs a CTA's start, about
 // as long as a tile (4 x 4096 x 2048 x 16: 1132 us in 4 segments, 997 in 9, 974 in 19).
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
@@ -109,8 +110,8 @@ void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
     else if (segments == 1)
       cost = waves(rows * blocks(gdr::space_channels(s->N, true)), 2, 0.084, 0.062) * s->T;
     else
-      cost = (waves(ctas * segments, 5, 0.31, 0.12) + 0.65 * waves(ctas * (segments - 1), 5, 0.31, 0.12)) *
-                 (len + 1.0) * tile + 25.0;
+      cost = (waves(ctas * segments, 5, 0.17, 0.066) +
+              0.65 * waves(ctas * (segments - 1), 5, 0.17, 0.066)) * (len + 0.3) * tile + 25.0;
     if (n == 1 || cost < best) {
       best = cost;
       per = len;

@@ -871,30 +871,32 @@ int space_bwd_channels(int N) { return kWarps * 4 * 32 / (N / 4); }
 cudaError_t launch_space_bwd_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                     cudaStream_t stream) {
   return by_states(a.N, f32, [&](auto t, auto n) {
-    constexpr int kBytes = static_cast<int>(sizeof(PreShared<decltype(t), n>));
-    auto* kern = sp.segments > 1 ? space_bwd_states_kernel<decltype(t), n, true>
-                                 : space_bwd_states_kernel<decltype(t), n, false>;
-    const cudaError_t err =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    if (err != cudaSuccess) return err;
-    kern<<<dim3(a.G * blocks_of(a, PreLayout<n>::kChannels), sp.segments, a.B), kThreads, kBytes,
-           stream>>>(a, sp);
-    return cudaGetLastError();
+    auto run = [&](auto cut) {
+      constexpr auto kern = &space_bwd_states_kernel<decltype(t), n, cut>;
+      constexpr int kBytes = static_cast<int>(sizeof(PreShared<decltype(t), n>));
+      const cudaError_t err = allow_shared<kern>(kBytes);
+      if (err != cudaSuccess) return err;
+      kern<<<dim3(a.G * blocks_of(a, PreLayout<n>::kChannels), sp.segments, a.B), kThreads, kBytes,
+             stream>>>(a, sp);
+      return cudaGetLastError();
+    };
+    return sp.segments > 1 ? run(std::true_type{}) : run(std::false_type{});
   });
 }
 
 cudaError_t launch_space_bwd(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                              cudaStream_t stream) {
   const cudaError_t err = by_states(a.N, f32, [&](auto t, auto n) {
-    auto* kern = a.z ? space_bwd_kernel<decltype(t), n, true> : space_bwd_kernel<decltype(t), n, false>;
-    const int kBytes = static_cast<int>(a.z ? sizeof(BwdShared<decltype(t), n, true>)
-                                            : sizeof(BwdShared<decltype(t), n, false>));
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    if (e != cudaSuccess) return e;
-    kern<<<dim3(a.G * blocks_of(a, BwdLayout<n>::kChannels), sp.segments, a.B), kBwdThreads, kBytes,
-           stream>>>(a, sp);
-    return cudaGetLastError();
+    auto run = [&](auto gated) {
+      constexpr auto kern = &space_bwd_kernel<decltype(t), n, gated>;
+      constexpr int kBytes = static_cast<int>(sizeof(BwdShared<decltype(t), n, gated>));
+      const cudaError_t e = allow_shared<kern>(kBytes);
+      if (e != cudaSuccess) return e;
+      kern<<<dim3(a.G * blocks_of(a, BwdLayout<n>::kChannels), sp.segments, a.B), kBwdThreads,
+             kBytes, stream>>>(a, sp);
+      return cudaGetLastError();
+    };
+    return a.z ? run(std::true_type{}) : run(std::false_type{});
   });
   if (err != cudaSuccess) return err;
   const long long n = static_cast<long long>(a.B) * a.T * a.G * 2 * a.N +
