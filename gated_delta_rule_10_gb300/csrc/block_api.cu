@@ -92,8 +92,8 @@ double waves(long long n, int most, double first, double next) {
 // one beside it), cut 0.17 and 0.066, and a third of a tile for a CTA's start. (4 x 4096 x
 // 4096 channels x 16: 598 us uncut, 565 in 32 segments, 590 in 13; 1 x 65536 x 2048: 5510
 // uncut, 1133 in 38, 1867 in 14.)
-// The backward walks forward for its kept states anyway; a segment costs a CTA's start, about
-// as long as a tile (4 x 4096 x 2048 x 16: 1132 us in 4 segments, 997 in 9, 974 in 19).
+// The backward walks forward for its kept states anyway; a segment costs a CTA's start, 0.7
+// tiles (4 x 4096 x 2048 x 16: 1132 us in 4 segments, 988 in 14, 959 in 19).
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
   const int tile = backward ? gdr::kSpaceTile : 32;
   const int tiles = (s->T + tile - 1) / tile, each = s->D / s->G;
@@ -106,7 +106,7 @@ void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
     const int len = (tiles + n - 1) / n, segments = (tiles + len - 1) / len;
     double cost;
     if (backward)
-      cost = waves(ctas * segments, 2, 0.7, 0.3) * (len + 1.0);
+      cost = waves(ctas * segments, 2, 0.7, 0.3) * (len + 0.7);
     else if (segments == 1)
       cost = waves(rows * blocks(gdr::space_channels(s->N, true)), 2, 0.084, 0.062) * s->T;
     else

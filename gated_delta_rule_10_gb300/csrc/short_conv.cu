@@ -99,7 +99,11 @@ __device__ __forceinline__ void load_filter(const ConvArgs& a, int c, f32x2 (&w)
     f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) g[i] = a.bias ? __ldg(a.bias + c + i) : 0.f;
+  for (int i = 0; i < V / 4; ++i) {
+    const float4 v = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + c) + i)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    g[4 * i] = v.x; g[4 * i + 1] = v.y; g[4 * i + 2] = v.z; g[4 * i + 3] = v.w;
+  }
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) {
 #pragma unroll
@@ -455,37 +459,49 @@ __global__ void __launch_bounds__(1024) filter_grad_kernel(const ConvArgs a, int
   });
 }
 
-// One token of each sequence: a thread has 8 channels of one.
-template <typename T, int K>
+// One token of each sequence: a thread has 8 channels of R sequences, for which it reads the
+// filter (more bytes than a sequence's rows) once.
+template <typename T, int K, int R>
 __global__ void __launch_bounds__(kFwdThreads) short_conv_step_kernel(const ConvArgs a,
                                                                       long long total) {
   constexpr int V = 8;
   const long long id = static_cast<long long>(blockIdx.x) * kFwdThreads + threadIdx.x;
   if (id >= total) return;
   const int nv = a.D / V, c = static_cast<int>(id % nv) * V;
-  const long long b = id / nv;
-  T* st = static_cast<T*>(a.state_out) + b * (K - 1) * a.D + c;
-  Raw<T, V> r[K];
+  const long long b0 = id / nv * R;
+  T* st = static_cast<T*>(a.state_out) + b0 * (K - 1) * a.D + c;
+  Raw<T, V> r[R][K];
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) r[k].load(st + static_cast<long long>(k) * a.D);
-  r[K - 1].load(static_cast<const T*>(a.x) + b * a.xs + c);
-  f32x2 w[K][V / 2], s[V / 2];
-  load_filter<K, V>(a, c, w, s);
+  for (int i = 0; i < R; ++i) {
+    if (b0 + i >= a.B) break;
 #pragma unroll
-  for (int k = K - 1; k >= 0; --k) {
-    f32x2 v[V / 2];
-    r[k].get(v);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) s[i] = fma2(w[k][i], v[i], s[i]);
+    for (int k = 0; k < K - 1; ++k) r[i][k].load(st + (i * (K - 1) + k) * static_cast<long long>(a.D));
+    r[i][K - 1].load(static_cast<const T*>(a.x) + (b0 + i) * a.xs + c);
   }
-  if (a.silu)
+  f32x2 w[K][V / 2], bias[V / 2];
+  load_filter<K, V>(a, c, w, bias);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) s[i] = mul2(s[i], sigmoid2(s[i]));
-  Raw<T, V> out;
-  out.put(s);
-  out.store(static_cast<T*>(a.y) + b * a.D + c);
+  for (int i = 0; i < R; ++i) {
+    if (b0 + i >= a.B) break;
+    f32x2 s[V / 2];
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) r[k + 1].store(st + static_cast<long long>(k) * a.D);
+    for (int j = 0; j < V / 2; ++j) s[j] = bias[j];
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      f32x2 v[V / 2];
+      r[i][k].get(v);
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) s[j] = fma2(w[k][j], v[j], s[j]);
+    }
+    if (a.silu)
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) s[j] = mul2(s[j], sigmoid2(s[j]));
+    Raw<T, V> out;
+    out.put(s);
+    out.store(static_cast<T*>(a.y) + (b0 + i) * a.D + c);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) r[i][k + 1].store(st + (i * (K - 1) + k) * static_cast<long long>(a.D));
+  }
 }
 
 template <class F>
@@ -497,15 +513,24 @@ cudaError_t by_taps(int K, bool f32, F f) {
   return typed(integral_constant<int, 4>{});
 }
 
-// Tokens of a run of the backward: 64 where that fills the SMs with two CTAs each, else fewer
-// (4 x 4096 x 4096 bf16: 118 us with 64, 133 with 32), and the CTAs' rows of partial sums,
-// one for each batch row and kRuns runs.
+// Tokens of a run of the backward, and the CTAs' rows of partial sums, one for each batch row
+// and kRuns runs. The run is what takes least time by waves of two CTAs an SM, a run being
+// K - 1 tokens and its start, about 6 in all, longer than its own (4 x 4096 x 4096 bf16: 118 us
+// with runs of 64 in 3.4 waves, 133 with 32).
 int bwd_groups(int T, int run) { return (T + kRuns * run - 1) / (kRuns * run); }
 int bwd_run(int B, int T, int D) {
   const long long slices = static_cast<long long>((D + 127) / 128) * B;
-  int run = 64;
-  while (run > 8 && slices * bwd_groups(T, run) < 2 * 152) run /= 2;
-  return run;
+  int best = 128;
+  long long least = 0;
+  for (int run = 128; run >= 8; --run) {
+    const long long waves = (slices * bwd_groups(T, run) + 2 * 152 - 1) / (2 * 152);
+    const long long cost = waves * (run + 6);
+    if (run == 128 || cost < least) {
+      least = cost;
+      best = run;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -542,14 +567,21 @@ cudaError_t launch_short_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t stre
 }
 
 cudaError_t launch_short_conv_step(const ConvArgs& a, bool f32, cudaStream_t stream) {
-  const long long total = static_cast<long long>(a.B) * (a.D / 8);
-  const long long grid = (total + kFwdThreads - 1) / kFwdThreads;
-  if (grid > 2147483647LL) return cudaErrorInvalidValue;
-  return by_taps(a.K, f32, [&](auto t, auto k) {
-    short_conv_step_kernel<decltype(t), k>
-        <<<static_cast<unsigned>(grid), kFwdThreads, 0, stream>>>(a, total);
-    return cudaGetLastError();
-  });
+  auto run = [&](auto rows) {
+    constexpr int R = decltype(rows)::value;
+    const long long total = (static_cast<long long>(a.B) + R - 1) / R * (a.D / 8);
+    const long long grid = (total + kFwdThreads - 1) / kFwdThreads;
+    if (grid > 2147483647LL) return cudaErrorInvalidValue;
+    return by_taps(a.K, f32, [&](auto t, auto k) {
+      short_conv_step_kernel<decltype(t), k, R>
+          <<<static_cast<unsigned>(grid), kFwdThreads, 0, stream>>>(a, total);
+      return cudaGetLastError();
+    });
+  };
+  // two sequences a thread where that leaves two CTAs for each SM
+  if (static_cast<long long>(a.B) * (a.D / 8) >= 4 * 152 * kFwdThreads)
+    return run(std::integral_constant<int, 2>{});
+  return run(std::integral_constant<int, 1>{});
 }
 
 }  // namespace gdr

@@ -772,13 +772,17 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
       }
     }
     const int blocks = gridDim.x / a.G, block = blockIdx.x % blocks;
-    for (int i = tid; i < nt * 2 * N; i += kBwdThreads) {
-      const int t = i / (2 * N), j = i % (2 * N);
-      float s = sm.dbc[0][t][j];
+    for (int i = tid; i < nt * N / 2; i += kBwdThreads) {      // four sums each
+      const int t = i / (N / 2), j = i % (N / 2) * 4;
+      float4 s = *reinterpret_cast<const float4*>(&sm.dbc[0][t][j]);
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) s += sm.dbc[w][t][j];
-      sp.bc_part[(((static_cast<size_t>(block) * a.B + b) * a.T + t0 + t) * a.G + ch.group) * 2 * N +
-                 j] = s;
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.dbc[w][t][j]);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+      *reinterpret_cast<float4*>(
+          sp.bc_part +
+          (((static_cast<size_t>(block) * a.B + b) * a.T + t0 + t) * a.G + ch.group) * 2 * N + j) = s;
     }
     __syncthreads();
     if (a.dt_bias) {
