@@ -493,7 +493,7 @@ cudaError_t launch_as(const SpaceArgs& a, const SpaceSplit& sp, int segments, bo
     using L = Layout<n, NARROW>;
     constexpr int kBytes = static_cast<int>(sizeof(Shared<decltype(t), n, NARROW>));
     constexpr auto kern = &space_kernel<decltype(t), n, NARROW, WALK>;
-    const cudaError_t err = allow_shared<kern>(kBytes);
+    const cudaError_t err = allow_shared<kern, kBytes>();
     if (err != cudaSuccess) return err;
     const int each = a.D / a.G, per = (each + L::kChannels - 1) / L::kChannels;
     kern<<<dim3(a.G * per, segments, a.B), L::kThreads, kBytes, stream>>>(a, sp);

@@ -81,19 +81,11 @@ __device__ __forceinline__ void store_pairs(T* p, const f32x2 (&x)[4]) {
   store8(p, f);
 }
 
-// Lets a kernel have `bytes` of shared memory, once per device.
-template <auto Kern>
-cudaError_t allow_shared(int bytes) {
-  constexpr int kMaxDevices = 64;
-  static bool done[kMaxDevices] = {};
-  int dev = 0;
-  const cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev < kMaxDevices && done[dev]) return cudaSuccess;
-  const cudaError_t set =
-      cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (set == cudaSuccess && dev < kMaxDevices) done[dev] = true;
-  return set;
+// Lets a kernel have `BYTES` of shared memory.
+template <auto Kern, int BYTES>
+cudaError_t allow_shared() {
+  static_assert(BYTES <= 232448, "shared memory of one CTA");
+  return cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
 }
 
 // The channels of a CTA: `width` at most, all of one group.

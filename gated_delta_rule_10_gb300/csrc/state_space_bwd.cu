@@ -878,7 +878,7 @@ cudaError_t launch_space_bwd_states(const SpaceArgs& a, const SpaceSplit& sp, bo
     auto run = [&](auto cut) {
       constexpr auto kern = &space_bwd_states_kernel<decltype(t), n, cut>;
       constexpr int kBytes = static_cast<int>(sizeof(PreShared<decltype(t), n>));
-      const cudaError_t err = allow_shared<kern>(kBytes);
+      const cudaError_t err = allow_shared<kern, kBytes>();
       if (err != cudaSuccess) return err;
       kern<<<dim3(a.G * blocks_of(a, PreLayout<n>::kChannels), sp.segments, a.B), kThreads, kBytes,
              stream>>>(a, sp);
@@ -894,7 +894,7 @@ cudaError_t launch_space_bwd(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
     auto run = [&](auto gated) {
       constexpr auto kern = &space_bwd_kernel<decltype(t), n, gated>;
       constexpr int kBytes = static_cast<int>(sizeof(BwdShared<decltype(t), n, gated>));
-      const cudaError_t e = allow_shared<kern>(kBytes);
+      const cudaError_t e = allow_shared<kern, kBytes>();
       if (e != cudaSuccess) return e;
       kern<<<dim3(a.G * blocks_of(a, BwdLayout<n>::kChannels), sp.segments, a.B), kBwdThreads,
              kBytes, stream>>>(a, sp);
