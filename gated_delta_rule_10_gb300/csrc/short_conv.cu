@@ -3,10 +3,13 @@
 // with taps that stop at a document's first token, and its gradients
 //   ds = dy act'(s),  dx_t = sum_j w[K-1-j] ds_{t+j},  dw[K-1-j] = sum_t ds_t x_{t-j}.
 //
-// Streams bound by HBM: a thread walks a run of consecutive tokens of 8 channels (a 16-byte
-// vector of bf16; the backward 4, for its sums) with the last K - 1 inputs in registers,
-// so that a token is read once per run plus K - 1 rows before it, and loads of several
-// tokens are in flight. Neighbouring threads have neighbouring channels.
+// Streams: a thread walks a run of consecutive tokens of 4 channels with the last K - 1 inputs
+// in registers, so that a token is read once per run plus K - 1 rows before it; the next
+// batch's loads are in flight while one is computed, in two sets of registers in turn (one,
+// copied: 12% slower). Neighbouring threads have neighbouring channels. 65536 x 4096 bf16: 178
+// us, 0.89 of measured HBM bandwidth (8 channels a thread, filter in single loads: 494 us).
+// Gradients of 4 x 4096 x 4096: 112 us, 0.53; 20 of them are the activation's two special
+// functions a value, 9 the second launch, and K = 2 takes 80.
 #include <type_traits>
 
 #include "column_sum.cuh"

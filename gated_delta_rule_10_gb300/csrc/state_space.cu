@@ -4,21 +4,23 @@
 //
 // Not a product of matrices: every (token, channel, state) has a decay of its own, so it is
 // an exponential and four multiply-adds each, against 8 bytes of bf16 for a token and
-// channel. What bounds it is the exponential unit and the fp32 pipe; multiply-adds run two
-// to an instruction.
+// channel. What bounds it is the issue of instructions (63% of the slots), the fp32 pipe (51%)
+// and the exponential unit (42%), not HBM (1.5 TB/s): 525 us for 4 x 4096 x 4096 channels x
+// 16 bf16, 1067 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
 //
-// Cut into segments, a thread holds 8 states of two channels and walks the tokens in order; N / 8 neighbouring
-// lanes share the channels and add their parts of y. (With one channel a thread, every B and
-// C read from shared memory served half as many states, and that was the bound.) A tile of
-// tokens is staged in shared memory as u and u x for each channel and B, C in fp32; the next
-// tile's inputs are copied to shared memory meanwhile, without registers (prefetched in
-// registers, the kernel had four warps a scheduler at most and waited for half of its
-// time). A thread stages what it has copied itself, and takes y from where it has staged u, so
-// that two barriers a tile are enough.
+// Cut into segments, a thread holds 8 states of two channels and walks the tokens in order;
+// N / 8 neighbouring lanes share the channels and add their parts of y. A tile of tokens is
+// staged in shared memory as u and u x for each channel and B, C in fp32; the next tile's
+// inputs are copied to shared memory meanwhile, without registers (prefetched in registers:
+// 681 us for the first shape, then 583). With one channel a thread every B and C read from
+// shared memory served half as many states: 714. A thread stages what it has copied itself,
+// and takes y from where it has staged u, so that two barriers a tile are enough.
 //
 // Few sequences are cut into segments until the CTAs fill the SMs: a first launch walks all
 // but the last one from zero for their end states and sums of u, a second chains them
-// (exp(A sum u) is a whole segment's decay).
+// (exp(A sum u) is a whole segment's decay). Uncut, a thread has 4 states of one channel, so
+// that there are four times the threads: the CTAs fill the SMs sooner, and short calls wait
+// less (2 x 257 tokens: 27 us where one launch does).
 #include <type_traits>
 
 #include "state_space.cuh"
@@ -212,8 +214,8 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128, (sizeof(T) == 2 ? 5 : 2) /
         const f32x2 u2 = both(u[o]), g2 = both(g[o]);
         f32x2& h0 = h[o][2 * q];
         f32x2& h1 = h[o][2 * q + 1];
-        h0 = fma2(exp2_pair(mul2(A2[o][2 * q], u2)), h0, mul2(g2, bq.x));
-        h1 = fma2(exp2_pair(mul2(A2[o][2 * q + 1], u2)), h1, mul2(g2, bq.y));
+        h0 = fma2(g2, bq.x, mul2(exp2_pair(mul2(A2[o][2 * q], u2)), h0));
+        h1 = fma2(g2, bq.y, mul2(exp2_pair(mul2(A2[o][2 * q + 1], u2)), h1));
         if (WALK) part[o] = fma2(cq.y, h1, q ? fma2(cq.x, h0, part[o]) : mul2(cq.x, h0));
       }
     }
@@ -454,11 +456,15 @@ __global__ void __launch_bounds__(kFlatThreads) space_step_kernel(const SpaceArg
         const int group = d / each;
         const float4 B = read4(static_cast<const T*>(a.Bm) + b * a.bs + group * N + n);
         const float4 C = read4(static_cast<const T*>(a.Cm) + b * a.cs + group * N + n);
-        const float v = kLog2e * ud, g = ud * xd;
-        h[r].x = fmaf(exp2_fast(A[r].x * v), h[r].x, g * B.x);
-        h[r].y = fmaf(exp2_fast(A[r].y * v), h[r].y, g * B.y);
-        h[r].z = fmaf(exp2_fast(A[r].z * v), h[r].z, g * B.z);
-        h[r].w = fmaf(exp2_fast(A[r].w * v), h[r].w, g * B.w);
+        const f32x2 v = both(kLog2e * ud), g = both(ud * xd);
+        const f32x2 lo = fma2(g, pair(B.x, B.y),
+                              mul2(exp2_pair(mul2(pair(A[r].x, A[r].y), v)),
+                                         pair(h[r].x, h[r].y)));
+        const f32x2 hi = fma2(g, pair(B.z, B.w),
+                              mul2(exp2_pair(mul2(pair(A[r].z, A[r].w), v)),
+                                         pair(h[r].z, h[r].w)));
+        split(lo, h[r].x, h[r].y);
+        split(hi, h[r].z, h[r].w);
         s = fmaf(C.x, h[r].x, fmaf(C.y, h[r].y, fmaf(C.z, h[r].z, C.w * h[r].w)));
         __stcs(reinterpret_cast<float4*>(hp + static_cast<size_t>(d) * N + n), h[r]);
       }

@@ -11,14 +11,18 @@
 //   backward.
 // - Gradients, tile by tile backward: a tile's states are computed again from its first one,
 //   kept every 4 tokens in shared memory, then by 4 tokens in registers with their decays.
-// Three exponentials and about 22 multiply-adds for each (token, channel, state) in all:
-// bound by the fp32 pipe.
+// Three exponentials and about 22 multiply-adds for each (token, channel, state) in all. The
+// second launch is 70% of the time (4 x 4096 x 2048 channels x 16 bf16: 920 us in all): two
+// warps a scheduler, which 255 registers a thread and 111 KB of shared memory a CTA leave,
+// issue 46% of the time. With half the states a thread (three CTAs an SM) it issues 58% of the
+// time but 30% more, and takes as long; so does half the tokens in registers.
 //
-// A thread has 4 states of 4 channels, so that the sums over channels (dB, dC) and those over
-// states (q, sum A w, C h) each start inside a thread. What is left goes over lanes by
-// halves: a lane passes on half of its sums and keeps the other half. Which one is by
-// lane, so a lane's registers hold its states in the order n ^ lane (channels alike), and no
-// register has to be selected; B and C are in shared memory in all four orders.
+// A thread has 4 states of 4 channels (pairs of channels share an instruction), so that the
+// sums over channels (dB, dC) and those over states (q, sum A w, C h) each start inside a
+// thread. What is left goes over lanes by halves: a lane passes on half of its sums and keeps
+// the other half. Which one is by lane, so a lane's registers hold its states in the order
+// n ^ lane (pairs of channels alike), and no register has to be selected; B and C are in
+// shared memory in all four orders.
 #include <type_traits>
 
 #include "state_space.cuh"
@@ -209,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
         for (int j = 0; j < 2; ++j) {
           const int i = 2 * q + j;
           const f32x2 d = exp2_pair(mul2(A2[o][i], u2[o]));
-          h[o][i] = fma2(d, h[o][i], mul2(g2[o], j ? bq.y : bq.x));
+          h[o][i] = fma2(g2[o], j ? bq.y : bq.x, mul2(d, h[o][i]));
           if (back) {
-            P[o][i] = mul2(P[o][i], d);
+            P[o][i] = mul2(d, P[o][i]);
             e[o][i] = fma2(P[o][i], mul2(j ? cq.y : cq.x, p2[o]), e[o][i]);
           }
         }
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
         for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            h[p][j] = fma2(exp2_pair(mul2(A2[p][j], u[p])), h[p][j], mul2(g[p], b2[j]));
+            h[p][j] = fma2(g[p], b2[j], mul2(exp2_pair(mul2(A2[p][j], u[p])), h[p][j]));
       }
     }
     // and back
@@ -843,7 +847,7 @@ __global__ void __launch_bounds__(256) space_sums_kernel(const SpaceArgs a, cons
     } else {
       const long long j = i - bc - da;
 #pragma unroll 4
-      for (int k = 0; k < parts; ++k) s += sp.d_part[k * 2 * a.D + j];
+      for (int k = 0; k < parts; ++k) s += sp.d_part[k * 2LL * a.D + j];
       if (j < a.D) {
         if (a.skip) a.dskip[j] = s;
       } else if (a.dt_bias) {

@@ -787,7 +787,10 @@ gdr_status gdr_short_conv_step(const gdr_conv_shape* shape, const void* x, const
  * Sizes: N in {8, 16, 32, 64}; D / G a multiple of 8, D up to 2^20; T up to 2^30, B up to
  * 65535. Pointers are 16-byte aligned (starts any), strides multiples of 16 bytes. A is
  * finite and usually negative. The state, the decays and every sum are fp32; y is rounded
- * once. A value that is not finite reaches the later tokens of its document and channel (a
+ * once. Against 64 bits (2-norm) states and fp32 outputs and gradients come to about 1e-6, and
+ * to 3e-6 where equal slow steps (memories of thousands of tokens) round the same way every
+ * time; token by token (gdr_state_space_step) such a state rounds after every one, up to 2^-25
+ * of it for each token that it keeps (1e-4 for memories of 10^4). A value that is not finite reaches the later tokens of its document and channel (a
  * group's channels, from Bm), in the gradients also the earlier ones.
  */
 typedef struct {
@@ -811,7 +814,8 @@ gdr_status gdr_state_space_fwd(const gdr_state_space_shape* shape, const void* x
  * [B,T,D] and dBm, dCm [B,T,G,N] in dtype, dA [D,N], dskip, ddt_bias [D] and dh0 [B,D,N] fp32.
  * dskip, dz and ddt_bias are needed with skip, z and dt_bias and else not written; dh0 may be
  * NULL. dhT and dh0 may be one buffer. workspace: at least gdr_state_space_bwd_workspace()
- * bytes, 16-byte aligned (the states at every 16th token among them: D * N * 4 bytes each).
+ * bytes, 16-byte aligned (the states at every 16th token, D * N * 4 bytes each, and 8 * N
+ * bytes of partial sums for each token and 2048 / N channels, among them).
  * No sum uses atomics.
  */
 gdr_status gdr_state_space_bwd_workspace(const gdr_state_space_shape* shape, size_t* bytes);
