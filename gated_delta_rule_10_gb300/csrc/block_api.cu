@@ -110,7 +110,7 @@ void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
     else if (segments == 1)
       cost = waves(rows * blocks(gdr::space_channels(s->N, true)), 2, 0.084, 0.062) * s->T;
     else
-      cost = (waves(ctas * segments, 5, 0.17, 0.066) +
+      cost = (waves(ctas * segments, 4, 0.17, 0.066) +
               0.65 * waves(ctas * (segments - 1), 5, 0.17, 0.066)) * (len + 0.3) * tile + 25.0;
     if (n == 1 || cost < best) {
       best = cost;

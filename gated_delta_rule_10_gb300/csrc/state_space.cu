@@ -57,7 +57,8 @@ struct __align__(16) Shared {
 // WALK: y and the end state, from the segment's start state. Else: the segment's own end
 // state (segment 0's from h0), its sum of u and whether a document starts in it.
 template <typename T, int N, bool NARROW, bool WALK>
-__global__ void __launch_bounds__(NARROW ? 256 : 128, (sizeof(T) == 2 ? 5 : 2) / (NARROW ? 2 : 1))
+__global__ void __launch_bounds__(NARROW ? 256 : 128,
+                                  sizeof(T) == 2 ? (NARROW ? 2 : WALK ? 4 : 5) : (NARROW ? 1 : 2))
     space_kernel(const SpaceArgs a, const SpaceSplit sp) {
   using L = Layout<N, NARROW>;
   constexpr int kThreads = L::kThreads, kOwn = L::kOwn, kStates = L::kStates;
