@@ -121,15 +121,25 @@ def test_conv_every_token_starts():
 
 
 def test_conv_long_runs():
-    """Enough channels for the forward's runs of 32 tokens."""
+    """Enough channels for the longest runs, both ways."""
     B, T, D, K = 2, 1100, 8192, 4
     x = conv_inputs(B, T, D, K, BF, 5, packed=True)
     y, _ = gdr.short_conv_fwd(x["x"], x["weight"], x["bias"], x["state"], starts=x["starts"])
+    g = gdr.short_conv_bwd(x["dy"], x["x"], x["weight"], x["bias"], x["state"], x["dstate"],
+                           starts=x["starts"])
     part = slice(4000, 4064)
+    dw = 0
     for b in range(B):
-        r, _ = block.short_conv(f64(x["x"][b, :, part]), f64(x["weight"][part]), f64(x["bias"][part]),
-                                f64(x["state"][b, :, part]), f64(x["starts"][b]))
+        args = (f64(x["x"][b, :, part]), f64(x["weight"][part]), f64(x["bias"][part]),
+                f64(x["state"][b, :, part]))
+        r, _ = block.short_conv(*args, f64(x["starts"][b]))
         near(y[b, :, part], r, 1e-6)
+        r = block.short_conv_gradients(f64(x["dy"][b, :, part]), *args, f64(x["dstate"][b, :, part]),
+                                       f64(x["starts"][b]))
+        near(g["x"][b, :, part], r["x"], 2e-6)
+        near(g["state"][b, :, part], r["state"], 2e-6)
+        dw = dw + r["weight"]
+    assert off(g["weight"][part], dw) <= 1e-5
 
 
 @DTYPES
@@ -430,6 +440,68 @@ def test_space_step(N, D, G, S, dtype):
         ry, rh = space_oracle(x, b, False)
         near(y[b], ry[0], 2e-6)
         near(state[b], rh, 2e-6)
+
+
+def test_space_step_sequences_apart():
+    """Parts of projections, more sequences than a warp has channels, widths that end inside
+    a warp."""
+    N, D, S = 37, 200, 16
+    x = space_inputs(N, 1, D, 1, S, BF, 21)
+    p = torch.zeros(N, 8 + 3 * D + 2 * S, device="cuda", dtype=BF)
+    part = lambda at, n, like: p[:, at:at + n].copy_(like)  # noqa: E731
+    parts = [part(8 + i * D, D, x[n][:, 0]) for i, n in enumerate(("x", "dt", "z"))]
+    bc = [part(8 + 3 * D + i * S, S, x[n][:, 0, 0]).unsqueeze(1) for i, n in enumerate(("B", "C"))]
+    s1, s2 = x["h0"].clone(), x["h0"].clone()
+    kw = dict(skip=x["skip"], dt_bias=x["dt_bias"])
+    y1 = gdr.state_space_step(parts[0], parts[1], x["A"], bc[0], bc[1], s1, z=parts[2], **kw)
+    y2 = gdr.state_space_step(x["x"][:, 0], x["dt"][:, 0], x["A"], x["B"][:, 0], x["C"][:, 0], s2,
+                              z=x["z"][:, 0], **kw)
+    assert torch.equal(y1, y2) and torch.equal(s1, s2)
+    for b in (0, 17, N - 1):
+        ry, rh = space_oracle(x, b, False)
+        near(y1[b], ry[0], 2e-6)
+        near(s1[b], rh, 2e-6)
+
+
+@pytest.mark.parametrize("shape", [(3, 40, 4096, 1, 16), (4, 300, 2048, 1, 16), (2, 64, 1024, 2, 64)],
+                         ids=ids)
+def test_space_wide_layers(shape):
+    """Channels of many CTAs, uncut and cut: a few of them, and all sums over channels, from
+    the oracle on those channels alone and from the others' own calls."""
+    B, T, D, G, N = shape
+    x = space_inputs(*shape, BF, 22, packed=True)
+    y, hT = space_fwd(x)
+    g = space_bwd(x)
+    each = D // G
+    tol = 2e-6 + T * 2.0 ** -22
+    cut = slice(each - 8, each)                      # the last channels of the first group
+    sub = {n: (v if v is None or not torch.is_tensor(v) else
+               v[..., cut].contiguous() if n in ("x", "dt", "z", "dy") else
+               v[cut].contiguous() if n in ("A", "skip", "dt_bias") else
+               v[:, cut].contiguous() if n in ("h0", "dhT") else
+               v[:, :, :1].contiguous() if n in ("B", "C") else v) for n, v in x.items()}
+    for b in range(B):
+        ry, rh = space_oracle(sub, b, False)
+        near(y[b, :, cut], ry, tol)
+        near(hT[b, cut], rh, tol)
+        r = space_oracle(sub, b, True)
+        for n in ("x", "dt", "z"):
+            near(g[n][b, :, cut], r[n], tol, n)
+        near(g["h0"][b, cut], r["h0"], tol)
+    # dB and dC are sums over channels: of the parts' own calls, in fp32
+    total = {n: torch.zeros(B, T, 1, N, device="cuda", dtype=torch.float64) for n in ("B", "C")}
+    for at in range(0, each, 512):
+        part = slice(at, min(at + 512, each))
+        sub = {n: (v if v is None or not torch.is_tensor(v) else
+                   v[..., part].float().contiguous() if n in ("x", "dt", "z", "dy") else
+                   v[part].contiguous() if n in ("A", "skip", "dt_bias") else
+                   v[:, part].contiguous() if n in ("h0", "dhT") else
+                   v[:, :, :1].float().contiguous() if n in ("B", "C") else v) for n, v in x.items()}
+        p = space_bwd(sub)
+        for n in total:
+            total[n] += p[n].double()
+    for n in total:
+        near(g[n][:, :, :1], f64(total[n]), 2 * tol, "d" + n)
 
 
 def test_space_prompt_then_steps_is_one_prompt():
