@@ -8,8 +8,8 @@
 // batch's loads are in flight while one is computed, in two sets of registers in turn (one,
 // copied: 12% slower). Neighbouring threads have neighbouring channels. 65536 x 4096 bf16: 178
 // us, 0.89 of measured HBM bandwidth (8 channels a thread, filter in single loads: 494 us).
-// Gradients of 4 x 4096 x 4096: 112 us, 0.53; 20 of them are the activation's two special
-// functions a value, 9 the second launch, and K = 2 takes 80.
+// Gradients of 4 x 4096 x 4096: 117 us, 0.5; 20 of them are the activation's two special
+// functions a value, 6 the second launch, and K = 2 takes 80.
 #include <type_traits>
 
 #include "column_sum.cuh"
@@ -518,8 +518,8 @@ cudaError_t by_taps(int K, bool f32, F f) {
 
 // Tokens of a run of the backward, and the CTAs' rows of partial sums, one for each batch row
 // and kRuns runs. The run is what takes least time by waves of two CTAs an SM, a run being
-// K - 1 tokens and its start, about 6 in all, longer than its own (4 x 4096 x 4096 bf16: 118 us
-// with runs of 64 in 3.4 waves, 133 with 32).
+// K - 1 tokens and its start, about 6 in all, longer than its own (4 x 4096 x 4096 bf16: 107 us
+// with runs of 74 in 2.95 waves, 115 with 64 in 3.4, 130 with 32).
 int bwd_groups(int T, int run) { return (T + kRuns * run - 1) / (kRuns * run); }
 int bwd_run(int B, int T, int D) {
   const long long slices = static_cast<long long>((D + 127) / 128) * B;

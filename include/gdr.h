@@ -790,8 +790,9 @@ gdr_status gdr_short_conv_step(const gdr_conv_shape* shape, const void* x, const
  * once. Against 64 bits (2-norm) states and fp32 outputs and gradients come to about 1e-6, and
  * to 3e-6 where equal slow steps (memories of thousands of tokens) round the same way every
  * time; token by token (gdr_state_space_step) such a state rounds after every one, up to 2^-25
- * of it for each token that it keeps (1e-4 for memories of 10^4). A value that is not finite reaches the later tokens of its document and channel (a
- * group's channels, from Bm), in the gradients also the earlier ones.
+ * of it for each token that it keeps (1e-4 for memories of 10^4). A value that is not finite
+ * reaches the later tokens of its document and channel (a group's channels, from Bm), in the
+ * gradients also the earlier ones.
  */
 typedef struct {
   int B, T, D, G, N;
