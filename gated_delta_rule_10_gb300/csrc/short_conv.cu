@@ -4,12 +4,12 @@
 //   ds = dy act'(s),  dx_t = sum_j w[K-1-j] ds_{t+j},  dw[K-1-j] = sum_t ds_t x_{t-j}.
 //
 // Streams: a thread walks a run of consecutive tokens of 4 channels with the last K - 1 inputs
-// in registers, so that a token is read once per run plus K - 1 rows before it; the next
-// batch's loads are in flight while one is computed, in two sets of registers in turn (one,
-// copied: 12% slower). Neighbouring threads have neighbouring channels. 65536 x 4096 bf16: 178
-// us, 0.89 of measured HBM bandwidth (8 channels a thread, filter in single loads: 494 us).
-// Gradients of 4 x 4096 x 4096: 117 us, 0.5; 20 of them are the activation's two special
-// functions a value, 6 the second launch, and K = 2 takes 80.
+// in registers, so that a token is read once per run plus K - 1 rows before it. What comes next
+// is copied to the thread's own places in shared memory, two batches of 4 tokens ahead, which
+// takes no registers and no barrier. Neighbouring threads have neighbouring channels.
+// 65536 x 4096 bf16: 165 us, 0.96 of measured HBM bandwidth (two batches of 8 in registers:
+// 176; 8 channels a thread, filter in single loads: 494). Gradients of 4 x 4096 x 4096: 94 us,
+// 0.63 (batches in registers: 113); K = 2 takes 71, and 6 are the second launch.
 #include <type_traits>
 
 #include "column_sum.cuh"
@@ -22,7 +22,7 @@ namespace {
 
 // V elements as they are in memory (V = 4 or 8).
 template <typename T, int V>
-struct Raw {
+struct __align__(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Raw {
   static constexpr int kWords = V * sizeof(T) / 4;
   uint32_t u[kWords];
   __device__ __forceinline__ void load(const T* p) {
@@ -137,8 +137,31 @@ __device__ __forceinline__ int reach(const unsigned char* starts, int t) {
   return r;
 }
 
+// The starts of four tokens, a byte each, of which `left` are there. As one word where they
+// may be read so: nothing is done with it before it is needed (bytes put together at once
+// cost the gradients 10% in waits for them).
+__device__ __forceinline__ unsigned four_starts(const unsigned char* p, int left) {
+  if (left >= 4 && (reinterpret_cast<uintptr_t>(p) & 3) == 0)
+    return __ldg(reinterpret_cast<const unsigned*>(p));
+  unsigned m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < left) m |= static_cast<unsigned>(p[k]) << (8 * k);
+  return m;
+}
+
+// A thread's V channels of a row, to shared memory.
+template <typename T, int V>
+__device__ __forceinline__ void copy_row(Raw<T, V>* to, const T* from) {
+  constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  static_assert(kBytes == 8 || kBytes == 16, "");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(kBytes)
+               : "memory");
+}
+
 constexpr int kFwdThreads = 128;
-constexpr int kBatch = 8;          // tokens requested together, one batch ahead
+constexpr int kBatch = 4;          // tokens requested together
+constexpr int kFwdStages = 3;      // batches on their way or in use (4: fp32 takes 198 us for 173)
 
 template <typename T, int K>
 __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs a, int run,
@@ -155,29 +178,18 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
   const T* x = static_cast<const T*>(a.x) + static_cast<long long>(b) * a.T * a.xs + c;
   T* y = static_cast<T*>(a.y) + static_cast<long long>(b) * a.T * a.D + c;
   f32x2 w[K][H], bias[H], prev[K - 1][H];    // prev[j]: the row j + 1 tokens back
-  struct Batch {
-    Raw<T, V> x[kBatch];
-    unsigned starts;
-  } even, odd;
+  __shared__ Raw<T, V> ring[kFwdStages][kBatch][kFwdThreads];
+  unsigned marks[kFwdStages];                              // the batches' documents' starts
   const T* xp = x + static_cast<long long>(t0) * a.xs;     // the next batch's
-  auto fetch = [&](Batch& f, int t) {
-    f.starts = 0;
-    if (t + kBatch <= t1) {
+  auto fetch = [&](int stage, int t) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k, xp += a.xs) f.x[k].load(xp);
-      if (starts)
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
-    } else {
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k, xp += a.xs)
-        if (t + k < t1) {
-          f.x[k].load(xp);
-          if (starts) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
-        }
-    }
+    for (int k = 0; k < kBatch; ++k, xp += a.xs)
+      if (t + k < t1) copy_row(&ring[stage][k][threadIdx.x], xp);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    marks[stage] = starts && t < t1 ? four_starts(starts + t, t1 - t) : 0;
   };
-  fetch(even, t0);
+#pragma unroll
+  for (int i = 0; i < kFwdStages - 1; ++i) fetch(i, t0 + i * kBatch);
   load_filter<K, V>(a, c, w, bias);
   {
     Raw<T, V> r[K - 1];
@@ -216,28 +228,29 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
 #pragma unroll
     for (int i = 0; i < H; ++i) prev[0][i] = v[i];
   };
-  auto tokens = [&](const Batch& f, int t) {
-    if (t + kBatch <= t1 && f.starts == 0) {
+  auto tokens = [&](int stage, int t) {
+    if (t + kBatch <= t1 && marks[stage] == 0) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) token(f.x[k]);
+      for (int k = 0; k < kBatch; ++k) token(ring[stage][k][threadIdx.x]);
     } else {
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (t + k >= t1) break;
-        if ((f.starts >> k) & 1)
+#pragma unroll 1
+      for (int k = 0; k < kBatch && t + k < t1; ++k) {
+        if ((marks[stage] >> (8 * k)) & 0xff)
 #pragma unroll
           for (int j = 0; j < K - 1; ++j)
 #pragma unroll
             for (int i = 0; i < H; ++i) prev[j][i] = 0;
-        token(f.x[k]);
+        token(ring[stage][k][threadIdx.x]);
       }
     }
   };
-  for (int t = t0; t < t1; t += 2 * kBatch) {
-    fetch(odd, t + kBatch);
-    tokens(even, t);
-    fetch(even, t + 2 * kBatch);
-    tokens(odd, t + kBatch);
+  for (int t = t0; t < t1; t += kFwdStages * kBatch) {
+#pragma unroll
+    for (int i = 0; i < kFwdStages; ++i) {
+      fetch((i + kFwdStages - 1) % kFwdStages, t + (i + kFwdStages - 1) * kBatch);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kFwdStages - 1) : "memory");
+      tokens(i, t + i * kBatch);
+    }
   }
   if (t1 == a.T && a.state_out) {     // prev is the last rows, zeros behind a start
 #pragma unroll
@@ -254,14 +267,17 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
 // neighbouring runs, whose filter gradients it adds up in a fixed order to one row of
 // `partial` ([K + 1, D], the last row the bias's); column_sum adds those rows. A run walks
 // K - 1 tokens past its end for what they pass back.
-constexpr int kRuns = 8;
+constexpr int kRuns = 4;
 constexpr int kBwdThreads = 32 * kRuns;
 constexpr int kBwdBatch = 4;
+constexpr int kStages = 3;         // batches on their way or in use (6 leave fewer CTAs: 159 us)
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 4 : 2)
     short_conv_bwd_kernel(const ConvArgs a, int run, int groups, int slices) {
   constexpr int V = 4, H = V / 2;
+  extern __shared__ __align__(16) unsigned char raw_smem[];
+  Raw<T, V>* ring = reinterpret_cast<Raw<T, V>*>(raw_smem);   // [kStages][kBwdBatch][2][threads]
   __shared__ __align__(16) float sums[kRuns][K + 1][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slice = blockIdx.x % slices, c = (slice * 32 + lane) * V;
@@ -281,34 +297,24 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
                       : nullptr;
     const int stop = min(t1 + K - 1, a.T);
     f32x2 w[K][H], bias[H], prev[K - 1][H], acc[K][H];   // acc[j]: dx of the token j back (j > 0)
-    struct Batch {
-      Raw<T, V> x[kBwdBatch], y[kBwdBatch];
-      unsigned starts;
-    } even, odd;
     const T* xf = xp + static_cast<long long>(t0) * a.xs;     // the next batch's
     const T* yf = dyp + static_cast<long long>(t0) * a.D;
-    auto fetch = [&](Batch& f, int t) {
-      f.starts = 0;
-      if (t + kBwdBatch <= stop) {
-#pragma unroll
-        for (int k = 0; k < kBwdBatch; ++k, xf += a.xs, yf += a.D) {
-          f.x[k].load(xf);
-          f.y[k].load(yf);
-        }
-        if (starts)
-#pragma unroll
-          for (int k = 0; k < kBwdBatch; ++k) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
-      } else {
-#pragma unroll
-        for (int k = 0; k < kBwdBatch; ++k, xf += a.xs, yf += a.D)
-          if (t + k < stop) {
-            f.x[k].load(xf);
-            f.y[k].load(yf);
-            if (starts) f.starts |= (starts[t + k] != 0 ? 1u : 0u) << k;
-          }
-      }
+    unsigned marks[kStages];          // the batches' documents' starts
+    auto place = [&](int stage, int k, int which) {
+      return ring + ((stage * kBwdBatch + k) * 2 + which) * kBwdThreads + threadIdx.x;
     };
-    fetch(even, t0);
+    auto fetch = [&](int stage, int t) {
+#pragma unroll
+      for (int k = 0; k < kBwdBatch; ++k, xf += a.xs, yf += a.D)
+        if (t + k < stop) {
+          copy_row(place(stage, k, 0), xf);
+          copy_row(place(stage, k, 1), yf);
+        }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      marks[stage] = starts ? four_starts(starts + t, stop - t) : 0;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, t0 + i * kBwdBatch);
     load_filter<K, V>(a, c, w, bias);
     {
       Raw<T, V> r[K - 1];
@@ -394,29 +400,26 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < H; ++i) prev[0][i] = v[i];
     };
-    auto tokens = [&](Batch& f, int t) {
-      if (f.starts == 0 && back == K - 1 && t - (K - 1) >= t0 && t + kBwdBatch <= t1) {
+    auto tokens = [&](int stage, int t) {
+      auto load = [&](int k, int which) { return *place(stage, k, which); };
+      if (marks[stage] == 0 && back == K - 1 && t - (K - 1) >= t0 && t + kBwdBatch <= t1) {
 #pragma unroll
-        for (int k = 0; k < kBwdBatch; ++k) token(f.x[k], f.y[k], t + k, std::true_type{});
+        for (int k = 0; k < kBwdBatch; ++k) token(load(k, 0), load(k, 1), t + k, std::true_type{});
       } else {
 #pragma unroll 1
         for (int k = 0; k < kBwdBatch && t + k < stop; ++k) {
-          back = (f.starts >> k) & 1 ? 0 : min(back + 1, K - 1);
-          // (a register array has no address: the batch moves on instead)
-          token(f.x[0], f.y[0], t + k, std::false_type{});
-#pragma unroll
-          for (int i = 0; i + 1 < kBwdBatch; ++i) {
-            f.x[i] = f.x[i + 1];
-            f.y[i] = f.y[i + 1];
-          }
+          back = (marks[stage] >> (8 * k)) & 0xff ? 0 : min(back + 1, K - 1);
+          token(load(k, 0), load(k, 1), t + k, std::false_type{});
         }
       }
     };
-    for (int t = t0; t < stop; t += 2 * kBwdBatch) {
-      fetch(odd, t + kBwdBatch);
-      tokens(even, t);
-      fetch(even, t + 2 * kBwdBatch);
-      tokens(odd, t + kBwdBatch);
+    for (int t = t0; t < stop; t += kStages * kBwdBatch) {
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) {
+        fetch((i + kStages - 1) % kStages, t + (i + kStages - 1) * kBwdBatch);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        tokens(i, t + i * kBwdBatch);
+      }
     }
     if (stop == a.T) {   // what is behind the last token comes from the state's gradient
 #pragma unroll
@@ -517,16 +520,17 @@ cudaError_t by_taps(int K, bool f32, F f) {
 }
 
 // Tokens of a run of the backward, and the CTAs' rows of partial sums, one for each batch row
-// and kRuns runs. The run is what takes least time by waves of two CTAs an SM, a run being
-// K - 1 tokens and its start, about 6 in all, longer than its own (4 x 4096 x 4096 bf16: 107 us
-// with runs of 74 in 2.95 waves, 115 with 64 in 3.4, 130 with 32).
+// and kRuns runs. The run is what takes least time by waves of four CTAs an SM, a run being
+// K - 1 tokens and its start, about 6 in all, longer than its own (4 x 4096 x 4096 bf16, as it
+// was with two larger CTAs an SM: 107 us with runs of 74 in 2.95 waves, 115 with 64 in 3.4,
+// 130 with 32).
 int bwd_groups(int T, int run) { return (T + kRuns * run - 1) / (kRuns * run); }
 int bwd_run(int B, int T, int D) {
   const long long slices = static_cast<long long>((D + 127) / 128) * B;
-  int best = 128;
+  int best = 128;                       // multiples of 4: see four_starts
   long long least = 0;
-  for (int run = 128; run >= 8; --run) {
-    const long long waves = (slices * bwd_groups(T, run) + 2 * 152 - 1) / (2 * 152);
+  for (int run = 128; run >= 8; run -= 4) {
+    const long long waves = (slices * bwd_groups(T, run) + 4 * 152 - 1) / (4 * 152);
     const long long cost = waves * (run + 6);
     if (run == 128 || cost < least) {
       least = cost;
@@ -562,8 +566,12 @@ cudaError_t launch_short_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t stre
   const long long grid = static_cast<long long>(slices) * a.B * groups;
   if (grid > 2147483647LL) return cudaErrorInvalidValue;
   return by_taps(a.K, f32, [&](auto t, auto k) {
+    constexpr int kBytes = kStages * kBwdBatch * 2 * kBwdThreads * 4 * sizeof(decltype(t));
+    const cudaError_t err = cudaFuncSetAttribute(
+        short_conv_bwd_kernel<decltype(t), k>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (err != cudaSuccess) return err;
     short_conv_bwd_kernel<decltype(t), k>
-        <<<static_cast<unsigned>(grid), kBwdThreads, 0, stream>>>(a, run, groups, slices);
+        <<<static_cast<unsigned>(grid), kBwdThreads, kBytes, stream>>>(a, run, groups, slices);
     filter_grad_kernel<<<((a.K + 1) * a.D + 31) / 32, 1024, 0, stream>>>(a, a.B * groups);
     return cudaGetLastError();
   });
