@@ -12,7 +12,7 @@
 // are persistent, walk the rows and request the next row's vectors before the current
 // row's sums, so that loads are in flight through the barriers. 65536 x 4096 bf16: 396 us, all
 // of measured HBM (462 with an exact division in the sigmoid); gradients of 16384 x 2048: 95
-// us, 0.83, of which 7 are the second launch.
+// us, 0.84, of which 7 are the second launch.
 #include "block_norms.h"
 
 #include <type_traits>
@@ -170,12 +170,34 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
   }
 }
 
+// 16 bytes at a time from global to shared memory.
+template <typename T>
+__device__ __forceinline__ void copy8(uint4* to, const T* from) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + i)),
+                 "l"(reinterpret_cast<const uint4*>(from) + i)
+                 : "memory");
+}
+
+// Rows on their way or in use: the inputs are copied to the thread's own places in shared
+// memory, which takes no registers and no barrier. One row ahead; two ahead take as long or
+// longer (65536 x 512 bf16: 100 us for 87). Of more than 4096 columns the next row is requested
+// as soon as the current one is in registers, into its places (4096 x 8192 bf16: 105 us, 115
+// with places for two rows, 159 in registers, which spilled).
+constexpr int kInputs = 5;      // sum, dy, dres, x, gate
+template <int VEC>
+constexpr int stages() { return VEC == 1 ? 2 : 1; }
+
 // Each thread keeps its columns' sums in registers over all its rows; the CTA's row groups
 // add theirs at the end, in a fixed order, to one row of `partial` ([2, D]: m and dpre).
 template <typename T, int TPR, int VEC>
 __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads<TPR>() : 1)
     block_norms_bwd_kernel(const BlockNormsBwdArgs a) {
   constexpr int kThreads = threads<TPR>(), kRows = kThreads / TPR;
+  constexpr int kStages = stages<VEC>(), kWords = sizeof(T) / 2;
+  extern __shared__ __align__(16) unsigned char raw_smem[];
+  uint4* ring = reinterpret_cast<uint4*>(raw_smem);   // [stage][input][vector][thread][kWords]
   __shared__ float2 red[2][16];
   __shared__ float sums[kRows > 1 ? kThreads * 8 : 1];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
@@ -185,30 +207,51 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
   for (int i = 0; i < VEC; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dm[i][j] = dp[i][j] = 0;
-  struct Row {
-    Raw8<T> x[VEC], g[VEC], r[VEC], y[VEC], d[VEC];
-  } in;
-  auto fetch = [&](long long row) {
+  const T* const in[kInputs] = {static_cast<const T*>(a.sum), static_cast<const T*>(a.dy),
+                                static_cast<const T*>(a.dres), static_cast<const T*>(a.x),
+                                static_cast<const T*>(a.gate)};
+  auto place = [&](int stage, int k, int i) {
+    return ring + (((stage * kInputs + k) * VEC + i) * kThreads + threadIdx.x) * kWords;
+  };
+  // what is not there stays zero: columns past D, a missing dres or gate
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int c = lane + i * TPR;
-      in.d[i].zero();
-      in.g[i].zero();
-      if (row < a.rows && c < nv) {
-        in.r[i].load(static_cast<const T*>(a.sum) + row * a.D + 8 * c);
-        in.y[i].load(static_cast<const T*>(a.dy) + row * a.D + 8 * c);
-        if (a.dres) in.d[i].load(static_cast<const T*>(a.dres) + row * a.D + 8 * c);
-        in.x[i].load(static_cast<const T*>(a.x) + row * a.D + 8 * c);
-        if (a.gate) in.g[i].load(static_cast<const T*>(a.gate) + row * a.D + 8 * c);
-      } else {
-        in.r[i].zero();
-        in.y[i].zero();
-        in.x[i].zero();
-      }
-    }
+  for (int st = 0; st < kStages; ++st)
+#pragma unroll
+    for (int k = 0; k < kInputs; ++k)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) place(st, k, i)[w] = make_uint4(0u, 0u, 0u, 0u);
+  auto fetch = [&](int stage, long long row) {
+    if (row < a.rows)
+#pragma unroll
+      for (int k = 0; k < kInputs; ++k)
+        if (in[k])
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const int c = lane + i * TPR;
+            if (c < nv) copy8(place(stage, k, i), in[k] + row * a.D + 8 * c);
+          }
+    if (kRows > 1 && row >= a.rows)      // beside the last rows: adds nothing
+#pragma unroll
+      for (int k = 0; k < kInputs; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) place(stage, k, i)[w] = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto get = [&](int stage, int k, int i, f32x2 (&v)[4]) {
+    Raw8<T> r;
+    const uint4* p = place(stage, k, i);
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) r.u[w] = p[w];
+    pairs(r, v);
   };
   const long long step = static_cast<long long>(gridDim.x) * kRows;
-  fetch(static_cast<long long>(blockIdx.x) * kRows + sub);
+  const long long first = static_cast<long long>(blockIdx.x) * kRows;
+#pragma unroll
+  for (int st = 0; st < (kStages > 1 ? kStages - 1 : 1); ++st) fetch(st, first + sub + st * step);
   {
     float s[VEC][8], p[VEC][8];
     load_weights<TPR, VEC>(a.post, a.scale, a.pre, lane, nv, s, p);
@@ -221,48 +264,53 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
       }
   }
   const float n = static_cast<float>(a.D);
-  for (long long r0 = static_cast<long long>(blockIdx.x) * kRows; r0 < a.rows; r0 += step) {
+  int stage = 0;
+  for (long long r0 = first; r0 < a.rows; r0 += step) {
     const long long row = r0 + sub;
     const bool live = row < a.rows;
-    const Row cur = in;
+    if (kStages > 1) {
+      const int next = stage == 0 ? kStages - 1 : stage - 1;
+      fetch(next, row + (kStages - 1) * step);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     f32x2 ss = 0, dot = 0, xx = 0;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       f32x2 r[4], dy[4];
-      pairs(cur.r[i], r);
-      pairs(cur.y[i], dy);
+      get(stage, 0, i, r);
+      get(stage, 1, i, dy);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         ss = fma2(r[j], r[j], ss);
         dot = fma2(mul2(wp[i][j], dy[j]), r[j], dot);
       }
     }
-    fetch(row + step);
     float s0 = sum2(ss), s1 = sum2(dot);
     row_sum<TPR>(s0, s1, red[0]);
     const float ir = rsqrtf(s0 / n + a.eps);
     const f32x2 ir2 = both(ir), mr = both(-ir * ir * (s1 / n));
     dot = 0;
-    f32x2 dr[VEC][4], sg[VEC][4];
+    f32x2 dr[VEC][4], sg[VEC][4], x[VEC][4];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int c = lane + i * TPR;
-      f32x2 r[4], dy[4], x[4], g[4];
-      pairs(cur.r[i], r);
-      pairs(cur.y[i], dy);
-      pairs(cur.x[i], x);
-      pairs(cur.g[i], g);
-      pairs(cur.d[i], dr[i]);
+      f32x2 r[4], dy[4], g[4];
+      get(stage, 0, i, r);
+      get(stage, 1, i, dy);
+      get(stage, 2, i, dr[i]);
+      get(stage, 3, i, x[i]);
+      get(stage, 4, i, g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         dp[i][j] = fma2(dy[j], mul2(r[j], ir2), dp[i][j]);
         dr[i][j] = fma2(ir2, fma2(wp[i][j], dy[j], mul2(r[j], mr)), dr[i][j]);
         sg[i][j] = a.gate ? sigmoid2(g[j]) : both(1.f);
-        xx = fma2(x[j], x[j], xx);
-        dot = fma2(mul2(mul2(dr[i][j], ws[i][j]), sg[i][j]), x[j], dot);
+        xx = fma2(x[i][j], x[i][j], xx);
+        dot = fma2(mul2(mul2(dr[i][j], ws[i][j]), sg[i][j]), x[i][j], dot);
       }
       if (live && c < nv) store_pairs(static_cast<T*>(a.dresidual) + row * a.D + 8 * c, dr[i]);
     }
+    if (kStages == 1) fetch(0, row + step);
     s0 = sum2(xx);
     s1 = sum2(dot);
     row_sum<TPR>(s0, s1, red[1]);
@@ -271,19 +319,19 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int c = lane + i * TPR;
-      f32x2 x[4], dx[4], dg[4];
-      pairs(cur.x[i], x);
+      f32x2 dx[4], dg[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x2 nx = mul2(x[j], ix2), d = mul2(dr[i][j], sg[i][j]), t = mul2(d, ws[i][j]);
+        const f32x2 nx = mul2(x[i][j], ix2), d = mul2(dr[i][j], sg[i][j]), t = mul2(d, ws[i][j]);
         dm[i][j] = fma2(d, nx, dm[i][j]);
         dg[j] = mul2(mul2(t, nx), fma2(sg[i][j], both(-1.f), both(1.f)));
-        dx[j] = mul2(ix2, fma2(x[j], mx, t));
+        dx[j] = mul2(ix2, fma2(x[i][j], mx, t));
       }
       if (!(live && c < nv)) continue;
       store_pairs(static_cast<T*>(a.dx) + row * a.D + 8 * c, dx);
       if (a.gate) store_pairs(static_cast<T*>(a.dgate) + row * a.D + 8 * c, dg);
     }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 #pragma unroll
   for (int part = 0; part < 2; ++part)
@@ -374,7 +422,11 @@ cudaError_t bwd(const BlockNormsBwdArgs& a, cudaStream_t stream) {
   return by_width<1>(a.D, [&](auto tpr, auto vec) {
     constexpr int kThreads = threads<tpr>(), kRows = kThreads / tpr;
     const int grid = ctas(a.rows, kRows, kBwdCtas * 256 / kThreads);
-    block_norms_bwd_kernel<T, tpr, vec><<<grid, kThreads, 0, stream>>>(a);
+    constexpr int kBytes = stages<vec>() * kInputs * vec * 8 * sizeof(T) * kThreads;
+    const cudaError_t err = cudaFuncSetAttribute(block_norms_bwd_kernel<T, tpr, vec>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (err != cudaSuccess) return err;
+    block_norms_bwd_kernel<T, tpr, vec><<<grid, kThreads, kBytes, stream>>>(a);
     block_weights_kernel<<<(2 * a.D + 31) / 32, 1024, 0, stream>>>(a, grid);
     return cudaGetLastError();
   });
