@@ -285,13 +285,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
 
 // ------------------------------------------------------------------ gradients
 
-constexpr int kWarps = 4;
-constexpr int kBwdThreads = 32 * kWarps;
 constexpr int kTile = kSpaceTile;
 constexpr int kSub = 4;           // tokens whose decays and states are in registers
 
 template <int N>
 struct BwdLayout {
+  static constexpr int kWarps = N == 8 ? 2 : 4;      // (what shared memory has room for)
+  static constexpr int kBwdThreads = 32 * kWarps;
   static constexpr int kStateLanes = N / 4, kChannelLanes = 32 / kStateLanes;
   static constexpr int kWarpChannels = 4 * kChannelLanes, kChannels = kWarps * kWarpChannels;
   static constexpr int kOrders = kChannelLanes < 4 ? kChannelLanes : 4;   // of the states
@@ -307,20 +307,32 @@ struct BwdLayout {
 template <typename T, int N, bool Z>
 struct __align__(16) BwdShared {
   using L = BwdLayout<N>;
-  // u; u x, then q; p, then C h; sum A w, then ddt
+  static constexpr int kBwdThreads = L::kBwdThreads;
+  // u; u x, then q; p, then C h
   float u[kTile][L::kChannels], g[kTile][L::kChannels], p[kTile][L::kChannels];
-  float r[kTile][L::kChannels];
   float b[L::kOrders][L::kOrder], c[L::kOrders][L::kOrder];
-  ulonglong2 h[kTile / kSub][4][kBwdThreads];
-  float dbc[kWarps][kTile][2 * N];
+  // States kept every kSub tokens, a thread's in its own places. Once a warp has taken those of
+  // kSub tokens back into registers, its places there (512 bytes for each of the tokens) hold
+  // the tokens' sums: 2 N of dB and dC, then, where there is room, sum A w (then ddt) of the
+  // warp's channels.
+  ulonglong2 h[kTile / kSub][kSub][kBwdThreads];
+  float r_apart[N == 64 ? kTile : 1][L::kChannels];
   float px[kBwdThreads][8];           // dskip of a thread's 8 channels
-  // copies for the next tile: inputs, and the kept states
+  // copies: two tiles' inputs, and the next tile's first states
   float4 kept[4][kBwdThreads];
-  T x[kTile][L::kChannels], dt[kTile][L::kChannels], dy[kTile][L::kChannels];
-  T z[Z ? kTile : 1][L::kChannels];
+  T x[2][kTile][L::kChannels], dt[2][kTile][L::kChannels], dy[2][kTile][L::kChannels];
+  T z[2][Z ? kTile : 1][L::kChannels];
   T bc[2][kTile][N];
   float bias[L::kChannels], skip[L::kChannels];
   unsigned starts[4];
+
+  __device__ __forceinline__ float* dbc(int warp, int t) {
+    return reinterpret_cast<float*>(&h[t / kSub][t % kSub][32 * warp]);
+  }
+  __device__ __forceinline__ float* r(int t, int c) {
+    if (N == 64) return &r_apart[t][c];
+    return dbc(c / L::kWarpChannels, t) + 2 * N + c % L::kWarpChannels;
+  }
 };
 
 // v[i] -> v[i ^ mask]
@@ -364,19 +376,11 @@ __device__ __forceinline__ void from_items(const Items& in, int order, float4 (&
 __device__ __forceinline__ float pass(float x, int lanes) {
   return __shfl_xor_sync(0xffffffffu, x, lanes);
 }
-// 8 elements read from global memory as pairs.
-template <typename T>
-__device__ __forceinline__ void raw_pairs(const Raw8<T>& r, f32x2 (&x)[4]) {
-  float f[8];
-  r.get(f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = pair(f[2 * i], f[2 * i + 1]);
-}
-
 template <typename T, int N, bool Z>
-__global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 : 1)
     space_bwd_kernel(const SpaceArgs a, const SpaceSplit sp) {
   using L = BwdLayout<N>;
+  constexpr int kWarps = L::kWarps, kBwdThreads = L::kBwdThreads;
   extern __shared__ __align__(16) unsigned char raw_smem[];
   BwdShared<T, N, Z>& sm = *reinterpret_cast<BwdShared<T, N, Z>*>(raw_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -435,17 +439,17 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
   float ksum[4] = {0.f, 0.f, 0.f, 0.f};      // sums of u up to the tile, of this thread's channels
   bool kclear = false;
   // copies a tile's inputs and the state entering it
-  auto fetch = [&](int t0) {
+  auto fetch = [&](int t0, int buf) {
     const int nt = min(kTile, t_end - t0);
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
       const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
       if (v < L::kVecs && t < nt && ch.first + d < ch.end) {
         const long long row = row0 + t0 + t;
-        copy8(&sm.x[t][d], static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
-        copy8(&sm.dt[t][d], static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
-        copy8(&sm.dy[t][d], static_cast<const T*>(a.dy) + row * a.D + ch.first + d);
-        if (Z) copy8(&sm.z[t][d], static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
+        copy8(&sm.x[buf][t][d], static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
+        copy8(&sm.dt[buf][t][d], static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
+        copy8(&sm.dy[buf][t][d], static_cast<const T*>(a.dy) + row * a.D + ch.first + d);
+        if (Z) copy8(&sm.z[buf][Z ? t : 0][d], static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
       }
     }
 #pragma unroll
@@ -473,9 +477,10 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
   };
 
   const int t_last = (t_end - 1) / kTile * kTile;
-  fetch(t_last);
+  fetch(t_last, 0);
   __syncthreads();
-  for (int t0 = t_last; t0 >= t_begin; t0 -= kTile) {
+  int buf = 0;
+  for (int t0 = t_last; t0 >= t_begin; t0 -= kTile, buf ^= 1) {
     const int nt = min(kTile, t_end - t0);
     copies_done();
     // u, u x and p of what this thread has copied
@@ -488,10 +493,10 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
       for (int j = 0; j < 4; ++j) x[j] = u[j] = p[j] = 0;
       if (t < nt && ch.first + d < ch.end) {
         f32x2 bias[4], z[4];
-        read8(&sm.x[t][d], x);
-        read8(&sm.dt[t][d], u);
-        read8(&sm.dy[t][d], p);
-        if (Z) read8(&sm.z[Z ? t : 0][d], z);
+        read8(&sm.x[buf][t][d], x);
+        read8(&sm.dt[buf][t][d], u);
+        read8(&sm.dy[buf][t][d], p);
+        if (Z) read8(&sm.z[buf][Z ? t : 0][d], z);
         read8(&sm.bias[d], bias);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -548,7 +553,7 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
       }
     }
     __syncthreads();
-    if (t0 > t_begin) fetch(t0 - kTile);
+    if (t0 > t_begin) fetch(t0 - kTile, buf ^ 1);
     const unsigned starts = sm.starts[0];
 
     // forward through the tile, a state kept every kSub tokens
@@ -657,26 +662,26 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
             for (int j = 0; j < 4; ++j) E[p][j] = 0;
         }
         // over the state lanes: by halves over the 4 channels, then whole
-        auto over_states = [&](const f32x2 (&v)[2], float* out) {
+        auto over_states = [&](const f32x2 (&v)[2], float* out) {      // out: of channel cbase
           float lo, hi, lo1, hi1;
           split(v[0], lo, hi);
           split(v[1], lo1, hi1);
           lo += pass(lo1, 1);
           hi += pass(hi1, 1);
           if constexpr (L::kStateLanes == 2) {
-            *reinterpret_cast<float2*>(out + c0) = make_float2(lo, hi);
+            *reinterpret_cast<float2*>(out + 2 * swap) = make_float2(lo, hi);
           } else {
             const bool up = sl & 2;
             float keep = up ? hi : lo;
             keep += pass(up ? lo : hi, 2);
             if constexpr (L::kStateLanes >= 8) keep += pass(keep, 4);
             if constexpr (L::kStateLanes >= 16) keep += pass(keep, 8);
-            if (sl < 4) out[c0 + up] = keep;
+            if (sl < 4) out[2 * swap + up] = keep;
           }
         };
-        over_states(q, sm.g[t]);
-        over_states(r, sm.r[t]);
-        if (Z) over_states(y, sm.p[t]);
+        over_states(q, &sm.g[t][cbase]);
+        over_states(r, sm.r(t, cbase));
+        if (Z) over_states(y, &sm.p[t][cbase]);
         // over the channel lanes
         float vb[4], vc[4];
 #pragma unroll
@@ -689,7 +694,7 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
         vb[2] += pass(vb[3], kStep);
         vc[0] += pass(vc[1], kStep);
         vc[2] += pass(vc[3], kStep);
-        float* out = sm.dbc[warp][t];
+        float* out = sm.dbc(warp, t);
         if constexpr (L::kChannelLanes >= 4) {
           vb[0] += pass(vb[2], 2 * kStep);
           vc[0] += pass(vc[2], 2 * kStep);
@@ -713,18 +718,7 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
       }
     }
 
-    // the tile's outputs; the inputs once more, as the next tile's are on their way
-    Raw8<T> rx[L::kPer], rdt[L::kPer], ry[L::kPer], rz[L::kPer];
-#pragma unroll
-    for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
-      if (v >= L::kVecs || t >= nt || ch.first + d >= ch.end) continue;
-      const long long row = row0 + t0 + t;
-      rx[i].load(static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
-      rdt[i].load(static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
-      ry[i].load(static_cast<const T*>(a.dy) + row * a.D + ch.first + d);
-      if (Z) rz[i].load(static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
-    }
+    // the tile's outputs
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
@@ -733,13 +727,13 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
       const size_t out = static_cast<size_t>(row0 + t0 + t) * a.D + ch.first + d;
       const f32x2 one = both(1.f), minus = both(-1.f);
       f32x2 x[4], q[4], w[4], p[4], skip[4];
-      raw_pairs(rx[i], x);
-      raw_pairs(ry[i], p);
+      read8(&sm.x[buf][t][d], x);
+      read8(&sm.dy[buf][t][d], p);
       read8(&sm.g[t][d], q);
       read8(&sm.skip[d], skip);
       if (Z) {
         f32x2 z[4], y[4], dz[4];
-        raw_pairs(rz[i], z);
+        read8(&sm.z[buf][Z ? t : 0][d], z);
         read8(&sm.p[t][d], y);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -752,10 +746,10 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
         store_pairs(static_cast<T*>(a.dz) + out, dz);
       }
       f32x2 bias[4], u[4], dt[4], dx[4];
-      raw_pairs(rdt[i], dt);
+      read8(&sm.dt[buf][t][d], dt);
       read8(&sm.bias[d], bias);
       read8(&sm.u[t][d], u);
-      read8(&sm.r[t][d], w);
+      read8(sm.r(t, d), w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         dx[j] = mul2(u[j], q[j]);
@@ -766,7 +760,7 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
       }
       store_pairs(static_cast<T*>(a.dx) + out, dx);
       store_pairs(static_cast<T*>(a.ddt) + out, w);
-      if (a.dt_bias) write8(&sm.r[t][d], w);
+      if (a.dt_bias) write8(sm.r(t, d), w);
       if (a.skip) {
         f32x2 sum[4];
         read8(sm.px[tid], sum);
@@ -778,10 +772,10 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
     const int blocks = gridDim.x / a.G, block = blockIdx.x % blocks;
     for (int i = tid; i < nt * N / 2; i += kBwdThreads) {      // four sums each
       const int t = i / (N / 2), j = i % (N / 2) * 4;
-      float4 s = *reinterpret_cast<const float4*>(&sm.dbc[0][t][j]);
+      float4 s = *reinterpret_cast<const float4*>(sm.dbc(0, t) + j);
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) {
-        const float4 v = *reinterpret_cast<const float4*>(&sm.dbc[w][t][j]);
+        const float4 v = *reinterpret_cast<const float4*>(sm.dbc(w, t) + j);
         s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
       }
       *reinterpret_cast<float4*>(
@@ -794,7 +788,7 @@ __global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1)
       for (int i = 0; i < L::kSums; ++i) {
         const int d = tid + i * kBwdThreads;
         if (d < L::kChannels)
-          for (int t = 0; t < nt; ++t) dbias[i] += sm.r[t][d];
+          for (int t = 0; t < nt; ++t) dbias[i] += *sm.r(t, d);
       }
     }
   }
@@ -874,7 +868,7 @@ int blocks_of(const SpaceArgs& a, int channels) {
 
 }  // namespace
 
-int space_bwd_channels(int N) { return kWarps * 4 * 32 / (N / 4); }
+int space_bwd_channels(int N) { return (N == 8 ? 2 : 4) * 4 * 32 / (N / 4); }
 
 cudaError_t launch_space_bwd_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                     cudaStream_t stream) {
@@ -900,8 +894,8 @@ cudaError_t launch_space_bwd(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
       constexpr int kBytes = static_cast<int>(sizeof(BwdShared<decltype(t), n, gated>));
       const cudaError_t e = allow_shared<kern, kBytes>();
       if (e != cudaSuccess) return e;
-      kern<<<dim3(a.G * blocks_of(a, BwdLayout<n>::kChannels), sp.segments, a.B), kBwdThreads,
-             kBytes, stream>>>(a, sp);
+      kern<<<dim3(a.G * blocks_of(a, BwdLayout<n>::kChannels), sp.segments, a.B),
+             BwdLayout<n>::kBwdThreads, kBytes, stream>>>(a, sp);
       return cudaGetLastError();
     };
     return a.z ? run(std::true_type{}) : run(std::false_type{});
