@@ -587,8 +587,9 @@ __global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 
             h[p][j] = fma2(g[p], b2[j], mul2(exp2_pair(mul2(A2[p][j], u[p])), h[p][j]));
       }
     }
-    // and back
-    for (int s = subs - 1; s >= 0; --s) {
+    // and back; MARKED: documents may start in the tile (else no branch parts the tokens)
+    auto back = [&](int s, auto marked) {
+      constexpr bool MARKED = decltype(marked)::value;
       Items da[kSub], ah[kSub];     // decays, decayed states
 #pragma unroll
       for (int p = 0; p < 2; ++p)
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 
             ah[k][p][j] = mul2(da[k][p][j], h[p][j]);
             h[p][j] = fma2(g[p], b2[j], ah[k][p][j]);
           }
-        if ((starts >> t) & 1) {
+        if (MARKED && ((starts >> t) & 1)) {
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 
             E[p][j] = mul2(da[k][p][j], e);
           }
         }
-        if ((starts >> t) & 1) {
+        if (MARKED && ((starts >> t) & 1)) {
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -716,7 +717,11 @@ __global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 
           out[N + n0 + (2 ^ nx)] = vc[2];
         }
       }
-    }
+    };
+    if (starts == 0)
+      for (int s = subs - 1; s >= 0; --s) back(s, std::false_type{});
+    else
+      for (int s = subs - 1; s >= 0; --s) back(s, std::true_type{});
 
     // the tile's outputs
     __syncthreads();
