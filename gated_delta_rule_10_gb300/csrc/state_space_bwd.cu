@@ -556,19 +556,21 @@ __global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 
     if (t0 > t_begin) fetch(t0 - kTile, buf ^ 1);
     const unsigned starts = sm.starts[0];
 
-    // forward through the tile, a state kept every kSub tokens
+    // forward through the tile, a state kept every kSub tokens; MARKED: documents may start in
+    // the tile (else no branch parts the tokens)
     const int subs = (nt + kSub - 1) / kSub;
-    for (int s = 0; s < subs; ++s) {
+    auto forth = [&](int s, auto marked) {
+      constexpr bool MARKED = decltype(marked)::value;
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           sm.h[s][2 * p + j][tid] = make_ulonglong2(h[p][2 * j], h[p][2 * j + 1]);
-      if (s + 1 == subs) break;
+      if (s + 1 == subs) return;
 #pragma unroll
       for (int k = 0; k < kSub; ++k) {
         const int t = s * kSub + k;
-        if ((starts >> t) & 1) {
+        if (MARKED && ((starts >> t) & 1)) {
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -586,8 +588,12 @@ __global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 
           for (int j = 0; j < 4; ++j)
             h[p][j] = fma2(g[p], b2[j], mul2(exp2_pair(mul2(A2[p][j], u[p])), h[p][j]));
       }
-    }
-    // and back; MARKED: documents may start in the tile (else no branch parts the tokens)
+    };
+    if (starts == 0)
+      for (int s = 0; s < subs; ++s) forth(s, std::false_type{});
+    else
+      for (int s = 0; s < subs; ++s) forth(s, std::true_type{});
+    // and back
     auto back = [&](int s, auto marked) {
       constexpr bool MARKED = decltype(marked)::value;
       Items da[kSub], ah[kSub];     // decays, decayed states
