@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
     const unsigned starts = sm.starts[0];
     if (starts == 0 && nt == L::kTile) {
       if (CUT && !cleared) {
-#pragma unroll 2
+#pragma unroll 4
         for (int t = 0; t < L::kTile; ++t) token(t, false, true);
       } else {
 #pragma unroll 4
@@ -829,35 +829,38 @@ __global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 
   }
 }
 
-// Adds up the partial sums: dBm and dCm over the CTAs' channels, dA, dskip and ddt_bias over
-// batch rows and segments.
+// Adds up the partial sums, four neighbouring ones a thread: dBm and dCm over the CTAs'
+// channels, dA, dskip and ddt_bias over batch rows and segments.
+__device__ __forceinline__ float4 add_rows(const float* from, long long stride, int rows) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < rows; ++k) {
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(from + k * stride));
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  return s;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) space_sums_kernel(const SpaceArgs a, const SpaceSplit sp) {
   const long long bc = static_cast<long long>(a.B) * a.T * a.G * 2 * a.N;
   const long long da = static_cast<long long>(a.D) * a.N;
   const int parts = a.B * sp.segments;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < bc + da + 2 * a.D;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    float s = 0.f;
+  for (long long i = 4 * (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x);
+       i < bc + da + 2 * a.D; i += 4LL * gridDim.x * 256) {
     if (i < bc) {
-#pragma unroll 4
-      for (int k = 0; k < sp.blocks; ++k) s += sp.bc_part[k * bc + i];
+      const float4 s = add_rows(sp.bc_part + i, bc, sp.blocks);
       const int n = static_cast<int>(i % a.N), which = static_cast<int>(i / a.N % 2);
-      const long long at = i / (2 * a.N) * a.N + n;
-      static_cast<T*>(which ? a.dCm : a.dBm)[at] = static_cast<T>(s);
+      T* out = static_cast<T*>(which ? a.dCm : a.dBm) + i / (2 * a.N) * a.N + n;
+      store2(out, s.x, s.y);
+      store2(out + 2, s.z, s.w);
     } else if (i < bc + da) {
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) s += sp.dA_part[k * da + i - bc];
-      a.dA[i - bc] = s;
+      *reinterpret_cast<float4*>(a.dA + i - bc) = add_rows(sp.dA_part + i - bc, da, parts);
     } else {
       const long long j = i - bc - da;
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) s += sp.d_part[k * 2LL * a.D + j];
-      if (j < a.D) {
-        if (a.skip) a.dskip[j] = s;
-      } else if (a.dt_bias) {
-        a.ddt_bias[j - a.D] = s;
-      }
+      float* out = j < a.D ? (a.skip ? a.dskip + j : nullptr)
+                           : (a.dt_bias ? a.ddt_bias + j - a.D : nullptr);
+      if (out) *reinterpret_cast<float4*>(out) = add_rows(sp.d_part + j, 2LL * a.D, parts);
     }
   }
 }
@@ -914,7 +917,7 @@ cudaError_t launch_space_bwd(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
   if (err != cudaSuccess) return err;
   const long long n = static_cast<long long>(a.B) * a.T * a.G * 2 * a.N +
                       static_cast<long long>(a.D) * (a.N + 2);
-  const long long want = (n + 255) / 256;
+  const long long want = (n / 4 + 255) / 256;      // n is a multiple of 8
   const unsigned grid = static_cast<unsigned>(want < 152 * 32 ? want : 152 * 32);
   if (f32)
     space_sums_kernel<float><<<grid, 256, 0, stream>>>(a, sp);
