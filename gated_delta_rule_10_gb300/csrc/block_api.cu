@@ -2,6 +2,7 @@
 // convolution, the state space recurrence and the norms after and before a block.
 // Argument checks and kernel dispatch; nothing here allocates device memory or
 // synchronises.
+#include <algorithm>
 #include <cmath>
 
 #include "api_util.h"
@@ -89,16 +90,18 @@ double waves(long long n, int most, double first, double next) {
 // Forward: uncut, a CTA has half the channels, and needs no other launch; a cut costs a walk
 // over all segments but the last for their end states (0.65 of the other walk's time), and the
 // chain. Times of a token (us, bf16): uncut 0.084 and 0.062 (a CTA alone on its SM; a second
-// one beside it), cut 0.17 and 0.066, and a third of a tile for a CTA's start. (4 x 4096 x
-// 4096 channels x 16: 598 us uncut, 565 in 32 segments, 590 in 13; 1 x 65536 x 2048: 5510
-// uncut, 1133 in 38, 1867 in 14.)
+// one beside it), cut 0.17 and 0.066, and a third of a tile for a CTA's start; 3% more where
+// all CTAs start together and stage their tiles in step. (4 x 4096 x 4096 channels x 16: 598
+// us uncut, 487 in 8 segments, 558 in 7; 1 x 65536 x 2048: 5510 uncut, 1158 in 19 segments,
+// 985 in 38, 958 in 114.)
 // The backward walks forward for its kept states anyway; a segment costs a CTA's start, 0.7
-// tiles (4 x 4096 x 2048 x 16: 1132 us in 4 segments, 988 in 14, 959 in 19).
+// tiles (4 x 4096 x 2048 x 16: 955 us in 4 segments, 839 in 14, 814 in 19).
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
   const int tile = backward ? gdr::kSpaceTile : 32;
   const int tiles = (s->T + tile - 1) / tile, each = s->D / s->G;
   auto blocks = [&](int channels) { return (each + channels - 1) / channels; };
-  sp->blocks = blocks(backward ? gdr::space_bwd_channels(s->N) : gdr::space_channels(s->N, false));
+  sp->blocks = blocks(backward ? gdr::space_bwd_channels(s->N, s->dtype == GDR_F32)
+                               : gdr::space_channels(s->N, false));
   const long long rows = static_cast<long long>(s->B) * s->G, ctas = rows * sp->blocks;
   double best = 0.0;
   int per = tiles;
@@ -111,7 +114,8 @@ void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
       cost = waves(rows * blocks(gdr::space_channels(s->N, true)), 2, 0.084, 0.062) * s->T;
     else
       cost = (waves(ctas * segments, 4, 0.17, 0.066) +
-              0.65 * waves(ctas * (segments - 1), 5, 0.17, 0.066)) * (len + 0.3) * tile + 25.0;
+              0.65 * waves(ctas * (segments - 1), 5, 0.17, 0.066)) * (len + 0.3) * tile *
+                 (1.0 + 0.03 * std::min(1.0, 4.0 * kSms / (ctas * segments))) + 25.0;
     if (n == 1 || cost < best) {
       best = cost;
       per = len;
@@ -177,7 +181,8 @@ gdr_status gdr_short_conv_bwd_workspace(const gdr_conv_shape* shape, size_t* byt
   const gdr_status st = check_conv(shape, false);
   if (st != GDR_OK) return st;
   if (!bytes) return GDR_ERR_INVALID_ARG;
-  *bytes = gdr::short_conv_bwd_workspace_bytes(shape->B, shape->T, shape->D, shape->K);
+  *bytes = gdr::short_conv_bwd_workspace_bytes(shape->B, shape->T, shape->D, shape->K,
+                                               shape->dtype == GDR_F32);
   return GDR_OK;
 }
 
@@ -193,7 +198,8 @@ gdr_status gdr_short_conv_bwd(const gdr_conv_shape* shape, const void* x, const 
       !aligned(dbias, 16) || !aligned(dstate, 16) || (dstate && dstate == dstate_out))
     return GDR_ERR_INVALID_ARG;
   st = check_workspace(workspace, ws_bytes, gdr::short_conv_bwd_workspace_bytes(
-                                                shape->B, shape->T, shape->D, shape->K));
+                                                shape->B, shape->T, shape->D, shape->K,
+                                                shape->dtype == GDR_F32));
   if (st != GDR_OK) return st;
   gdr::ConvArgs a = conv_args(shape);
   a.x = x; a.weight = weight; a.bias = bias; a.starts = starts; a.state = state;

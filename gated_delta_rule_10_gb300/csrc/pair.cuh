@@ -65,11 +65,6 @@ __device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
   split(add2(both(1.f), exp2_pair(mul2(x, both(-kLog2e)))), lo, hi);
   return pair(rcp_fast(lo), rcp_fast(hi));
 }
-// x sigmoid(x) and its slope
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
-__device__ __forceinline__ float silu_slope(float x) {
-  const float s = sigmoid(x);
-  return s * fmaf(x, 1.f - s, 1.f);
-}
 
 }  // namespace gdr

@@ -270,10 +270,12 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
 constexpr int kRuns = 4;
 constexpr int kBwdThreads = 32 * kRuns;
 constexpr int kBwdBatch = 4;
+// CTAs of an SM, which registers bound
+constexpr int bwd_ctas(int K, bool f32) { return f32 && K > 2 ? 3 : 4; }
 constexpr int kStages = 3;         // batches on their way or in use (6 leave fewer CTAs: 159 us)
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(kBwdThreads, bwd_ctas(K, sizeof(T) == 4))
     short_conv_bwd_kernel(const ConvArgs a, int run, int groups, int slices) {
   constexpr int V = 4, H = V / 2;
   extern __shared__ __align__(16) unsigned char raw_smem[];
@@ -525,12 +527,13 @@ cudaError_t by_taps(int K, bool f32, F f) {
 // was with two larger CTAs an SM: 107 us with runs of 74 in 2.95 waves, 115 with 64 in 3.4,
 // 130 with 32).
 int bwd_groups(int T, int run) { return (T + kRuns * run - 1) / (kRuns * run); }
-int bwd_run(int B, int T, int D) {
+int bwd_run(int B, int T, int D, int K, bool f32) {
+  const int ctas = bwd_ctas(K, f32) * 152;
   const long long slices = static_cast<long long>((D + 127) / 128) * B;
   int best = 128;                       // multiples of 4: see four_starts
   long long least = 0;
   for (int run = 128; run >= 8; run -= 4) {
-    const long long waves = (slices * bwd_groups(T, run) + 4 * 152 - 1) / (4 * 152);
+    const long long waves = (slices * bwd_groups(T, run) + ctas - 1) / ctas;
     const long long cost = waves * (run + 6);
     if (run == 128 || cost < least) {
       least = cost;
@@ -542,8 +545,9 @@ int bwd_run(int B, int T, int D) {
 
 }  // namespace
 
-size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int K) {
-  return static_cast<size_t>(B) * bwd_groups(T, bwd_run(B, T, D)) * (K + 1) * D * sizeof(float);
+size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int K, bool f32) {
+  return static_cast<size_t>(B) * bwd_groups(T, bwd_run(B, T, D, K, f32)) * (K + 1) * D *
+         sizeof(float);
 }
 
 cudaError_t launch_short_conv(const ConvArgs& a, bool f32, cudaStream_t stream) {
@@ -562,7 +566,8 @@ cudaError_t launch_short_conv(const ConvArgs& a, bool f32, cudaStream_t stream) 
 }
 
 cudaError_t launch_short_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t stream) {
-  const int run = bwd_run(a.B, a.T, a.D), groups = bwd_groups(a.T, run), slices = (a.D + 127) / 128;
+  const int run = bwd_run(a.B, a.T, a.D, a.K, f32), groups = bwd_groups(a.T, run);
+  const int slices = (a.D + 127) / 128;
   const long long grid = static_cast<long long>(slices) * a.B * groups;
   if (grid > 2147483647LL) return cudaErrorInvalidValue;
   return by_taps(a.K, f32, [&](auto t, auto k) {

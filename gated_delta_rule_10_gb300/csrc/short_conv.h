@@ -17,7 +17,7 @@ struct ConvArgs {
   bool silu;
   long long xs;
 };
-size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int K);
+size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int K, bool f32);
 cudaError_t launch_short_conv(const ConvArgs& a, bool f32, cudaStream_t stream);
 cudaError_t launch_short_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t stream);
 cudaError_t launch_short_conv_step(const ConvArgs& a, bool f32, cudaStream_t stream);

@@ -44,7 +44,7 @@ struct SpaceSplit {
 };
 
 int space_channels(int N, bool narrow);   // channels of a CTA: forward, backward
-int space_bwd_channels(int N);
+int space_bwd_channels(int N, bool f32);
 cudaError_t launch_space_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                 cudaStream_t stream);
 cudaError_t launch_space_chain(const SpaceArgs& a, const SpaceSplit& sp, bool backward,

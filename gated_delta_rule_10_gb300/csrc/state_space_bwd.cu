@@ -12,10 +12,11 @@
 // - Gradients, tile by tile backward: a tile's states are computed again from its first one,
 //   kept every 4 tokens in shared memory, then by 4 tokens in registers with their decays.
 // Three exponentials and about 22 multiply-adds for each (token, channel, state) in all. The
-// second launch is 74% of the time (4 x 4096 x 2048 channels x 16 bf16: 905 us in all): two
-// warps a scheduler, which 255 registers a thread and 111 KB of shared memory a CTA leave,
-// issue 47% of the time. With half the states a thread (three CTAs an SM) it issues 58% of the
-// time but 30% more, and takes as long; so does half the tokens in registers.
+// second launch is 73% of the time (4 x 4096 x 2048 channels x 16 bf16: 804 us in all): two
+// warps a scheduler, which 252 registers a thread and 111 KB of shared memory a CTA leave,
+// issue 50% of the time. With half the states a thread (three CTAs an SM) it issues 58% of the
+// time but 30% more, and takes as long; so does half the tokens in registers. Tiles without a
+// document's start take a walk without branches (851 -> 831 us).
 //
 // A thread has 4 states of 4 channels (pairs of channels share an instruction), so that the
 // sums over channels (dB, dC) and those over states (q, sum A w, C h) each start inside a
@@ -288,9 +289,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
 constexpr int kTile = kSpaceTile;
 constexpr int kSub = 4;           // tokens whose decays and states are in registers
 
-template <int N>
+// Warps of a CTA: what lets shared memory hold 8 warps an SM, or as many as it can.
+constexpr int bwd_warps(int N, bool f32) {
+  if (N == 8) return f32 ? 1 : 2;      // (fp32: 641 us for 4 x 4096 x 1024 with two, 524)
+  return 4;
+}
+
+template <int N, bool F32>
 struct BwdLayout {
-  static constexpr int kWarps = N == 8 ? 2 : 4;      // (what shared memory has room for)
+  static constexpr int kWarps = bwd_warps(N, F32);
   static constexpr int kBwdThreads = 32 * kWarps;
   static constexpr int kStateLanes = N / 4, kChannelLanes = 32 / kStateLanes;
   static constexpr int kWarpChannels = 4 * kChannelLanes, kChannels = kWarps * kWarpChannels;
@@ -306,7 +313,7 @@ struct BwdLayout {
 
 template <typename T, int N, bool Z>
 struct __align__(16) BwdShared {
-  using L = BwdLayout<N>;
+  using L = BwdLayout<N, sizeof(T) == 4>;
   static constexpr int kBwdThreads = L::kBwdThreads;
   // u; u x, then q; p, then C h
   float u[kTile][L::kChannels], g[kTile][L::kChannels], p[kTile][L::kChannels];
@@ -377,9 +384,9 @@ __device__ __forceinline__ float pass(float x, int lanes) {
   return __shfl_xor_sync(0xffffffffu, x, lanes);
 }
 template <typename T, int N, bool Z>
-__global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
     space_bwd_kernel(const SpaceArgs a, const SpaceSplit sp) {
-  using L = BwdLayout<N>;
+  using L = BwdLayout<N, sizeof(T) == 4>;
   constexpr int kWarps = L::kWarps, kBwdThreads = L::kBwdThreads;
   extern __shared__ __align__(16) unsigned char raw_smem[];
   BwdShared<T, N, Z>& sm = *reinterpret_cast<BwdShared<T, N, Z>*>(raw_smem);
@@ -829,39 +836,54 @@ __global__ void __launch_bounds__(BwdLayout<N>::kBwdThreads, sizeof(T) == 2 ? 2 
   }
 }
 
-// Adds up the partial sums, four neighbouring ones a thread: dBm and dCm over the CTAs'
-// channels, dA, dskip and ddt_bias over batch rows and segments.
-__device__ __forceinline__ float4 add_rows(const float* from, long long stride, int rows) {
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = 0; k < rows; ++k) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(from + k * stride));
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-  }
-  return s;
+// Adds up the partial sums in a fixed order, four neighbouring ones a thread. The first CTAs
+// take dA, dskip and ddt_bias, over batch rows and segments: 128 of them a CTA, every eighth row
+// a warp (all rows in one thread's turn: 20 us for 4 x 4096 x 2048 x 16, two thirds of it these
+// few threads' wait). The others take dBm and dCm, over the CTAs' channels.
+constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) space_sums_kernel(const SpaceArgs a, const SpaceSplit sp) {
-  const long long bc = static_cast<long long>(a.B) * a.T * a.G * 2 * a.N;
+__global__ void __launch_bounds__(kSumThreads)
+    space_sums_kernel(const SpaceArgs a, const SpaceSplit sp, int first) {
+  __shared__ float4 part[kSumWarps][32];
   const long long da = static_cast<long long>(a.D) * a.N;
-  const int parts = a.B * sp.segments;
-  for (long long i = 4 * (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x);
-       i < bc + da + 2 * a.D; i += 4LL * gridDim.x * 256) {
-    if (i < bc) {
-      const float4 s = add_rows(sp.bc_part + i, bc, sp.blocks);
-      const int n = static_cast<int>(i % a.N), which = static_cast<int>(i / a.N % 2);
-      T* out = static_cast<T*>(which ? a.dCm : a.dBm) + i / (2 * a.N) * a.N + n;
-      store2(out, s.x, s.y);
-      store2(out + 2, s.z, s.w);
-    } else if (i < bc + da) {
-      *reinterpret_cast<float4*>(a.dA + i - bc) = add_rows(sp.dA_part + i - bc, da, parts);
-    } else {
-      const long long j = i - bc - da;
-      float* out = j < a.D ? (a.skip ? a.dskip + j : nullptr)
+  if (static_cast<int>(blockIdx.x) < first) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = a.B * sp.segments;
+    const long long i = 4 * (32LL * blockIdx.x + lane), j = i - da;
+    const bool live = j < 2 * a.D;
+    const float* from = j < 0 ? sp.dA_part + i : sp.d_part + j;
+    const long long stride = j < 0 ? da : 2LL * a.D;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live)
+#pragma unroll 8
+      for (int k = warp; k < rows; k += kSumWarps)
+        s = add4(s, __ldcs(reinterpret_cast<const float4*>(from + k * stride)));
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp > 0 || !live) return;
+#pragma unroll
+    for (int w = 1; w < kSumWarps; ++w) s = add4(s, part[w][lane]);
+    float* out = j < 0       ? a.dA + i
+                 : j < a.D ? (a.skip ? a.dskip + j : nullptr)
                            : (a.dt_bias ? a.ddt_bias + j - a.D : nullptr);
-      if (out) *reinterpret_cast<float4*>(out) = add_rows(sp.d_part + j, 2LL * a.D, parts);
-    }
+    if (out) *reinterpret_cast<float4*>(out) = s;
+    return;
+  }
+  const long long bc = static_cast<long long>(a.B) * a.T * a.G * 2 * a.N;
+  for (long long i = 4 * (static_cast<long long>(blockIdx.x - first) * kSumThreads + threadIdx.x);
+       i < bc; i += 4LL * (gridDim.x - first) * kSumThreads) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
+    for (int k = 0; k < sp.blocks; ++k)
+      s = add4(s, __ldcs(reinterpret_cast<const float4*>(sp.bc_part + i + k * bc)));
+    const int n = static_cast<int>(i % a.N), which = static_cast<int>(i / a.N % 2);
+    T* out = static_cast<T*>(which ? a.dCm : a.dBm) + i / (2 * a.N) * a.N + n;
+    store2(out, s.x, s.y);
+    store2(out + 2, s.z, s.w);
   }
 }
 
@@ -882,7 +904,7 @@ int blocks_of(const SpaceArgs& a, int channels) {
 
 }  // namespace
 
-int space_bwd_channels(int N) { return (N == 8 ? 2 : 4) * 4 * 32 / (N / 4); }
+int space_bwd_channels(int N, bool f32) { return bwd_warps(N, f32) * 4 * 32 / (N / 4); }
 
 cudaError_t launch_space_bwd_states(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
                                     cudaStream_t stream) {
@@ -908,21 +930,22 @@ cudaError_t launch_space_bwd(const SpaceArgs& a, const SpaceSplit& sp, bool f32,
       constexpr int kBytes = static_cast<int>(sizeof(BwdShared<decltype(t), n, gated>));
       const cudaError_t e = allow_shared<kern, kBytes>();
       if (e != cudaSuccess) return e;
-      kern<<<dim3(a.G * blocks_of(a, BwdLayout<n>::kChannels), sp.segments, a.B),
-             BwdLayout<n>::kBwdThreads, kBytes, stream>>>(a, sp);
+      using L = BwdLayout<n, sizeof(decltype(t)) == 4>;
+      kern<<<dim3(a.G * blocks_of(a, L::kChannels), sp.segments, a.B), L::kBwdThreads, kBytes,
+             stream>>>(a, sp);
       return cudaGetLastError();
     };
     return a.z ? run(std::true_type{}) : run(std::false_type{});
   });
   if (err != cudaSuccess) return err;
-  const long long n = static_cast<long long>(a.B) * a.T * a.G * 2 * a.N +
-                      static_cast<long long>(a.D) * (a.N + 2);
-  const long long want = (n / 4 + 255) / 256;      // n is a multiple of 8
-  const unsigned grid = static_cast<unsigned>(want < 152 * 32 ? want : 152 * 32);
+  const int first = static_cast<int>((static_cast<long long>(a.D) * (a.N + 2) + 127) / 128);
+  const long long want =      // the sums are a multiple of 16
+      (static_cast<long long>(a.B) * a.T * a.G * 2 * a.N / 4 + kSumThreads - 1) / kSumThreads;
+  const unsigned grid = first + static_cast<unsigned>(want < 152 * 32 ? want : 152 * 32);
   if (f32)
-    space_sums_kernel<float><<<grid, 256, 0, stream>>>(a, sp);
+    space_sums_kernel<float><<<grid, kSumThreads, 0, stream>>>(a, sp, first);
   else
-    space_sums_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, sp);
+    space_sums_kernel<__nv_bfloat16><<<grid, kSumThreads, 0, stream>>>(a, sp, first);
   return cudaGetLastError();
 }
 

@@ -816,7 +816,8 @@ gdr_status gdr_state_space_fwd(const gdr_state_space_shape* shape, const void* x
  * dskip, dz and ddt_bias are needed with skip, z and dt_bias and else not written; dh0 may be
  * NULL. dhT and dh0 may be one buffer. workspace: at least gdr_state_space_bwd_workspace()
  * bytes, 16-byte aligned (the states at every 16th token, D * N * 4 bytes each, and 8 * N
- * bytes of partial sums for each token and 2048 / N channels, among them).
+ * bytes of partial sums for each token and 2048 / N channels, 128 for N = 8 and 64 for N = 8
+ * in fp32, among them).
  * No sum uses atomics.
  */
 gdr_status gdr_state_space_bwd_workspace(const gdr_state_space_shape* shape, size_t* bytes);
