@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "gdr.h"
 
 namespace gdr {
@@ -18,6 +20,18 @@ inline gdr_status check_workspace(const void* ws, size_t have, size_t need) {
   if (need == 0) return GDR_OK;
   if (!ws || have < need) return GDR_ERR_WORKSPACE;
   return aligned(ws, 16) ? GDR_OK : GDR_ERR_INVALID_ARG;
+}
+// No output is an input's or another output's buffer (those that are there). Only equal
+// addresses are seen: callers keep the rest of what they were asked for.
+inline bool apart(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    for (const void* i : ins)
+      if (i == *o) return false;
+    for (const void* const* q = outs.begin(); q != o; ++q)
+      if (*q == *o) return false;
+  }
+  return true;
 }
 
 }  // namespace gdr

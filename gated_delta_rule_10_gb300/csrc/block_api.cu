@@ -14,6 +14,7 @@ namespace {
 
 using gdr::align256;
 using gdr::aligned;
+using gdr::apart;
 using gdr::check_workspace;
 using gdr::given16;
 using gdr::status_of;
@@ -169,7 +170,7 @@ gdr_status gdr_short_conv_fwd(const gdr_conv_shape* shape, const void* x, const 
   const gdr_status st = check_conv(shape, false);
   if (st != GDR_OK) return st;
   if (!given16(x) || !given16(weight) || !aligned(bias, 16) || !aligned(state, 16) || !given16(y) ||
-      !aligned(state_out, 16) || (state && state == state_out))
+      !aligned(state_out, 16) || !apart({y, state_out}, {x, state}))
     return GDR_ERR_INVALID_ARG;
   gdr::ConvArgs a = conv_args(shape);
   a.x = x; a.weight = weight; a.bias = bias; a.starts = starts; a.state = state;
@@ -195,12 +196,14 @@ gdr_status gdr_short_conv_bwd(const gdr_conv_shape* shape, const void* x, const 
   if (st != GDR_OK) return st;
   if (!given16(x) || !given16(weight) || !aligned(bias, 16) || !aligned(state, 16) ||
       !given16(dy) || !aligned(dstate_out, 16) || !given16(dx) || !given16(dweight) ||
-      !aligned(dbias, 16) || !aligned(dstate, 16) || (dstate && dstate == dstate_out))
+      !aligned(dbias, 16) || !aligned(dstate, 16))
     return GDR_ERR_INVALID_ARG;
   st = check_workspace(workspace, ws_bytes, gdr::short_conv_bwd_workspace_bytes(
                                                 shape->B, shape->T, shape->D, shape->K,
                                                 shape->dtype == GDR_F32));
   if (st != GDR_OK) return st;
+  if (!apart({dx, dweight, dbias, dstate}, {x, weight, bias, state, dy, dstate_out}))
+    return GDR_ERR_INVALID_ARG;
   gdr::ConvArgs a = conv_args(shape);
   a.x = x; a.weight = weight; a.bias = bias; a.starts = starts; a.state = state;
   a.dy = dy; a.dstate_out = dstate_out; a.dx = dx; a.dweight = dweight; a.dbias = dbias;
@@ -244,6 +247,8 @@ gdr_status gdr_state_space_fwd(const gdr_state_space_shape* shape, const void* x
   cut(shape, false, &sp);
   st = check_workspace(workspace, ws_bytes, lay_out(shape, false, nullptr, &sp));
   if (st != GDR_OK) return st;
+  if (!apart({y}, {x, dt, Bm, Cm, z, h0, hT}) || !apart({hT}, {x, dt, A, Bm, Cm, z}))
+    return GDR_ERR_INVALID_ARG;
   lay_out(shape, false, static_cast<char*>(workspace), &sp);
   gdr::SpaceArgs a = space_args(shape);
   a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.skip = skip; a.z = z; a.dt_bias = dt_bias;
@@ -287,6 +292,11 @@ gdr_status gdr_state_space_bwd(const gdr_state_space_shape* shape, const void* x
   cut(shape, true, &sp);
   st = check_workspace(workspace, ws_bytes, lay_out(shape, true, nullptr, &sp));
   if (st != GDR_OK) return st;
+  // (dh0 may be dhT; what is not written may be anything)
+  if (!apart({dx, ddt, dA, dBm, dCm, skip ? dskip : nullptr, z ? dz : nullptr,
+              dt_bias ? ddt_bias : nullptr, dh0},
+             {x, dt, A, Bm, Cm, skip, z, dt_bias, h0, dy}))
+    return GDR_ERR_INVALID_ARG;
   lay_out(shape, true, static_cast<char*>(workspace), &sp);
   gdr::SpaceArgs a = space_args(shape);
   a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.skip = skip; a.z = z; a.dt_bias = dt_bias;

@@ -734,8 +734,9 @@ gdr_status gdr_rotary_table(int length, int rot, double base, const gdr_rotary_s
  *
  * Sizes: K from 2 to 4; D a multiple of 8, at most 2^20; T up to 2^30, B up to 65535.
  * Pointers are 16-byte aligned (starts any), x_stride a multiple of 16 bytes. Arithmetic
- * is fp32, rounded once. Outputs overlap no input (state_out not state either). A value
- * that is not finite reaches its own and the next K - 1 tokens of its document.
+ * is fp32, rounded once. Outputs overlap neither inputs (state_out not state either) nor one
+ * another; equal addresses are refused. A value that is not finite reaches its own and the
+ * next K - 1 tokens of its document.
  */
 typedef struct {
   int B, T, D, K;
@@ -782,11 +783,14 @@ gdr_status gdr_short_conv_step(const gdr_conv_shape* shape, const void* x, const
  * tokens of the former are their stride's elements apart (0: dense), batch rows T tokens
  * apart, so that parts of one projection are taken as they are. h0 [B,D,N] fp32 or NULL
  * (zero), hT the end state or NULL; starts as above: a start clears the state before its
- * token. y is dense. h0 and hT may be one buffer; other outputs overlap no input.
+ * token. y is dense. h0 and hT may be one buffer; other outputs overlap neither inputs nor one
+ * another (equal addresses are refused).
  *
  * Sizes: N in {8, 16, 32, 64}; D / G a multiple of 8, D up to 2^20; T up to 2^30, B up to
  * 65535. Pointers are 16-byte aligned (starts any), strides multiples of 16 bytes. A is
- * finite and usually negative. The state, the decays and every sum are fp32; y is rounded
+ * finite and usually negative: the sums of u and the products of decays over a segment of the
+ * tokens are formed, so where those pass 3.4e38 (growth beyond exp(88)) results are not
+ * finite, also from states of zero. The state, the decays and every sum are fp32; y is rounded
  * once. Against 64 bits (2-norm) states and fp32 outputs and gradients come to about 1e-6, and
  * to 3e-6 where equal slow steps (memories of thousands of tokens) round the same way every
  * time; token by token (gdr_state_space_step) such a state rounds after every one, up to 2^-25

@@ -197,6 +197,46 @@ def test_norms(L):
     assert bwd(ins, outs, P + 4) == INVALID
 
 
+def test_outputs_are_apart(L):
+    """An output that is an input's or another output's buffer is refused, whichever it is."""
+    s = ctypes.byref(conv())
+    ins, outs = [P * i for i in range(1, 6)], [P * i for i in (6, 7)]
+    for o in range(2):
+        for i in (0, 4):                             # x, state
+            bad = list(outs)
+            bad[o] = ins[i]
+            assert L.gdr_short_conv_fwd(s, *ins, *bad, NULL) == INVALID
+    assert L.gdr_short_conv_fwd(s, *ins, outs[0], outs[0], NULL) == INVALID
+    # x weight bias starts state dy dstate_out | dx dweight dbias dstate
+    ins, outs = [P * i for i in range(1, 8)], [P * i for i in range(8, 12)]
+    for o in range(4):
+        for i in (0, 1, 2, 4, 5, 6):
+            bad = list(outs)
+            bad[o] = ins[i]
+            assert L.gdr_short_conv_bwd(s, *ins, *bad, 99 * P, BIG, NULL) == INVALID
+        bad = list(outs)
+        bad[o] = outs[o - 1]
+        assert L.gdr_short_conv_bwd(s, *ins, *bad, 99 * P, BIG, NULL) == INVALID
+    s = ctypes.byref(space())
+    # x dt A B C skip z dt_bias starts h0 | y hT
+    ins, outs = [P * i for i in range(1, 11)], [P * i for i in (11, 12)]
+    for i in (0, 1, 3, 4, 6, 9):
+        assert L.gdr_state_space_fwd(s, *ins, ins[i], outs[1], 99 * P, BIG, NULL) == INVALID
+    for i in (0, 1, 2, 3, 4, 6):
+        assert L.gdr_state_space_fwd(s, *ins, outs[0], ins[i], 99 * P, BIG, NULL) == INVALID
+    assert L.gdr_state_space_fwd(s, *ins, outs[0], outs[0], 99 * P, BIG, NULL) == INVALID
+    # x dt A B C skip z dt_bias starts h0 dy dhT | dx ddt dA dB dC dskip dz ddt_bias dh0
+    ins, outs = [P * i for i in range(1, 13)], [P * i for i in range(13, 22)]
+    for o in range(9):
+        for i in (0, 1, 2, 3, 4, 5, 6, 7, 9, 10):
+            bad = list(outs)
+            bad[o] = ins[i]
+            assert L.gdr_state_space_bwd(s, *ins, *bad, 99 * P, BIG, NULL) == INVALID
+        bad = list(outs)
+        bad[o] = outs[o - 1]
+        assert L.gdr_state_space_bwd(s, *ins, *bad, 99 * P, BIG, NULL) == INVALID
+
+
 def test_python_refusals():
     """The wrappers name the argument; tensors on the CPU are refused."""
     x, w = torch.zeros(1, 8, 64), torch.zeros(64, 4)

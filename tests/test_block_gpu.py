@@ -313,6 +313,20 @@ def test_space_fast_decays(dtype):
     check_space(x)
 
 
+@DTYPES
+@pytest.mark.parametrize("T", [40, 700])
+def test_space_extreme_step_sizes(T, dtype):
+    """Steps of zero (dt of minus infinity, of the type's lowest value: tokens that leave the
+    state as it is) and steps after which nothing of the state is left."""
+    x = space_inputs(2, T, 24, 1, 16, dtype, 12)
+    x["dt"][0, 3::7] = -torch.inf
+    x["dt"][0, 5::11] = torch.finfo(dtype).min
+    x["dt"][1, ::2] = -200.0
+    x["dt"][1, 1::8] = 1e3
+    x["x"][1, 1::8] = 1e-3
+    check_space(x)
+
+
 def test_space_every_token_starts():
     x = space_inputs(1, 70, 16, 1, 16, BF, 7)
     x["starts"] = torch.ones(1, 70, dtype=torch.uint8, device="cuda")
