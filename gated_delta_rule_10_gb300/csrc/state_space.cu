@@ -5,8 +5,8 @@
 // Not a product of matrices: every (token, channel, state) has a decay of its own, so it is
 // an exponential and four multiply-adds each, against 8 bytes of bf16 for a token and
 // channel. What bounds it is the issue of instructions (60% of the slots), shared memory (57%)
-// and the fp32 pipe (51%), not HBM (1.7 TB/s): 493 us for 4 x 4096 x 4096 channels x 16 bf16,
-// 989 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
+// and the fp32 pipe (51%), not HBM (1.7 TB/s): 483 us for 4 x 4096 x 4096 channels x 16 bf16,
+// 951 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
 //
 // Cut into segments, a thread holds 8 states of two channels and walks the tokens in order;
 // N / 8 neighbouring lanes share the channels and add their parts of y. A tile of tokens is
@@ -14,7 +14,9 @@
 // inputs are copied to shared memory meanwhile, without registers (prefetched in registers:
 // 681 us for the first shape, then 583). With one channel a thread every B and C read from
 // shared memory served half as many states: 714. A thread stages what it has copied itself,
-// and takes y from where it has staged u, so that two barriers a tile are enough.
+// and takes y from where it has staged u. A warp stages the channels that it walks, so that only
+// B and C, in two places in turn, need the CTA's barrier, one a tile (with two: 487 us; 664 for
+// 644 with 8 states). With 64 states, whose B and C take more room, and uncut it is two.
 //
 // Few sequences are cut into segments until the CTAs fill the SMs: a first launch walks all
 // but the last one from zero for their end states and sums of u, a second chains them
@@ -36,7 +38,10 @@ struct Layout {
   static constexpr int kStates = NARROW ? 4 : 8;                 // states of each
   static constexpr int kLanes = N / kStates;                     // lanes of a channel
   static constexpr int kChannels = kOwn * kThreads / kLanes;     // channels of a CTA
-  static constexpr int kTile = NARROW || N > 16 ? 32 : N;        // tokens of a tile
+  // A warp stages the channels that it walks.
+  static constexpr bool kApart = !NARROW && N < 64;
+  static constexpr int kTile = NARROW || N == 64 ? 32 : N == 32 ? 16 : N;   // tokens of a tile
+  static constexpr int kRow = (kApart ? kOwn * 32 / kLanes : kChannels) / 8;   // vectors of 8
   static constexpr int kVecs = kTile * kChannels / 8;            // vectors of 8 channels in a tile
   static constexpr int kPer = (kVecs + kThreads - 1) / kThreads;
   static constexpr int kBcVecs = 2 * kTile * N / 8;              // vectors of B and C
@@ -47,7 +52,7 @@ template <typename T, int N, bool NARROW>
 struct __align__(16) Shared {
   using L = Layout<N, NARROW>;
   float u[L::kTile][L::kChannels], g[L::kTile][L::kChannels];    // u (then y), u x
-  float bc[2][L::kTile][N];
+  float bc[L::kApart ? 2 : 1][2][L::kTile][N];
   T x[2][L::kTile][L::kChannels], dt[L::kTile][L::kChannels], z[2][L::kTile][L::kChannels];
   T raw_bc[2][L::kTile][N];
   float bias[L::kChannels], skip[L::kChannels];
@@ -117,12 +122,17 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
   }
 
   bool mark = false;
+  // what a thread copies, stages and stores: vectors of 8 channels of a tile's tokens
+  const int first = L::kApart ? tid % 32 : tid, step = L::kApart ? 32 : kThreads;
+  const int wide = L::kApart ? tid / 32 * (8 * L::kRow) : 0;
+  auto token_of = [&](int i) { return (first + i * step) / L::kRow; };
+  auto channel_of = [&](int i) { return wide + 8 * ((first + i * step) % L::kRow); };
   // copies a tile's inputs: x, dt and z, B and C; `k` of two places for what the tile's end needs
   auto fetch = [&](int t0, int k) {
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kThreads, t = v / (L::kChannels / 8), d = 8 * (v % (L::kChannels / 8));
-      if (v < L::kVecs && t0 + t < t_end && ch.first + d < ch.end) {
+      const int t = token_of(i), d = channel_of(i);
+      if (t < L::kTile && t0 + t < t_end && ch.first + d < ch.end) {
         const long long row = row0 + t0 + t;
         copy8(&sm.x[k][t][d], static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
         copy8(&sm.dt[t][d], static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
@@ -147,8 +157,8 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
     copies_done();
 #pragma unroll
     for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kThreads, t = v / (L::kChannels / 8), d = 8 * (v % (L::kChannels / 8));
-      if (v >= L::kVecs) break;
+      const int t = token_of(i), d = channel_of(i);
+      if (t >= L::kTile) break;
       f32x2 x[4], u[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = u[j] = 0;
@@ -176,15 +186,15 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = 0;
       if (t0 + t < t_end) read8(&sm.raw_bc[which][t][n], x);
-      write8(&sm.bc[which][t][n], x);
+      write8(&sm.bc[L::kApart ? k : 0][which][t][n], x);
     }
     const unsigned m = __ballot_sync(0xffffffffu, mark);
-    if (tid == 0) sm.starts[0] = m;
+    if (tid == 0) sm.starts[L::kApart ? k : 0] = m;
   };
 
   int cleared = 0;
   // one token, which may be a document's first: this thread's parts of its channels' y
-  auto token = [&](int t, bool first, float (&y)[kOwn]) {
+  auto token = [&](int k, int t, bool first, float (&y)[kOwn]) {
     float u[kOwn], g[kOwn];
     if constexpr (kOwn == 2) {
       const float2 v = *reinterpret_cast<const float2*>(&sm.u[t][ci]);
@@ -202,8 +212,8 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
 #pragma unroll
         for (int i = 0; i < kStates / 2; ++i) h[o][i] = 0;
     }
-    const ulonglong2* B = reinterpret_cast<const ulonglong2*>(&sm.bc[0][t][n0]);
-    const ulonglong2* C = reinterpret_cast<const ulonglong2*>(&sm.bc[1][t][n0]);
+    const ulonglong2* B = reinterpret_cast<const ulonglong2*>(&sm.bc[k][0][t][n0]);
+    const ulonglong2* C = reinterpret_cast<const ulonglong2*>(&sm.bc[k][1][t][n0]);
     f32x2 part[kOwn];
 #pragma unroll
     for (int q = 0; q < kStates / 4; ++q) {
@@ -277,32 +287,35 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
   for (int t0 = t_begin; t0 < t_end; t0 += L::kTile, k ^= 1) {
     fetch(t0 + L::kTile, k ^ 1);
     const int nt = min(L::kTile, t_end - t0);
-    const unsigned starts = sm.starts[0];
+    const int place = L::kApart ? k : 0;
+    const unsigned starts = sm.starts[place];
     // (tokens behind the end have u = B = C = 0 and leave the states as they are)
     if (starts == 0 && nt == L::kTile) {
 #pragma unroll 2
       for (int t = 0; t < L::kTile; t += 4) {
         float y[4][kOwn];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) token(t + k, false, y[k]);
+        for (int j = 0; j < 4; ++j) token(place, t + j, false, y[j]);
         if (WALK) put(t, y);
       }
     } else {
       for (int t = 0; t < nt; t += 4) {
         float y[4][kOwn];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) token(t + k, (starts >> (t + k)) & 1, y[k]);
+        for (int j = 0; j < 4; ++j) token(place, t + j, (starts >> (t + j)) & 1, y[j]);
         if (WALK) put(t, y);
       }
       cleared |= starts != 0;
     }
-    __syncthreads();
+    if (L::kApart)
+      __syncwarp();
+    else
+      __syncthreads();
     if (WALK) {
 #pragma unroll
       for (int i = 0; i < L::kPer; ++i) {
-        const int v = tid + i * kThreads, t = v / (L::kChannels / 8);
-        const int d = 8 * (v % (L::kChannels / 8));
-        if (v >= L::kVecs || t0 + t >= t_end || ch.first + d >= ch.end) continue;
+        const int t = token_of(i), d = channel_of(i);
+        if (t >= L::kTile || t0 + t >= t_end || ch.first + d >= ch.end) continue;
         f32x2 x[4], z[4], skip[4], y[4];
         read8(&sm.u[t][d], y);
         if (a.skip) {
