@@ -90,11 +90,12 @@ double waves(long long n, int most, double first, double next) {
 // sequences are cut until the CTAs fill the SMs.
 // Forward: uncut, a CTA has half the channels, and needs no other launch; a cut costs a walk
 // over all segments but the last for their end states (0.65 of the other walk's time), and the
-// chain. Times of a token (us, bf16): uncut 0.084 and 0.062 (a CTA alone on its SM; a second
-// one beside it), cut 0.17 and 0.066, and a third of a tile for a CTA's start; 3% more where
-// all CTAs start together and stage their tiles in step. (4 x 4096 x 4096 channels x 16: 598
-// us uncut, 487 in 8 segments, 558 in 7; 1 x 65536 x 2048: 5510 uncut, 1158 in 19 segments,
-// 985 in 38, 958 in 114.)
+// chain. Times of a token (us, bf16): uncut 0.084 and 0.054 (a CTA alone on its SM; a second
+// one beside it), cut 0.17 and 0.055, and a third of a tile for a CTA's start; 3% more where
+// all CTAs start together and stage their tiles in step. The further launches take 5 us one
+// behind the other, and 8 of the host's. (1 x 512 x 4096 channels x 16: 45 us uncut, 29 in 16
+// segments; 4 x 4096 x 4096: 598 uncut, 483 in 8 segments, 558 in 7; 1 x 65536 x 2048: 5510
+// uncut, 1158 in 19 segments, 985 in 38, 958 in 114.)
 // The backward walks forward for its kept states anyway; a segment costs a CTA's start, 0.7
 // tiles (4 x 4096 x 2048 x 16: 955 us in 4 segments, 839 in 14, 814 in 19).
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
@@ -112,11 +113,11 @@ void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
     if (backward)
       cost = waves(ctas * segments, 2, 0.7, 0.3) * (len + 0.7);
     else if (segments == 1)
-      cost = waves(rows * blocks(gdr::space_channels(s->N, true)), 2, 0.084, 0.062) * s->T;
+      cost = waves(rows * blocks(gdr::space_channels(s->N, true)), 2, 0.084, 0.054) * s->T;
     else
-      cost = (waves(ctas * segments, 4, 0.17, 0.066) +
-              0.65 * waves(ctas * (segments - 1), 5, 0.17, 0.066)) * (len + 0.3) * tile *
-                 (1.0 + 0.03 * std::min(1.0, 4.0 * kSms / (ctas * segments))) + 25.0;
+      cost = (waves(ctas * segments, 4, 0.17, 0.055) +
+              0.65 * waves(ctas * (segments - 1), 5, 0.17, 0.055)) * (len + 0.3) * tile *
+                 (1.0 + 0.03 * std::min(1.0, 4.0 * kSms / (ctas * segments))) + 13.0;
     if (n == 1 || cost < best) {
       best = cost;
       per = len;
