@@ -12,8 +12,8 @@
 // - Gradients, tile by tile backward: a tile's states are computed again from its first one,
 //   kept every 4 tokens in shared memory, then by 4 tokens in registers with their decays.
 // Three exponentials and about 22 multiply-adds for each (token, channel, state) in all. The
-// second launch is 73% of the time (4 x 4096 x 2048 channels x 16 bf16: 804 us in all): two
-// warps a scheduler, which 252 registers a thread and 111 KB of shared memory a CTA leave,
+// second launch is 73% of the time (4 x 4096 x 2048 channels x 16 bf16: 805 us in all): two
+// warps a scheduler, which 255 registers a thread and 111 KB of shared memory a CTA leave,
 // issue 50% of the time. With half the states a thread (three CTAs an SM) it issues 58% of the
 // time but 30% more, and takes as long; so does half the tokens in registers. Tiles without a
 // document's start take a walk without branches (851 -> 831 us).
@@ -577,18 +577,18 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
 #pragma unroll
       for (int k = 0; k < kSub; ++k) {
         const int t = s * kSub + k;
-        if (MARKED && ((starts >> t) & 1)) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[p][j] = 0;
-        }
         const float4 B = *reinterpret_cast<const float4*>(Border + t * N + n0);
         const f32x2 b2[4] = {both(B.x), both(B.y), both(B.z), both(B.w)};
         const f32x2 u[2] = {*reinterpret_cast<const f32x2*>(&sm.u[t][c0]),
                             *reinterpret_cast<const f32x2*>(&sm.u[t][c1])};
         const f32x2 g[2] = {*reinterpret_cast<const f32x2*>(&sm.g[t][c0]),
                             *reinterpret_cast<const f32x2*>(&sm.g[t][c1])};
+        if (MARKED && ((starts >> t) & 1)) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[p][j] = 0;
+        }
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -600,10 +600,66 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
       for (int s = 0; s < subs; ++s) forth(s, std::false_type{});
     else
       for (int s = 0; s < subs; ++s) forth(s, std::true_type{});
+    // a token's sums over lanes: q, sum A w and C h over a channel's states, dB and dC over channels
+    struct Sums {
+      f32x2 q[2], r[2], y[2];
+      float b[4], c[4];
+    };
+    auto over_lanes = [&](int t, Sums& v) {
+      // over the state lanes: by halves over the 4 channels, then whole
+      auto over_states = [&](const f32x2 (&x)[2], float* out) {      // out: of channel cbase
+        float lo, hi, lo1, hi1;
+        split(x[0], lo, hi);
+        split(x[1], lo1, hi1);
+        lo += pass(lo1, 1);
+        hi += pass(hi1, 1);
+        if constexpr (L::kStateLanes == 2) {
+          *reinterpret_cast<float2*>(out + 2 * swap) = make_float2(lo, hi);
+        } else {
+          const bool up = sl & 2;
+          float keep = up ? hi : lo;
+          keep += pass(up ? lo : hi, 2);
+          if constexpr (L::kStateLanes >= 8) keep += pass(keep, 4);
+          if constexpr (L::kStateLanes >= 16) keep += pass(keep, 8);
+          if (sl < 4) out[2 * swap + up] = keep;
+        }
+      };
+      over_states(v.q, &sm.g[t][cbase]);
+      over_states(v.r, sm.r(t, cbase));
+      if (Z) over_states(v.y, &sm.p[t][cbase]);
+      // over the channel lanes
+      constexpr int kStep = L::kStateLanes;     // lanes to the next channel lane
+      v.b[0] += pass(v.b[1], kStep);
+      v.b[2] += pass(v.b[3], kStep);
+      v.c[0] += pass(v.c[1], kStep);
+      v.c[2] += pass(v.c[3], kStep);
+      float* out = sm.dbc(warp, t);
+      if constexpr (L::kChannelLanes >= 4) {
+        v.b[0] += pass(v.b[2], 2 * kStep);
+        v.c[0] += pass(v.c[2], 2 * kStep);
+        if constexpr (L::kChannelLanes >= 8) {
+          // one half of the lanes goes on with dB, the other with dC
+          const bool up = cl & 4;
+          float keep = up ? v.c[0] : v.b[0];
+          keep += pass(up ? v.b[0] : v.c[0], 4 * kStep);
+          if constexpr (L::kChannelLanes >= 16) keep += pass(keep, 8 * kStep);
+          if (cl < 8) out[(up ? N : 0) + n0 + nx] = keep;
+        } else {
+          out[n0 + nx] = v.b[0];
+          out[N + n0 + nx] = v.c[0];
+        }
+      } else {
+        out[n0 + nx] = v.b[0];
+        out[n0 + (2 ^ nx)] = v.b[2];
+        out[N + n0 + nx] = v.c[0];
+        out[N + n0 + (2 ^ nx)] = v.c[2];
+      }
+    };
     // and back
     auto back = [&](int s, auto marked) {
       constexpr bool MARKED = decltype(marked)::value;
       Items da[kSub], ah[kSub];     // decays, decayed states
+      Sums sums[2];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -647,7 +703,8 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
         const float4 C = *reinterpret_cast<const float4*>(Corder + t * N + n0);
         const f32x2 b2[4] = {both(B.x), both(B.y), both(B.z), both(B.w)};
         const f32x2 cc[4] = {both(C.x), both(C.y), both(C.z), both(C.w)};
-        f32x2 db[4], dc[4], q[2], r[2], y[2];
+        f32x2 db[4], dc[4];
+        f32x2 (&q)[2] = sums[k & 1].q, (&r)[2] = sums[k & 1].r, (&y)[2] = sums[k & 1].y;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const int c = p ? c1 : c0;
@@ -675,61 +732,16 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j) E[p][j] = 0;
         }
-        // over the state lanes: by halves over the 4 channels, then whole
-        auto over_states = [&](const f32x2 (&v)[2], float* out) {      // out: of channel cbase
-          float lo, hi, lo1, hi1;
-          split(v[0], lo, hi);
-          split(v[1], lo1, hi1);
-          lo += pass(lo1, 1);
-          hi += pass(hi1, 1);
-          if constexpr (L::kStateLanes == 2) {
-            *reinterpret_cast<float2*>(out + 2 * swap) = make_float2(lo, hi);
-          } else {
-            const bool up = sl & 2;
-            float keep = up ? hi : lo;
-            keep += pass(up ? lo : hi, 2);
-            if constexpr (L::kStateLanes >= 8) keep += pass(keep, 4);
-            if constexpr (L::kStateLanes >= 16) keep += pass(keep, 8);
-            if (sl < 4) out[2 * swap + up] = keep;
-          }
-        };
-        over_states(q, &sm.g[t][cbase]);
-        over_states(r, sm.r(t, cbase));
-        if (Z) over_states(y, &sm.p[t][cbase]);
-        // over the channel lanes
-        float vb[4], vc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          vb[j] = sum2(db[j]);
-          vc[j] = sum2(dc[j]);
+          sums[k & 1].b[j] = sum2(db[j]);
+          sums[k & 1].c[j] = sum2(dc[j]);
         }
-        constexpr int kStep = L::kStateLanes;     // lanes to the next channel lane
-        vb[0] += pass(vb[1], kStep);
-        vb[2] += pass(vb[3], kStep);
-        vc[0] += pass(vc[1], kStep);
-        vc[2] += pass(vc[3], kStep);
-        float* out = sm.dbc(warp, t);
-        if constexpr (L::kChannelLanes >= 4) {
-          vb[0] += pass(vb[2], 2 * kStep);
-          vc[0] += pass(vc[2], 2 * kStep);
-          if constexpr (L::kChannelLanes >= 8) {
-            // one half of the lanes goes on with dB, the other with dC
-            const bool up = cl & 4;
-            float keep = up ? vc[0] : vb[0];
-            keep += pass(up ? vb[0] : vc[0], 4 * kStep);
-            if constexpr (L::kChannelLanes >= 16) keep += pass(keep, 8 * kStep);
-            if (cl < 8) out[(up ? N : 0) + n0 + nx] = keep;
-          } else {
-            out[n0 + nx] = vb[0];
-            out[N + n0 + nx] = vc[0];
-          }
-        } else {
-          out[n0 + nx] = vb[0];
-          out[n0 + (2 ^ nx)] = vb[2];
-          out[N + n0 + nx] = vc[0];
-          out[N + n0 + (2 ^ nx)] = vc[2];
-        }
+        // a token's sums go over the lanes behind the next one's loads, which would else wait
+        // for them to be written (8 states 2%, 32 and 64 states and fp32 1% faster)
+        if (k < kSub - 1) over_lanes(t + 1, sums[(k + 1) & 1]);
       }
+      over_lanes(s * kSub, sums[0]);
     };
     if (starts == 0)
       for (int s = subs - 1; s >= 0; --s) back(s, std::false_type{});
