@@ -94,8 +94,8 @@ double waves(long long n, int most, double first, double next) {
 // one beside it), cut 0.17 and 0.055, and a third of a tile for a CTA's start; 3% more where
 // all CTAs start together and stage their tiles in step. The further launches take 5 us one
 // behind the other, and 8 of the host's. (1 x 512 x 4096 channels x 16: 45 us uncut, 29 in 16
-// segments; 4 x 4096 x 4096: 598 uncut, 483 in 8 segments, 558 in 7; 1 x 65536 x 2048: 5510
-// uncut, 1158 in 19 segments, 985 in 38, 958 in 114.)
+// segments; 4 x 4096 x 4096: 598 uncut, 485 in 8 or 32 segments, 558 in 7; 1 x 65536 x 2048:
+// 5510 uncut, 1158 in 19 segments, 985 in 38, 958 in 114.)
 // The backward walks forward for its kept states anyway; a segment costs a CTA's start, 0.7
 // tiles (4 x 4096 x 2048 x 16: 955 us in 4 segments, 839 in 14, 814 in 19).
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {

@@ -4,9 +4,9 @@
 //
 // Not a product of matrices: every (token, channel, state) has a decay of its own, so it is
 // an exponential and four multiply-adds each, against 8 bytes of bf16 for a token and
-// channel. What bounds it is the issue of instructions (60% of the slots), shared memory (57%)
-// and the fp32 pipe (51%), not HBM (1.7 TB/s): 483 us for 4 x 4096 x 4096 channels x 16 bf16,
-// 951 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
+// channel. What bounds it is the issue of instructions (63% of the slots), shared memory (62%)
+// and the fp32 pipe (53%), not HBM (1.9 TB/s): 486 us for 4 x 4096 x 4096 channels x 16 bf16,
+// 957 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
 //
 // Cut into segments, a thread holds 8 states of two channels and walks the tokens in order;
 // N / 8 neighbouring lanes share the channels and add their parts of y. A tile of tokens is
