@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
 }
 
 __global__ void __launch_bounds__(1024) block_weights_kernel(const BlockNormsBwdArgs a, int rows) {
-  column_sum(a.partial, rows, 2 * a.D, [&](int i, float s) {
+  column_sum<32>(a.partial, rows, 2 * a.D, [&](int i, float s) {
     if (i >= a.D) {
       a.dpre[i - a.D] = s;
     } else {

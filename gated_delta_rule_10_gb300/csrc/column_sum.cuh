@@ -1,25 +1,29 @@
-// Column sums of a gradient's partial rows, in a fixed order: a CTA takes 32 columns, its
-// 32 warps every 32nd row; `put(column, sum)` stores the result.
+// Column sums of a gradient's partial rows, in a fixed order: a CTA takes 32 columns, each of
+// its WARPS warps every WARPS-th row; `put(column, sum)` stores the result. More warps wait
+// less for few columns' rows, fewer let more CTAs run at once (the filter's gradient, 288 rows
+// of 20480 columns: 8 warps 2 us faster than 32; the norms', 304 of 4096: 1 us slower).
 #pragma once
 
 #include <cuda_runtime.h>
 
 namespace gdr {
 
-template <class Put>
+template <int WARPS, class Put>
 __device__ __forceinline__ void column_sum(const float* partial, int rows, int columns, Put put) {
-  __shared__ float s[32][33];
+  constexpr int kOwn = 32 / WARPS;      // columns that a warp finishes
+  __shared__ float s[WARPS][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float x = 0.f;
   if (c < columns)
-#pragma unroll 4
-    for (int r = warp; r < rows; r += 32) x += partial[static_cast<size_t>(r) * columns + c];
+#pragma unroll 8
+    for (int r = warp; r < rows; r += WARPS) x += partial[static_cast<size_t>(r) * columns + c];
   s[warp][lane] = x;
   __syncthreads();
-  x = s[lane][warp];   // column `warp` of the block
+  const int own = warp * kOwn + lane / WARPS;
+  x = s[lane % WARPS][own];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  if (lane == 0 && blockIdx.x * 32 + warp < columns) put(blockIdx.x * 32 + warp, x);
+  for (int off = WARPS / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  if (lane % WARPS == 0 && blockIdx.x * 32 + own < columns) put(blockIdx.x * 32 + own, x);
 }
 
 }  // namespace gdr

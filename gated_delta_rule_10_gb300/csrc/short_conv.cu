@@ -8,8 +8,8 @@
 // is copied to the thread's own places in shared memory, two batches of 4 tokens ahead, which
 // takes no registers and no barrier. Neighbouring threads have neighbouring channels.
 // 65536 x 4096 bf16: 165 us, 0.96 of measured HBM bandwidth (two batches of 8 in registers:
-// 176; 8 channels a thread, filter in single loads: 494). Gradients of 4 x 4096 x 4096: 94 us,
-// 0.63 (batches in registers: 113); K = 2 takes 71, and 6 are the second launch.
+// 176; 8 channels a thread, filter in single loads: 494). Gradients of 4 x 4096 x 4096: 91 us,
+// 0.65 (batches in registers: 113); K = 2 takes 72, and 5 are the second launch.
 #include <type_traits>
 
 #include "column_sum.cuh"
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(K, sizeof(T) == 4))
   }
 }
 
-__global__ void __launch_bounds__(1024) filter_grad_kernel(const ConvArgs a, int rows) {
-  column_sum(a.partial, rows, (a.K + 1) * a.D, [&](int i, float s) {
+__global__ void __launch_bounds__(256) filter_grad_kernel(const ConvArgs a, int rows) {
+  column_sum<8>(a.partial, rows, (a.K + 1) * a.D, [&](int i, float s) {
     const int k = i / a.D, d = i % a.D;
     if (k < a.K)
       a.dweight[static_cast<long long>(d) * a.K + k] = s;
@@ -577,7 +577,7 @@ cudaError_t launch_short_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t stre
     if (err != cudaSuccess) return err;
     short_conv_bwd_kernel<decltype(t), k>
         <<<static_cast<unsigned>(grid), kBwdThreads, kBytes, stream>>>(a, run, groups, slices);
-    filter_grad_kernel<<<((a.K + 1) * a.D + 31) / 32, 1024, 0, stream>>>(a, a.B * groups);
+    filter_grad_kernel<<<((a.K + 1) * a.D + 31) / 32, 256, 0, stream>>>(a, a.B * groups);
     return cudaGetLastError();
   });
 }
