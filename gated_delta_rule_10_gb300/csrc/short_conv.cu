@@ -8,8 +8,9 @@
 // is copied to the thread's own places in shared memory, two batches of 4 tokens ahead, which
 // takes no registers and no barrier. Neighbouring threads have neighbouring channels.
 // 65536 x 4096 bf16: 165 us, 0.96 of measured HBM bandwidth (two batches of 8 in registers:
-// 176; 8 channels a thread, filter in single loads: 494). Gradients of 4 x 4096 x 4096: 91 us,
-// 0.65 (batches in registers: 113); K = 2 takes 72, and 5 are the second launch.
+// 176; 8 channels a thread, filter in single loads: 494). Gradients of 4 x 4096 x 4096: 86 us,
+// 0.69 (batches in registers: 113; a branch for the activation at each token: 91); K = 2 takes 71,
+// and 5 are the second launch.
 #include <type_traits>
 
 #include "column_sum.cuh"
@@ -344,8 +345,8 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(K, sizeof(T) == 4))
         r.store(dst + static_cast<long long>(K - 1 + e) * a.D);
     };
     // one token; INNER: of the run, with K - 1 others of its document and the run behind it
-    auto token = [&](const Raw<T, V>& raw_x, const Raw<T, V>& raw_y, int now, auto inner) {
-      constexpr bool INNER = decltype(inner)::value;
+    auto token = [&](const Raw<T, V>& raw_x, const Raw<T, V>& raw_y, int now, auto inner, auto activated) {
+      constexpr bool INNER = decltype(inner)::value, SILU = decltype(activated)::value;
       f32x2 v[H], g[H];
       raw_x.get(v);
       raw_y.get(g);
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(K, sizeof(T) == 4))
             for (int i = 0; i < H; ++i) prev[j][i] = 0;
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        if (a.silu) {
+        if (SILU) {
           f32x2 s = fma2(w[K - 1][i], v[i], bias[i]);
 #pragma unroll
           for (int j = 0; j < K - 1; ++j) s = fma2(w[K - 2 - j][i], prev[j][i], s);
@@ -402,27 +403,33 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(K, sizeof(T) == 4))
 #pragma unroll
       for (int i = 0; i < H; ++i) prev[0][i] = v[i];
     };
-    auto tokens = [&](int stage, int t) {
+    auto tokens = [&](int stage, int t, auto activated) {
       auto load = [&](int k, int which) { return *place(stage, k, which); };
       if (marks[stage] == 0 && back == K - 1 && t - (K - 1) >= t0 && t + kBwdBatch <= t1) {
 #pragma unroll
-        for (int k = 0; k < kBwdBatch; ++k) token(load(k, 0), load(k, 1), t + k, std::true_type{});
+        for (int k = 0; k < kBwdBatch; ++k) token(load(k, 0), load(k, 1), t + k, std::true_type{}, activated);
       } else {
 #pragma unroll 1
         for (int k = 0; k < kBwdBatch && t + k < stop; ++k) {
           back = (marks[stage] >> (8 * k)) & 0xff ? 0 : min(back + 1, K - 1);
-          token(load(k, 0), load(k, 1), t + k, std::false_type{});
+          token(load(k, 0), load(k, 1), t + k, std::false_type{}, activated);
         }
       }
     };
-    for (int t = t0; t < stop; t += kStages * kBwdBatch) {
+    auto walk = [&](auto activated) {
+      for (int t = t0; t < stop; t += kStages * kBwdBatch) {
 #pragma unroll
-      for (int i = 0; i < kStages; ++i) {
-        fetch((i + kStages - 1) % kStages, t + (i + kStages - 1) * kBwdBatch);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        tokens(i, t + i * kBwdBatch);
+        for (int i = 0; i < kStages; ++i) {
+          fetch((i + kStages - 1) % kStages, t + (i + kStages - 1) * kBwdBatch);
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+          tokens(i, t + i * kBwdBatch, activated);
+        }
       }
-    }
+    };
+    if (a.silu)
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
     if (stop == a.T) {   // what is behind the last token comes from the state's gradient
 #pragma unroll
       for (int j = 1; j < K; ++j) {
