@@ -154,30 +154,41 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
     mark = a.starts && tid < L::kTile && t0 + tid < t_end && a.starts[row0 + t0 + tid] != 0;
   };
   // what this thread has copied, as the walk reads it
+  const bool full = ch.first + L::kChannels <= ch.end;
   auto stage = [&](int t0, int k) {
     copies_done();
+    // PLAIN: nothing of the tile is missing and u is a softplus, so that no branch parts the
+    // vectors' long chains
+    auto steps = [&](auto plain) {
+      constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-    for (int i = 0; i < L::kPer; ++i) {
-      const int t = token_of(i), d = channel_of(i);
-      if (t >= L::kTile) break;
-      f32x2 x[4], u[4];
+      for (int i = 0; i < L::kPer; ++i) {
+        const int t = token_of(i), d = channel_of(i);
+        if (t >= L::kTile) break;
+        f32x2 x[4], u[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = u[j] = 0;
-      if (t0 + t < t_end && ch.first + d < ch.end) {
-        f32x2 bias[4];
-        read8(&sm.x[k][t][d], x);
-        read8(&sm.dt[t][d], u);
-        read8(&sm.bias[d], bias);
+        for (int j = 0; j < 4; ++j) x[j] = u[j] = 0;
+        if (PLAIN || (t0 + t < t_end && ch.first + d < ch.end)) {
+          f32x2 bias[4];
+          read8(&sm.x[k][t][d], x);
+          read8(&sm.dt[t][d], u);
+          read8(&sm.bias[d], bias);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          u[j] = add2(u[j], bias[j]);
-          if (a.softplus) u[j] = softplus2(u[j]);
-          x[j] = mul2(u[j], x[j]);
+          for (int j = 0; j < 4; ++j) u[j] = add2(u[j], bias[j]);
+          if (PLAIN || a.softplus)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = softplus2(u[j]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = mul2(u[j], x[j]);
         }
+        write8(&sm.u[t][d], u);
+        write8(&sm.g[t][d], x);
       }
-      write8(&sm.u[t][d], u);
-      write8(&sm.g[t][d], x);
-    }
+    };
+    if (full && a.softplus && t0 + L::kTile <= t_end)
+      steps(std::true_type{});
+    else
+      steps(std::false_type{});
 #pragma unroll
     for (int i = 0; i < L::kBcPer; ++i) {
       const int v = tid + i * kThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
@@ -326,25 +337,33 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
       __syncwarp();
     else
       __syncthreads();
-    if (WALK) {
+    auto finish = [&](auto plain) {
+      constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
       for (int i = 0; i < L::kPer; ++i) {
         const int t = token_of(i), d = channel_of(i);
-        if (t >= L::kTile || t0 + t >= t_end || ch.first + d >= ch.end) continue;
+        if (t >= L::kTile || (!PLAIN && (t0 + t >= t_end || ch.first + d >= ch.end))) continue;
         f32x2 x[4], z[4], skip[4], y[4];
         read8(&sm.u[t][d], y);
-        if (a.skip) {
+        if (PLAIN || a.skip) {
           read8(&sm.x[k][t][d], x);
           read8(&sm.skip[d], skip);
-        }
-        if (a.z) read8(&sm.z[k][t][d], z);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (a.skip) y[j] = fma2(skip[j], x[j], y[j]);
-          if (a.z) y[j] = mul2(y[j], mul2(z[j], sigmoid2(z[j])));
+          for (int j = 0; j < 4; ++j) y[j] = fma2(skip[j], x[j], y[j]);
+        }
+        if (PLAIN || a.z) {
+          read8(&sm.z[k][t][d], z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], mul2(z[j], sigmoid2(z[j])));
         }
         store_pairs(static_cast<T*>(a.y) + (row0 + t0 + t) * a.D + ch.first + d, y);
       }
+    };
+    if (WALK) {
+      if (full && nt == L::kTile && a.skip && a.z)
+        finish(std::true_type{});
+      else
+        finish(std::false_type{});
     }
     if (t0 + L::kTile < t_end) {
       stage(t0 + L::kTile, k ^ 1);

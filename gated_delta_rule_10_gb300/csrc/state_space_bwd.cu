@@ -145,12 +145,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
         if (CUT) read8(&sm.dy[t][d], p);
         if (CUT && a.z) read8(&sm.z[t][d], z);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          u[j] = add2(u[j], bias[j]);
-          if (a.softplus) u[j] = softplus2(u[j]);
-          x[j] = mul2(u[j], x[j]);
-          if (CUT && a.z) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
-        }
+        for (int j = 0; j < 4; ++j) u[j] = add2(u[j], bias[j]);
+        if (a.softplus)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = softplus2(u[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = mul2(u[j], x[j]);
+        if (CUT && a.z)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
       }
       write8(&sm.u[t][d], u);
       write8(&sm.g[t][d], x);
@@ -506,9 +509,12 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
         if (Z) read8(&sm.z[buf][Z ? t : 0][d], z);
         read8(&sm.bias[d], bias);
 #pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = add2(u[j], bias[j]);
+        if (a.softplus)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = softplus2(u[j]);
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
-          u[j] = add2(u[j], bias[j]);
-          if (a.softplus) u[j] = softplus2(u[j]);
           x[j] = mul2(u[j], x[j]);
           if (Z) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
         }
@@ -765,11 +771,13 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
         f32x2 z[4], y[4], dz[4];
         read8(&sm.z[buf][Z ? t : 0][d], z);
         read8(&sm.p[t][d], y);
+        if (a.skip)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = fma2(skip[j], x[j], y[j]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // silu = z sg, its slope sg (1 + z (1 - sg)) = sg + silu (1 - sg)
           const f32x2 sg = sigmoid2(z[j]), act = mul2(z[j], sg);
-          if (a.skip) y[j] = fma2(skip[j], x[j], y[j]);
           dz[j] = mul2(mul2(p[j], y[j]), fma2(act, fma2(sg, minus, one), sg));
           p[j] = mul2(p[j], act);
         }
@@ -783,11 +791,15 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         dx[j] = mul2(u[j], q[j]);
-        if (a.skip) dx[j] = fma2(skip[j], p[j], dx[j]);
         // (A2 is log2(e) A)
         w[j] = fma2(x[j], q[j], mul2(w[j], both(1.f / kLog2e)));
-        if (a.softplus) w[j] = mul2(w[j], sigmoid2(add2(dt[j], bias[j])));
       }
+      if (a.skip)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dx[j] = fma2(skip[j], p[j], dx[j]);
+      if (a.softplus)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], sigmoid2(add2(dt[j], bias[j])));
       store_pairs(static_cast<T*>(a.dx) + out, dx);
       store_pairs(static_cast<T*>(a.ddt) + out, w);
       if (a.dt_bias) write8(sm.r(t, d), w);
