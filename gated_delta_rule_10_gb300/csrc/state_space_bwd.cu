@@ -127,38 +127,47 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
     }
     mark = a.starts && tid < L::kTile && t0 + tid < t_end && a.starts[row0 + t0 + tid] != 0;
   };
-  // what this thread has copied, as the walk reads it
+  // what this thread has copied, as the walk reads it; PLAIN: nothing of the tile is missing,
+  // u is a softplus and there is a gate, so that no branch parts the vectors' long chains
+  const bool full = ch.first + L::kChannels <= ch.end;
   auto stage = [&](int t0) {
     copies_done();
+    auto steps = [&](auto plain) {
+      constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-    for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kThreads, t = v / (L::kChannels / 8), d = 8 * (v % (L::kChannels / 8));
-      if (v >= L::kVecs) break;
-      f32x2 x[4], u[4], p[4];
+      for (int i = 0; i < L::kPer; ++i) {
+        const int v = tid + i * kThreads, t = v / (L::kChannels / 8), d = 8 * (v % (L::kChannels / 8));
+        if (v >= L::kVecs) break;
+        f32x2 x[4], u[4], p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = u[j] = p[j] = 0;
-      if (t0 + t < t_end && ch.first + d < ch.end) {
-        f32x2 bias[4], z[4];
-        read8(&sm.x[t][d], x);
-        read8(&sm.dt[t][d], u);
-        read8(&sm.bias[d], bias);
-        if (CUT) read8(&sm.dy[t][d], p);
-        if (CUT && a.z) read8(&sm.z[t][d], z);
+        for (int j = 0; j < 4; ++j) x[j] = u[j] = p[j] = 0;
+        if (PLAIN || (t0 + t < t_end && ch.first + d < ch.end)) {
+          f32x2 bias[4], z[4];
+          read8(&sm.x[t][d], x);
+          read8(&sm.dt[t][d], u);
+          read8(&sm.bias[d], bias);
+          if (CUT) read8(&sm.dy[t][d], p);
+          if (CUT && (PLAIN || a.z)) read8(&sm.z[t][d], z);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = add2(u[j], bias[j]);
-        if (a.softplus)
+          for (int j = 0; j < 4; ++j) u[j] = add2(u[j], bias[j]);
+          if (PLAIN || a.softplus)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) u[j] = softplus2(u[j]);
+            for (int j = 0; j < 4; ++j) u[j] = softplus2(u[j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = mul2(u[j], x[j]);
-        if (CUT && a.z)
+          for (int j = 0; j < 4; ++j) x[j] = mul2(u[j], x[j]);
+          if (CUT && (PLAIN || a.z))
 #pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
+            for (int j = 0; j < 4; ++j) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
+        }
+        write8(&sm.u[t][d], u);
+        write8(&sm.g[t][d], x);
+        if (CUT) write8(&sm.p[t][d], p);
       }
-      write8(&sm.u[t][d], u);
-      write8(&sm.g[t][d], x);
-      if (CUT) write8(&sm.p[t][d], p);
-    }
+    };
+    if (full && a.softplus && (!CUT || a.z) && t0 + L::kTile <= t_end)
+      steps(std::true_type{});
+    else
+      steps(std::false_type{});
 #pragma unroll
     for (int i = 0; i < L::kBcPer; ++i) {
       const int v = tid + i * kThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
@@ -489,40 +498,49 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
   const int t_last = (t_end - 1) / kTile * kTile;
   fetch(t_last, 0);
   __syncthreads();
+  const bool full = ch.first + L::kChannels <= ch.end;
   int buf = 0;
   for (int t0 = t_last; t0 >= t_begin; t0 -= kTile, buf ^= 1) {
     const int nt = min(kTile, t_end - t0);
     copies_done();
-    // u, u x and p of what this thread has copied
+    // u, u x and p of what this thread has copied; PLAIN: as above
+    const bool plain = full && nt == kTile && a.softplus && a.skip;
+    auto steps = [&](auto all) {
+      constexpr bool PLAIN = decltype(all)::value;
 #pragma unroll
-    for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
-      if (v >= L::kVecs) break;
-      f32x2 x[4], u[4], p[4];
+      for (int i = 0; i < L::kPer; ++i) {
+        const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
+        if (v >= L::kVecs) break;
+        f32x2 x[4], u[4], p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = u[j] = p[j] = 0;
-      if (t < nt && ch.first + d < ch.end) {
-        f32x2 bias[4], z[4];
-        read8(&sm.x[buf][t][d], x);
-        read8(&sm.dt[buf][t][d], u);
-        read8(&sm.dy[buf][t][d], p);
-        if (Z) read8(&sm.z[buf][Z ? t : 0][d], z);
-        read8(&sm.bias[d], bias);
+        for (int j = 0; j < 4; ++j) x[j] = u[j] = p[j] = 0;
+        if (PLAIN || (t < nt && ch.first + d < ch.end)) {
+          f32x2 bias[4], z[4];
+          read8(&sm.x[buf][t][d], x);
+          read8(&sm.dt[buf][t][d], u);
+          read8(&sm.dy[buf][t][d], p);
+          if (Z) read8(&sm.z[buf][Z ? t : 0][d], z);
+          read8(&sm.bias[d], bias);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = add2(u[j], bias[j]);
-        if (a.softplus)
+          for (int j = 0; j < 4; ++j) u[j] = add2(u[j], bias[j]);
+          if (PLAIN || a.softplus)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) u[j] = softplus2(u[j]);
+            for (int j = 0; j < 4; ++j) u[j] = softplus2(u[j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = mul2(u[j], x[j]);
-          if (Z) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
+          for (int j = 0; j < 4; ++j) {
+            x[j] = mul2(u[j], x[j]);
+            if (Z) p[j] = mul2(p[j], mul2(z[j], sigmoid2(z[j])));
+          }
         }
+        write8(&sm.u[t][d], u);
+        write8(&sm.g[t][d], x);
+        write8(&sm.p[t][d], p);
       }
-      write8(&sm.u[t][d], u);
-      write8(&sm.g[t][d], x);
-      write8(&sm.p[t][d], p);
-    }
+    };
+    if (plain)
+      steps(std::true_type{});
+    else
+      steps(std::false_type{});
     // B and C in all orders
 #pragma unroll
     for (int i = 0; i < L::kBcPer; ++i) {
@@ -756,61 +774,66 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
 
     // the tile's outputs
     __syncthreads();
+    auto finish = [&](auto all) {
+      constexpr bool PLAIN = decltype(all)::value;
+      f32x2 sum[4];
+      read8(sm.px[tid], sum);
 #pragma unroll
-    for (int i = 0; i < L::kPer; ++i) {
-      const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
-      if (v >= L::kVecs || t >= nt || ch.first + d >= ch.end) continue;
-      const size_t out = static_cast<size_t>(row0 + t0 + t) * a.D + ch.first + d;
-      const f32x2 one = both(1.f), minus = both(-1.f);
-      f32x2 x[4], q[4], w[4], p[4], skip[4];
-      read8(&sm.x[buf][t][d], x);
-      read8(&sm.dy[buf][t][d], p);
-      read8(&sm.g[t][d], q);
-      read8(&sm.skip[d], skip);
-      if (Z) {
-        f32x2 z[4], y[4], dz[4];
-        read8(&sm.z[buf][Z ? t : 0][d], z);
-        read8(&sm.p[t][d], y);
-        if (a.skip)
+      for (int i = 0; i < L::kPer; ++i) {
+        const int v = tid + i * kBwdThreads, t = v / L::kRow, d = 8 * (v % L::kRow);
+        if (v >= L::kVecs || (!PLAIN && (t >= nt || ch.first + d >= ch.end))) continue;
+        const size_t out = static_cast<size_t>(row0 + t0 + t) * a.D + ch.first + d;
+        const f32x2 one = both(1.f), minus = both(-1.f);
+        f32x2 x[4], q[4], w[4], p[4], skip[4];
+        read8(&sm.x[buf][t][d], x);
+        read8(&sm.dy[buf][t][d], p);
+        read8(&sm.g[t][d], q);
+        read8(&sm.skip[d], skip);
+        if (Z) {
+          f32x2 z[4], y[4], dz[4];
+          read8(&sm.z[buf][Z ? t : 0][d], z);
+          read8(&sm.p[t][d], y);
+          if (PLAIN || a.skip)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = fma2(skip[j], x[j], y[j]);
+            for (int j = 0; j < 4; ++j) y[j] = fma2(skip[j], x[j], y[j]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // silu = z sg, its slope sg (1 + z (1 - sg)) = sg + silu (1 - sg)
+            const f32x2 sg = sigmoid2(z[j]), act = mul2(z[j], sg);
+            dz[j] = mul2(mul2(p[j], y[j]), fma2(act, fma2(sg, minus, one), sg));
+            p[j] = mul2(p[j], act);
+          }
+          store_pairs(static_cast<T*>(a.dz) + out, dz);
+        }
+        f32x2 bias[4], u[4], dt[4], dx[4];
+        read8(&sm.dt[buf][t][d], dt);
+        read8(&sm.bias[d], bias);
+        read8(&sm.u[t][d], u);
+        read8(sm.r(t, d), w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          // silu = z sg, its slope sg (1 + z (1 - sg)) = sg + silu (1 - sg)
-          const f32x2 sg = sigmoid2(z[j]), act = mul2(z[j], sg);
-          dz[j] = mul2(mul2(p[j], y[j]), fma2(act, fma2(sg, minus, one), sg));
-          p[j] = mul2(p[j], act);
+          dx[j] = mul2(u[j], q[j]);
+          // (A2 is log2(e) A)
+          w[j] = fma2(x[j], q[j], mul2(w[j], both(1.f / kLog2e)));
         }
-        store_pairs(static_cast<T*>(a.dz) + out, dz);
-      }
-      f32x2 bias[4], u[4], dt[4], dx[4];
-      read8(&sm.dt[buf][t][d], dt);
-      read8(&sm.bias[d], bias);
-      read8(&sm.u[t][d], u);
-      read8(sm.r(t, d), w);
+        if (PLAIN || a.skip)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        dx[j] = mul2(u[j], q[j]);
-        // (A2 is log2(e) A)
-        w[j] = fma2(x[j], q[j], mul2(w[j], both(1.f / kLog2e)));
-      }
-      if (a.skip)
+          for (int j = 0; j < 4; ++j) dx[j] = fma2(skip[j], p[j], dx[j]);
+        if (PLAIN || a.softplus)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dx[j] = fma2(skip[j], p[j], dx[j]);
-      if (a.softplus)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], sigmoid2(add2(dt[j], bias[j])));
-      store_pairs(static_cast<T*>(a.dx) + out, dx);
-      store_pairs(static_cast<T*>(a.ddt) + out, w);
-      if (a.dt_bias) write8(sm.r(t, d), w);
-      if (a.skip) {
-        f32x2 sum[4];
-        read8(sm.px[tid], sum);
+          for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], sigmoid2(add2(dt[j], bias[j])));
+        store_pairs(static_cast<T*>(a.dx) + out, dx);
+        store_pairs(static_cast<T*>(a.ddt) + out, w);
+        write8(sm.r(t, d), w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[j] = fma2(p[j], x[j], sum[j]);
-        write8(sm.px[tid], sum);
       }
-    }
+      write8(sm.px[tid], sum);
+    };
+    if (plain)
+      finish(std::true_type{});
+    else
+      finish(std::false_type{});
     const int blocks = gridDim.x / a.G, block = blockIdx.x % blocks;
     for (int i = tid; i < nt * N / 2; i += kBwdThreads) {      // four sums each
       const int t = i / (N / 2), j = i % (N / 2) * 4;
