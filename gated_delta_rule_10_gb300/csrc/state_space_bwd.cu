@@ -253,10 +253,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
     const unsigned starts = sm.starts[0];
     if (starts == 0 && nt == L::kTile) {
       if (CUT && !cleared) {
-#pragma unroll 4
+#pragma unroll
         for (int t = 0; t < L::kTile; ++t) token(t, false, true);
       } else {
-#pragma unroll 4
+#pragma unroll
         for (int t = 0; t < L::kTile; ++t) token(t, false, false);
       }
     } else {
@@ -852,8 +852,13 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
 #pragma unroll
       for (int i = 0; i < L::kSums; ++i) {
         const int d = tid + i * kBwdThreads;
-        if (d < L::kChannels)
+        if (d >= L::kChannels) break;
+        if (nt == kTile) {
+#pragma unroll
+          for (int t = 0; t < kTile; ++t) dbias[i] += *sm.r(t, d);
+        } else {
           for (int t = 0; t < nt; ++t) dbias[i] += *sm.r(t, d);
+        }
       }
     }
   }
