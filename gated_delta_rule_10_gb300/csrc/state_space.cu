@@ -5,8 +5,8 @@
 // Not a product of matrices: every (token, channel, state) has a decay of its own, so it is
 // an exponential and four multiply-adds each, against 8 bytes of bf16 for a token and
 // channel. What bounds it is the issue of instructions (63% of the slots), shared memory (62%)
-// and the fp32 pipe (53%), not HBM (1.9 TB/s): 486 us for 4 x 4096 x 4096 channels x 16 bf16,
-// 957 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
+// and the fp32 pipe (53%), not HBM (2 TB/s): 468 us for 4 x 4096 x 4096 channels x 16 bf16,
+// 906 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
 //
 // Cut into segments, a thread holds 8 states of two channels and walks the tokens in order;
 // N / 8 neighbouring lanes share the channels and add their parts of y. A tile of tokens is
@@ -129,32 +129,39 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
   auto token_of = [&](int i) { return (first + i * step) / L::kRow; };
   auto channel_of = [&](int i) { return wide + 8 * ((first + i * step) % L::kRow); };
   // copies a tile's inputs: x, dt and z, B and C; `k` of two places for what the tile's end needs
+  const bool full = ch.first + L::kChannels <= ch.end;
   auto fetch = [&](int t0, int k) {
+    auto copies = [&](auto plain) {      // PLAIN: nothing of the tile is missing
+      constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-    for (int i = 0; i < L::kPer; ++i) {
-      const int t = token_of(i), d = channel_of(i);
-      if (t < L::kTile && t0 + t < t_end && ch.first + d < ch.end) {
-        const long long row = row0 + t0 + t;
-        copy8(&sm.x[k][t][d], static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
-        copy8(&sm.dt[t][d], static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
-        if (WALK && a.z)
-          copy8(&sm.z[k][t][d], static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
+      for (int i = 0; i < L::kPer; ++i) {
+        const int t = token_of(i), d = channel_of(i);
+        if (t < L::kTile && (PLAIN || (t0 + t < t_end && ch.first + d < ch.end))) {
+          const long long row = row0 + t0 + t;
+          copy8(&sm.x[k][t][d], static_cast<const T*>(a.x) + row * a.xs + ch.first + d);
+          copy8(&sm.dt[t][d], static_cast<const T*>(a.dt) + row * a.dts + ch.first + d);
+          if (WALK && a.z)
+            copy8(&sm.z[k][t][d], static_cast<const T*>(a.z) + row * a.zs + ch.first + d);
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < L::kBcPer; ++i) {
-      const int v = tid + i * kThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
-      const int t = w / (N / 8), n = 8 * (w % (N / 8));
-      if (v < (WALK ? L::kBcVecs : L::kBcVecs / 2) && t0 + t < t_end)
-        copy8(&sm.raw_bc[which][t][n],
-              (which ? static_cast<const T*>(a.Cm) + (row0 + t0 + t) * a.cs
-                     : static_cast<const T*>(a.Bm) + (row0 + t0 + t) * a.bs) +
-                  ch.group * N + n);
-    }
+      for (int i = 0; i < L::kBcPer; ++i) {
+        const int v = tid + i * kThreads, which = v / (L::kBcVecs / 2), w = v % (L::kBcVecs / 2);
+        const int t = w / (N / 8), n = 8 * (w % (N / 8));
+        if (v < (WALK ? L::kBcVecs : L::kBcVecs / 2) && (PLAIN || t0 + t < t_end))
+          copy8(&sm.raw_bc[which][t][n],
+                (which ? static_cast<const T*>(a.Cm) + (row0 + t0 + t) * a.cs
+                       : static_cast<const T*>(a.Bm) + (row0 + t0 + t) * a.bs) +
+                    ch.group * N + n);
+      }
+    };
+    if (full && t0 + L::kTile <= t_end)
+      copies(std::true_type{});
+    else
+      copies(std::false_type{});
     mark = a.starts && tid < L::kTile && t0 + tid < t_end && a.starts[row0 + t0 + tid] != 0;
   };
   // what this thread has copied, as the walk reads it
-  const bool full = ch.first + L::kChannels <= ch.end;
   auto stage = [&](int t0, int k) {
     copies_done();
     // PLAIN: nothing of the tile is missing and u is a softplus, so that no branch parts the
@@ -316,7 +323,9 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
         }
         put(L::kTile - 4, y[(L::kTile / 4 + 1) % 2]);
       } else {
-#pragma unroll 2
+        // (N = 16 bf16 1% faster unrolled whole, fp32 4% slower)
+        constexpr int kAhead = sizeof(T) == 2 && L::kTile <= 16 ? 4 : 2;
+#pragma unroll kAhead
         for (int t = 0; t < L::kTile; t += 4) {
           float y[4][kOwn];
 #pragma unroll
