@@ -183,7 +183,7 @@ __device__ __forceinline__ void copy8(uint4* to, const T* from) {
 // Rows on their way or in use: the inputs are copied to the thread's own places in shared
 // memory, which takes no registers and no barrier. One row ahead; two ahead take as long or
 // longer (65536 x 512 bf16: 100 us for 87). Of more than 4096 columns the next row is requested
-// as soon as the current one is in registers, into its places (4096 x 8192 bf16: 105 us, 115
+// as soon as the current one is in registers, into its places (4096 x 8192 bf16: 103 us, 115
 // with places for two rows, 159 in registers, which spilled).
 constexpr int kInputs = 5;      // sum, dy, dres, x, gate
 template <int VEC>
@@ -285,27 +285,38 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
         dot = fma2(mul2(wp[i][j], dy[j]), r[j], dot);
       }
     }
+    // (what waits for no sum, ahead of the first)
+    f32x2 dr[VEC][4], sg[VEC][4], x[VEC][4];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      get(stage, 3, i, x[i]);
+      get(stage, 4, i, sg[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xx = fma2(x[i][j], x[i][j], xx);
+      if (a.gate) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sg[i][j] = sigmoid2(sg[i][j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sg[i][j] = both(1.f);
+      }
+    }
     float s0 = sum2(ss), s1 = sum2(dot);
     row_sum<TPR>(s0, s1, red[0]);
     const float ir = rsqrtf(s0 / n + a.eps);
     const f32x2 ir2 = both(ir), mr = both(-ir * ir * (s1 / n));
     dot = 0;
-    f32x2 dr[VEC][4], sg[VEC][4], x[VEC][4];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int c = lane + i * TPR;
-      f32x2 r[4], dy[4], g[4];
+      f32x2 r[4], dy[4];
       get(stage, 0, i, r);
       get(stage, 1, i, dy);
       get(stage, 2, i, dr[i]);
-      get(stage, 3, i, x[i]);
-      get(stage, 4, i, g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         dp[i][j] = fma2(dy[j], mul2(r[j], ir2), dp[i][j]);
         dr[i][j] = fma2(ir2, fma2(wp[i][j], dy[j], mul2(r[j], mr)), dr[i][j]);
-        sg[i][j] = a.gate ? sigmoid2(g[j]) : both(1.f);
-        xx = fma2(x[i][j], x[i][j], xx);
         dot = fma2(mul2(mul2(dr[i][j], ws[i][j]), sg[i][j]), x[i][j], dot);
       }
       if (live && c < nv) store_pairs(static_cast<T*>(a.dresidual) + row * a.D + 8 * c, dr[i]);

@@ -7,7 +7,7 @@
 // in registers, so that a token is read once per run plus K - 1 rows before it. What comes next
 // is copied to the thread's own places in shared memory, two batches of 4 tokens ahead, which
 // takes no registers and no barrier. Neighbouring threads have neighbouring channels.
-// 65536 x 4096 bf16: 165 us, 0.96 of measured HBM bandwidth (two batches of 8 in registers:
+// 65536 x 4096 bf16: 163 us, 0.97 of measured HBM bandwidth (two batches of 8 in registers:
 // 176; 8 channels a thread, filter in single loads: 494). Gradients of 4 x 4096 x 4096: 86 us,
 // 0.69 (batches in registers: 113; a branch for the activation at each token: 91); K = 2 takes 71,
 // and 5 are the second launch.
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
         for (int i = 0; i < H; ++i) prev[j][i] = 0;
   }
   T* yp = y + static_cast<long long>(t0) * a.D;
-  auto token = [&](const Raw<T, V>& raw) {
+  auto token = [&](const Raw<T, V>& raw, auto activated) {
     f32x2 v[H], s[H];
     raw.get(v);
 #pragma unroll
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
       s[i] = fma2(w[K - 1][i], v[i], bias[i]);
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) s[i] = fma2(w[K - 2 - j][i], prev[j][i], s[i]);
-      if (a.silu) s[i] = mul2(s[i], sigmoid2(s[i]));
+      if (decltype(activated)::value) s[i] = mul2(s[i], sigmoid2(s[i]));
     }
     Raw<T, V> out;
     out.put(s);
@@ -229,10 +229,10 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
 #pragma unroll
     for (int i = 0; i < H; ++i) prev[0][i] = v[i];
   };
-  auto tokens = [&](int stage, int t) {
+  auto tokens = [&](int stage, int t, auto activated) {
     if (t + kBatch <= t1 && marks[stage] == 0) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) token(ring[stage][k][threadIdx.x]);
+      for (int k = 0; k < kBatch; ++k) token(ring[stage][k][threadIdx.x], activated);
     } else {
 #pragma unroll 1
       for (int k = 0; k < kBatch && t + k < t1; ++k) {
@@ -241,18 +241,24 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_kernel(const ConvArgs 
           for (int j = 0; j < K - 1; ++j)
 #pragma unroll
             for (int i = 0; i < H; ++i) prev[j][i] = 0;
-        token(ring[stage][k][threadIdx.x]);
+        token(ring[stage][k][threadIdx.x], activated);
       }
     }
   };
-  for (int t = t0; t < t1; t += kFwdStages * kBatch) {
+  auto walk = [&](auto activated) {
+    for (int t = t0; t < t1; t += kFwdStages * kBatch) {
 #pragma unroll
-    for (int i = 0; i < kFwdStages; ++i) {
-      fetch((i + kFwdStages - 1) % kFwdStages, t + (i + kFwdStages - 1) * kBatch);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kFwdStages - 1) : "memory");
-      tokens(i, t + i * kBatch);
+      for (int i = 0; i < kFwdStages; ++i) {
+        fetch((i + kFwdStages - 1) % kFwdStages, t + (i + kFwdStages - 1) * kBatch);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kFwdStages - 1) : "memory");
+        tokens(i, t + i * kBatch, activated);
+      }
     }
-  }
+  };
+  if (a.silu)
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
   if (t1 == a.T && a.state_out) {     // prev is the last rows, zeros behind a start
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
