@@ -4,8 +4,8 @@
 //
 // Not a product of matrices: every (token, channel, state) has a decay of its own, so it is
 // an exponential and four multiply-adds each, against 8 bytes of bf16 for a token and
-// channel. What bounds it is the issue of instructions (63% of the slots), shared memory (62%)
-// and the fp32 pipe (53%), not HBM (2 TB/s): 468 us for 4 x 4096 x 4096 channels x 16 bf16,
+// channel. What bounds it is the issue of instructions (62% of the slots), shared memory (61%)
+// and the fp32 pipe (56%), not HBM (2 TB/s): 468 us for 4 x 4096 x 4096 channels x 16 bf16,
 // 906 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
 //
 // Cut into segments, a thread holds 8 states of two channels and walks the tokens in order;
@@ -15,8 +15,8 @@
 // 681 us for the first shape, then 583). With one channel a thread every B and C read from
 // shared memory served half as many states: 714. A thread stages what it has copied itself,
 // and takes y from where it has staged u. A warp stages the channels that it walks, so that only
-// B and C, in two places in turn, need the CTA's barrier, one a tile (with two: 487 us; 664 for
-// 644 with 8 states). With 64 states, whose B and C take more room, and uncut it is two.
+// B and C, in two places in turn, need the CTA's barrier, one a tile (with two 1% more, 3% with
+// 8 states); whole tiles are requested, staged and finished without branches (484 -> 468 us). With 64 states, whose B and C take more room, and uncut it is two.
 //
 // Few sequences are cut into segments until the CTAs fill the SMs: a first launch walks all
 // but the last one from zero for their end states and sums of u, a second chains them

@@ -12,11 +12,12 @@
 // - Gradients, tile by tile backward: a tile's states are computed again from its first one,
 //   kept every 4 tokens in shared memory, then by 4 tokens in registers with their decays.
 // Three exponentials and about 22 multiply-adds for each (token, channel, state) in all. The
-// second launch is 73% of the time (4 x 4096 x 2048 channels x 16 bf16: 805 us in all): two
+// second launch is 73% of the time (4 x 4096 x 2048 channels x 16 bf16: 763 us in all): two
 // warps a scheduler, which 255 registers a thread and 111 KB of shared memory a CTA leave,
-// issue 50% of the time. With half the states a thread (three CTAs an SM) it issues 58% of the
+// issue 51% of the time. With half the states a thread (three CTAs an SM) it issues 58% of the
 // time but 30% more, and takes as long; so does half the tokens in registers. Tiles without a
-// document's start take a walk without branches (851 -> 831 us).
+// document's start take a walk without branches (851 -> 831 us), whole tiles are staged and
+// finished without them (804 -> 770).
 //
 // A thread has 4 states of 4 channels (pairs of channels share an instruction), so that the
 // sums over channels (dB, dC) and those over states (q, sum A w, C h) each start inside a
