@@ -16,7 +16,8 @@
 // shared memory served half as many states: 714. A thread stages what it has copied itself,
 // and takes y from where it has staged u. A warp stages the channels that it walks, so that only
 // B and C, in two places in turn, need the CTA's barrier, one a tile (with two 1% more, 3% with
-// 8 states); whole tiles are requested, staged and finished without branches (484 -> 468 us). With 64 states, whose B and C take more room, and uncut it is two.
+// 8 states); with 64 states, whose B and C take more room, and uncut it is two. Whole tiles are
+// requested, staged and finished without branches (484 -> 468 us).
 //
 // Few sequences are cut into segments until the CTAs fill the SMs: a first launch walks all
 // but the last one from zero for their end states and sums of u, a second chains them
