@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
             const int c = lane + i * TPR;
             if (c < nv) copy8(place(stage, k, i), in[k] + row * a.D + 8 * c);
           }
-    if (kRows > 1 && row >= a.rows)      // beside the last rows: adds nothing
+    if (kRows > 1 && row >= a.rows)      // beside the last rows: zeros
 #pragma unroll
       for (int k = 0; k < kInputs; ++k)
 #pragma unroll
@@ -303,7 +303,9 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
     }
     float s0 = sum2(ss), s1 = sum2(dot);
     row_sum<TPR>(s0, s1, red[0]);
-    const float ir = rsqrtf(s0 / n + a.eps);
+    // (zero for a row that is not there, which then adds nothing: with eps = 0 its zeros would
+    // have no finite norm)
+    const float ir = kRows == 1 || live ? rsqrtf(s0 / n + a.eps) : 0.f;
     const f32x2 ir2 = both(ir), mr = both(-ir * ir * (s1 / n));
     dot = 0;
 #pragma unroll
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(threads<TPR>(), sizeof(T) == 2 ? 512 / threads
     s0 = sum2(xx);
     s1 = sum2(dot);
     row_sum<TPR>(s0, s1, red[1]);
-    const float ix = rsqrtf(s0 / n + a.eps);
+    const float ix = kRows == 1 || live ? rsqrtf(s0 / n + a.eps) : 0.f;
     const f32x2 ix2 = both(ix), mx = both(-ix * ix * (s1 / n));
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
