@@ -216,7 +216,8 @@ gdr_status gdr_short_conv_step(const gdr_conv_shape* shape, const void* x, const
                                const float* bias, void* state, void* y, gdr_stream_t stream) {
   const gdr_status st = check_conv(shape, true);
   if (st != GDR_OK) return st;
-  if (!given16(x) || !given16(weight) || !aligned(bias, 16) || !given16(state) || !given16(y))
+  if (!given16(x) || !given16(weight) || !aligned(bias, 16) || !given16(state) || !given16(y) ||
+      !apart({y, state}, {x, weight, bias}))
     return GDR_ERR_INVALID_ARG;
   gdr::ConvArgs a = conv_args(shape);
   a.x = x; a.weight = weight; a.bias = bias; a.state_out = state; a.y = y;

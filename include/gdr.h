@@ -763,7 +763,7 @@ gdr_status gdr_short_conv_bwd(const gdr_conv_shape* shape, const void* x, const 
                               gdr_stream_t stream);
 
 /* One token of each of B sequences (T = 1): x [B,D] (rows x_stride apart), state [B,K-1,D]
- * is read and moved on by one row in place, y [B,D]. */
+ * is read and moved on by one row in place, y [B,D]. y and state are buffers of their own. */
 gdr_status gdr_short_conv_step(const gdr_conv_shape* shape, const void* x, const float* weight,
                                const float* bias, void* state, void* y, gdr_stream_t stream);
 

@@ -1,0 +1,79 @@
+"""Refusals of the block operators, one argument changed at a time: every pointer of a call is an
+address of its own, the call as it stands is past the check in question (its status says so), and
+the change alone makes it a refusal. No call reaches a launch: its sizes need more CTAs than a grid
+has, which the host finds, or its workspace is too small."""
+import ctypes
+
+import pytest
+import torch
+
+import gated_delta_rule_10_gb300 as gdr
+from gated_delta_rule_10_gb300 import block
+
+OK, INVALID, CUDA, WORKSPACE = 0, 1, 3, 4
+ALL = (1 << 64) - 1              # a workspace of any size
+
+
+@pytest.fixture(scope="module")
+def L():
+    from gated_delta_rule_10_gb300 import build
+    build.build()
+    return block._lib()
+
+
+def conv(**kw):
+    base = dict(B=65535, T=1 << 30, D=1 << 20, K=4, dtype=gdr.GDR_BF16, silu=1, x_stride=0)
+    return gdr.ConvShape(**{**base, **kw})
+
+
+def space(**kw):
+    base = dict(B=2, T=1000, D=64, G=2, N=16, dtype=gdr.GDR_BF16, softplus=1, x_stride=0,
+                dt_stride=0, z_stride=0, b_stride=0, c_stride=0)
+    return gdr.StateSpaceShape(**{**base, **kw})
+
+
+class Call:
+    """A call by the names of its pointers, in order: `ins`, `outs` (what it writes, a state that
+    it updates among them), which of them may be NULL and which need no alignment."""
+
+    def __init__(self, call, order, outs, null=(), any_address=()):
+        self.call, self.order, self.outs = call, order.split(), outs.split()
+        self.null, self.any_address = null, any_address
+        self.ins = [n for n in self.order if n not in self.outs]
+        self.base = {n: 4096 * (i + 1) for i, n in enumerate(self.order)}
+
+    def __call__(self, **change):
+        p = {**self.base, **change}
+        return self.call([p[n] for n in self.order])
+
+    def check_pointers(self, passed):
+        """`passed`: the status of the call as it stands."""
+        assert self() == passed
+        for n in self.order:
+            assert self(**{n: None}) == (passed if n in self.null else INVALID), n
+            step = 1 if n in self.any_address else 8
+            assert self(**{n: self.base[n] + step}) == \
+                (passed if n in self.any_address else INVALID), n
+
+    def check_apart(self, allowed=()):
+        for i, o in enumerate(self.outs):
+            for n in self.ins + self.outs[:i]:
+                if (n, o) not in allowed:
+                    assert self(**{o: self.base[n]}) == INVALID, (n, o)
+
+
+# a lost refusal of these calls would launch on the addresses, which are no memory
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="for machines without a GPU")
+
+
+def conv_step_call(L):
+    s = conv(T=1, B=(1 << 31) - 1)
+    return Call(lambda p: L.gdr_short_conv_step(ctypes.byref(s), *p, None),
+                "x weight bias state y", "state y", null=("bias",))
+
+
+def test_conv_step_outputs_are_apart(L):
+    """y and the state are no other buffer of the call."""
+    f = conv_step_call(L)
+    assert f() == CUDA
+    f.check_apart()
