@@ -320,7 +320,7 @@ gdr_status gdr_state_space_step(const gdr_state_space_shape* shape, const void* 
   if (st != GDR_OK) return st;
   if (!given16(x) || !given16(dt) || !given16(A) || !given16(Bm) || !given16(Cm) ||
       !aligned(skip, 16) || !aligned(z, 16) || !aligned(dt_bias, 16) || !given16(state) ||
-      !given16(y))
+      !given16(y) || !apart({y, state}, {x, dt, A, Bm, Cm, skip, z, dt_bias}))
     return GDR_ERR_INVALID_ARG;
   gdr::SpaceArgs a = space_args(shape);
   a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.skip = skip; a.z = z; a.dt_bias = dt_bias;

@@ -834,7 +834,8 @@ gdr_status gdr_state_space_bwd(const gdr_state_space_shape* shape, const void* x
                                gdr_stream_t stream);
 
 /* One token of each of B sequences (T = 1): state [B,D,N] fp32 is read as h_{t-1} and
- * overwritten with h_t; the strides are those between sequences. */
+ * overwritten with h_t; the strides are those between sequences. y and state are buffers of
+ * their own. */
 gdr_status gdr_state_space_step(const gdr_state_space_shape* shape, const void* x, const void* dt,
                                 const float* A, const void* Bm, const void* Cm, const float* skip,
                                 const void* z, const float* dt_bias, float* state, void* y,

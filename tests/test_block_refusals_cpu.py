@@ -77,3 +77,15 @@ def test_conv_step_outputs_are_apart(L):
     f = conv_step_call(L)
     assert f() == CUDA
     f.check_apart()
+
+
+def space_step_call(L):
+    s = space(T=1, B=(1 << 31) - 1, D=1 << 20, G=1)
+    return Call(lambda p: L.gdr_state_space_step(ctypes.byref(s), *p, None),
+                "x dt A B C skip z dt_bias state y", "state y", null=("skip", "z", "dt_bias"))
+
+
+def test_space_step_outputs_are_apart(L):
+    f = space_step_call(L)
+    assert f() == CUDA
+    f.check_apart()
