@@ -171,7 +171,7 @@ gdr_status gdr_short_conv_fwd(const gdr_conv_shape* shape, const void* x, const 
   const gdr_status st = check_conv(shape, false);
   if (st != GDR_OK) return st;
   if (!given16(x) || !given16(weight) || !aligned(bias, 16) || !aligned(state, 16) || !given16(y) ||
-      !aligned(state_out, 16) || !apart({y, state_out}, {x, state}))
+      !aligned(state_out, 16) || !apart({y, state_out}, {x, weight, bias, starts, state}))
     return GDR_ERR_INVALID_ARG;
   gdr::ConvArgs a = conv_args(shape);
   a.x = x; a.weight = weight; a.bias = bias; a.starts = starts; a.state = state;
@@ -203,7 +203,7 @@ gdr_status gdr_short_conv_bwd(const gdr_conv_shape* shape, const void* x, const 
                                                 shape->B, shape->T, shape->D, shape->K,
                                                 shape->dtype == GDR_F32));
   if (st != GDR_OK) return st;
-  if (!apart({dx, dweight, dbias, dstate}, {x, weight, bias, state, dy, dstate_out}))
+  if (!apart({dx, dweight, dbias, dstate}, {x, weight, bias, starts, state, dy, dstate_out}))
     return GDR_ERR_INVALID_ARG;
   gdr::ConvArgs a = conv_args(shape);
   a.x = x; a.weight = weight; a.bias = bias; a.starts = starts; a.state = state;

@@ -89,3 +89,22 @@ def test_space_step_outputs_are_apart(L):
     f = space_step_call(L)
     assert f() == CUDA
     f.check_apart()
+
+
+def conv_calls(L):
+    s = conv()
+    fwd = Call(lambda p: L.gdr_short_conv_fwd(ctypes.byref(s), *p, None),
+               "x weight bias starts state y state_out", "y state_out",
+               null=("bias", "starts", "state", "state_out"), any_address=("starts",))
+    bwd = Call(lambda p, ws=1 << 20, n=ALL: L.gdr_short_conv_bwd(ctypes.byref(s), *p, ws, n, None),
+               "x weight bias starts state dy dstate_out dx dweight dbias dstate",
+               "dx dweight dbias dstate",
+               null=("bias", "starts", "state", "dstate_out", "dbias", "dstate"),
+               any_address=("starts",))
+    return fwd, bwd
+
+
+def test_conv_outputs_are_apart(L):
+    for f in conv_calls(L):
+        assert f() == CUDA
+        f.check_apart()
