@@ -249,7 +249,8 @@ gdr_status gdr_state_space_fwd(const gdr_state_space_shape* shape, const void* x
   cut(shape, false, &sp);
   st = check_workspace(workspace, ws_bytes, lay_out(shape, false, nullptr, &sp));
   if (st != GDR_OK) return st;
-  if (!apart({y}, {x, dt, Bm, Cm, z, h0, hT}) || !apart({hT}, {x, dt, A, Bm, Cm, z}))
+  // (hT may be h0)
+  if (!apart({y, hT}, {x, dt, A, Bm, Cm, skip, z, dt_bias, starts}) || !apart({y}, {h0}))
     return GDR_ERR_INVALID_ARG;
   lay_out(shape, false, static_cast<char*>(workspace), &sp);
   gdr::SpaceArgs a = space_args(shape);
@@ -295,9 +296,12 @@ gdr_status gdr_state_space_bwd(const gdr_state_space_shape* shape, const void* x
   st = check_workspace(workspace, ws_bytes, lay_out(shape, true, nullptr, &sp));
   if (st != GDR_OK) return st;
   // (dh0 may be dhT; what is not written may be anything)
-  if (!apart({dx, ddt, dA, dBm, dCm, skip ? dskip : nullptr, z ? dz : nullptr,
-              dt_bias ? ddt_bias : nullptr, dh0},
-             {x, dt, A, Bm, Cm, skip, z, dt_bias, h0, dy}))
+  float* const gskip = skip ? dskip : nullptr;
+  void* const gz = z ? dz : nullptr;
+  float* const gbias = dt_bias ? ddt_bias : nullptr;
+  if (!apart({dx, ddt, dA, dBm, dCm, gskip, gz, gbias, dh0},
+             {x, dt, A, Bm, Cm, skip, z, dt_bias, starts, h0, dy}) ||
+      !apart({dx, ddt, dA, dBm, dCm, gskip, gz, gbias}, {dhT}))
     return GDR_ERR_INVALID_ARG;
   lay_out(shape, true, static_cast<char*>(workspace), &sp);
   gdr::SpaceArgs a = space_args(shape);

@@ -108,3 +108,23 @@ def test_conv_outputs_are_apart(L):
     for f in conv_calls(L):
         assert f() == CUDA
         f.check_apart()
+
+
+def space_calls(L, s=None):
+    s = s or space()
+    fwd = Call(lambda p, n=ALL: L.gdr_state_space_fwd(ctypes.byref(s), *p, 1 << 20, n, None),
+               "x dt A B C skip z dt_bias starts h0 y hT", "y hT",
+               null=("skip", "z", "dt_bias", "starts", "h0", "hT"), any_address=("starts",))
+    bwd = Call(lambda p, n=ALL: L.gdr_state_space_bwd(ctypes.byref(s), *p, 1 << 20, n, None),
+               "x dt A B C skip z dt_bias starts h0 dy dhT dx ddt dA dB dC dskip dz ddt_bias dh0",
+               "dx ddt dA dB dC dskip dz ddt_bias dh0",
+               null=("skip", "z", "dt_bias", "starts", "h0", "dhT", "dh0"), any_address=("starts",))
+    return fwd, bwd
+
+
+@no_gpu
+def test_space_outputs_are_apart(L):
+    """But the states of a prompt, and the gradients of them, may be one buffer."""
+    fwd, bwd = space_calls(L)
+    fwd.check_apart(allowed=[("h0", "hT")])
+    bwd.check_apart(allowed=[("dhT", "dh0")])
