@@ -341,7 +341,7 @@ gdr_status gdr_block_norms(long long rows, int D, gdr_dtype dtype, const void* x
   if (rows == 0) return GDR_OK;
   if (!given16(x) || !aligned(gate, 16) || !given16(residual) || !given16(post_weight) ||
       !aligned(scale, 16) || !given16(pre_weight) || !given16(residual_out) || !given16(y) ||
-      y == residual_out)
+      !apart({residual_out, y}, {post_weight, scale, pre_weight}))
     return GDR_ERR_INVALID_ARG;
   gdr::BlockNormsArgs a{x, gate, residual, post_weight, scale, pre_weight, residual_out, y, rows,
                         D, eps};
@@ -373,6 +373,13 @@ gdr_status gdr_block_norms_bwd(long long rows, int D, gdr_dtype dtype, const voi
     return GDR_ERR_INVALID_ARG;
   st = check_workspace(workspace, ws_bytes, gdr::block_norms_bwd_workspace_bytes(rows, D));
   if (st != GDR_OK) return st;
+  // (rows may be written over rows of the inputs)
+  float* const gscale = scale ? dscale : nullptr;
+  if (!apart({dpost, gscale, dpre}, {post_weight, scale, pre_weight}) ||
+      (rows > 0 && (!apart({dpost, gscale, dpre}, {dy, dres, x, gate, sum}) ||
+                    !apart({dx, gate ? dgate : nullptr, dresidual, dpost, gscale, dpre},
+                           {post_weight, scale, pre_weight}))))
+    return GDR_ERR_INVALID_ARG;
   const cudaStream_t cs = stream_of(stream);
   if (rows == 0) {   // empty sums
     for (float* p : {dpost, scale ? dscale : dpre, dpre}) {

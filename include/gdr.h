@@ -851,7 +851,8 @@ gdr_status gdr_state_space_step(const gdr_state_space_shape* shape, const void* 
  *
  * x, gate, residual, residual_out, y in dtype; post_weight, scale, pre_weight [D] fp32;
  * gate and scale may be NULL (ones). Arithmetic is fp32. residual_out may be x, gate or
- * residual, and y any of them that is not residual_out; other overlaps are not allowed.
+ * residual, and y any of them that is not residual_out; other overlaps are not allowed (equal
+ * addresses are refused).
  * Pointers are 16-byte aligned; D a multiple of 8, at most 8192, rows < 2^31
  * (GDR_ERR_UNSUPPORTED beyond). rows = 0 launches nothing. The sums of squares must stay
  * below 3.4e38, and rows that are not finite give what gdr_add_rmsnorm's do.
@@ -865,7 +866,7 @@ gdr_status gdr_block_norms(long long rows, int D, gdr_dtype dtype, const void* x
  * Gradients of gdr_block_norms for dy of y and dres of residual_out (in dtype; dres may be
  * NULL). sum is the forward's residual_out. dx, dgate (with gate), dresidual [rows,D] in
  * dtype; dpost, dscale (with scale), dpre [D] fp32. dx, dgate and dresidual may be any of
- * the inputs of their kind (each a different one). workspace: at least
+ * the inputs of their kind (each a different one); other overlaps as above. workspace: at least
  * gdr_block_norms_bwd_workspace() bytes, 16-byte aligned. No sum uses atomics.
  */
 gdr_status gdr_block_norms_bwd_workspace(long long rows, int D, size_t* bytes);

@@ -128,3 +128,25 @@ def test_space_outputs_are_apart(L):
     fwd, bwd = space_calls(L)
     fwd.check_apart(allowed=[("h0", "hT")])
     bwd.check_apart(allowed=[("dhT", "dh0")])
+
+
+def norms_calls(L, rows=100, n=ALL):
+    fwd = Call(lambda p: L.gdr_block_norms(rows, 256, gdr.GDR_BF16, *p[:6], 1e-6, *p[6:], None),
+               "x gate residual post scale pre sum y", "sum y", null=("gate", "scale"))
+    bwd = Call(lambda p: L.gdr_block_norms_bwd(rows, 256, gdr.GDR_BF16, *p[:8], 1e-6, *p[8:],
+                                               1 << 20, n, None),
+               "dy dres x gate sum post scale pre dx dgate dresidual dpost dscale dpre",
+               "dx dgate dresidual dpost dscale dpre", null=("dres", "gate", "scale"))
+    return fwd, bwd
+
+
+@no_gpu
+def test_norms_outputs_are_apart(L):
+    """But rows may be written over rows that are read."""
+    fwd, bwd = norms_calls(L)
+    fwd.check_apart(allowed=[(i, o) for i in ("x", "gate", "residual") for o in ("sum", "y")])
+    bwd.check_apart(allowed=[(i, o) for i in ("dy", "dres", "x", "gate", "sum")
+                             for o in ("dx", "dgate", "dresidual")])
+    _, none = norms_calls(L, rows=0)         # the rows' pointers are not looked at, the weights' are
+    for o, n in (("dpost", "dpre"), ("dpost", "dscale"), ("dpre", "post"), ("dscale", "scale")):
+        assert none(**{o: none.base[n]}) == INVALID, (n, o)
