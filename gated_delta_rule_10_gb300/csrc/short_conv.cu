@@ -26,6 +26,17 @@ template <typename T, int V>
 struct __align__(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Raw {
   static constexpr int kWords = V * sizeof(T) / 4;
   uint32_t u[kWords];
+  // of 16 bytes or more, from rows that the kernel itself writes later
+  __device__ __forceinline__ void load_written(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      u[4 * i] = q.x;
+      u[4 * i + 1] = q.y;
+      u[4 * i + 2] = q.z;
+      u[4 * i + 3] = q.w;
+    }
+  }
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (kWords == 2) {
       const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
@@ -496,7 +507,8 @@ __global__ void __launch_bounds__(kFwdThreads) short_conv_step_kernel(const Conv
   for (int i = 0; i < R; ++i) {
     if (b0 + i >= a.B) break;
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) r[i][k].load(st + (i * (K - 1) + k) * static_cast<long long>(a.D));
+    for (int k = 0; k < K - 1; ++k)
+      r[i][k].load_written(st + (i * (K - 1) + k) * static_cast<long long>(a.D));
     r[i][K - 1].load(static_cast<const T*>(a.x) + (b0 + i) * a.xs + c);
   }
   f32x2 w[K][V / 2], bias[V / 2];

@@ -1,12 +1,34 @@
 """GPU tests of the block operators at the edges of what their header allows, against the float64
 oracle. Bars as in test_block_gpu.py, or derived at the test."""
 import pytest
+import torch
 
 import gated_delta_rule_10_gb300 as gdr
 from oracle import block
-from test_block_gpu import DTYPES, f64, near, norms_inputs, off
+from test_block_gpu import DTYPES, f64, near, norms_inputs, off, rnd
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ short convolution
+
+@DTYPES
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("N,D", [(3, 72), (153, 4096)])       # one and two sequences a thread
+def test_conv_steps_move_the_state_in_place(N, D, K, dtype):
+    """The state is read and moved on by one kernel: token after token, its rows are the last
+    tokens', bit for bit, also of the odd sequence."""
+    gen = torch.Generator(device="cuda").manual_seed(N + K)
+    w, b = rnd(gen, D, K) * 0.5, rnd(gen, D)
+    state = rnd(gen, N, K - 1, D).to(dtype)
+    rows = [state[:, k].clone() for k in range(K - 1)]
+    for _ in range(6):
+        x = rnd(gen, N, D).to(dtype)
+        y = gdr.short_conv_step(x, w, b, state)
+        rows.append(x)
+        s = f64(b) + sum(f64(w[:, k]) * f64(rows[len(rows) - K + k]) for k in range(K))
+        near(y, block.silu(s), 1e-6)
+        assert all(torch.equal(state[:, k], rows[len(rows) - K + 1 + k]) for k in range(K - 1))
 
 
 # ------------------------------------------------------------------ norms around a block
