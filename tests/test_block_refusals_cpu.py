@@ -56,10 +56,13 @@ class Call:
                 (passed if n in self.any_address else INVALID), n
 
     def check_apart(self, allowed=()):
+        """`allowed`: pairs that may be one buffer, which get as far as the call as it stands."""
+        passed = self()
+        assert passed == CUDA
         for i, o in enumerate(self.outs):
             for n in self.ins + self.outs[:i]:
-                if (n, o) not in allowed:
-                    assert self(**{o: self.base[n]}) == INVALID, (n, o)
+                want = passed if (n, o) in allowed else INVALID
+                assert self(**{o: self.base[n]}) == want, (n, o)
 
 
 # a lost refusal of these calls would launch on the addresses, which are no memory
@@ -69,14 +72,12 @@ no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="for machines with
 def conv_step_call(L):
     s = conv(T=1, B=(1 << 31) - 1)
     return Call(lambda p: L.gdr_short_conv_step(ctypes.byref(s), *p, None),
-                "x weight bias state y", "state y", null=("bias",))
+                "x weight bias state y", "state y", null=["bias"])
 
 
 def test_conv_step_outputs_are_apart(L):
     """y and the state are no other buffer of the call."""
-    f = conv_step_call(L)
-    assert f() == CUDA
-    f.check_apart()
+    conv_step_call(L).check_apart()
 
 
 def space_step_call(L):
@@ -86,9 +87,7 @@ def space_step_call(L):
 
 
 def test_space_step_outputs_are_apart(L):
-    f = space_step_call(L)
-    assert f() == CUDA
-    f.check_apart()
+    space_step_call(L).check_apart()
 
 
 def conv_calls(L):
@@ -106,7 +105,6 @@ def conv_calls(L):
 
 def test_conv_outputs_are_apart(L):
     for f in conv_calls(L):
-        assert f() == CUDA
         f.check_apart()
 
 
@@ -150,3 +148,71 @@ def test_norms_outputs_are_apart(L):
     _, none = norms_calls(L, rows=0)         # the rows' pointers are not looked at, the weights' are
     for o, n in (("dpost", "dpre"), ("dpost", "dscale"), ("dpre", "post"), ("dscale", "scale")):
         assert none(**{o: none.base[n]}) == INVALID, (n, o)
+
+
+# ------------------------------------------------------------------ pointers
+
+def test_conv_pointers_one_by_one(L):
+    for f in (*conv_calls(L), conv_step_call(L)):
+        f.check_pointers(CUDA)
+
+
+def test_space_pointers_one_by_one(L):
+    """Before the workspace's size is looked at."""
+    space_step_call(L).check_pointers(CUDA)
+    short = lambda f: Call(lambda p: f.call(p, 16), " ".join(f.order), " ".join(f.outs),  # noqa: E731
+                           f.null, f.any_address)
+    fwd, bwd = space_calls(L)
+    short(fwd).check_pointers(WORKSPACE)
+    bwd = short(bwd)
+    bwd.check_pointers(WORKSPACE)
+    # a gradient is needed with what it is of
+    for of, grad in (("skip", "dskip"), ("z", "dz"), ("dt_bias", "ddt_bias")):
+        for bad in (None, bwd.base[grad] + 8):
+            assert bwd(**{grad: bad}) == INVALID
+            assert bwd(**{of: None, grad: bad}) == WORKSPACE
+
+
+@no_gpu
+def test_norms_pointers_one_by_one(L):
+    norms_calls(L)[0].check_pointers(CUDA)
+
+
+def test_norms_gradients_pointers_one_by_one(L):
+    _, bwd = norms_calls(L, n=16)
+    bwd.check_pointers(WORKSPACE)
+    for of, grad in (("gate", "dgate"), ("scale", "dscale")):
+        for bad in (None, bwd.base[grad] + 8):
+            assert bwd(**{grad: bad}) == INVALID
+            assert bwd(**{of: None, grad: bad}) == WORKSPACE
+    # without rows only the weights' pointers are looked at
+    _, none = norms_calls(L, rows=0)
+    for n in ("post", "pre", "dpost", "dpre", "dscale"):
+        assert none(**{n: None}) == INVALID and none(**{n: none.base[n] + 8}) == INVALID
+
+
+def test_workspaces(L):
+    """One byte less than asked for, none and one that is not aligned are refused."""
+    n = ctypes.c_size_t()
+    s = conv(B=2, T=100, D=64)
+    assert L.gdr_short_conv_bwd_workspace(ctypes.byref(s), ctypes.byref(n)) == OK and n.value > 0
+    p = [4096 * i for i in range(1, 12)]
+    assert L.gdr_short_conv_bwd(ctypes.byref(s), *p, 1 << 20, n.value - 1, None) == WORKSPACE
+    assert L.gdr_short_conv_bwd(ctypes.byref(s), *p, None, n.value, None) == WORKSPACE
+    assert L.gdr_short_conv_bwd(ctypes.byref(s), *p, (1 << 20) + 4, n.value, None) == INVALID
+    s = space()
+    for name, count in (("fwd", 12), ("bwd", 21)):
+        f = getattr(L, "gdr_state_space_" + name)
+        assert getattr(L, "gdr_state_space_%s_workspace" % name)(ctypes.byref(s),
+                                                                 ctypes.byref(n)) == OK
+        p = [4096 * i for i in range(1, count + 1)]
+        assert n.value > 0
+        assert f(ctypes.byref(s), *p, 1 << 20, n.value - 1, None) == WORKSPACE
+        assert f(ctypes.byref(s), *p, None, n.value, None) == WORKSPACE
+        assert f(ctypes.byref(s), *p, (1 << 20) + 8, n.value, None) == INVALID
+    assert L.gdr_block_norms_bwd_workspace(100, 256, ctypes.byref(n)) == OK and n.value > 0
+    f = lambda ws, size: L.gdr_block_norms_bwd(  # noqa: E731
+        100, 256, gdr.GDR_BF16, *range(4096, 9 * 4096, 4096), 1e-6,
+        *range(9 * 4096, 15 * 4096, 4096), ws, size, None)
+    assert f(1 << 20, n.value - 1) == WORKSPACE and f(None, n.value) == WORKSPACE
+    assert f((1 << 20) + 4, n.value) == INVALID
