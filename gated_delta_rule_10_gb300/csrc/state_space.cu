@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(NARROW ? 256 : 128,
         const f32x2 u2 = both(u[o]), g2 = both(g[o]);
         f32x2& h0 = h[o][2 * q];
         f32x2& h1 = h[o][2 * q + 1];
-        h0 = fma2(g2, bq.x, mul2(exp2_pair(mul2(A2[o][2 * q], u2)), h0));
-        h1 = fma2(g2, bq.y, mul2(exp2_pair(mul2(A2[o][2 * q + 1], u2)), h1));
+        h0 = fma2(g2, bq.x, mul2(decay2(A2[o][2 * q], u2), h0));
+        h1 = fma2(g2, bq.y, mul2(decay2(A2[o][2 * q + 1], u2), h1));
         if (WALK) part[o] = fma2(cq.y, h1, q ? fma2(cq.x, h0, part[o]) : mul2(cq.x, h0));
       }
     }
@@ -516,11 +516,9 @@ __global__ void __launch_bounds__(kFlatThreads) space_step_kernel(const SpaceArg
         const float4 C = read4(static_cast<const T*>(a.Cm) + b * a.cs + group * N + n);
         const f32x2 v = both(kLog2e * ud), g = both(ud * xd);
         const f32x2 lo = fma2(g, pair(B.x, B.y),
-                              mul2(exp2_pair(mul2(pair(A[r].x, A[r].y), v)),
-                                         pair(h[r].x, h[r].y)));
+                              mul2(decay2(pair(A[r].x, A[r].y), v), pair(h[r].x, h[r].y)));
         const f32x2 hi = fma2(g, pair(B.z, B.w),
-                              mul2(exp2_pair(mul2(pair(A[r].z, A[r].w), v)),
-                                         pair(h[r].z, h[r].w)));
+                              mul2(decay2(pair(A[r].z, A[r].w), v), pair(h[r].z, h[r].w)));
         split(lo, h[r].x, h[r].y);
         split(hi, h[r].z, h[r].w);
         s = fmaf(C.x, h[r].x, fmaf(C.y, h[r].y, fmaf(C.z, h[r].z, C.w * h[r].w)));

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int i = 2 * q + j;
-          const f32x2 d = exp2_pair(mul2(A2[o][i], u2[o]));
+          const f32x2 d = decay2(A2[o][i], u2[o]);
           h[o][i] = fma2(g2[o], j ? bq.y : bq.x, mul2(d, h[o][i]));
           if (back) {
             P[o][i] = mul2(d, P[o][i]);
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
         for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            h[p][j] = fma2(g[p], b2[j], mul2(exp2_pair(mul2(A2[p][j], u[p])), h[p][j]));
+            h[p][j] = fma2(g[p], b2[j], mul2(decay2(A2[p][j], u[p]), h[p][j]));
       }
     };
     if (starts == 0)
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(BwdLayout<N, sizeof(T) == 4>::kBwdThreads, 2)
         for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            da[k][p][j] = exp2_pair(mul2(A2[p][j], u[p]));
+            da[k][p][j] = decay2(A2[p][j], u[p]);
             ah[k][p][j] = mul2(da[k][p][j], h[p][j]);
             h[p][j] = fma2(g[p], b2[j], ah[k][p][j]);
           }

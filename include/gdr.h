@@ -792,9 +792,11 @@ gdr_status gdr_short_conv_step(const gdr_conv_shape* shape, const void* x, const
  * tokens are formed, so where those pass 3.4e38 (growth beyond exp(88)) results are not
  * finite, also from states of zero. The state, the decays and every sum are fp32; y is rounded
  * once. Against 64 bits (2-norm) states and fp32 outputs and gradients come to about 1e-6, and
- * to 3e-6 where equal slow steps (memories of thousands of tokens) round the same way every
- * time; token by token (gdr_state_space_step) such a state rounds after every one, up to 2^-25
- * of it for each token that it keeps (1e-4 for memories of 10^4). A value that is not finite
+ * to 5e-6 with memories of thousands of tokens. Where a slow state's steps are all equal it rounds
+ * the same way every time, by up to 2^-25 of it for each token of a piece that is walked: 1e-5 for
+ * few sequences, which are cut into many pieces, but 1.2e-4 for 4096 tokens of a large batch, which
+ * are walked in two, and token by token (gdr_state_space_step). A sum that cancels (dBm and dCm of
+ * one token, over the channels) loses what cancels. A value that is not finite
  * reaches the later tokens of its document and channel (a group's channels, from Bm), in the
  * gradients also the earlier ones.
  */
