@@ -146,7 +146,8 @@ def test_norms_outputs_are_apart(L):
     bwd.check_apart(allowed=[(i, o) for i in ("dy", "dres", "x", "gate", "sum")
                              for o in ("dx", "dgate", "dresidual")])
     _, none = norms_calls(L, rows=0)         # the rows' pointers are not looked at, the weights' are
-    for o, n in (("dpost", "dpre"), ("dpost", "dscale"), ("dpre", "post"), ("dscale", "scale")):
+    for o, n in (("dpost", "dpre"), ("dpost", "dscale"), ("dpre", "post"), ("dscale", "scale"),
+                 ("dpost", "pre")):
         assert none(**{o: none.base[n]}) == INVALID, (n, o)
 
 
