@@ -90,14 +90,20 @@ double waves(long long n, int most, double first, double next) {
 // sequences are cut until the CTAs fill the SMs.
 // Forward: uncut, a CTA has half the channels, and needs no other launch; a cut costs a walk
 // over all segments but the last for their end states (0.65 of the other walk's time), and the
-// chain. Times of a token (us, bf16): uncut 0.084 and 0.054 (a CTA alone on its SM; a second
+// chain. Times of a token (us, bf16, 16 states): uncut 0.084 and 0.054 (a CTA alone on its SM; a second
 // one beside it), cut 0.17 and 0.055, and a third of a tile for a CTA's start; 3% more where
 // all CTAs start together and stage their tiles in step. The further launches take 5 us one
 // behind the other, and 8 of the host's. (1 x 512 x 4096 channels x 16: 45 us uncut, 29 in 16
-// segments; 4 x 4096 x 4096: 598 uncut, 485 in 8 or 32 segments, 558 in 7; 1 x 65536 x 2048:
-// 5510 uncut, 1158 in 19 segments, 985 in 38, 958 in 114.)
+// segments; 4 x 4096 x 4096: 542 uncut, 473 in 8 or 32 segments, 539 in 7; 1 x 65536 x 2048:
+// 4961 uncut, 1046 in 19 segments, 938 in 38, 912 in 114.)
 // The backward walks forward for its kept states anyway; a segment costs a CTA's start, 0.7
-// tiles (4 x 4096 x 2048 x 16: 955 us in 4 segments, 839 in 14, 814 in 19).
+// tiles (4 x 4096 x 2048 x 16: 906 us in 4 segments, 794 in 14, 770 in 19, 764 in 24).
+// fp32 and the other numbers of states are cut by the same times, though an SM holds three fp32
+// CTAs where four and five are counted, and one in the gradients of 16 states where two are: the
+// cut is near the best one all the same (4 x 4096 x 2048, against the best of 8 to 10 others:
+// fp32 299 us for 290, 8 states 180 for 180, 32 443 for 439, 64 902 for 899; gradients in fp32
+// 1060 for 1057, 8 states 633 for 629, 32 1346 for 1329, 64 2621 for 2586; at worst, fp32 of 1 x
+// 16384 x 2048, 309 for 291).
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
   const int tile = backward ? gdr::kSpaceTile : 32;
   const int tiles = (s->T + tile - 1) / tile, each = s->D / s->G;

@@ -12,7 +12,7 @@
 // are persistent, walk the rows and request the next row's vectors before the current
 // row's sums, so that loads are in flight through the barriers. 65536 x 4096 bf16: 396 us, all
 // of measured HBM (462 with an exact division in the sigmoid); gradients of 16384 x 2048: 94
-// us, 0.84, of which 7 are the second launch.
+// us, 0.84, of which 6 are the second launch.
 #include "block_norms.h"
 
 #include <type_traits>

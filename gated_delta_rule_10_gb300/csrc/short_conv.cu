@@ -548,9 +548,8 @@ cudaError_t by_taps(int K, bool f32, F f) {
 
 // Tokens of a run of the backward, and the CTAs' rows of partial sums, one for each batch row
 // and kRuns runs. The run is what takes least time by waves of four CTAs an SM, a run being
-// K - 1 tokens and its start, about 6 in all, longer than its own (4 x 4096 x 4096 bf16, as it
-// was with two larger CTAs an SM: 107 us with runs of 74 in 2.95 waves, 115 with 64 in 3.4,
-// 130 with 32).
+// K - 1 tokens and its start, about 6 in all, longer than its own (4 x 4096 x 4096 bf16: 91 us
+// with runs of 116 in 1.9 waves, 95 with 120 or 64, 100 with 48, 103 with 32).
 int bwd_groups(int T, int run) { return (T + kRuns * run - 1) / (kRuns * run); }
 int bwd_run(int B, int T, int D, int K, bool f32) {
   const int ctas = bwd_ctas(K, f32) * 152;

@@ -6,7 +6,7 @@
 // an exponential and four multiply-adds each, against 8 bytes of bf16 for a token and
 // channel. What bounds it is the issue of instructions (62% of the slots), shared memory (61%)
 // and the fp32 pipe (56%), not HBM (2 TB/s): 468 us for 4 x 4096 x 4096 channels x 16 bf16,
-// 906 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
+// 908 for 1 x 65536 x 2048. Multiply-adds run two to an instruction.
 //
 // Cut into segments, a thread holds 8 states of two channels and walks the tokens in order;
 // N / 8 neighbouring lanes share the channels and add their parts of y. A tile of tokens is

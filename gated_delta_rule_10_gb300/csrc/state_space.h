@@ -40,7 +40,7 @@ struct SpaceSplit {
   int* kept_clear = nullptr;  // [B, tiles] nonzero: a document started since the segment did
   float* dA_part = nullptr;   // [B * segments, D, N]
   float* d_part = nullptr;    // [B * segments, 2, D] of dskip and ddt_bias
-  float* bc_part = nullptr;   // [blocks, B, T, 2, N] of dBm and dCm
+  float* bc_part = nullptr;   // [blocks, B, T, G, 2, N] of dBm and dCm
 };
 
 int space_channels(int N, bool narrow);   // channels of a CTA: forward, backward

@@ -12,7 +12,7 @@
 // - Gradients, tile by tile backward: a tile's states are computed again from its first one,
 //   kept every 4 tokens in shared memory, then by 4 tokens in registers with their decays.
 // Three exponentials and about 22 multiply-adds for each (token, channel, state) in all. The
-// second launch is 73% of the time (4 x 4096 x 2048 channels x 16 bf16: 763 us in all): two
+// second launch is 73% of the time (4 x 4096 x 2048 channels x 16 bf16: 756 us in all): two
 // warps a scheduler, which 255 registers a thread and 111 KB of shared memory a CTA leave,
 // issue 51% of the time. With half the states a thread (three CTAs an SM) it issues 58% of the
 // time but 30% more, and takes as long; so does half the tokens in registers. Tiles without a
@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (CUT ? 4 : 5) : 1)
 constexpr int kTile = kSpaceTile;
 constexpr int kSub = 4;           // tokens whose decays and states are in registers
 
-// Warps of a CTA: what lets shared memory hold 8 warps an SM, or as many as it can.
+// Warps of a CTA. Of shared memory two CTAs have room on an SM, which are 8 warps, or 4 with 8
+// states (86 KB each); of fp32 one with 16 states (147 KB), and with 8 three of one warp.
 constexpr int bwd_warps(int N, bool f32) {
   if (N == 8) return f32 ? 1 : 2;      // (fp32: 641 us for 4 x 4096 x 1024 with two, 524)
   return 4;
