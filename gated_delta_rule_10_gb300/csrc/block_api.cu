@@ -90,9 +90,9 @@ double waves(long long n, int most, double first, double next) {
 // sequences are cut until the CTAs fill the SMs.
 // Forward: uncut, a CTA has half the channels, and needs no other launch; a cut costs a walk
 // over all segments but the last for their end states (0.65 of the other walk's time), and the
-// chain. Times of a token (us, bf16, 16 states): uncut 0.084 and 0.054 (a CTA alone on its SM; a second
-// one beside it), cut 0.17 and 0.055, and a third of a tile for a CTA's start; 3% more where
-// all CTAs start together and stage their tiles in step. The further launches take 5 us one
+// chain. Times of a token (us, bf16, 16 states): uncut 0.084 and 0.054 (a CTA alone on its SM; a
+// second one beside it), cut 0.17 and 0.055, and a third of a tile for a CTA's start; 3% more
+// where all CTAs start together and stage their tiles in step. The further launches take 5 us one
 // behind the other, and 8 of the host's. (1 x 512 x 4096 channels x 16: 45 us uncut, 29 in 16
 // segments; 4 x 4096 x 4096: 542 uncut, 473 in 8 or 32 segments, 539 in 7; 1 x 65536 x 2048:
 // 4961 uncut, 1046 in 19 segments, 938 in 38, 912 in 114.)
@@ -102,8 +102,8 @@ double waves(long long n, int most, double first, double next) {
 // CTAs where four and five are counted, and one in the gradients of 16 states where two are: the
 // cut is near the best one all the same (4 x 4096 x 2048, against the best of 8 to 10 others:
 // fp32 299 us for 290, 8 states 180 for 180, 32 443 for 439, 64 902 for 899; gradients in fp32
-// 1060 for 1057, 8 states 633 for 629, 32 1346 for 1329, 64 2621 for 2586; at worst, fp32 of 1 x
-// 16384 x 2048, 309 for 291).
+// 1060 for 1057, 8 states 633 for 629, 32 1346 for 1329, 64 2621 for 2586; the worst measured, fp32
+// of 1 x 16384 x 2048, 309 for 291).
 void cut(const gdr_state_space_shape* s, bool backward, gdr::SpaceSplit* sp) {
   const int tile = backward ? gdr::kSpaceTile : 32;
   const int tiles = (s->T + tile - 1) / tile, each = s->D / s->G;

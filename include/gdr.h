@@ -795,9 +795,9 @@ gdr_status gdr_short_conv_step(const gdr_conv_shape* shape, const void* x, const
  * to 5e-6 with memories of thousands of tokens. Where a slow state's steps are all equal it rounds
  * the same way every time, by up to 2^-25 of it for each token of a piece that is walked: 1e-5 for
  * few sequences, which are cut into many pieces, but 1.2e-4 for 4096 tokens of a large batch, which
- * are walked in two, and token by token (gdr_state_space_step). Growing states (A above zero) gather
- * up to 2^-24 for each token. A sum that cancels (dBm and dCm of one token, over the channels)
- * loses what cancels. A value that is not finite reaches the later tokens of its document and
+ * are walked in two, and token by token (gdr_state_space_step). Growing states (A above zero)
+ * gather up to 2^-24 for each token. A sum that cancels (dBm and dCm of one token, over the
+ * channels) loses what cancels. A value that is not finite reaches the later tokens of its document and
  * channel (a group's channels, from Bm), in the gradients also the earlier ones.
  */
 typedef struct {
